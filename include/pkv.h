@@ -373,6 +373,92 @@ PKV_API pkv_status pkv_spec_verify_attn_noalloc(const void* q, const int8_t* k_c
                                                 int32_t split_tokens, int32_t max_splits, void* out,
                                                 int32_t* dev_err, void* stream);
 
+/*
+ * The 4-bit cache [no counterpart on the pages; the next step down from the int8 and e4m3 caches of
+ * P91's review]. A row of head_dim = 256 elements is 128 bytes of e2m1 codes (element 2i in the low
+ * half of byte i, element 2i + 1 in the high half) and 16 e4m3 bytes, one scale per 16 consecutive
+ * elements; one fp32 scale per tensor (a device scalar) multiplies them all:
+ *   element i = e2m1(code i) * e4m3(scale byte i / 16) * scale.
+ * e2m1 magnitudes are 0, 0.5, 1, 1.5, 2, 3, 4, 6 for the codes 0..7; bit 3 of a code is the sign.
+ * Codes:  k_fp4 / v_fp4 uint8 [num_blocks][block_size][num_kv_heads][128], byte strides stride_blk,
+ *   stride_tok, stride_head. Scales: k_bscale / v_bscale uint8 [num_blocks][block_size][num_kv_heads]
+ *   [16], byte strides scale_stride_blk, scale_stride_tok, scale_stride_head. Bases 16-byte aligned,
+ *   strides positive multiples of 16; every block-id x stride product is formed in 64 bits.
+ * k_scale / v_scale: device pointers to one fp32 each, positive, finite and normal.
+ *
+ * kv_cache_write_fp4 - quantize a chunk's new K and V rows and store them through the block table.
+ *   Rows, positions, query_start_loc and max_q_len as for pkv_kv_cache_write (new rows 32-byte
+ *   aligned, new_stride_tok a multiple of 16 elements). Per group of 16 elements x of a row, g the
+ *   tensor's scale, every step one fp32 rounding:
+ *     a = max |x|;  s = e4m3(a / (6 g)) to nearest even, at most 448;  d = s g;
+ *     code = e2m1(x / d) to nearest even, magnitudes past 6 (infinity included) stored as 6, with the
+ *     sign of x. Where d is zero, subnormal or infinite the magnitudes are 0; a group holding a NaN
+ *     stores a NaN scale byte (0x7F) and codes 0.
+ *   Rows outside the table or pool, and requests with q_len > seq_len, are not written and set
+ *   PKV_ERR_DEVICE_BOUNDS; slots not addressed by a new row are untouched.
+ */
+PKV_API pkv_status pkv_kv_cache_write_fp4(const void* k_new, const void* v_new, int64_t new_stride_tok,
+                                          const int32_t* block_table, int64_t bt_stride, int32_t max_blocks,
+                                          const int32_t* seq_lens, const int32_t* query_start_loc,
+                                          int32_t num_reqs, int32_t max_q_len, uint8_t* k_fp4, uint8_t* v_fp4,
+                                          uint8_t* k_bscale, uint8_t* v_bscale, const float* k_scale,
+                                          const float* v_scale, int64_t num_blocks, int64_t stride_blk,
+                                          int64_t stride_tok, int64_t stride_head, int64_t scale_stride_blk,
+                                          int64_t scale_stride_tok, int64_t scale_stride_head, int32_t block_size,
+                                          int32_t num_kv_heads, int32_t head_dim, int32_t* dev_err, void* stream);
+
+/*
+ * kv_fp4_dequant_dense - read positions [pos_begin[r], pos_end[r]) of the 4-bit cache back as dense
+ * bf16, each at its own position:
+ *   k_dense[r][pos][h][i] = bf16_rn(fp32_rn((e2m1 * e4m3) * (*k_scale)))  (the first product is exact)
+ * and the same for V; dense outputs [num_reqs][max_ctx][num_kv_heads][256] contiguous, 32-byte
+ * aligned, other positions not written. The consumer is pkv_paged_prefill_attn on the dense rows with
+ * block_size = max_ctx and the identity table, as after pkv_kv_fp8_dequant_dense; a caller that keeps
+ * the dense rows of a prompt reads back only each chunk's new positions.
+ * pos_begin / pos_end: device int32 [num_reqs], 0 <= pos_begin; positions past max_ctx are left out and
+ * set PKV_ERR_DEVICE_BOUNDS. max_tokens: host upper bound on pos_end[r] - pos_begin[r] (sizes the grid;
+ * longer ranges are still read). Positions in a bad block read as zero (PKV_ERR_DEVICE_BOUNDS).
+ */
+PKV_API pkv_status pkv_kv_fp4_dequant_dense(const uint8_t* k_fp4, const uint8_t* v_fp4, const uint8_t* k_bscale,
+                                            const uint8_t* v_bscale, const float* k_scale, const float* v_scale,
+                                            int64_t num_blocks, int64_t stride_blk, int64_t stride_tok,
+                                            int64_t stride_head, int64_t scale_stride_blk,
+                                            int64_t scale_stride_tok, int64_t scale_stride_head,
+                                            const int32_t* block_table, int64_t bt_stride, int32_t max_blocks,
+                                            const int32_t* pos_begin, const int32_t* pos_end, int32_t num_reqs,
+                                            int32_t max_tokens, int32_t block_size, int32_t num_kv_heads,
+                                            int32_t head_dim, void* k_dense, void* v_dense, int64_t max_ctx,
+                                            int32_t* dev_err, void* stream);
+
+/*
+ * spec_verify_attn_fp4 - speculative-verify (T tokens a request) or decode (T = 1) attention over the
+ * 4-bit cache, in one call: partials and merge, the keys divided over the SMs from seq_lens on the
+ * device (no split to choose, so a captured graph stays balanced as the sequences grow).
+ *   q, out bf16 [num_reqs*T][num_q_heads][256], tokens and positions as for
+ *   pkv_spec_verify_attn_partial: token t of request r sits at position seq_lens[r] - T + t and attends
+ *   the keys up to it. out = softmax(softmax_scale q . k) v with fp32 scores, sums and accumulation;
+ *   the probabilities meet V in fp16. A token before position 0 (seq_lens[r] < T, an empty request
+ *   included) attends nothing and gives zeros.
+ * Keys in a block whose id is out of range, or past the table, read as zero (k = v = 0) and
+ * PKV_ERR_DEVICE_BOUNDS is recorded.
+ * workspace: caller-owned device memory, 16-byte aligned, contents scratch; calls that may overlap on
+ * the GPU (two streams, two graphs) need one each. pkv_spec_verify_fp4_workspace_bytes(n) bytes let n
+ * CTAs run: pass the device's SM count; a smaller one (at least that of n = 1) runs on fewer SMs.
+ * Requirements: num_q_heads / num_kv_heads <= 32; block_size a multiple of 8; q, out, caches, scale
+ * caches and their strides 16-byte aligned.
+ */
+PKV_API size_t pkv_spec_verify_fp4_workspace_bytes(int32_t num_ctas);
+PKV_API pkv_status pkv_spec_verify_attn_fp4(const void* q, const uint8_t* k_fp4, const uint8_t* v_fp4,
+                                            const uint8_t* k_bscale, const uint8_t* v_bscale, const float* k_scale,
+                                            const float* v_scale, int64_t num_blocks, int64_t stride_blk,
+                                            int64_t stride_tok, int64_t stride_head, int64_t scale_stride_blk,
+                                            int64_t scale_stride_tok, int64_t scale_stride_head,
+                                            const int32_t* block_table, int64_t bt_stride, int32_t max_blocks,
+                                            const int32_t* seq_lens, int32_t num_reqs, int32_t T,
+                                            int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                            int32_t block_size, float softmax_scale, void* out, void* workspace,
+                                            int64_t workspace_bytes, int32_t* dev_err, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

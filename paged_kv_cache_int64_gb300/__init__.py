@@ -21,6 +21,7 @@ __all__ = [
     "PKV_ERR_TIMEOUT", "PKV_QK_BF16", "PKV_QK_INT8", "PKV_KV_BF16", "PKV_KV_INT8", "PKV_KV_FP8", "PkvError", "lib",
     "library_path", "kv_cache_write", "kv_int8_stats_quant", "paged_prefill_attn_fp8", "kv_fp8_dequant_dense", "paged_prefill_attn", "paged_prefill_workspace_bytes", "spec_verify_workspace_bytes", "spec_verify_pick_split",
     "spec_verify_attn_partial", "spec_verify_attn_partial_fp8", "spec_verify_combine", "EXPORTED_SYMBOLS",
+    "kv_cache_write_fp4", "kv_fp4_dequant_dense", "spec_verify_attn_fp4", "spec_verify_fp4_workspace_bytes",
 ]
 
 PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA, PKV_ERR_DEVICE_BOUNDS, PKV_ERR_TIMEOUT = range(6)
@@ -33,6 +34,8 @@ EXPORTED_SYMBOLS = (
     "pkv_spec_verify_combine", "pkv_spec_verify_attn_partial_fp8", "pkv_spec_verify_noalloc_capacity_bytes",
     "pkv_spec_verify_attn_noalloc", "pkv_kv_cache_write", "pkv_paged_prefill_attn_fp8",
     "pkv_paged_prefill_workspace_bytes", "pkv_testing_set_wait_limit_ns", "pkv_spec_verify_pick_split",
+    "pkv_kv_cache_write_fp4", "pkv_kv_fp4_dequant_dense", "pkv_spec_verify_fp4_workspace_bytes",
+    "pkv_spec_verify_attn_fp4",
 )
 
 library_path = _build.LIB
@@ -80,6 +83,17 @@ def _load():
                                      vp, vp, i64, i64, vp, vp, i32, i32, i32, vp, vp]
     L.pkv_paged_prefill_attn_fp8.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, vp, i64, i32, vp, vp, i32, i32,
                                              i32, i32, i32, i32, i32, f32, vp, vp, i64, vp, vp]
+    cache4 = [i64] * 7  # num_blocks, three code strides, three scale strides
+    L.pkv_kv_cache_write_fp4.argtypes = [vp, vp, i64, vp, i64, i32, vp, vp, i32, i32, vp, vp, vp, vp, vp, vp, *cache4,
+                                         i32, i32, i32, vp, vp]
+    L.pkv_kv_fp4_dequant_dense.argtypes = [vp, vp, vp, vp, vp, vp, *cache4, vp, i64, i32, vp, vp, i32, i32, i32, i32,
+                                           i32, vp, vp, i64, vp, vp]
+    L.pkv_spec_verify_attn_fp4.argtypes = [vp, vp, vp, vp, vp, vp, vp, *cache4, vp, i64, i32, vp, i32, i32, i32, i32,
+                                           i32, i32, f32, vp, vp, i64, vp, vp]
+    L.pkv_spec_verify_fp4_workspace_bytes.argtypes = [i32]
+    L.pkv_spec_verify_fp4_workspace_bytes.restype = sz
+    for name in ("pkv_kv_cache_write_fp4", "pkv_kv_fp4_dequant_dense", "pkv_spec_verify_attn_fp4"):
+        getattr(L, name).restype = i32
     for name in ("pkv_paged_prefill_attn_fp8", "pkv_kv_cache_write", "pkv_kv_int8_stats_quant", "pkv_kv_fp8_dequant_dense", "pkv_paged_prefill_attn",
                  "pkv_spec_verify_attn_partial", "pkv_spec_verify_combine", "pkv_spec_verify_attn_partial_fp8"):
         getattr(L, name).restype = i32
@@ -292,3 +306,99 @@ def spec_verify_combine(part_o, part_lse, seq_lens, T, split_tokens, out, stream
 
 def splits_needed(max_seq_len: int, split_tokens: int) -> int:
     return max(1, math.ceil(max_seq_len / split_tokens))
+
+
+# ---------------------------------------------------------------------------------------------
+# the 4-bit cache: e2m1 codes uint8 [nb][bs][hkv][128], e4m3 scale bytes uint8 [nb][bs][hkv][16],
+# one fp32 scale per tensor
+# ---------------------------------------------------------------------------------------------
+
+def _cache4(k_fp4, v_fp4, k_bscale, v_bscale, k_scale, v_scale):
+    """The checked cache's device and the ABI's (num_blocks, strides) arguments, block_size, heads."""
+    nb, bs, hkv, row = k_fp4.shape
+    assert row == 128 and k_bscale.shape == (nb, bs, hkv, 16), "codes [nb][bs][hkv][128], scales [nb][bs][hkv][16]"
+    assert v_fp4.shape == k_fp4.shape and v_bscale.shape == k_bscale.shape
+    assert k_fp4.dtype == v_fp4.dtype == k_bscale.dtype == v_bscale.dtype == torch.uint8, "the 4-bit cache is uint8 tensors"
+    cs, ss = k_fp4.stride(), k_bscale.stride()
+    assert cs == v_fp4.stride() and ss == v_bscale.stride() and cs[3] == 1 and ss[3] == 1
+    assert k_scale.dtype == torch.float32 and v_scale.dtype == torch.float32
+    dev = k_fp4.device
+    assert dev.type == "cuda" and dev == v_fp4.device == k_bscale.device == v_bscale.device == k_scale.device == v_scale.device
+    return dev, (nb, cs[0], cs[1], cs[2], ss[0], ss[1], ss[2]), bs, hkv
+
+
+def _dptr(t, dev):
+    if t is None:
+        return None
+    assert t.device == dev, "tensors of one call must be on one device"
+    return t.data_ptr()
+
+
+def _launch(fn, dev, stream, *args):
+    """fn(*args, stream) with the tensors' device current and, unless given, on its current stream."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    if dev.index == torch.cuda.current_device():
+        rc = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, stream.cuda_stream)
+    if rc != PKV_OK:
+        _check(rc)
+
+
+def kv_cache_write_fp4(k_new, v_new, block_table, seq_lens, query_start_loc, max_q_len, k_fp4, v_fp4, k_bscale,
+                       v_bscale, k_scale, v_scale, dev_err=None, stream=None):
+    """Quantize the chunk's new rows k_new / v_new (bf16 [total_q][hkv][256], token stride free) to 4 bits
+    and store them into the paged cache at positions seq_lens[r] - q_len + i."""
+    dev, cache, bs, hkv = _cache4(k_fp4, v_fp4, k_bscale, v_bscale, k_scale, v_scale)
+    assert k_new.dtype == torch.bfloat16 and v_new.dtype == torch.bfloat16 and k_new.stride() == v_new.stride()
+    assert k_new.shape == v_new.shape and k_new.dim() == 3 and k_new.shape[1] == hkv
+    d = k_new.shape[2]
+    assert k_new.stride(2) == 1 and k_new.stride(1) == d, "new rows: [total][hkv][D], heads contiguous"
+    R = block_table.shape[0]
+    assert seq_lens.shape[0] == R and query_start_loc.shape[0] == R + 1
+    _launch(lib.pkv_kv_cache_write_fp4, dev, stream, _dptr(k_new, dev), _dptr(v_new, dev), k_new.stride(0),
+            _dptr(_i32(block_table), dev), block_table.stride(0), block_table.shape[1], _dptr(_i32(seq_lens), dev),
+            _dptr(_i32(query_start_loc), dev), R, int(max_q_len), k_fp4.data_ptr(), v_fp4.data_ptr(),
+            k_bscale.data_ptr(), v_bscale.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *cache, bs, hkv, d,
+            _dptr(dev_err, dev))
+
+
+def kv_fp4_dequant_dense(k_fp4, v_fp4, k_bscale, v_bscale, block_table, pos_begin, pos_end, max_tokens, k_scale, v_scale,
+                         k_dense, v_dense, dev_err=None, stream=None):
+    """Positions [pos_begin[r], pos_end[r]) of the 4-bit cache -> dense bf16 [R][max_ctx][hkv][256], each at
+    its own position."""
+    dev, cache, bs, hkv = _cache4(k_fp4, v_fp4, k_bscale, v_bscale, k_scale, v_scale)
+    assert k_dense.is_contiguous() and v_dense.is_contiguous() and k_dense.dtype == v_dense.dtype == torch.bfloat16
+    R, max_ctx = k_dense.shape[:2]
+    assert k_dense.shape == v_dense.shape and k_dense.dim() == 4 and k_dense.shape[2] == hkv
+    assert block_table.shape[0] == R and pos_begin.shape[0] == R and pos_end.shape[0] == R
+    _launch(lib.pkv_kv_fp4_dequant_dense, dev, stream, k_fp4.data_ptr(), v_fp4.data_ptr(), k_bscale.data_ptr(),
+            v_bscale.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *cache, _dptr(_i32(block_table), dev),
+            block_table.stride(0), block_table.shape[1], _dptr(_i32(pos_begin), dev), _dptr(_i32(pos_end), dev), R,
+            int(max_tokens), bs, hkv, k_dense.shape[3], _dptr(k_dense, dev), _dptr(v_dense, dev), max_ctx,
+            _dptr(dev_err, dev))
+
+
+def spec_verify_fp4_workspace_bytes(num_ctas=None) -> int:
+    """bytes of spec_verify_attn_fp4's workspace for num_ctas CTAs (default: the current device's SM count)."""
+    if num_ctas is None:
+        num_ctas = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
+    return int(lib.pkv_spec_verify_fp4_workspace_bytes(int(num_ctas)))
+
+
+def spec_verify_attn_fp4(q, k_fp4, v_fp4, k_bscale, v_bscale, k_scale, v_scale, block_table, seq_lens, T, softmax_scale,
+                         out, workspace, dev_err=None, stream=None):
+    """Verify (T tokens a request) or decode (T = 1) attention over the 4-bit cache; q / out bf16
+    [R*T][Hq][256]. workspace: a CUDA byte tensor of spec_verify_fp4_workspace_bytes() bytes, one for each
+    stream or graph whose calls may overlap."""
+    dev, cache, bs, hkv = _cache4(k_fp4, v_fp4, k_bscale, v_bscale, k_scale, v_scale)
+    assert q.dtype == out.dtype == torch.bfloat16 and q.is_contiguous() and out.is_contiguous()
+    R, T = block_table.shape[0], int(T)
+    assert q.dim() == 3 and q.shape == out.shape and q.shape[0] == R * T and seq_lens.shape[0] == R
+    _launch(lib.pkv_spec_verify_attn_fp4, dev, stream, _dptr(q, dev), k_fp4.data_ptr(), v_fp4.data_ptr(),
+            k_bscale.data_ptr(), v_bscale.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *cache,
+            _dptr(_i32(block_table), dev), block_table.stride(0), block_table.shape[1], _dptr(_i32(seq_lens), dev), R, T,
+            q.shape[1], hkv, q.shape[2], bs, float(softmax_scale), _dptr(out, dev), _dptr(workspace, dev),
+            _ws_bytes(workspace), _dptr(dev_err, dev))

@@ -1,0 +1,60 @@
+// kv_fp4.cuh - the 4-bit cache row shared by its writer, its reader and the attention over it.
+//
+// A row of 256 elements is 128 bytes of e2m1 codes (element 2i in the low half of byte i, 2i + 1 in
+// the high half) and 16 e4m3 bytes, one scale per group of 16 consecutive elements; one fp32 scale
+// per tensor multiplies them all: element = e2m1(code) * e4m3(group) * scale. An e2m1 magnitude
+// (0, 0.5, 1, 1.5, 2, 3, 4, 6) has 2 significant bits and an e4m3 value 4, so their product has at
+// most 6, between 2^-10 and 2688 when it is not zero: fp16 (and bf16) hold it exactly.
+#pragma once
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "sm103.cuh"
+
+namespace pkv {
+
+constexpr int kFp4D = 256;                    // elements of a row
+constexpr int kFp4Group = 16;                 // elements of a scale
+constexpr int kFp4RowBytes = kFp4D / 2;       // codes of a row
+constexpr int kFp4Groups = kFp4D / kFp4Group;  // scale bytes of a row
+
+// Byte i of w (two codes) -> fp16 pair (low half: the low nibble).
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&o)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+      : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// One e4m3 byte -> fp16 in both halves.
+__device__ __forceinline__ uint32_t e4m3_dup_f16(uint32_t byte) {
+  return e4m3x2_to_f16x2((uint16_t)((byte & 0xffu) * 0x101u));
+}
+
+// 32 contiguous bytes, 32-byte aligned, as one access.
+struct alignas(32) Bytes32 {
+  uint32_t w[8];
+};
+__device__ __forceinline__ Bytes32 ldg_bytes32(const void* p) {
+  Bytes32 r;
+  asm("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+      : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]), "=r"(r.w[7])
+      : "l"(p));
+  return r;
+}
+__device__ __forceinline__ void stg_bytes32(void* p, const Bytes32& r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r.w[0]), "r"(r.w[1]), "r"(r.w[2]),
+               "r"(r.w[3]), "r"(r.w[4]), "r"(r.w[5]), "r"(r.w[6]), "r"(r.w[7])
+               : "memory");
+}
+
+}  // namespace pkv

@@ -1,0 +1,148 @@
+// kv_fp4_dequant.cu - pkv_kv_fp4_dequant_dense: rows of the paged 4-bit cache back to dense bf16.
+//
+//   dense[r][pos][h][i] = bf16_rn((e2m1(code) * e4m3(group)) * scale) for pos_begin[r] <= pos < pos_end[r]
+// The first product is exact (6 significant bits); the second is one fp32 rounding.
+//
+// One lane holds one group: 8 bytes of codes and a scale byte in, 32 bytes out (one 256-bit store);
+// a warp covers the K row and the V row of one (position, head), four of them in flight.
+#include <cuda_bf16.h>
+
+#include "host_common.h"
+#include "kv_fp4.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kIter = 4;
+
+struct ReadArgs {
+  const uint8_t* k_fp4;
+  const uint8_t* v_fp4;
+  const uint8_t* k_bscale;
+  const uint8_t* v_bscale;
+  const float* k_scale;
+  const float* v_scale;
+  int64_t num_blocks, stride_blk, stride_tok, stride_head;
+  int64_t scale_stride_blk, scale_stride_tok, scale_stride_head;
+  const int32_t* block_table;
+  int64_t bt_stride;
+  int32_t max_blocks;
+  const int32_t* pos_begin;
+  const int32_t* pos_end;
+  int32_t block_size, num_kv_heads, chunks;
+  __nv_bfloat16* k_dense;
+  __nv_bfloat16* v_dense;
+  int64_t max_ctx;
+  int* dev_err;
+};
+
+__global__ void __launch_bounds__(kWarps * 32) kv_fp4_dequant_kernel(const ReadArgs a) {
+  const int r = blockIdx.x / a.chunks;
+  const int chunk = blockIdx.x - r * a.chunks;
+  const int lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
+  const int64_t begin = max(__ldg(a.pos_begin + r), 0);
+  int64_t end = __ldg(a.pos_end + r);
+  if (end > a.max_ctx) {
+    if (chunk == 0 && threadIdx.x == 0) record_error(a.dev_err, kErrDeviceBounds);
+    end = a.max_ctx;
+  }
+  if (begin >= end) return;
+  const int hkv = a.num_kv_heads;
+  const int which = lane >> 4, grp = lane & 15;
+  const uint8_t* codes = which ? a.v_fp4 : a.k_fp4;
+  const uint8_t* scales = which ? a.v_bscale : a.k_bscale;
+  __nv_bfloat16* dense = which ? a.v_dense : a.k_dense;
+  const float g = __ldg(which ? a.v_scale : a.k_scale);
+  const int64_t nrows = (end - begin) * hkv;
+  const int64_t stride = (int64_t)a.chunks * kWarps * kIter;
+  for (int64_t base = ((int64_t)chunk * kWarps + warp) * kIter; base < nrows; base += stride) {
+    uint2 c[kIter];
+    uint32_t sb[kIter];
+    int64_t dst[kIter];
+#pragma unroll
+    for (int u = 0; u < kIter; ++u) {
+      const int64_t row = base + u;
+      dst[u] = -1;
+      c[u] = make_uint2(0, 0);
+      sb[u] = 0;
+      if (row >= nrows) continue;
+      const int h = (int)(row % hkv);
+      const int64_t pos = begin + row / hkv;
+      const int64_t col = pos / a.block_size, slot = pos % a.block_size;
+      dst[u] = (((int64_t)r * a.max_ctx + pos) * hkv + h) * kFp4D + grp * kFp4Group;
+      const int64_t blk = col < a.max_blocks ? (int64_t)__ldg(a.block_table + (int64_t)r * a.bt_stride + col) : -1;
+      if (blk < 0 || blk >= a.num_blocks) {  // reads as zero
+        if (lane == 0) record_error(a.dev_err, kErrDeviceBounds);
+        continue;
+      }
+      c[u] = __ldg(reinterpret_cast<const uint2*>(codes + blk * a.stride_blk + slot * a.stride_tok +
+                                                  (int64_t)h * a.stride_head + grp * 8));
+      sb[u] = __ldg(scales + blk * a.scale_stride_blk + slot * a.scale_stride_tok + (int64_t)h * a.scale_stride_head + grp);
+    }
+#pragma unroll
+    for (int u = 0; u < kIter; ++u) {
+      if (dst[u] < 0) continue;
+      const uint32_t s2 = e4m3_dup_f16(sb[u]);
+      Bytes32 o;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t v[4];
+        e2m1x8_to_f16(half ? c[u].y : c[u].x, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t p = hmul2_u32(v[i], s2);
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p));
+          o.w[4 * half + i] = pack_bf16x2(__fmul_rn(f.x, g), __fmul_rn(f.y, g));
+        }
+      }
+      stg_bytes32(dense + dst[u], o);
+    }
+  }
+}
+
+}  // namespace
+
+}  // namespace pkv
+
+extern "C" pkv_status pkv_kv_fp4_dequant_dense(
+    const uint8_t* k_fp4, const uint8_t* v_fp4, const uint8_t* k_bscale, const uint8_t* v_bscale, const float* k_scale,
+    const float* v_scale, int64_t num_blocks, int64_t stride_blk, int64_t stride_tok, int64_t stride_head,
+    int64_t scale_stride_blk, int64_t scale_stride_tok, int64_t scale_stride_head, const int32_t* block_table,
+    int64_t bt_stride, int32_t max_blocks, const int32_t* pos_begin, const int32_t* pos_end, int32_t num_reqs,
+    int32_t max_tokens, int32_t block_size, int32_t num_kv_heads, int32_t head_dim, void* k_dense, void* v_dense,
+    int64_t max_ctx, int32_t* dev_err, void* stream) {
+  using namespace pkv;
+  clear_error();
+  PKV_UNSUP(head_dim == kFp4D, "kv_fp4_dequant_dense: head_dim must be 256 (got %d)", head_dim);
+  PKV_ARG(num_reqs >= 0 && max_tokens >= 0, "kv_fp4_dequant_dense: bad size argument");
+  if (num_reqs == 0 || max_tokens == 0) return PKV_OK;  // nothing to do, nothing read
+  PKV_ARG(k_fp4 && v_fp4 && k_bscale && v_bscale && k_scale && v_scale && block_table && pos_begin && pos_end &&
+              k_dense && v_dense,
+          "kv_fp4_dequant_dense: null pointer argument");
+  PKV_ARG(num_blocks > 0 && block_size > 0 && num_kv_heads > 0 && max_blocks > 0 && bt_stride >= max_blocks &&
+              max_ctx > 0,
+          "kv_fp4_dequant_dense: bad size argument");
+  PKV_ARG(stride_blk > 0 && stride_tok > 0 && stride_head > 0 && scale_stride_blk > 0 && scale_stride_tok > 0 &&
+              scale_stride_head > 0,
+          "kv_fp4_dequant_dense: strides must be positive");
+  PKV_ARG(aligned16(k_fp4) && aligned16(v_fp4) && aligned16(k_bscale) && aligned16(v_bscale) && stride_blk % 16 == 0 &&
+              stride_tok % 16 == 0 && stride_head % 16 == 0 && scale_stride_blk % 16 == 0 &&
+              scale_stride_tok % 16 == 0 && scale_stride_head % 16 == 0,
+          "kv_fp4_dequant_dense: caches, scale caches and their strides must be 16-byte aligned");
+  PKV_ARG((reinterpret_cast<uintptr_t>(k_dense) & 31) == 0 && (reinterpret_cast<uintptr_t>(v_dense) & 31) == 0,
+          "kv_fp4_dequant_dense: dense outputs must be 32-byte aligned");
+  ReadArgs a{k_fp4, v_fp4, k_bscale, v_bscale, k_scale, v_scale, num_blocks, stride_blk, stride_tok, stride_head,
+             scale_stride_blk, scale_stride_tok, scale_stride_head, block_table, bt_stride, max_blocks, pos_begin,
+             pos_end, block_size, num_kv_heads, 0, static_cast<__nv_bfloat16*>(k_dense),
+             static_cast<__nv_bfloat16*>(v_dense), max_ctx, dev_err};
+  const int64_t rows = (int64_t)max_tokens * num_kv_heads, per_cta = (int64_t)kWarps * kIter;
+  const int64_t want = (rows + per_cta - 1) / per_cta;
+  const int64_t cap = ((1ll << 30) - 1) / num_reqs + 1;
+  a.chunks = (int32_t)(want < cap ? want : cap);
+  PKV_ARG((int64_t)a.chunks * num_reqs < (1ll << 31), "kv_fp4_dequant_dense: grid too large");
+  kv_fp4_dequant_kernel<<<(unsigned)(a.chunks * num_reqs), kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  return check_launch("kv_fp4_dequant_dense");
+}
