@@ -1,8 +1,37 @@
 // spec_verify_fp4.cu - pkv_spec_verify_attn_fp4: decode / speculative-verify attention over the paged
 // 4-bit cache.
 //
-// One CTA per query row (token, head): its 8 warps stride over the keys, each with a running maximum
-// and sum; a lane holds 8 of the 256 dimensions. The warps' partials are merged in shared memory.
+// For a KV head, the columns are the query rows that share it (tokens x group, kCols of them) and the
+// MMAs are swapped, so the 128 keys of a tile are the M dimension:
+//   S^T = K Q^T (M 128 keys, N kCols, K 256),  P = 2^(S f - m),  O^T += V^T P^T (M 2 x 128, K 128 keys),
+// out = O / sum P * v_scale, f = softmax_scale log2(e) k_scale. An element e2m1 * e4m3 is exact in fp16
+// (6 significant bits), so both products run as fp16 MMAs on the exact stored values; a query row is
+// scaled by a power of two (folded back into f), so that any bf16 row keeps its 8 bits in fp16.
+//
+// A tile of 128 keys is 36 KB, 0.83 us of an SM's share of the measured copy rate, in which the SM has
+// to widen 65,536 codes. What that design follows from:
+//   - Neither operand goes back to shared memory: writing 128 KB of fp16 and reading it for the MMAs
+//     would take 2,048 of the ~1,600 cycles. Both are A operands in tensor memory.
+//   - K rows are the M axis as they lie: a thread widens one key row into its TMEM lane.
+//   - V has to be transposed (M is head_dim). ldmatrix.m16n16.trans.b8 transposes 16 keys x 16 bytes;
+//     a byte holds two elements of one key, so one select per nibble side pairs the nibbles of two
+//     keys in a byte, and the conversion makes the (key, key + 1) pair that a TMEM column holds. Lane
+//     i of a 32-lane block is then element 2 i of the block's 32 (i < 16) or 2 (i - 16) + 1, which only
+//     the epilogue has to know.
+//   - The scales of V change along both axes of that layout: one warp lays a tile's 2,048 scales out as
+//     fp16, transposed, once.
+//   - The softmax checks one maximum per thread against the running one and shares it by a vote: the
+//     weights may grow to 2^15 before a column's maximum is moved (they start at 2^8), so that most
+//     tiles have no reduction over the keys, and the sums stay in registers until the end.
+//
+// The keys are divided evenly: the tiles of a "line" (one KV head's, for all requests one after the
+// other) are cut into equal ranges, one a CTA, and the CTAs of the lines (heads) work side by side on
+// the same pages. Request pieces that a cut divides are merged by a second, small kernel; a CTA has
+// at most one piece that began before it and one that ends after it, so two slots of workspace. The
+// pipeline runs on from one request to the next.
+//
+// Roles (24 warps): 0 TMA producer; 1 QK issuer; 2 PV issuer; 3 V scales; 4-7 K rows; 8-15 V columns;
+// 16-23 softmax, two warpgroups of kCols / 2 columns each.
 #include <cuda_bf16.h>
 
 #include "host_common.h"
@@ -12,109 +41,974 @@ namespace pkv {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kBN = 128;                  // keys of a tile
+constexpr int kThreads = 768;
+constexpr int kStages = 4;
+constexpr int kCodeTile = kBN * kFp4RowBytes;  // 16 KB
+constexpr int kScaleTile = kBN * kFp4Groups;   // 2 KB
+constexpr int kHalfStage = kCodeTile + kScaleTile;
+constexpr int kMaxCols = 32;
+constexpr uint32_t kTmemCols = 512;
+constexpr float kUnset = -3e38f;          // running maximum of a column that has seen no key
+constexpr float kStart = 8.0f;            // a new maximum's weight is 2^8 ...
+constexpr float kMove = 15.0f;            // ... and the maximum moves when a weight would pass 2^15
 
-struct Args {
-  const __nv_bfloat16* q;
-  const uint8_t* k_fp4;
-  const uint8_t* v_fp4;
-  const uint8_t* k_bscale;
-  const uint8_t* v_bscale;
-  const float* k_scale;
-  const float* v_scale;
-  int64_t num_blocks, stride_blk, stride_tok, stride_head;
-  int64_t scale_stride_blk, scale_stride_tok, scale_stride_head;
-  const int32_t* block_table;
-  int64_t bt_stride;
-  int32_t max_blocks;
-  const int32_t* seq_lens;
-  int32_t T, num_q_heads, group, block_size;
-  float scale_log2;
-  __nv_bfloat16* out;
-  int* dev_err;
+// Workspace of a CTA: two slots (0: the piece that began before it, 1: the piece that goes on after
+// it) of O [kMaxCols][256], m and l [kMaxCols], and a note for the merge.
+struct Slot {
+  float o[kMaxCols][kFp4D];
+  float m[kMaxCols], l[kMaxCols];
+};
+struct Note {
+  int32_t valid, r, unit, unused;
+  int64_t unit_end, total;  // line positions: where the piece's unit ends, the line's tiles
+  int64_t pad[12];
+};
+struct CtaWorkspace {
+  Slot slot[2];
+  Note note;
+};
+static_assert(sizeof(CtaWorkspace) % 16 == 0, "workspace of a CTA");
+
+template <int kCols>
+struct Geo {
+  static constexpr int kGC = kCols / 2;          // columns of a softmax warpgroup
+  static constexpr int kQChunk = kCols * 128;    // fp16 [kCols rows][64]
+  static constexpr int kQBuf = 4 * kQChunk;
+  static constexpr int kPRow = 64;               // bytes of a key's row of P^T (32 columns, 64-byte swizzle)
+  static constexpr int kPBuf = kBN * kPRow;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffP = kOffQ + 2 * kQBuf;
+  static constexpr int kOffSf = kOffP + 2 * kPBuf;          // V scales, fp16 [8 chunks][32 key quads][2 groups][4 keys]
+  static constexpr int kSfBuf = kBN * kFp4Groups * 2;
+  static constexpr int kOffStage = kOffSf + 2 * kSfBuf;
+  static constexpr int kStage = 2 * kHalfStage;             // K codes, K scales, V codes, V scales
+  static constexpr int kTiles = kOffStage + kStages * kStage;
+  __host__ __device__ static constexpr uint32_t col_k(int b) { return 128u * b; }
+  static constexpr uint32_t kColV = 256u;                   // two halves of head_dim, 64 columns each
+  __host__ __device__ static constexpr uint32_t col_s(int b) { return 384u + (uint32_t)(b * kCols); }
+  static constexpr uint32_t kColO = 384u + 2u * kCols;      // two halves of head_dim
+  static_assert(kColO + 2 * kCols <= kTmemCols, "tensor memory");
+  static_assert(kOffStage % 1024 == 0 && kHalfStage % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms");
 };
 
-__device__ __forceinline__ void row8(const uint8_t* codes, const uint8_t* scales, int lane, float (&x)[8]) {
-  const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(codes) + lane);
-  const uint32_t s2 = e4m3_dup_f16(__ldg(scales + (lane >> 1)));
-  uint32_t v[4];
-  e2m1x8_to_f16(w, v);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t p = hmul2_u32(v[i], s2);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p));
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
-}
+template <int kCols>
+struct alignas(16) Shared {
+  uint64_t k_full[kStages], k_empty[kStages];    // K codes and scales of a tile
+  uint64_t v_full[kStages], v_empty[kStages];    // V codes and scales
+  uint64_t q_ready[4], q_free[2];                // Q of run s (buffer s % 2; barrier s % 4: the K rows may be 3 runs ahead of the softmax)
+  uint64_t kt_ready[2], kt_free[2];              // K in tensor memory
+  uint64_t s_full[2], s_free[2];                 // S^T
+  uint64_t sf_ready[2], sf_free[2];              // transposed V scales
+  uint64_t vt_ready[2], vt_free[2];              // V in tensor memory, per half of head_dim
+  uint64_t p_full[2], pv_done[2];                // P^T written; PV of the tile complete
+  uint64_t drain;
+  uint32_t armed[2][kStages];
+  uint32_t k_bad[kStages], v_bad[kStages];       // key segments in a bad block
+  uint32_t tmem_base;
+  int abort;
+  int v_nan;                                     // a NaN V scale was left out for a key that some columns do not see
+  int r0, u0, t00;                               // first tile of the CTA's range
+  long long wsum[kThreads / 32];
+  long long total;
+  int32_t row_off[kCols];                        // column -> token * Hq + head in group
+  int32_t tok[kCols];                            // column -> token
+  alignas(16) float f[8][kCols];                 // column factors of the segment (ring: the softmax may be 4 behind)
+  alignas(16) float m[kCols];                    // running maxima, log2
+  float red[2][4][kCols / 2];
+  float fin[kCols];
+};
 
-__global__ void __launch_bounds__(kWarps * 32) spec_verify_fp4_kernel(const Args a) {
-  __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][kFp4D];
-  const int64_t row = blockIdx.x;
-  const int qh = (int)(row % a.num_q_heads);
-  const int64_t tok = row / a.num_q_heads;
-  const int r = (int)(tok / a.T), t = (int)(tok % a.T);
-  const int h = qh / a.group;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n = __ldg(a.seq_lens + r) - a.T + t + 1;  // visible keys
-  float q[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) q[i] = __bfloat162float(a.q[row * kFp4D + lane * 8 + i]);
-  const float f = a.scale_log2 * __ldg(a.k_scale);
-  float m = -INFINITY, l = 0.0f, o[8] = {};
-  for (int pos = warp; pos < n; pos += kWarps) {
-    const int col = pos / a.block_size, slot = pos % a.block_size;
-    const int64_t blk = col < a.max_blocks ? (int64_t)__ldg(a.block_table + (int64_t)r * a.bt_stride + col) : -1;
-    float s = 0.0f, v[8] = {};
-    if (blk < 0 || blk >= a.num_blocks) {
-      if (lane == 0) record_error(a.dev_err, kErrDeviceBounds);
-    } else {
-      const int64_t off = blk * a.stride_blk + slot * a.stride_tok + (int64_t)h * a.stride_head;
-      const int64_t soff = blk * a.scale_stride_blk + slot * a.scale_stride_tok + (int64_t)h * a.scale_stride_head;
-      float k[8];
-      row8(a.k_fp4 + off, a.k_bscale + soff, lane, k);
-      row8(a.v_fp4 + off, a.v_bscale + soff, lane, v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s += q[i] * k[i];
-#pragma unroll
-      for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+struct Params {
+  CUtensorMap kc, vc, ks, vs;      // codes [nb][bs][hkv][128 B], scales [nb][bs][hkv][16 B]: boxes of seg keys
+  CUtensorMap kcb, vcb, ksb, vsb;  // boxes of 128 keys (block_size >= 128)
+  const __nv_bfloat16* q;
+  const uint8_t* v_bscale;
+  int64_t scale_stride_blk, scale_stride_tok, scale_stride_head;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* block_table;
+  int64_t bt_stride, num_blocks;
+  int32_t max_blocks, big_ok, block_size, seg;
+  const int32_t* seq_lens;
+  int32_t num_reqs, T, group, num_q_heads;
+  int32_t tpc, n_tg;               // tokens of a CTA's columns; column groups of a KV head
+  int32_t lines, units, ctas;      // lines; units of a request in a line; CTAs of a line
+  float scale_log2;
+  __nv_bfloat16* out;
+  CtaWorkspace* ws;
+  int* dev_err;
+  uint64_t wait_limit_ns;
+};
+
+__device__ __forceinline__ int64_t line_begin(int64_t total, int c, int ctas) { return total * c / ctas; }
+
+// The tiles of a CTA, as runs of consecutive tiles of one (request, unit). Every role walks the same runs.
+struct Cursor {
+  int r, u, t;
+  int64_t left;
+};
+struct Run {
+  int r, u, t0, n, len, tiles;
+};
+__device__ __forceinline__ bool next_run(const Params& p, Cursor& c, Run& s) {
+  if (c.left <= 0) return false;
+  int len = 0;
+  while (true) {
+    if (c.r >= p.num_reqs) return false;
+    len = __ldg(p.seq_lens + c.r);
+    if (len > 0) break;
+    ++c.r;
+  }
+  s.r = c.r;
+  s.u = c.u;
+  s.t0 = c.t;
+  s.len = len;
+  s.tiles = (int)(((int64_t)len + kBN - 1) / kBN);
+  s.n = (int)min((int64_t)(s.tiles - s.t0), c.left);
+  if (s.n <= 0) return false;
+  c.left -= s.n;
+  c.t += s.n;
+  if (c.t == s.tiles) {
+    c.t = 0;
+    if (++c.u == p.units) {
+      c.u = 0;
+      ++c.r;
     }
-    s *= f;
-    const float m_new = fmaxf(m, s);
-    const float alpha = exp2f(m - m_new), p = exp2f(s - m_new);
-    l = l * alpha + p;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = o[i] * alpha + p * v[i];
-    m = m_new;
   }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) s_o[warp][lane * 8 + i] = o[i];
-  __syncthreads();
-  const int d = threadIdx.x;
-  float M = -INFINITY;
-  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w]);
-  float L = 0.0f, O = 0.0f;
-  for (int w = 0; w < kWarps; ++w) {
-    if (s_m[w] == -INFINITY) continue;
-    const float e = exp2f(s_m[w] - M);
-    L += e * s_l[w];
-    O += e * s_o[w][d];
-  }
-  a.out[row * kFp4D + d] = __float2bfloat16(n > 0 ? O / L * __ldg(a.v_scale) : 0.0f);
+  return true;
 }
 
-constexpr size_t kWorkspacePerCta = 2 * (32 * kFp4D + 32) * sizeof(float) + 256;
+__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ bool group_any(int id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
+// One arrival for the warp, after every lane's preceding accesses.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t wl) {
+  return __all_sync(0xffffffffu, mbar_wait_suspend(bar, parity, abort, wl));
+}
+
+template <int kGC>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t a, uint32_t (&r)[kGC]) {
+  if constexpr (kGC == 8) tmem_ld_32x32b_x8(a, r);
+  else tmem_ld_32x32b_x16(a, r);
+}
+template <int kGC>
+__device__ __forceinline__ void tmem_st_cols(uint32_t a, const uint32_t (&r)[kGC]) {
+  if constexpr (kGC == 8) tmem_st_32x32b_x8(a, r);
+  else tmem_st_32x32b_x16(a, r);
+}
+
+// kGC columns over the warp's lanes: lane l ends with column l % kGC's maximum or sum.
+template <int kGC, bool kMax>
+__device__ __forceinline__ float reduce_columns(float (&v)[kGC], int lane) {
+#pragma unroll
+  for (int o = kGC / 2; o >= 1; o >>= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int q = 0; q < o; ++q) {
+      const float keep = up ? v[q + o] : v[q], send = up ? v[q] : v[q + o];
+      const float got = __shfl_xor_sync(0xffffffffu, send, o);
+      v[q] = kMax ? fmaxf(keep, got) : keep + got;
+    }
+  }
+  float x = v[0];
+#pragma unroll
+  for (int o = kGC; o < 32; o <<= 1) {
+    const float got = __shfl_xor_sync(0xffffffffu, x, o);
+    x = kMax ? fmaxf(x, got) : x + got;
+  }
+  return x;
+}
+
+__device__ __forceinline__ void ldmatrix_t8_x2(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// 16 lanes x 16 columns (two groups of 8): thread t holds lane t / 4 (registers 0, 1 of a group of four)
+// and t / 4 + 8 (registers 2, 3), columns 2 (t % 4) and the next.
+__device__ __forceinline__ void tmem_st_16x256b_x2(uint32_t a, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(a), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// Bytes 0 and 2 of w as two fp16 pairs.
+__device__ __forceinline__ void e2m1_bytes02(uint32_t w, uint32_t& a, uint32_t& b) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b2;\n\t}"
+      : "=r"(a), "=r"(b)
+      : "r"(w));
+}
+
+template <int kCols>
+__global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __grid_constant__ Params p) {
+  using Gm = Geo<kCols>;
+  constexpr int kGC = Gm::kGC;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Shared<kCols>& sh = *reinterpret_cast<Shared<kCols>*>(smem + Gm::kTiles);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int line = blockIdx.x % p.lines, cta = blockIdx.x / p.lines;
+  const int nq_max = p.tpc * p.group;
+
+  // ------------------------------------------------------------------ barriers, tensor memory, range
+  if (warp == 2) {
+    tmem_alloc(&sh.tmem_base, kTmemCols);
+    tmem_relinquish();
+  }
+  const int live_groups = nq_max > kGC ? 2 : 1;  // softmax warpgroups with a live column
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&sh.k_full[s], 1);
+      mbar_init(&sh.k_empty[s], 4);
+      mbar_init(&sh.v_full[s], 1);
+      mbar_init(&sh.v_empty[s], 9);
+      sh.armed[0][s] = sh.armed[1][s] = 0;
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sh.q_ready[b], 4);
+      mbar_init(&sh.q_ready[2 + b], 4);
+      mbar_init(&sh.q_free[b], 1);
+      mbar_init(&sh.kt_ready[b], 4);
+      mbar_init(&sh.kt_free[b], 1);
+      mbar_init(&sh.s_full[b], 1);
+      mbar_init(&sh.s_free[b], 4 * live_groups);
+      mbar_init(&sh.sf_ready[b], 1);
+      mbar_init(&sh.sf_free[b], 8);
+      mbar_init(&sh.vt_ready[b], 4);
+      mbar_init(&sh.vt_free[b], 1);
+      mbar_init(&sh.p_full[b], 4 * live_groups);
+      mbar_init(&sh.pv_done[b], 1);
+    }
+    mbar_init(&sh.drain, 2);
+    sh.abort = 0;
+    sh.v_nan = 0;
+    sh.r0 = -1;
+    fence_mbar_init();
+  }
+  if (tid < kCols) {
+    const int t = tid / p.group;
+    sh.tok[tid] = t;
+    sh.row_off[tid] = t * p.num_q_heads + (tid - t * p.group);
+  }
+  // the line's tiles, and zeros for the rows of empty requests (each CTA its share of the requests)
+  long long mine = 0;
+  for (int r = tid; r < p.num_reqs; r += kThreads) {
+    const int len = __ldg(p.seq_lens + r);
+    if (len > 0) mine += ((int64_t)len + kBN - 1) / kBN;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) sh.wsum[warp] = mine;
+  for (int r = blockIdx.x; r < p.num_reqs; r += gridDim.x) {
+    if (__ldg(p.seq_lens + r) > 0) continue;
+    uint4* o = reinterpret_cast<uint4*>(p.out + (int64_t)r * p.T * p.num_q_heads * kFp4D);
+    const int64_t n = (int64_t)p.T * p.num_q_heads * (kFp4D / 8);
+    for (int64_t i = tid; i < n; i += kThreads) o[i] = make_uint4(0, 0, 0, 0);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  long long total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) total += sh.wsum[w];
+  const int64_t line_total = total * p.units;
+  const int64_t begin = line_begin(line_total, cta, p.ctas), end = line_begin(line_total, cta + 1, p.ctas);
+  __syncthreads();
+  if (begin < end) {  // the requests that hold the range's first and last tile
+    long long before = 0;
+    for (int base = 0; base < p.num_reqs; base += kThreads) {
+      const int r = base + tid;
+      const int len = r < p.num_reqs ? __ldg(p.seq_lens + r) : 0;
+      const long long tiles = len > 0 ? ((int64_t)len + kBN - 1) / kBN : 0;
+      long long inc = tiles * p.units;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      if (lane == 31) sh.wsum[warp] = inc;
+      __syncthreads();
+      long long sum = 0;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) inc += sh.wsum[w];
+        sum += sh.wsum[w];
+      }
+      const long long at = before + inc - tiles * p.units;
+      if (tiles > 0 && at <= begin && begin < at + tiles * p.units) {
+        sh.r0 = r;
+        sh.u0 = (int)((begin - at) / tiles);
+        sh.t00 = (int)((begin - at) % tiles);
+      }
+      if (tiles > 0 && at < end && end <= at + tiles * p.units) {
+        // for the merge: does the unit of the last tile begin in this range and go on past it?
+        const int64_t u = (end - 1 - at) / tiles, unit_begin = at + u * tiles;
+        Note& note = p.ws[blockIdx.x].note;
+        note.r = r;
+        note.unit = p.lines > 1 ? line : (int)u;
+        note.unit_end = unit_begin + tiles;
+        note.total = line_total;
+        note.valid = unit_begin >= begin && unit_begin + tiles > end;
+      }
+      before += sum;
+      __syncthreads();
+      if (before >= end) break;  // CTA-uniform
+    }
+  } else if (tid == 0) {
+    p.ws[blockIdx.x].note.valid = 0;
+  }
+  const Cursor start{sh.r0, sh.u0, sh.t00, sh.r0 >= 0 ? end - begin : 0};
+  const uint32_t tmem = sh.tmem_base;
+  volatile int* abort = &sh.abort;
+  const uint64_t wl = p.wait_limit_ns;
+  const int G = p.seg;
+  CtaWorkspace& ws = p.ws[blockIdx.x];
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------------------ producer
+    const int nseg = kBN / G;
+    Cursor cur = start;
+    Run run;
+    int i = 0;
+    bool ok = true;
+    while (ok && next_run(p, cur, run)) {
+      const int unit = p.lines > 1 ? line : run.u;
+      const int kvh = unit / p.n_tg;
+      for (int j = 0; j < run.n; ++j, ++i) {
+        const int st = i % kStages, round = i / kStages;
+        const int key0 = (run.t0 + j) * kBN;
+        int blk = -1;
+        if (lane < nseg && key0 + lane * G < run.len) {
+          const int col = (key0 + lane * G) / p.block_size;
+          blk = col < p.max_blocks ? __ldg(p.block_table + (int64_t)run.r * p.bt_stride + col) : -2;
+          if (blk < 0 || (int64_t)blk >= p.num_blocks) blk = -2;
+        }
+        const uint32_t bad = __ballot_sync(0xffffffffu, blk == -2);
+        const uint32_t nload = __popc(__ballot_sync(0xffffffffu, blk >= 0));
+        const int blk0 = __shfl_sync(0xffffffffu, blk, 0);
+        const int slot0 = key0 % p.block_size;
+        const bool big = p.big_ok && blk0 >= 0 && slot0 + kBN <= p.block_size;  // one block holds the tile
+        const uint32_t rows = big ? (uint32_t)kBN : nload * (uint32_t)G;
+        if (bad && lane == 0) record_error(p.dev_err, kErrDeviceBounds);
+        for (int which = 0; which < 2; ++which) {  // K, then V
+          uint64_t* full = which ? &sh.v_full[st] : &sh.k_full[st];
+          bool got = true;
+          if (lane == 0 && round >= 1)
+            got = mbar_wait_suspend(which ? &sh.v_empty[st] : &sh.k_empty[st], (round - 1) & 1, abort, wl);
+          ok = __shfl_sync(0xffffffffu, got, 0);
+          if (!ok) break;
+          uint8_t* codes = smem + Gm::kOffStage + st * Gm::kStage + which * kHalfStage;
+          uint8_t* scales = codes + kCodeTile;
+          if (lane == 0) {
+            (which ? sh.v_bad : sh.k_bad)[st] = bad;
+            mbar_arm_tx(full, rows * (uint32_t)(kFp4RowBytes + kFp4Groups), &sh.armed[which][st]);
+            if (big) {
+              tma_load_4d(codes, which ? &p.vcb : &p.kcb, full, 0, kvh, slot0, blk0);
+              tma_load_4d(scales, which ? &p.vsb : &p.ksb, full, 0, kvh, slot0, blk0);
+            }
+          }
+          __syncwarp();
+          if (!big && blk >= 0) {
+            const int slot = (key0 + lane * G) % p.block_size;
+            tma_load_4d(codes + lane * G * kFp4RowBytes, which ? &p.vc : &p.kc, full, 0, kvh, slot, blk);
+            tma_load_4d(scales + lane * G * kFp4Groups, which ? &p.vs : &p.ks, full, 0, kvh, slot, blk);
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------------------ QK issuer
+    if (lane == 0) {
+      constexpr uint32_t id = idesc_f16(128, kCols, false, false, false);
+      const uint32_t q_base = smem_u32(smem + Gm::kOffQ);
+      Cursor cur = start;
+      Run run;
+      int i = 0, s = 0;
+      bool ok = true;
+      for (; ok && next_run(p, cur, run); ++s) {
+        ok = mbar_wait_suspend(&sh.q_ready[s & 3], (s >> 2) & 1, abort, wl);
+        for (int j = 0; ok && j < run.n; ++j, ++i) {
+          const int b = i & 1;
+          ok = (i < 2 || mbar_wait_suspend(&sh.s_free[b], ((i >> 1) - 1) & 1, abort, wl)) &&
+               mbar_wait_suspend(&sh.kt_ready[b], (i >> 1) & 1, abort, wl);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t qb = q_base + (s & 1) * Gm::kQBuf;
+#pragma unroll
+          for (int ks = 0; ks < 16; ++ks)
+            umma_f16_ts(tmem + Gm::col_s(b), tmem + Gm::col_k(b) + ks * 8,
+                        smem_desc(qb + (ks >> 2) * Gm::kQChunk + (ks & 3) * 32, 16, 1024), id, ks > 0);
+          umma_commit(&sh.s_full[b]);
+          umma_commit(&sh.kt_free[b]);
+        }
+        if (ok) umma_commit(&sh.q_free[s & 1]);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------------------------------------------------------ PV issuer
+    if (lane == 0) {
+      constexpr uint32_t id = idesc_f16(128, kCols, false, false, true);
+      const uint32_t p_base = smem_u32(smem + Gm::kOffP);
+      Cursor cur = start;
+      Run run;
+      int i = 0;
+      bool ok = true;
+      while (ok && next_run(p, cur, run)) {
+        for (int j = 0; ok && j < run.n; ++j, ++i) {
+          const int b = i & 1;
+          ok = mbar_wait_suspend(&sh.p_full[b], (i >> 1) & 1, abort, wl);
+          const uint32_t pb = p_base + b * Gm::kPBuf;
+          for (int hh = 0; ok && hh < 2; ++hh) {
+            ok = mbar_wait_suspend(&sh.vt_ready[hh], i & 1, abort, wl);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              umma_f16_ts(tmem + Gm::kColO + hh * kCols, tmem + Gm::kColV + hh * 64 + ks * 8,
+                          smem_desc(pb + ks * 16 * Gm::kPRow, 0, 8 * Gm::kPRow, kLayoutSW64), id,
+                          (j > 0 || ks > 0) ? 1u : 0u);
+            umma_commit(&sh.vt_free[hh]);
+          }
+          if (ok) umma_commit(&sh.pv_done[b]);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // ------------------------------------------------------------------------------ V scales
+    // lane = four keys: their 4 x 16 e4m3 bytes as fp16, [chunk of 32 elements][key quad][group][key].
+    // Keys past the request or in a bad block get 0. A NaN scale of a key that some columns of the CTA
+    // do not see would reach them as 0 * NaN: it is left out here and put into the columns that see
+    // the key by the epilogue.
+    Cursor cur = start;
+    Run run;
+    int i = 0;
+    bool ok = true;
+    while (ok && next_run(p, cur, run)) {
+      const int unit = p.lines > 1 ? line : run.u;
+      const int seen_by_all = run.len - p.T + (unit % p.n_tg) * p.tpc;  // the last such key
+      for (int j = 0; ok && j < run.n; ++j, ++i) {
+        const int st = i % kStages, b = i & 1;
+        ok = i < 2 || warp_wait(&sh.sf_free[b], ((i >> 1) - 1) & 1, abort, wl);
+        if (ok) ok = warp_wait(&sh.v_full[st], (i / kStages) & 1, abort, wl);
+        if (!ok) break;
+        const uint4* src = reinterpret_cast<const uint4*>(smem + Gm::kOffStage + st * Gm::kStage + kHalfStage + kCodeTile);
+        uint32_t w[4][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint4 v = src[lane * 4 + k];
+          w[k][0] = v.x; w[k][1] = v.y; w[k][2] = v.z; w[k][3] = v.w;
+        }
+        const int key0 = (run.t0 + j) * kBN;
+        const uint32_t bad = sh.v_bad[st];
+        if (bad || key0 + kBN > run.len || key0 + kBN - 1 > seen_by_all) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int key = key0 + lane * 4 + k;
+            const bool dead = key >= run.len || ((bad >> ((lane * 4 + k) / G)) & 1u);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if (dead) w[k][q] = 0;
+              if (key > seen_by_all) {
+                const uint32_t nan = __vcmpeq4(w[k][q] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                if (nan) {
+                  w[k][q] &= ~nan;
+                  sh.v_nan = 1;
+                }
+              }
+            }
+          }
+        }
+        uint8_t* dst = smem + Gm::kOffSf + b * Gm::kSfBuf + lane * 16;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t lo01 = __byte_perm(w[0][q], w[1][q], 0x5140), hi01 = __byte_perm(w[0][q], w[1][q], 0x7362);
+          const uint32_t lo23 = __byte_perm(w[2][q], w[3][q], 0x5140), hi23 = __byte_perm(w[2][q], w[3][q], 0x7362);
+          *reinterpret_cast<uint4*>(dst + (2 * q) * 512) =
+              make_uint4(e4m3x2_to_f16x2((uint16_t)lo01), e4m3x2_to_f16x2((uint16_t)lo23),
+                         e4m3x2_to_f16x2((uint16_t)(lo01 >> 16)), e4m3x2_to_f16x2((uint16_t)(lo23 >> 16)));
+          *reinterpret_cast<uint4*>(dst + (2 * q + 1) * 512) =
+              make_uint4(e4m3x2_to_f16x2((uint16_t)hi01), e4m3x2_to_f16x2((uint16_t)hi23),
+                         e4m3x2_to_f16x2((uint16_t)(hi01 >> 16)), e4m3x2_to_f16x2((uint16_t)(hi23 >> 16)));
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sh.v_empty[st]);
+          mbar_arrive(&sh.sf_ready[b]);
+        }
+      }
+    }
+  } else if (warp < 8) {
+    // ------------------------------------------------------------------------------ K rows
+    const int k = (warp & 3) * 32 + lane;  // the key row of a tile
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const float kg = __ldg(p.k_scale);
+    Cursor cur = start;
+    Run run;
+    int i = 0;
+    bool ok = true;
+    for (int s = 0; ok && next_run(p, cur, run); ++s) {
+      const int unit = p.lines > 1 ? line : run.u;
+      const int t_base = (unit % p.n_tg) * p.tpc;
+      const int nq = min(p.tpc, p.T - t_base) * p.group;
+      if (s >= 2) ok = warp_wait(&sh.q_free[s & 1], ((s >> 1) - 1) & 1, abort, wl);
+      if (!ok) break;
+      // Q: four threads a row, 64 elements (one swizzled chunk) each
+      {
+        const __nv_bfloat16* base = p.q + (((int64_t)run.r * p.T + t_base) * p.num_q_heads +
+                                           (int64_t)(unit / p.n_tg) * p.group) * kFp4D;
+        for (int row = k >> 2; row < kCols; row += 32) {
+          const int c = k & 3;
+          uint4 v[8];
+          const uint4* src = reinterpret_cast<const uint4*>(base + (int64_t)(row < nq ? sh.row_off[row] : 0) * kFp4D + c * 64);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) v[x] = row < nq ? __ldg(src + x) : make_uint4(0, 0, 0, 0);
+          uint32_t mx = 0;
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            mx = __vmaxu2(mx, v[x].x & 0x7fff7fffu);
+            mx = __vmaxu2(mx, v[x].y & 0x7fff7fffu);
+            mx = __vmaxu2(mx, v[x].z & 0x7fff7fffu);
+            mx = __vmaxu2(mx, v[x].w & 0x7fff7fffu);
+          }
+          mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const int e = (int)(max(mx & 0xffffu, mx >> 16) >> 7);  // the row's largest exponent, biased
+          // rows are brought to [1, 2) by a power of two; rows with an infinity or NaN stay as they are
+          const int shift = e == 255 ? 0 : min(max(127 - e, -126), 126);
+          const float up = __int_as_float((127 + shift) << 23);
+          uint8_t* dst = smem + Gm::kOffQ + (s & 1) * Gm::kQBuf + c * Gm::kQChunk + row * 128;
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            uint32_t* wv = reinterpret_cast<uint32_t*>(&v[x]);
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              wv[y] = pack_f16x2(__uint_as_float(wv[y] << 16) * up, __uint_as_float(wv[y] & 0xffff0000u) * up);
+            *reinterpret_cast<uint4*>(dst + ((x ^ (row & 7)) * 16)) = v[x];
+          }
+          if (c == 0) sh.f[s & 7][row] = row < nq ? p.scale_log2 * __int_as_float((127 - shift) << 23) * kg : 0.0f;
+        }
+        fence_proxy_async_smem();
+        warp_arrive(&sh.q_ready[s & 3], lane);
+      }
+      for (int j = 0; ok && j < run.n; ++j, ++i) {
+        const int st = i % kStages, b = i & 1;
+        ok = warp_wait(&sh.k_full[st], (i / kStages) & 1, abort, wl);
+        if (ok && i >= 2) ok = warp_wait(&sh.kt_free[b], ((i >> 1) - 1) & 1, abort, wl);
+        if (!ok) break;
+        tc_fence_after();
+        const uint8_t* stage = smem + Gm::kOffStage + st * Gm::kStage;
+        uint4 sc = *reinterpret_cast<const uint4*>(stage + kCodeTile + k * 16);
+        const uint32_t bad = sh.k_bad[st];
+        if (bad && ((bad >> (k / G)) & 1u)) sc = make_uint4(0, 0, 0, 0);
+        const uint32_t scw[4] = {sc.x, sc.y, sc.z, sc.w};
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {  // 32 elements, two groups, 16 tensor-memory columns
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + k * 128 + ((c ^ (k & 7)) * 16));
+          const uint32_t s2 = e4m3x2_to_f16x2((uint16_t)(scw[c >> 1] >> (16 * (c & 1))));
+          const __half2 sh2 = *reinterpret_cast<const __half2*>(&s2);
+          const __half2 lo = __low2half2(sh2), hi = __high2half2(sh2);
+          const uint32_t slo = *reinterpret_cast<const uint32_t*>(&lo), shi = *reinterpret_cast<const uint32_t*>(&hi);
+          uint32_t o[16], x[4];
+          const uint32_t cw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            e2m1x8_to_f16(cw[y], x);
+#pragma unroll
+            for (int z = 0; z < 4; ++z) o[4 * y + z] = hmul2_u32(x[z], y < 2 ? slo : shi);
+          }
+          tmem_st_32x32b_x16(tmem + lane_off + Gm::col_k(b) + 16 * c, o);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sh.kt_ready[b]);
+          mbar_arrive(&sh.k_empty[st]);
+        }
+      }
+    }
+  } else if (warp < 16) {
+    // ------------------------------------------------------------------------------ V columns
+    const int c = warp - 8;        // chunk: elements 32 c .. 32 c + 31, 16 code bytes of a key
+    const int hh = c >> 2;
+    const uint32_t tv = tmem + ((uint32_t)((c & 3) * 32) << 16) + Gm::kColV + hh * 64;
+    Cursor cur = start;
+    Run run;
+    int i = 0;
+    bool ok = true;
+    while (ok && next_run(p, cur, run)) {
+      for (int j = 0; ok && j < run.n; ++j, ++i) {
+        const int st = i % kStages, b = i & 1;
+        ok = warp_wait(&sh.v_full[st], (i / kStages) & 1, abort, wl);
+        if (ok) ok = warp_wait(&sh.sf_ready[b], (i >> 1) & 1, abort, wl);
+        if (ok && i >= 1) ok = warp_wait(&sh.vt_free[hh], (i - 1) & 1, abort, wl);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t codes = smem_u32(smem + Gm::kOffStage + st * Gm::kStage + kHalfStage) + lane * 128 + ((c ^ (lane & 7)) * 16);
+        const uint8_t* sf = smem + Gm::kOffSf + b * Gm::kSfBuf + c * 512 + (lane & 3) * 16;
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb) {  // 32 keys
+          uint32_t w[4], even[8], odd[8];
+          ldmatrix_t8_x2(codes + kb * 32 * 128, w);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {  // 16 keys: bytes of four keys, for two groups
+            const uint4 s4 = *reinterpret_cast<const uint4*>(sf + kb * 128 + x * 64);
+            const uint32_t s01[2] = {s4.x, s4.z}, s23[2] = {s4.y, s4.w};
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              constexpr uint32_t kLow = 0x0f0f0f0fu;
+              const uint32_t v = w[2 * x + g], v4 = v >> 4;
+              const uint32_t lo = (v & kLow) | (v4 & ~kLow);         // bytes 0, 2: the low nibbles of keys 0 1, 2 3
+              const uint32_t hi = (v4 & kLow) | ((v >> 8) & ~kLow);  // the high nibbles
+              uint32_t a, d;
+              e2m1_bytes02(lo, a, d);
+              even[4 * x + 2 * g] = hmul2_u32(a, s01[g]);
+              even[4 * x + 2 * g + 1] = hmul2_u32(d, s23[g]);
+              e2m1_bytes02(hi, a, d);
+              odd[4 * x + 2 * g] = hmul2_u32(a, s01[g]);
+              odd[4 * x + 2 * g + 1] = hmul2_u32(d, s23[g]);
+            }
+          }
+          tmem_st_16x256b_x2(tv + kb * 16, even);
+          tmem_st_16x256b_x2(tv + (16u << 16) + kb * 16, odd);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sh.vt_ready[hh]);
+          mbar_arrive(&sh.v_empty[st]);
+          mbar_arrive(&sh.sf_free[b]);
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------------------ softmax
+    const int grp = (warp - 16) >> 2;
+    const int c0 = grp * kGC;
+    const int quarter = warp & 3;
+    const int k = quarter * 32 + lane;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const int bar_id = 1 + grp;
+    const float vg = __ldg(p.v_scale);
+    // the head_dim element of this thread's tensor-memory lane, less 128 per half (see V columns)
+    const int d_lane = quarter * 32 + (lane < 16 ? 2 * lane : 2 * (lane - 16) + 1);
+    Cursor cur = start;
+    Run run;
+    int i = 0;
+    bool ok = c0 < nq_max;  // a group without a live column has nothing to do
+    for (int s = 0; ok && next_run(p, cur, run); ++s) {
+      const int unit = p.lines > 1 ? line : run.u;
+      const int t_base = (unit % p.n_tg) * p.tpc;
+      const int nq = min(p.tpc, p.T - t_base) * p.group;
+      const int seen_by_all = run.len - p.T + t_base;  // token t_base's position: the last key every column sees
+      ok = warp_wait(&sh.q_ready[s & 3], (s >> 2) & 1, abort, wl);
+      const float* f = sh.f[s & 7] + c0;
+      float* m = sh.m + c0;
+      float l[kGC];
+#pragma unroll
+      for (int q = 0; q < kGC; ++q) l[q] = 0.0f;
+      if (k < kGC) m[k] = kUnset;
+      group_sync(bar_id);
+      for (int j = 0; j < run.n; ++j, ++i) {
+        const int b = i & 1;
+        const int past = (run.t0 + j) * kBN + k - seen_by_all;  // tokens from here on do see the key
+        const bool masked = (run.t0 + j) * kBN + kBN - 1 > seen_by_all;
+        if (ok) ok = warp_wait(&sh.s_full[b], (i >> 1) & 1, abort, wl);
+        float x[kGC];
+        bool over = false;
+        auto scores = [&](bool raw) {  // x = S f - m (or S f), -inf where the column does not see the key
+          uint32_t v[kGC];
+          tmem_ld_cols<kGC>(tmem + lane_off + Gm::col_s(b) + c0, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int q = 0; q < kGC; q += 4) {
+            const float4 f4 = *reinterpret_cast<const float4*>(f + q);
+            const float4 m4 = *reinterpret_cast<const float4*>(m + q);
+            x[q] = __fmaf_rn(__uint_as_float(v[q]), f4.x, raw ? 0.0f : -m4.x);
+            x[q + 1] = __fmaf_rn(__uint_as_float(v[q + 1]), f4.y, raw ? 0.0f : -m4.y);
+            x[q + 2] = __fmaf_rn(__uint_as_float(v[q + 2]), f4.z, raw ? 0.0f : -m4.z);
+            x[q + 3] = __fmaf_rn(__uint_as_float(v[q + 3]), f4.w, raw ? 0.0f : -m4.w);
+          }
+          if (masked) {
+#pragma unroll
+            for (int q = 0; q < kGC; ++q)
+              if (past > sh.tok[c0 + q]) x[q] = -INFINITY;
+          }
+        };
+        if (ok) {
+          tc_fence_after();
+          scores(false);
+          float mx = x[0];
+#pragma unroll
+          for (int q = 1; q < kGC; ++q) mx = fmaxf(mx, x[q]);
+          over = mx > kMove;
+        }
+        if (group_any(bar_id, over)) {  // some column's maximum moves (always so in a segment's first tile)
+          float alpha = 1.0f, m_new = 0.0f;
+          if (ok) scores(true);
+          {
+            const float mine_max = reduce_columns<kGC, true>(x, lane);
+            if (lane < kGC) sh.red[grp][quarter][lane] = mine_max;
+          }
+          group_sync(bar_id);
+          const int cl = lane & (kGC - 1);
+          {
+            const float cmax = fmaxf(fmaxf(sh.red[grp][0][cl], sh.red[grp][1][cl]),
+                                     fmaxf(sh.red[grp][2][cl], sh.red[grp][3][cl]));
+            const float m_old = m[cl];
+            m_new = m_old;
+            if (cmax - m_old > kMove) {
+              m_new = cmax - kStart;
+              alpha = ex2_approx(m_old - m_new);
+            }
+          }
+          group_sync(bar_id);
+          if (quarter == 0 && lane < kGC) m[lane] = m_new;
+          group_sync(bar_id);
+#pragma unroll
+          for (int q = 0; q < kGC; ++q) l[q] *= __shfl_sync(0xffffffffu, alpha, q);
+          if (j > 0) {
+            if (ok) ok = warp_wait(&sh.pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, abort, wl);
+            if (ok) {
+              tc_fence_after();
+#pragma unroll 1
+              for (int hh = 0; hh < 2; ++hh) {
+                uint32_t v[kGC];
+                tmem_ld_cols<kGC>(tmem + lane_off + Gm::kColO + hh * kCols + c0, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int q = 0; q < kGC; ++q)
+                  v[q] = __float_as_uint(__uint_as_float(v[q]) * __shfl_sync(0xffffffffu, alpha, q));
+                tmem_st_cols<kGC>(tmem + lane_off + Gm::kColO + hh * kCols + c0, v);
+              }
+              tmem_wait_st();
+            }
+          }
+          if (ok) scores(false);
+        }
+        tc_fence_before();
+        if (ok) warp_arrive(&sh.s_free[b], lane);
+        if (ok && i >= 2) ok = warp_wait(&sh.pv_done[b], ((i >> 1) - 1) & 1, abort, wl);
+#pragma unroll
+        for (int q = 0; q < kGC; ++q) {
+          x[q] = ex2_approx(x[q]);
+          l[q] += x[q];
+        }
+        if (ok) {  // row k of P^T, the group's 16-byte chunks; the 64-byte swizzle XORs them with bits 1-2 of k
+          uint8_t* prow = smem + Gm::kOffP + b * Gm::kPBuf + k * Gm::kPRow;
+#pragma unroll
+          for (int cc = 0; cc < kGC / 8; ++cc) {
+            const uint32_t chunk = (uint32_t)(grp * (kGC / 8) + cc) ^ ((uint32_t)(k >> 1) & 3u);
+            *reinterpret_cast<uint4*>(prow + chunk * 16) =
+                make_uint4(pack_f16x2(x[8 * cc], x[8 * cc + 1]), pack_f16x2(x[8 * cc + 2], x[8 * cc + 3]),
+                           pack_f16x2(x[8 * cc + 4], x[8 * cc + 5]), pack_f16x2(x[8 * cc + 6], x[8 * cc + 7]));
+          }
+          fence_proxy_async_smem();
+          tc_fence_before();
+          warp_arrive(&sh.p_full[b], lane);
+        }
+      }
+      // the segment's sums and O
+      if (ok) ok = warp_wait(&sh.pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, abort, wl);
+      const bool whole = run.n == run.tiles;
+      Slot& slot = ws.slot[run.t0 > 0 ? 0 : 1];
+      {
+        const float part = reduce_columns<kGC, false>(l, lane);
+        if (lane < kGC) sh.red[grp][quarter][lane] = part;
+      }
+      group_sync(bar_id);
+      if (quarter == 0 && lane < kGC) {
+        const float sum = sh.red[grp][0][lane] + sh.red[grp][1][lane] + sh.red[grp][2][lane] + sh.red[grp][3][lane];
+        sh.fin[c0 + lane] = whole ? (sum == 0.0f ? 0.0f : vg / sum) : 1.0f;
+        if (!whole && ok) {
+          slot.m[c0 + lane] = m[lane];
+          slot.l[c0 + lane] = sum;
+        }
+      }
+      group_sync(bar_id);
+      if (ok) {
+        tc_fence_after();
+        const bool nan = sh.v_nan != 0;
+        const int kvh = unit / p.n_tg;
+        const int64_t row0 = ((int64_t)run.r * p.T + t_base) * p.num_q_heads + (int64_t)kvh * p.group;
+#pragma unroll 1
+        for (int hh = 0; hh < 2; ++hh) {
+          uint32_t v[kGC];
+          tmem_ld_cols<kGC>(tmem + lane_off + Gm::kColO + hh * kCols + c0, v);
+          tmem_wait_ld();
+          const int d = hh * 128 + d_lane;
+          if (nan) {  // keys that only some columns see, with a NaN V scale
+            for (int key = max(seen_by_all + 1, run.t0 * kBN); key < min(run.len, (run.t0 + run.n) * kBN); ++key) {
+              const int col = key / p.block_size;
+              const int64_t blk = col < p.max_blocks ? (int64_t)__ldg(p.block_table + (int64_t)run.r * p.bt_stride + col) : -1;
+              if (blk < 0 || blk >= p.num_blocks) continue;
+              const uint8_t sb = __ldg(p.v_bscale + blk * p.scale_stride_blk + (key % p.block_size) * p.scale_stride_tok +
+                                       (int64_t)kvh * p.scale_stride_head + d / kFp4Group);
+              if ((sb & 0x7f) != 0x7f) continue;
+#pragma unroll
+              for (int q = 0; q < kGC; ++q)
+                if (key - seen_by_all <= sh.tok[c0 + q]) v[q] = 0x7fc00000u;
+            }
+          }
+#pragma unroll
+          for (int q = 0; q < kGC; ++q) {
+            if (c0 + q >= nq) break;
+            if (whole)
+              p.out[(row0 + sh.row_off[c0 + q]) * kFp4D + d] = __float2bfloat16(__uint_as_float(v[q]) * sh.fin[c0 + q]);
+            else
+              slot.o[c0 + q][d] = __uint_as_float(v[q]);
+          }
+        }
+        tc_fence_before();
+      }
+      // m, red and fin are read; the group's four warps go on or stop together (their barriers stay paired)
+      ok = !group_any(bar_id, !ok);
+    }
+  }
+
+  tc_fence_before();
+  const bool gave_up = __syncthreads_or(*abort != 0);
+  if (gave_up) {
+    // before the tensor memory is freed: wait for the copies of every armed phase and every MMA issued
+    if (warp == 0 && lane == 0)
+      for (int s = 0; s < kStages; ++s) {
+        drain_armed(&sh.k_full[s], sh.armed[0][s]);
+        drain_armed(&sh.v_full[s], sh.armed[1][s]);
+      }
+    if ((warp == 1 || warp == 2) && lane == 0) {
+      umma_commit(&sh.drain);
+      mbar_wait_drain(&sh.drain, 0);
+    }
+    tc_fence_before();
+    __syncthreads();
+  }
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+  if (tid == 0 && gave_up) record_error(p.dev_err, kErrTimeout);
+}
+
+// ------------------------------------------------------------------------------------------
+// merge of the pieces of a unit that several CTAs worked on
+// ------------------------------------------------------------------------------------------
+// Block (b, y): CTA b's note says whether a unit began in its range and went on; one warp a column adds
+// the pieces up: M = max m, out = v_scale sum 2^(m - M) O / sum 2^(m - M) l. Lane = 8 elements.
+__global__ void __launch_bounds__(256)
+    spec_verify_fp4_merge_kernel(const CtaWorkspace* __restrict__ ws, int32_t lines, int32_t ctas, int32_t T, int32_t group,
+                                 int32_t num_q_heads, int32_t tpc, int32_t n_tg, const float* __restrict__ v_scale,
+                                 __nv_bfloat16* __restrict__ out) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Note& note = ws[blockIdx.x].note;
+  if (!note.valid) return;
+  const int lane = threadIdx.x & 31, col = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int unit = note.unit, t_base = (unit % n_tg) * tpc;
+  if (col >= min(tpc, T - t_base) * group) return;
+  const int line = blockIdx.x % lines, c = blockIdx.x / lines;
+  const int64_t total = note.total;
+  // pieces c .. last: the smallest `last` whose range ends at or after the unit's end
+  const int pieces = (int)((note.unit_end * ctas + total - 1) / total) - c;
+  float M = -INFINITY, L = 0.0f;
+  float acc[8] = {};
+  auto piece = [&](int i) -> const Slot& { return ws[(int64_t)(c + i) * lines + line].slot[i == 0 ? 1 : 0]; };
+  auto has = [&](int i) {  // a range may be empty when there are fewer tiles than CTAs
+    return i < pieces && line_begin(total, c + i, ctas) < line_begin(total, c + i + 1, ctas);
+  };
+  for (int base = 0; base < pieces; base += 32) {
+    const bool live = has(base + lane) && piece(base + lane).l[col] != 0.0f;
+    float m = live ? piece(base + lane).m[col] : -INFINITY;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    M = fmaxf(M, m);
+  }
+  for (int base = 0; base < pieces; base += 32) {
+    const float l = has(base + lane) ? piece(base + lane).l[col] : 0.0f;
+    const float w = l != 0.0f ? exp2f(piece(base + lane).m[col] - M) : 0.0f;
+    float wl = w * l;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) wl += __shfl_xor_sync(0xffffffffu, wl, o);
+    L += wl;
+    const int n = min(32, pieces - base);
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      if (wi == 0.0f) continue;
+      const float4* src = reinterpret_cast<const float4*>(piece(base + i).o[col]) + lane * 2;
+      const float4 a = __ldg(src), b = __ldg(src + 1);
+      acc[0] += wi * a.x; acc[1] += wi * a.y; acc[2] += wi * a.z; acc[3] += wi * a.w;
+      acc[4] += wi * b.x; acc[5] += wi * b.y; acc[6] += wi * b.z; acc[7] += wi * b.w;
+    }
+  }
+  const float f = L == 0.0f ? 0.0f : __ldg(v_scale) / L;
+  const int t = t_base + col / group;
+  const int64_t row = ((int64_t)note.r * T + t) * num_q_heads + (int64_t)(unit / n_tg) * group + col % group;
+  reinterpret_cast<uint4*>(out + row * kFp4D)[lane] =
+      make_uint4(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f),
+                 pack_bf16x2(acc[4] * f, acc[5] * f), pack_bf16x2(acc[6] * f, acc[7] * f));
+}
+
+int gcd_int(int a, int b) {
+  while (b) {
+    const int t = a % b;
+    a = b;
+    b = t;
+  }
+  return a;
+}
+
+template <int kCols>
+pkv_status launch(const Params& p, cudaStream_t st) {
+  constexpr int kSmem = 1024 + Geo<kCols>::kTiles + (int)sizeof(Shared<kCols>);
+  static_assert(kSmem <= 227 * 1024, "dynamic shared memory of one CTA");
+  static std::atomic<uint64_t> attr_done{0};
+  once_per_device(attr_done, [] {
+    cudaFuncSetAttribute(spec_verify_fp4_kernel<kCols>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  });
+  const unsigned grid = (unsigned)(p.ctas * p.lines);
+  spec_verify_fp4_kernel<kCols><<<grid, kThreads, kSmem, st>>>(p);
+  pkv_status s = check_launch("spec_verify_attn_fp4");
+  if (s != PKV_OK) return s;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, (unsigned)(kCols / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, spec_verify_fp4_merge_kernel, (const CtaWorkspace*)p.ws, p.lines, p.ctas, p.T, p.group,
+                     p.num_q_heads, p.tpc, p.n_tg, p.v_scale, p.out);
+  return check_launch("spec_verify_attn_fp4 (merge)");
+}
 
 }  // namespace
 
 }  // namespace pkv
 
 extern "C" size_t pkv_spec_verify_fp4_workspace_bytes(int32_t num_ctas) {
-  return num_ctas > 0 ? (size_t)num_ctas * pkv::kWorkspacePerCta : 0;
+  return num_ctas > 0 ? (size_t)num_ctas * sizeof(pkv::CtaWorkspace) : 0;
 }
 
 extern "C" pkv_status pkv_spec_verify_attn_fp4(
@@ -137,7 +1031,7 @@ extern "C" pkv_status pkv_spec_verify_attn_fp4(
           "%s: bad size argument", name);
   PKV_UNSUP(num_q_heads % num_kv_heads == 0, "%s: num_q_heads %% num_kv_heads != 0", name);
   const int group = num_q_heads / num_kv_heads;
-  PKV_UNSUP(group <= 32, "%s: num_q_heads / num_kv_heads must be at most 32 (got %d)", name, group);
+  PKV_UNSUP(group <= kMaxCols, "%s: num_q_heads / num_kv_heads must be at most %d (got %d)", name, kMaxCols, group);
   PKV_UNSUP(block_size % 8 == 0, "%s: block_size must be a multiple of 8", name);
   PKV_ARG(stride_blk > 0 && stride_tok > 0 && stride_head > 0 && scale_stride_blk > 0 && scale_stride_tok > 0 &&
               scale_stride_head > 0,
@@ -148,14 +1042,70 @@ extern "C" pkv_status pkv_spec_verify_attn_fp4(
               scale_stride_head % 16 == 0,
           "%s: q, out, workspace, caches, scale caches and their strides must be 16-byte aligned", name);
   PKV_ARG(softmax_scale > 0.0f, "%s: softmax_scale must be positive", name);
-  PKV_ARG(workspace_bytes >= (int64_t)kWorkspacePerCta, "%s: the workspace needs at least %zu bytes", name,
-          kWorkspacePerCta);
-  const int64_t rows = (int64_t)num_reqs * T * num_q_heads;
-  PKV_ARG(rows < (1ll << 31), "%s: num_reqs * T * num_q_heads too large", name);
-  Args a{static_cast<const __nv_bfloat16*>(q), k_fp4, v_fp4, k_bscale, v_bscale, k_scale, v_scale, num_blocks,
-         stride_blk, stride_tok, stride_head, scale_stride_blk, scale_stride_tok, scale_stride_head, block_table,
-         bt_stride, max_blocks, seq_lens, T, num_q_heads, group, block_size, softmax_scale * 1.4426950408889634f,
-         static_cast<__nv_bfloat16*>(out), dev_err};
-  spec_verify_fp4_kernel<<<(unsigned)rows, kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
-  return check_launch(name);
+  PKV_ARG(workspace_bytes >= (int64_t)sizeof(CtaWorkspace), "%s: the workspace needs at least %zu bytes", name,
+          sizeof(CtaWorkspace));
+  Params p{};
+  // columns of a CTA: 16 when a KV head's query rows fit (half the padding, and half the softmax), else
+  // 32, the tokens spread over column groups that read the same keys
+  const bool narrow = (int64_t)T * group <= 16;
+  p.tpc = T < kMaxCols / group ? T : kMaxCols / group;
+  p.n_tg = (T + p.tpc - 1) / p.tpc;
+  const int64_t units = (int64_t)num_kv_heads * p.n_tg;
+  PKV_ARG(units < (1ll << 31) && (int64_t)num_reqs * T * num_q_heads < (1ll << 40), "%s: too many query rows", name);
+  // one line per unit (the heads of a request side by side) where that keeps nine tenths of the SMs busy,
+  // else one line with the units one after the other
+  int64_t ctas = workspace_bytes / (int64_t)sizeof(CtaWorkspace);
+  if (ctas > num_sms()) ctas = num_sms();
+  const bool side = units <= ctas && ctas / units * units * 10 >= ctas * 9;
+  p.lines = side ? (int)units : 1;
+  p.units = side ? 1 : (int)units;
+  p.ctas = (int)(ctas / p.lines);
+  const int G = gcd_int(block_size, kBN);
+  const uint64_t cdims[4] = {(uint64_t)kFp4RowBytes, (uint64_t)num_kv_heads, (uint64_t)block_size, (uint64_t)num_blocks};
+  const uint64_t cstr[3] = {(uint64_t)stride_head, (uint64_t)stride_tok, (uint64_t)stride_blk};
+  const uint64_t sdims[4] = {(uint64_t)kFp4Groups, (uint64_t)num_kv_heads, (uint64_t)block_size, (uint64_t)num_blocks};
+  const uint64_t sstr[3] = {(uint64_t)scale_stride_head, (uint64_t)scale_stride_tok, (uint64_t)scale_stride_blk};
+  p.big_ok = block_size >= kBN;
+  struct Map {
+    CUtensorMap* map;
+    const void* base;
+    bool scales, big;
+    const char* what;
+  };
+  const Map maps[8] = {{&p.kc, k_fp4, false, false, "k_fp4"},    {&p.vc, v_fp4, false, false, "v_fp4"},
+                       {&p.ks, k_bscale, true, false, "k_bscale"}, {&p.vs, v_bscale, true, false, "v_bscale"},
+                       {&p.kcb, k_fp4, false, true, "k_fp4"},    {&p.vcb, v_fp4, false, true, "v_fp4"},
+                       {&p.ksb, k_bscale, true, true, "k_bscale"}, {&p.vsb, v_bscale, true, true, "v_bscale"}};
+  for (const Map& m : maps) {
+    if (m.big && !p.big_ok) continue;
+    const uint32_t box[4] = {(uint32_t)(m.scales ? kFp4Groups : kFp4RowBytes), 1, (uint32_t)(m.big ? kBN : G), 1};
+    const pkv_status s = encode_tiled(m.map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, m.base, m.scales ? sdims : cdims,
+                                      m.scales ? sstr : cstr, box, m.what, !m.scales);
+    if (s != PKV_OK) return s;
+  }
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.v_bscale = v_bscale;
+  p.scale_stride_blk = scale_stride_blk;
+  p.scale_stride_tok = scale_stride_tok;
+  p.scale_stride_head = scale_stride_head;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.block_table = block_table;
+  p.bt_stride = bt_stride;
+  p.num_blocks = num_blocks;
+  p.max_blocks = max_blocks;
+  p.block_size = block_size;
+  p.seg = G;
+  p.seq_lens = seq_lens;
+  p.num_reqs = num_reqs;
+  p.T = T;
+  p.group = group;
+  p.num_q_heads = num_q_heads;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.ws = static_cast<CtaWorkspace*>(workspace);
+  p.dev_err = dev_err;
+  p.wait_limit_ns = take_wait_limit_ns();
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return narrow ? launch<16>(p, st) : launch<32>(p, st);
 }
