@@ -50,8 +50,8 @@ constexpr int kHalfStage = kCodeTile + kScaleTile;
 constexpr int kMaxCols = 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kUnset = -3e38f;          // running maximum of a column that has seen no key
-constexpr float kStart = 8.0f;            // a new maximum's weight is 2^8 ...
-constexpr float kMove = 15.0f;            // ... and the maximum moves when a weight would pass 2^15
+constexpr float kStart = 8.0f;            // a new maximum's weight is 2^8; the maximum moves when a thread's
+constexpr float kMove = 32768.0f;         // weights of one key add up to more than this (fp16 ends at 65,504)
 
 // Workspace of a CTA: two slots (0: the piece that began before it, 1: the piece that goes on after
 // it) of O [kMaxCols][256], m and l [kMaxCols], and a note for the merge.
@@ -114,14 +114,15 @@ struct alignas(16) Shared {
   int32_t row_off[kCols];                        // column -> token * Hq + head in group
   int32_t tok[kCols];                            // column -> token
   alignas(16) float f[8][kCols];                 // column factors of the segment (ring: the softmax may be 4 behind)
-  alignas(16) float m[kCols];                    // running maxima, log2
+  alignas(16) float m[kCols];                    // running maxima, log2, negated
   float red[2][4][kCols / 2];
   float fin[kCols];
 };
 
 struct Params {
-  CUtensorMap kc, vc, ks, vs;      // codes [nb][bs][hkv][128 B], scales [nb][bs][hkv][16 B]: boxes of seg keys
-  CUtensorMap kcb, vcb, ksb, vsb;  // boxes of 128 keys (block_size >= 128)
+  // K then V, each: codes [nb][bs][hkv][128 B] and scales [nb][bs][hkv][16 B] in boxes of seg keys, then
+  // both in boxes of 128 keys (block_size >= 128)
+  CUtensorMap map[8];
   const __nv_bfloat16* q;
   const uint8_t* v_bscale;
   int64_t scale_stride_blk, scale_stride_tok, scale_stride_head;
@@ -190,6 +191,11 @@ __device__ __forceinline__ bool group_any(int id, bool x) {
       : "=r"(r)
       : "r"(id), "r"((uint32_t)x)
       : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
 }
 // One arrival for the warp, after every lane's preceding accesses.
@@ -382,117 +388,159 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
 
   if (warp == 0) {
     // ------------------------------------------------------------------------------ producer
+    // K and V of a tile; the table entries of the next tile are read before this one is issued; one
+    // elected lane issues with warp-uniform operands.
     const int nseg = kBN / G;
+    Cursor cur = start;
+    Run run;
+    run.n = 0;
+    int j = -1;
+    // the next tile of the range: its first key, its head, and (lane = key segment) its table entries;
+    // -1: past the request, -2: not in the pool
+    auto advance = [&](int& key0, int& kvh, int& blk) {
+      if (++j >= run.n) {
+        j = 0;
+        if (!next_run(p, cur, run)) return false;
+      }
+      key0 = (run.t0 + j) * kBN;
+      kvh = (p.lines > 1 ? line : run.u) / p.n_tg;
+      blk = -1;
+      if (lane < nseg && key0 + lane * G < run.len) {
+        const int col = (key0 + lane * G) / p.block_size;
+        blk = col < p.max_blocks ? __ldg(p.block_table + (int64_t)run.r * p.bt_stride + col) : -2;
+      }
+      return true;
+    };
+    int key0, kvh, blk;
+    bool more = advance(key0, kvh, blk), ok = true;
+    for (int i = 0; more && ok; ++i) {
+      int key0_next = 0, kvh_next = 0, blk_next = -1;
+      more = advance(key0_next, kvh_next, blk_next);
+      const int st = i % kStages, round = i / kStages;
+      if (blk < -1 || (int64_t)blk >= p.num_blocks) blk = -2;
+      const uint32_t bad = __ballot_sync(0xffffffffu, blk == -2);
+      const uint32_t live = __ballot_sync(0xffffffffu, blk >= 0);
+      const int blk0 = __shfl_sync(0xffffffffu, blk, 0);
+      const int slot0 = key0 % p.block_size;
+      const bool big = p.big_ok && blk0 >= 0 && slot0 + kBN <= p.block_size;  // one block holds the tile
+      const uint32_t rows = big ? (uint32_t)kBN : (uint32_t)(__popc(live) * G);
+#pragma unroll 1
+      for (int which = 0; which < 2; ++which) {  // K, then V
+        uint64_t* full = (which ? sh.v_full : sh.k_full) + st;
+        if (round >= 1 && !warp_wait((which ? sh.v_empty : sh.k_empty) + st, (round - 1) & 1, abort, wl)) {
+          ok = false;
+          break;
+        }
+        uint8_t* codes = smem + Gm::kOffStage + st * Gm::kStage + which * kHalfStage;
+        uint8_t* scales = codes + kCodeTile;
+        const CUtensorMap* maps = &p.map[4 * which + (big ? 2 : 0)];
+        if (elect_one()) {
+          if (bad) record_error(p.dev_err, kErrDeviceBounds);
+          (which ? sh.v_bad : sh.k_bad)[st] = bad;
+          mbar_arm_tx(full, rows * (uint32_t)(kFp4RowBytes + kFp4Groups), &sh.armed[which][st]);
+          if (big) {
+            tma_load_4d(codes, maps, full, 0, kvh, slot0, blk0);
+            tma_load_4d(scales, maps + 1, full, 0, kvh, slot0, blk0);
+          }
+        }
+        __syncwarp();
+        if (!big) {
+          // eight boxes at a time from one elected block: the table entries are in registers first, so the
+          // copies go out a few clocks apart
+          int slot = slot0;
+#pragma unroll 1
+          for (int g0 = 0; g0 < nseg; g0 += 8) {
+            int ids[8];
+#pragma unroll
+            for (int g = 0; g < 8; ++g) ids[g] = __shfl_sync(0xffffffffu, blk, g0 + g);  // -1 past the last segment
+            int slots[8];
+#pragma unroll
+            for (int g = 0; g < 8; ++g) {
+              slots[g] = slot;
+              slot += G;
+              if (slot >= p.block_size) slot -= p.block_size;
+            }
+            if (elect_one()) {
+#pragma unroll
+              for (int g = 0; g < 8; ++g) {
+                const int sl = slots[g];
+                if (ids[g] >= 0) {
+                  tma_load_4d(codes + (g0 + g) * G * kFp4RowBytes, maps, full, 0, kvh, sl, ids[g]);
+                  tma_load_4d(scales + (g0 + g) * G * kFp4Groups, maps + 1, full, 0, kvh, sl, ids[g]);
+                }
+              }
+            }
+            __syncwarp();
+          }
+        }
+      }
+      key0 = key0_next;
+      kvh = kvh_next;
+      blk = blk_next;
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------------------ QK issuer
+    // The whole warp walks the tiles and one elected lane issues: with a warp-uniform address stream the
+    // MMAs follow one another at the tensor core's own rate (9.5 clocks each with 16 columns, 16.4 with
+    // 32); from inside a `lane == 0` branch each takes 45 and more.
+    constexpr uint32_t id = idesc_f16(128, kCols, false, false, false);
+    const uint64_t q_desc = smem_desc(smem_u32(smem + Gm::kOffQ), 16, 1024);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    Cursor cur = start;
+    Run run;
+    int i = 0;
+    bool ok = true;
+    for (int s = 0; ok && next_run(p, cur, run); ++s) {
+      ok = warp_wait(&sh.q_ready[s & 3], (s >> 2) & 1, abort, wl);
+      const uint64_t qd = q_desc + (uint64_t)((s & 1) * (Gm::kQBuf >> 4));
+      for (int j = 0; ok && j < run.n; ++j, ++i) {
+        const int b = i & 1;
+        if (i >= 2) ok = warp_wait(&sh.s_free[b], ((i >> 1) - 1) & 1, abort, wl);
+        if (ok) ok = warp_wait(&sh.kt_ready[b], (i >> 1) & 1, abort, wl);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tm + Gm::col_s(0) + b * kCols, a = tm + Gm::col_k(0) + b * 128;
+        if (elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < 16; ++ks)
+            umma_f16_ts(d, a + ks * 8, qd + (uint64_t)((ks >> 2) * (Gm::kQChunk >> 4) + (ks & 3) * 2), id, ks > 0);
+          umma_commit(&sh.s_full[b]);
+          umma_commit(&sh.kt_free[b]);
+          if (j == run.n - 1) umma_commit(&sh.q_free[s & 1]);
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------------------------ PV issuer
+    constexpr uint32_t id = idesc_f16(128, kCols, false, false, true);
+    const uint64_t p_desc = smem_desc(smem_u32(smem + Gm::kOffP), 0, 8 * Gm::kPRow, kLayoutSW64);
+    const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     Cursor cur = start;
     Run run;
     int i = 0;
     bool ok = true;
     while (ok && next_run(p, cur, run)) {
-      const int unit = p.lines > 1 ? line : run.u;
-      const int kvh = unit / p.n_tg;
-      for (int j = 0; j < run.n; ++j, ++i) {
-        const int st = i % kStages, round = i / kStages;
-        const int key0 = (run.t0 + j) * kBN;
-        int blk = -1;
-        if (lane < nseg && key0 + lane * G < run.len) {
-          const int col = (key0 + lane * G) / p.block_size;
-          blk = col < p.max_blocks ? __ldg(p.block_table + (int64_t)run.r * p.bt_stride + col) : -2;
-          if (blk < 0 || (int64_t)blk >= p.num_blocks) blk = -2;
-        }
-        const uint32_t bad = __ballot_sync(0xffffffffu, blk == -2);
-        const uint32_t nload = __popc(__ballot_sync(0xffffffffu, blk >= 0));
-        const int blk0 = __shfl_sync(0xffffffffu, blk, 0);
-        const int slot0 = key0 % p.block_size;
-        const bool big = p.big_ok && blk0 >= 0 && slot0 + kBN <= p.block_size;  // one block holds the tile
-        const uint32_t rows = big ? (uint32_t)kBN : nload * (uint32_t)G;
-        if (bad && lane == 0) record_error(p.dev_err, kErrDeviceBounds);
-        for (int which = 0; which < 2; ++which) {  // K, then V
-          uint64_t* full = which ? &sh.v_full[st] : &sh.k_full[st];
-          bool got = true;
-          if (lane == 0 && round >= 1)
-            got = mbar_wait_suspend(which ? &sh.v_empty[st] : &sh.k_empty[st], (round - 1) & 1, abort, wl);
-          ok = __shfl_sync(0xffffffffu, got, 0);
-          if (!ok) break;
-          uint8_t* codes = smem + Gm::kOffStage + st * Gm::kStage + which * kHalfStage;
-          uint8_t* scales = codes + kCodeTile;
-          if (lane == 0) {
-            (which ? sh.v_bad : sh.k_bad)[st] = bad;
-            mbar_arm_tx(full, rows * (uint32_t)(kFp4RowBytes + kFp4Groups), &sh.armed[which][st]);
-            if (big) {
-              tma_load_4d(codes, which ? &p.vcb : &p.kcb, full, 0, kvh, slot0, blk0);
-              tma_load_4d(scales, which ? &p.vsb : &p.ksb, full, 0, kvh, slot0, blk0);
-            }
-          }
-          __syncwarp();
-          if (!big && blk >= 0) {
-            const int slot = (key0 + lane * G) % p.block_size;
-            tma_load_4d(codes + lane * G * kFp4RowBytes, which ? &p.vc : &p.kc, full, 0, kvh, slot, blk);
-            tma_load_4d(scales + lane * G * kFp4Groups, which ? &p.vs : &p.ks, full, 0, kvh, slot, blk);
-          }
-          __syncwarp();
-        }
-        if (!ok) break;
-      }
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------------------------ QK issuer
-    if (lane == 0) {
-      constexpr uint32_t id = idesc_f16(128, kCols, false, false, false);
-      const uint32_t q_base = smem_u32(smem + Gm::kOffQ);
-      Cursor cur = start;
-      Run run;
-      int i = 0, s = 0;
-      bool ok = true;
-      for (; ok && next_run(p, cur, run); ++s) {
-        ok = mbar_wait_suspend(&sh.q_ready[s & 3], (s >> 2) & 1, abort, wl);
-        for (int j = 0; ok && j < run.n; ++j, ++i) {
-          const int b = i & 1;
-          ok = (i < 2 || mbar_wait_suspend(&sh.s_free[b], ((i >> 1) - 1) & 1, abort, wl)) &&
-               mbar_wait_suspend(&sh.kt_ready[b], (i >> 1) & 1, abort, wl);
+      for (int j = 0; ok && j < run.n; ++j, ++i) {
+        const int b = i & 1;
+        ok = warp_wait(&sh.p_full[b], (i >> 1) & 1, abort, wl);
+        const uint64_t pd = p_desc + (uint64_t)(b * (Gm::kPBuf >> 4));
+        for (int hh = 0; ok && hh < 2; ++hh) {
+          ok = warp_wait(&sh.vt_ready[hh], i & 1, abort, wl);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t qb = q_base + (s & 1) * Gm::kQBuf;
-#pragma unroll
-          for (int ks = 0; ks < 16; ++ks)
-            umma_f16_ts(tmem + Gm::col_s(b), tmem + Gm::col_k(b) + ks * 8,
-                        smem_desc(qb + (ks >> 2) * Gm::kQChunk + (ks & 3) * 32, 16, 1024), id, ks > 0);
-          umma_commit(&sh.s_full[b]);
-          umma_commit(&sh.kt_free[b]);
-        }
-        if (ok) umma_commit(&sh.q_free[s & 1]);
-      }
-    }
-    __syncwarp();
-  } else if (warp == 2) {
-    // ------------------------------------------------------------------------------ PV issuer
-    if (lane == 0) {
-      constexpr uint32_t id = idesc_f16(128, kCols, false, false, true);
-      const uint32_t p_base = smem_u32(smem + Gm::kOffP);
-      Cursor cur = start;
-      Run run;
-      int i = 0;
-      bool ok = true;
-      while (ok && next_run(p, cur, run)) {
-        for (int j = 0; ok && j < run.n; ++j, ++i) {
-          const int b = i & 1;
-          ok = mbar_wait_suspend(&sh.p_full[b], (i >> 1) & 1, abort, wl);
-          const uint32_t pb = p_base + b * Gm::kPBuf;
-          for (int hh = 0; ok && hh < 2; ++hh) {
-            ok = mbar_wait_suspend(&sh.vt_ready[hh], i & 1, abort, wl);
-            if (!ok) break;
-            tc_fence_after();
+          const uint32_t d = tm + Gm::kColO + hh * kCols, a = tm + Gm::kColV + hh * 64;
+          if (elect_one()) {
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
-              umma_f16_ts(tmem + Gm::kColO + hh * kCols, tmem + Gm::kColV + hh * 64 + ks * 8,
-                          smem_desc(pb + ks * 16 * Gm::kPRow, 0, 8 * Gm::kPRow, kLayoutSW64), id,
-                          (j > 0 || ks > 0) ? 1u : 0u);
+              umma_f16_ts(d, a + ks * 8, pd + (uint64_t)(ks * (16 * Gm::kPRow >> 4)), id, (j > 0 || ks > 0) ? 1u : 0u);
             umma_commit(&sh.vt_free[hh]);
+            if (hh == 1) umma_commit(&sh.pv_done[b]);
           }
-          if (ok) umma_commit(&sh.pv_done[b]);
+          __syncwarp();
         }
       }
     }
-    __syncwarp();
   } else if (warp == 3) {
     // ------------------------------------------------------------------------------ V scales
     // lane = four keys: their 4 x 16 e4m3 bytes as fp16, [chunk of 32 elements][key quad][group][key].
@@ -620,23 +668,26 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
         uint4 sc = *reinterpret_cast<const uint4*>(stage + kCodeTile + k * 16);
         const uint32_t bad = sh.k_bad[st];
         if (bad && ((bad >> (k / G)) & 1u)) sc = make_uint4(0, 0, 0, 0);
-        const uint32_t scw[4] = {sc.x, sc.y, sc.z, sc.w};
+#pragma unroll 1
+        for (int c2 = 0; c2 < 4; ++c2) {  // 64 elements: four groups, 32 tensor-memory columns
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {  // 32 elements, two groups, 16 tensor-memory columns
-          const uint4 v = *reinterpret_cast<const uint4*>(stage + k * 128 + ((c ^ (k & 7)) * 16));
-          const uint32_t s2 = e4m3x2_to_f16x2((uint16_t)(scw[c >> 1] >> (16 * (c & 1))));
-          const __half2 sh2 = *reinterpret_cast<const __half2*>(&s2);
-          const __half2 lo = __low2half2(sh2), hi = __high2half2(sh2);
-          const uint32_t slo = *reinterpret_cast<const uint32_t*>(&lo), shi = *reinterpret_cast<const uint32_t*>(&hi);
-          uint32_t o[16], x[4];
-          const uint32_t cw[4] = {v.x, v.y, v.z, v.w};
+          for (int h = 0; h < 2; ++h) {
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + k * 128 + (((2 * c2 + h) ^ (k & 7)) * 16));
+            const uint32_t s2 = e4m3x2_to_f16x2((uint16_t)(h ? sc.x >> 16 : sc.x));
+            const __half2 sh2 = *reinterpret_cast<const __half2*>(&s2);
+            const __half2 lo = __low2half2(sh2), hi = __high2half2(sh2);
+            const uint32_t slo = *reinterpret_cast<const uint32_t*>(&lo), shi = *reinterpret_cast<const uint32_t*>(&hi);
+            uint32_t o[16], x[4];
+            const uint32_t cw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            e2m1x8_to_f16(cw[y], x);
+            for (int y = 0; y < 4; ++y) {
+              e2m1x8_to_f16(cw[y], x);
 #pragma unroll
-            for (int z = 0; z < 4; ++z) o[4 * y + z] = hmul2_u32(x[z], y < 2 ? slo : shi);
+              for (int z = 0; z < 4; ++z) o[4 * y + z] = hmul2_u32(x[z], y < 2 ? slo : shi);
+            }
+            tmem_st_32x32b_x16(tmem + lane_off + Gm::col_k(0) + b * 128 + 32 * c2 + 16 * h, o);
           }
-          tmem_st_32x32b_x16(tmem + lane_off + Gm::col_k(b) + 16 * c, o);
+          sc = make_uint4(sc.y, sc.z, sc.w, 0);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -666,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
         tc_fence_after();
         const uint32_t codes = smem_u32(smem + Gm::kOffStage + st * Gm::kStage + kHalfStage) + lane * 128 + ((c ^ (lane & 7)) * 16);
         const uint8_t* sf = smem + Gm::kOffSf + b * Gm::kSfBuf + c * 512 + (lane & 3) * 16;
-#pragma unroll
+#pragma unroll 1
         for (int kb = 0; kb < 4; ++kb) {  // 32 keys
           uint32_t w[4], even[8], odd[8];
           ldmatrix_t8_x2(codes + kb * 32 * 128, w);
@@ -728,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
       float l[kGC];
 #pragma unroll
       for (int q = 0; q < kGC; ++q) l[q] = 0.0f;
-      if (k < kGC) m[k] = kUnset;
+      if (k < kGC) m[k] = -kUnset;
       group_sync(bar_id);
       for (int j = 0; j < run.n; ++j, ++i) {
         const int b = i & 1;
@@ -736,37 +787,54 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
         const bool masked = (run.t0 + j) * kBN + kBN - 1 > seen_by_all;
         if (ok) ok = warp_wait(&sh.s_full[b], (i >> 1) & 1, abort, wl);
         float x[kGC];
-        bool over = false;
-        auto scores = [&](bool raw) {  // x = S f - m (or S f), -inf where the column does not see the key
-          uint32_t v[kGC];
-          tmem_ld_cols<kGC>(tmem + lane_off + Gm::col_s(b) + c0, v);
-          tmem_wait_ld();
+        float tile_sum[2];
+        const uint32_t ts = tmem + lane_off + Gm::col_s(0) + b * kCols + c0;
+        for (int pass = 0;; ++pass) {
+          // weights 2^(S f - m), 0 where the column does not see the key. One that passes 2^15 shows in
+          // their sum (no weight is negative; the sum's pipe has room where the maximum's has none).
+          bool over = false;
+          if (ok) {
+            tc_fence_after();
+            uint32_t v[kGC];
+            tmem_ld_cols<kGC>(ts, v);
+            tmem_wait_ld();
 #pragma unroll
-          for (int q = 0; q < kGC; q += 4) {
-            const float4 f4 = *reinterpret_cast<const float4*>(f + q);
-            const float4 m4 = *reinterpret_cast<const float4*>(m + q);
-            x[q] = __fmaf_rn(__uint_as_float(v[q]), f4.x, raw ? 0.0f : -m4.x);
-            x[q + 1] = __fmaf_rn(__uint_as_float(v[q + 1]), f4.y, raw ? 0.0f : -m4.y);
-            x[q + 2] = __fmaf_rn(__uint_as_float(v[q + 2]), f4.z, raw ? 0.0f : -m4.z);
-            x[q + 3] = __fmaf_rn(__uint_as_float(v[q + 3]), f4.w, raw ? 0.0f : -m4.w);
+            for (int q = 0; q < kGC; q += 4) {
+              const float4 f4 = *reinterpret_cast<const float4*>(f + q);
+              const float4 m4 = *reinterpret_cast<const float4*>(m + q);
+              fma2(x[q], x[q + 1], __uint_as_float(v[q]), __uint_as_float(v[q + 1]), f4.x, f4.y, m4.x, m4.y);
+              fma2(x[q + 2], x[q + 3], __uint_as_float(v[q + 2]), __uint_as_float(v[q + 3]), f4.z, f4.w, m4.z, m4.w);
+            }
+            if (masked) {
+#pragma unroll
+              for (int q = 0; q < kGC; ++q)
+                if (past > sh.tok[c0 + q]) x[q] = -INFINITY;
+            }
+            if (pass == 1) {  // past 2^9 only by the rounding of scores of 2^24 and more
+#pragma unroll
+              for (int q = 0; q < kGC; ++q) x[q] = x[q] > 9.0f ? 9.0f : x[q];
+            }
+#pragma unroll
+            for (int q = 0; q < kGC; ++q) x[q] = ex2_approx(x[q]);
+            tile_sum[0] = x[0];
+            tile_sum[1] = x[1];
+#pragma unroll
+            for (int q = 2; q < kGC; q += 2) add2(tile_sum[0], tile_sum[1], tile_sum[0], tile_sum[1], x[q], x[q + 1]);
+            over = !(tile_sum[0] + tile_sum[1] <= kMove);  // (a NaN column hides nothing)
           }
-          if (masked) {
-#pragma unroll
-            for (int q = 0; q < kGC; ++q)
-              if (past > sh.tok[c0 + q]) x[q] = -INFINITY;
-          }
-        };
-        if (ok) {
-          tc_fence_after();
-          scores(false);
-          float mx = x[0];
-#pragma unroll
-          for (int q = 1; q < kGC; ++q) mx = fmaxf(mx, x[q]);
-          over = mx > kMove;
-        }
-        if (group_any(bar_id, over)) {  // some column's maximum moves (always so in a segment's first tile)
+          if (pass == 1 || !group_any(bar_id, over)) break;
+          // some column's maximum moves (always so in a run's first tile): exact maxima of this tile
           float alpha = 1.0f, m_new = 0.0f;
-          if (ok) scores(true);
+          if (ok) {
+            uint32_t v[kGC];
+            tmem_ld_cols<kGC>(ts, v);
+            tmem_wait_ld();
+#pragma unroll
+            for (int q = 0; q < kGC; ++q) {
+              x[q] = __uint_as_float(v[q]) * f[q];
+              if (masked && past > sh.tok[c0 + q]) x[q] = -INFINITY;
+            }
+          }
           {
             const float mine_max = reduce_columns<kGC, true>(x, lane);
             if (lane < kGC) sh.red[grp][quarter][lane] = mine_max;
@@ -776,15 +844,15 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
           {
             const float cmax = fmaxf(fmaxf(sh.red[grp][0][cl], sh.red[grp][1][cl]),
                                      fmaxf(sh.red[grp][2][cl], sh.red[grp][3][cl]));
-            const float m_old = m[cl];
+            const float m_old = -m[cl];
             m_new = m_old;
-            if (cmax - m_old > kMove) {
+            if (cmax - m_old > kStart) {
               m_new = cmax - kStart;
               alpha = ex2_approx(m_old - m_new);
             }
           }
           group_sync(bar_id);
-          if (quarter == 0 && lane < kGC) m[lane] = m_new;
+          if (quarter == 0 && lane < kGC) m[lane] = -m_new;
           group_sync(bar_id);
 #pragma unroll
           for (int q = 0; q < kGC; ++q) l[q] *= __shfl_sync(0xffffffffu, alpha, q);
@@ -805,16 +873,12 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
               tmem_wait_st();
             }
           }
-          if (ok) scores(false);
         }
         tc_fence_before();
         if (ok) warp_arrive(&sh.s_free[b], lane);
         if (ok && i >= 2) ok = warp_wait(&sh.pv_done[b], ((i >> 1) - 1) & 1, abort, wl);
 #pragma unroll
-        for (int q = 0; q < kGC; ++q) {
-          x[q] = ex2_approx(x[q]);
-          l[q] += x[q];
-        }
+        for (int q = 0; q < kGC; q += 2) add2(l[q], l[q + 1], l[q], l[q + 1], x[q], x[q + 1]);
         if (ok) {  // row k of P^T, the group's 16-byte chunks; the 64-byte swizzle XORs them with bits 1-2 of k
           uint8_t* prow = smem + Gm::kOffP + b * Gm::kPBuf + k * Gm::kPRow;
 #pragma unroll
@@ -842,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
         const float sum = sh.red[grp][0][lane] + sh.red[grp][1][lane] + sh.red[grp][2][lane] + sh.red[grp][3][lane];
         sh.fin[c0 + lane] = whole ? (sum == 0.0f ? 0.0f : vg / sum) : 1.0f;
         if (!whole && ok) {
-          slot.m[c0 + lane] = m[lane];
+          slot.m[c0 + lane] = -m[lane];
           slot.l[c0 + lane] = sum;
         }
       }
@@ -891,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
   const bool gave_up = __syncthreads_or(*abort != 0);
   if (gave_up) {
     // before the tensor memory is freed: wait for the copies of every armed phase and every MMA issued
-    if (warp == 0 && lane == 0)
+    if (tid == 0)
       for (int s = 0; s < kStages; ++s) {
         drain_armed(&sh.k_full[s], sh.armed[0][s]);
         drain_armed(&sh.v_full[s], sh.armed[1][s]);
@@ -1066,21 +1130,15 @@ extern "C" pkv_status pkv_spec_verify_attn_fp4(
   const uint64_t sdims[4] = {(uint64_t)kFp4Groups, (uint64_t)num_kv_heads, (uint64_t)block_size, (uint64_t)num_blocks};
   const uint64_t sstr[3] = {(uint64_t)scale_stride_head, (uint64_t)scale_stride_tok, (uint64_t)scale_stride_blk};
   p.big_ok = block_size >= kBN;
-  struct Map {
-    CUtensorMap* map;
-    const void* base;
-    bool scales, big;
-    const char* what;
-  };
-  const Map maps[8] = {{&p.kc, k_fp4, false, false, "k_fp4"},    {&p.vc, v_fp4, false, false, "v_fp4"},
-                       {&p.ks, k_bscale, true, false, "k_bscale"}, {&p.vs, v_bscale, true, false, "v_bscale"},
-                       {&p.kcb, k_fp4, false, true, "k_fp4"},    {&p.vcb, v_fp4, false, true, "v_fp4"},
-                       {&p.ksb, k_bscale, true, true, "k_bscale"}, {&p.vsb, v_bscale, true, true, "v_bscale"}};
-  for (const Map& m : maps) {
-    if (m.big && !p.big_ok) continue;
-    const uint32_t box[4] = {(uint32_t)(m.scales ? kFp4Groups : kFp4RowBytes), 1, (uint32_t)(m.big ? kBN : G), 1};
-    const pkv_status s = encode_tiled(m.map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, m.base, m.scales ? sdims : cdims,
-                                      m.scales ? sstr : cstr, box, m.what, !m.scales);
+  const void* const bases[4] = {k_fp4, k_bscale, v_fp4, v_bscale};
+  const char* const names[4] = {"k_fp4", "k_bscale", "v_fp4", "v_bscale"};
+  for (int i = 0; i < 8; ++i) {
+    const bool scales = i & 1, big = i & 2;
+    if (big && !p.big_ok) continue;
+    const int t = (i >> 2) * 2 + (scales ? 1 : 0);
+    const uint32_t box[4] = {(uint32_t)(scales ? kFp4Groups : kFp4RowBytes), 1, (uint32_t)(big ? kBN : G), 1};
+    const pkv_status s = encode_tiled(&p.map[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, bases[t], scales ? sdims : cdims,
+                                      scales ? sstr : cstr, box, names[t], !scales);
     if (s != PKV_OK) return s;
   }
   p.q = static_cast<const __nv_bfloat16*>(q);
