@@ -43,7 +43,6 @@ namespace {
 
 constexpr int kBN = 128;                  // keys of a tile
 constexpr int kThreads = 768;
-constexpr int kStages = 4;
 constexpr int kCodeTile = kBN * kFp4RowBytes;  // 16 KB
 constexpr int kScaleTile = kBN * kFp4Groups;   // 2 KB
 constexpr int kHalfStage = kCodeTile + kScaleTile;
@@ -73,38 +72,40 @@ static_assert(sizeof(CtaWorkspace) % 16 == 0, "workspace of a CTA");
 template <int kCols>
 struct Geo {
   static constexpr int kGC = kCols / 2;          // columns of a softmax warpgroup
+  static constexpr int kStages = kCols == 16 ? 4 : 3;
   static constexpr int kQChunk = kCols * 128;    // fp16 [kCols rows][64]
   static constexpr int kQBuf = 4 * kQChunk;
-  static constexpr int kPRow = 64;               // bytes of a key's row of P^T (32 columns, 64-byte swizzle)
-  static constexpr int kPBuf = kBN * kPRow;
+  static constexpr int kPRow = kCols * 4;        // bytes of a row of P^T: 2 kCols columns
+  static constexpr uint32_t kPLayout = kCols == 16 ? kLayoutSW64 : kLayoutSW128;
+  static constexpr int kPBuf = 2 * kBN * kPRow;
   static constexpr int kOffQ = 0;
   static constexpr int kOffP = kOffQ + 2 * kQBuf;
-  static constexpr int kOffSf = kOffP + 2 * kPBuf;          // V scales, fp16 [8 chunks][32 key quads][2 groups][4 keys]
+  static constexpr int kOffSf = kOffP + 2 * kPBuf;          // V scales, fp16 [4 quarters][32 key quads][4 groups][4 keys]
   static constexpr int kSfBuf = kBN * kFp4Groups * 2;
   static constexpr int kOffStage = kOffSf + 2 * kSfBuf;
   static constexpr int kStage = 2 * kHalfStage;             // K codes, K scales, V codes, V scales
   static constexpr int kTiles = kOffStage + kStages * kStage;
-  __host__ __device__ static constexpr uint32_t col_k(int b) { return 128u * b; }
-  static constexpr uint32_t kColV = 256u;                   // two halves of head_dim, 64 columns each
-  __host__ __device__ static constexpr uint32_t col_s(int b) { return 384u + (uint32_t)(b * kCols); }
-  static constexpr uint32_t kColO = 384u + 2u * kCols;      // two halves of head_dim
+  static constexpr uint32_t kColK = 0;                      // two K tiles, 128 columns each
+  static constexpr uint32_t kColV = 256;                    // the V tile: a column a key
+  static constexpr uint32_t kColS = 384;                    // two S^T
+  static constexpr uint32_t kColO = 384 + 2 * kCols;        // O^T of the even elements, then of the odd ones
   static_assert(kColO + 2 * kCols <= kTmemCols, "tensor memory");
   static_assert(kOffStage % 1024 == 0 && kHalfStage % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms");
 };
 
 template <int kCols>
 struct alignas(16) Shared {
-  uint64_t k_full[kStages], k_empty[kStages];    // K codes and scales of a tile
-  uint64_t v_full[kStages], v_empty[kStages];    // V codes and scales
+  static constexpr int kStages = Geo<kCols>::kStages;
+  uint64_t full[kStages], empty[kStages];        // codes and scales of a tile
   uint64_t q_ready[4], q_free[2];                // Q of run s (buffer s % 2; barrier s % 4: the K rows may be 3 runs ahead of the softmax)
   uint64_t kt_ready[2], kt_free[2];              // K in tensor memory
   uint64_t s_full[2], s_free[2];                 // S^T
   uint64_t sf_ready[2], sf_free[2];              // transposed V scales
-  uint64_t vt_ready[2], vt_free[2];              // V in tensor memory, per half of head_dim
+  uint64_t vt_ready[2], vt_free[2];              // V in tensor memory, per half of the keys
   uint64_t p_full[2], pv_done[2];                // P^T written; PV of the tile complete
   uint64_t drain;
-  uint32_t armed[2][kStages];
-  uint32_t k_bad[kStages], v_bad[kStages];       // key segments in a bad block
+  uint32_t armed[kStages];
+  uint32_t bad[kStages];                         // key segments in a bad block
   uint32_t tmem_base;
   int abort;
   int v_nan;                                     // a NaN V scale was left out for a key that some columns do not see
@@ -203,9 +204,37 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
 }
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t wl) {
-  return __all_sync(0xffffffffu, mbar_wait_suspend(bar, parity, abort, wl));
+// A wait whose threads sleep in the barrier test, in few instructions (the roles' loops share the
+// instruction cache): gives up after limit_ns, or when another thread of the CTA has.
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+  uint64_t t0 = 0;
+  while (!mbar_try_wait_suspend(bar, parity)) {
+    if (*abort) return false;
+    const uint64_t t = globaltimer_ns();
+    if (t0 == 0) {
+      t0 = t;
+    } else if (t - t0 > limit_ns) {
+      *abort = 1;
+      return false;
+    }
+  }
+  return true;
 }
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t wl) {
+  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort, wl));
+}
+// Stage and parity of the tile ring.
+template <int kStages>
+struct Ring {
+  int st = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++st == kStages) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+};
 
 template <int kGC>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t a, uint32_t (&r)[kGC]) {
@@ -253,20 +282,10 @@ __device__ __forceinline__ void tmem_st_16x256b_x2(uint32_t a, const uint32_t (&
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
-// Bytes 0 and 2 of w as two fp16 pairs.
-__device__ __forceinline__ void e2m1_bytes02(uint32_t w, uint32_t& a, uint32_t& b) {
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b2;\n\t}"
-      : "=r"(a), "=r"(b)
-      : "r"(w));
-}
-
 template <int kCols>
 __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __grid_constant__ Params p) {
   using Gm = Geo<kCols>;
-  constexpr int kGC = Gm::kGC;
+  constexpr int kGC = Gm::kGC, kStages = Gm::kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Shared<kCols>& sh = *reinterpret_cast<Shared<kCols>*>(smem + Gm::kTiles);
@@ -282,11 +301,9 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
   const int live_groups = nq_max > kGC ? 2 : 1;  // softmax warpgroups with a live column
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sh.k_full[s], 1);
-      mbar_init(&sh.k_empty[s], 4);
-      mbar_init(&sh.v_full[s], 1);
-      mbar_init(&sh.v_empty[s], 9);
-      sh.armed[0][s] = sh.armed[1][s] = 0;
+      mbar_init(&sh.full[s], 1);
+      mbar_init(&sh.empty[s], 4 + 8 + 1);  // K rows, V columns, V scales
+      sh.armed[s] = 0;
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sh.q_ready[b], 4);
@@ -314,6 +331,10 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
     sh.tok[tid] = t;
     sh.row_off[tid] = t * p.num_q_heads + (tid - t * p.group);
   }
+  // P^T: its zero half stays zero, the softmax writes the other
+  for (int x = tid; x < 2 * Gm::kPBuf / 16; x += kThreads)
+    reinterpret_cast<uint4*>(smem + Gm::kOffP)[x] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
   // the line's tiles, and zeros for the rows of empty requests (each CTA its share of the requests)
   long long mine = 0;
   for (int r = tid; r < p.num_reqs; r += kThreads) {
@@ -388,95 +409,84 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
 
   if (warp == 0) {
     // ------------------------------------------------------------------------------ producer
-    // K and V of a tile; the table entries of the next tile are read before this one is issued; one
-    // elected lane issues with warp-uniform operands.
+    // Lane = key segment (G keys, inside one block). Each lane walks its segment's place in the table a
+    // tile ahead of the copies, without divisions inside a run; one elected lane issues the tile's
+    // copies. Few instructions a tile: this code runs once in a tile, so it is fetched anew each time.
     const int nseg = kBN / G;
+    const int q128 = kBN / p.block_size, r128 = kBN % p.block_size;
     Cursor cur = start;
     Run run;
     run.n = 0;
-    int j = -1;
-    // the next tile of the range: its first key, its head, and (lane = key segment) its table entries;
-    // -1: past the request, -2: not in the pool
-    auto advance = [&](int& key0, int& kvh, int& blk) {
-      if (++j >= run.n) {
+    int j = 0, key = 0, col = 0, slot = 0, kvh = 0;  // of the tile that is looked up
+    const int32_t* table = nullptr;
+    bool more = true;
+    // moves on to the next tile and reads its table entry: -1 past the request, -2 past the table
+    auto look_up = [&]() -> int {
+      if (++j < run.n) {
+        key += kBN;
+        col += q128;
+        slot += r128;
+        if (slot >= p.block_size) {
+          slot -= p.block_size;
+          ++col;
+        }
+      } else {
+        more = next_run(p, cur, run);
+        if (!more) return -1;
         j = 0;
-        if (!next_run(p, cur, run)) return false;
+        kvh = (p.lines > 1 ? line : run.u) / p.n_tg;
+        key = run.t0 * kBN + lane * G;
+        col = key / p.block_size;
+        slot = key - col * p.block_size;
+        table = p.block_table + (int64_t)run.r * p.bt_stride;
       }
-      key0 = (run.t0 + j) * kBN;
-      kvh = (p.lines > 1 ? line : run.u) / p.n_tg;
-      blk = -1;
-      if (lane < nseg && key0 + lane * G < run.len) {
-        const int col = (key0 + lane * G) / p.block_size;
-        blk = col < p.max_blocks ? __ldg(p.block_table + (int64_t)run.r * p.bt_stride + col) : -2;
-      }
-      return true;
+      if (lane >= nseg || key >= run.len) return -1;
+      return col < p.max_blocks ? __ldg(table + col) : -2;
     };
-    int key0, kvh, blk;
-    bool more = advance(key0, kvh, blk), ok = true;
-    for (int i = 0; more && ok; ++i) {
-      int key0_next = 0, kvh_next = 0, blk_next = -1;
-      more = advance(key0_next, kvh_next, blk_next);
-      const int st = i % kStages, round = i / kStages;
-      if (blk < -1 || (int64_t)blk >= p.num_blocks) blk = -2;
-      const uint32_t bad = __ballot_sync(0xffffffffu, blk == -2);
-      const uint32_t live = __ballot_sync(0xffffffffu, blk >= 0);
-      const int blk0 = __shfl_sync(0xffffffffu, blk, 0);
-      const int slot0 = key0 % p.block_size;
-      const bool big = p.big_ok && blk0 >= 0 && slot0 + kBN <= p.block_size;  // one block holds the tile
-      const uint32_t rows = big ? (uint32_t)kBN : (uint32_t)(__popc(live) * G);
-#pragma unroll 1
-      for (int which = 0; which < 2; ++which) {  // K, then V
-        uint64_t* full = (which ? sh.v_full : sh.k_full) + st;
-        if (round >= 1 && !warp_wait((which ? sh.v_empty : sh.k_empty) + st, (round - 1) & 1, abort, wl)) {
-          ok = false;
-          break;
-        }
-        uint8_t* codes = smem + Gm::kOffStage + st * Gm::kStage + which * kHalfStage;
-        uint8_t* scales = codes + kCodeTile;
-        const CUtensorMap* maps = &p.map[4 * which + (big ? 2 : 0)];
+    int blk = look_up();
+    Ring<kStages> ring;
+    for (int i = 0; more; ++i, ring.next()) {
+      const int c_slot = slot, c_kvh = kvh;
+      int c_blk = blk;
+      blk = look_up();
+      uint64_t* full = &sh.full[ring.st];
+      if (i >= kStages && !warp_wait(&sh.empty[ring.st], ring.ph ^ 1, abort, wl)) break;
+      if ((int64_t)c_blk >= p.num_blocks) c_blk = -2;
+      const uint32_t bad = __ballot_sync(0xffffffffu, c_blk < -1);
+      const uint32_t live = __ballot_sync(0xffffffffu, c_blk >= 0);
+      // one block holds the tile (segment 0 is live then, or bad)
+      const bool big = p.big_ok && __shfl_sync(0xffffffffu, c_blk >= 0 && c_slot + kBN <= p.block_size, 0);
+      uint8_t* stage = smem + Gm::kOffStage + ring.st * Gm::kStage;
+      if (bad && lane == 0) record_error(p.dev_err, kErrDeviceBounds);
+      if (lane == 0) {
+        sh.bad[ring.st] = bad;
+        const uint32_t rows = big ? (uint32_t)kBN : (uint32_t)(__popc(live) * G);
+        mbar_arm_tx(full, rows * 2u * (uint32_t)(kFp4RowBytes + kFp4Groups), &sh.armed[ring.st]);
+      }
+      __syncwarp();
+      if (big) {
+        const int b0 = __shfl_sync(0xffffffffu, c_blk, 0), s0 = __shfl_sync(0xffffffffu, c_slot, 0);
         if (elect_one()) {
-          if (bad) record_error(p.dev_err, kErrDeviceBounds);
-          (which ? sh.v_bad : sh.k_bad)[st] = bad;
-          mbar_arm_tx(full, rows * (uint32_t)(kFp4RowBytes + kFp4Groups), &sh.armed[which][st]);
-          if (big) {
-            tma_load_4d(codes, maps, full, 0, kvh, slot0, blk0);
-            tma_load_4d(scales, maps + 1, full, 0, kvh, slot0, blk0);
-          }
+          tma_load_4d(stage, &p.map[2], full, 0, c_kvh, s0, b0);
+          tma_load_4d(stage + kCodeTile, &p.map[3], full, 0, c_kvh, s0, b0);
+          tma_load_4d(stage + kHalfStage, &p.map[6], full, 0, c_kvh, s0, b0);
+          tma_load_4d(stage + kHalfStage + kCodeTile, &p.map[7], full, 0, c_kvh, s0, b0);
         }
-        __syncwarp();
-        if (!big) {
-          // eight boxes at a time from one elected block: the table entries are in registers first, so the
-          // copies go out a few clocks apart
-          int slot = slot0;
+      } else {
 #pragma unroll 1
-          for (int g0 = 0; g0 < nseg; g0 += 8) {
-            int ids[8];
-#pragma unroll
-            for (int g = 0; g < 8; ++g) ids[g] = __shfl_sync(0xffffffffu, blk, g0 + g);  // -1 past the last segment
-            int slots[8];
-#pragma unroll
-            for (int g = 0; g < 8; ++g) {
-              slots[g] = slot;
-              slot += G;
-              if (slot >= p.block_size) slot -= p.block_size;
-            }
-            if (elect_one()) {
-#pragma unroll
-              for (int g = 0; g < 8; ++g) {
-                const int sl = slots[g];
-                if (ids[g] >= 0) {
-                  tma_load_4d(codes + (g0 + g) * G * kFp4RowBytes, maps, full, 0, kvh, sl, ids[g]);
-                  tma_load_4d(scales + (g0 + g) * G * kFp4Groups, maps + 1, full, 0, kvh, sl, ids[g]);
-                }
-              }
-            }
-            __syncwarp();
+        for (int g = 0; g < nseg; ++g) {
+          const int b = __shfl_sync(0xffffffffu, c_blk, g), s = __shfl_sync(0xffffffffu, c_slot, g);
+          if (b >= 0 && elect_one()) {
+            uint8_t* dst = stage + g * G * kFp4RowBytes;
+            uint8_t* dst_s = stage + kCodeTile + g * G * kFp4Groups;
+            tma_load_4d(dst, &p.map[0], full, 0, c_kvh, s, b);
+            tma_load_4d(dst_s, &p.map[1], full, 0, c_kvh, s, b);
+            tma_load_4d(dst + kHalfStage, &p.map[4], full, 0, c_kvh, s, b);
+            tma_load_4d(dst_s + kHalfStage, &p.map[5], full, 0, c_kvh, s, b);
           }
         }
       }
-      key0 = key0_next;
-      kvh = kvh_next;
-      blk = blk_next;
+      __syncwarp();
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------------------ QK issuer
@@ -499,11 +509,13 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
         if (ok) ok = warp_wait(&sh.kt_ready[b], (i >> 1) & 1, abort, wl);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tm + Gm::col_s(0) + b * kCols, a = tm + Gm::col_k(0) + b * 128;
+        const uint32_t d = tm + Gm::kColS + b * kCols, a = tm + Gm::kColK + b * 128;
         if (elect_one()) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int ks = 0; ks < 16; ++ks)
-            umma_f16_ts(d, a + ks * 8, qd + (uint64_t)((ks >> 2) * (Gm::kQChunk >> 4) + (ks & 3) * 2), id, ks > 0);
+            for (int ks = 0; ks < 4; ++ks)
+              umma_f16_ts(d, a + c * 32 + ks * 8, qd + (uint64_t)(c * (Gm::kQChunk >> 4) + ks * 2), id, (c | ks) ? 1u : 0u);
           umma_commit(&sh.s_full[b]);
           umma_commit(&sh.kt_free[b]);
           if (j == run.n - 1) umma_commit(&sh.q_free[s & 1]);
@@ -513,8 +525,8 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------------------------ PV issuer
-    constexpr uint32_t id = idesc_f16(128, kCols, false, false, true);
-    const uint64_t p_desc = smem_desc(smem_u32(smem + Gm::kOffP), 0, 8 * Gm::kPRow, kLayoutSW64);
+    constexpr uint32_t id = idesc_f16(128, 2 * kCols, false, false, true);
+    const uint64_t p_desc = smem_desc(smem_u32(smem + Gm::kOffP), 0, 8 * Gm::kPRow, Gm::kPLayout);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     Cursor cur = start;
     Run run;
@@ -529,11 +541,16 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
           ok = warp_wait(&sh.vt_ready[hh], i & 1, abort, wl);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t d = tm + Gm::kColO + hh * kCols, a = tm + Gm::kColV + hh * 64;
+          // 64 keys: 8 steps of 8 keys, 16 rows of P^T (an even and an odd one a key)
+          const uint32_t a = tm + Gm::kColV + hh * 64;
+          const uint64_t pdh = pd + (uint64_t)(hh * (128 * Gm::kPRow >> 4));
           if (elect_one()) {
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              umma_f16_ts(d, a + ks * 8, pd + (uint64_t)(ks * (16 * Gm::kPRow >> 4)), id, (j > 0 || ks > 0) ? 1u : 0u);
+              for (int ks = 0; ks < 4; ++ks)
+                umma_f16_ts(tm + Gm::kColO, a + c * 32 + ks * 8, pdh + (uint64_t)((4 * c + ks) * (16 * Gm::kPRow >> 4)), id,
+                            (j | hh | c | ks) ? 1u : 0u);
             umma_commit(&sh.vt_free[hh]);
             if (hh == 1) umma_commit(&sh.pv_done[b]);
           }
@@ -543,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
     }
   } else if (warp == 3) {
     // ------------------------------------------------------------------------------ V scales
-    // lane = four keys: their 4 x 16 e4m3 bytes as fp16, [chunk of 32 elements][key quad][group][key].
+    // lane = four keys: their 4 x 16 e4m3 bytes as fp16, [quarter of the row][key quad][group][key].
     // Keys past the request or in a bad block get 0. A NaN scale of a key that some columns of the CTA
     // do not see would reach them as 0 * NaN: it is left out here and put into the columns that see
     // the key by the epilogue.
@@ -551,13 +568,14 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
     Run run;
     int i = 0;
     bool ok = true;
+    Ring<kStages> ring;
     while (ok && next_run(p, cur, run)) {
       const int unit = p.lines > 1 ? line : run.u;
       const int seen_by_all = run.len - p.T + (unit % p.n_tg) * p.tpc;  // the last such key
-      for (int j = 0; ok && j < run.n; ++j, ++i) {
-        const int st = i % kStages, b = i & 1;
+      for (int j = 0; ok && j < run.n; ++j, ++i, ring.next()) {
+        const int st = ring.st, b = i & 1;
         ok = i < 2 || warp_wait(&sh.sf_free[b], ((i >> 1) - 1) & 1, abort, wl);
-        if (ok) ok = warp_wait(&sh.v_full[st], (i / kStages) & 1, abort, wl);
+        if (ok) ok = warp_wait(&sh.full[st], ring.ph, abort, wl);
         if (!ok) break;
         const uint4* src = reinterpret_cast<const uint4*>(smem + Gm::kOffStage + st * Gm::kStage + kHalfStage + kCodeTile);
         uint32_t w[4][4];
@@ -567,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
           w[k][0] = v.x; w[k][1] = v.y; w[k][2] = v.z; w[k][3] = v.w;
         }
         const int key0 = (run.t0 + j) * kBN;
-        const uint32_t bad = sh.v_bad[st];
+        const uint32_t bad = sh.bad[st];
         if (bad || key0 + kBN > run.len || key0 + kBN - 1 > seen_by_all) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -586,21 +604,20 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
             }
           }
         }
-        uint8_t* dst = smem + Gm::kOffSf + b * Gm::kSfBuf + lane * 16;
+        uint8_t* dst = smem + Gm::kOffSf + b * Gm::kSfBuf + lane * 32;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const uint32_t lo01 = __byte_perm(w[0][q], w[1][q], 0x5140), hi01 = __byte_perm(w[0][q], w[1][q], 0x7362);
           const uint32_t lo23 = __byte_perm(w[2][q], w[3][q], 0x5140), hi23 = __byte_perm(w[2][q], w[3][q], 0x7362);
-          *reinterpret_cast<uint4*>(dst + (2 * q) * 512) =
-              make_uint4(e4m3x2_to_f16x2((uint16_t)lo01), e4m3x2_to_f16x2((uint16_t)lo23),
-                         e4m3x2_to_f16x2((uint16_t)(lo01 >> 16)), e4m3x2_to_f16x2((uint16_t)(lo23 >> 16)));
-          *reinterpret_cast<uint4*>(dst + (2 * q + 1) * 512) =
-              make_uint4(e4m3x2_to_f16x2((uint16_t)hi01), e4m3x2_to_f16x2((uint16_t)hi23),
-                         e4m3x2_to_f16x2((uint16_t)(hi01 >> 16)), e4m3x2_to_f16x2((uint16_t)(hi23 >> 16)));
+          uint4* d = reinterpret_cast<uint4*>(dst + q * 1024);
+          d[0] = make_uint4(e4m3x2_to_f16x2((uint16_t)lo01), e4m3x2_to_f16x2((uint16_t)lo23),
+                            e4m3x2_to_f16x2((uint16_t)(lo01 >> 16)), e4m3x2_to_f16x2((uint16_t)(lo23 >> 16)));
+          d[1] = make_uint4(e4m3x2_to_f16x2((uint16_t)hi01), e4m3x2_to_f16x2((uint16_t)hi23),
+                            e4m3x2_to_f16x2((uint16_t)(hi01 >> 16)), e4m3x2_to_f16x2((uint16_t)(hi23 >> 16)));
         }
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&sh.v_empty[st]);
+          mbar_arrive(&sh.empty[st]);
           mbar_arrive(&sh.sf_ready[b]);
         }
       }
@@ -614,6 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
     Run run;
     int i = 0;
     bool ok = true;
+    Ring<kStages> ring;
     for (int s = 0; ok && next_run(p, cur, run); ++s) {
       const int unit = p.lines > 1 ? line : run.u;
       const int t_base = (unit % p.n_tg) * p.tpc;
@@ -658,15 +676,15 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
         fence_proxy_async_smem();
         warp_arrive(&sh.q_ready[s & 3], lane);
       }
-      for (int j = 0; ok && j < run.n; ++j, ++i) {
-        const int st = i % kStages, b = i & 1;
-        ok = warp_wait(&sh.k_full[st], (i / kStages) & 1, abort, wl);
+      for (int j = 0; ok && j < run.n; ++j, ++i, ring.next()) {
+        const int st = ring.st, b = i & 1;
+        ok = warp_wait(&sh.full[st], ring.ph, abort, wl);
         if (ok && i >= 2) ok = warp_wait(&sh.kt_free[b], ((i >> 1) - 1) & 1, abort, wl);
         if (!ok) break;
         tc_fence_after();
         const uint8_t* stage = smem + Gm::kOffStage + st * Gm::kStage;
         uint4 sc = *reinterpret_cast<const uint4*>(stage + kCodeTile + k * 16);
-        const uint32_t bad = sh.k_bad[st];
+        const uint32_t bad = sh.bad[st];
         if (bad && ((bad >> (k / G)) & 1u)) sc = make_uint4(0, 0, 0, 0);
 #pragma unroll 1
         for (int c2 = 0; c2 < 4; ++c2) {  // 64 elements: four groups, 32 tensor-memory columns
@@ -685,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
 #pragma unroll
               for (int z = 0; z < 4; ++z) o[4 * y + z] = hmul2_u32(x[z], y < 2 ? slo : shi);
             }
-            tmem_st_32x32b_x16(tmem + lane_off + Gm::col_k(0) + b * 128 + 32 * c2 + 16 * h, o);
+            tmem_st_32x32b_x16(tmem + lane_off + Gm::kColK + b * 128 + 32 * c2 + 16 * h, o);
           }
           sc = make_uint4(sc.y, sc.z, sc.w, 0);
         }
@@ -694,61 +712,65 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&sh.kt_ready[b]);
-          mbar_arrive(&sh.k_empty[st]);
+          mbar_arrive(&sh.empty[st]);
         }
       }
     }
   } else if (warp < 16) {
     // ------------------------------------------------------------------------------ V columns
-    const int c = warp - 8;        // chunk: elements 32 c .. 32 c + 31, 16 code bytes of a key
-    const int hh = c >> 2;
-    const uint32_t tv = tmem + ((uint32_t)((c & 3) * 32) << 16) + Gm::kColV + hh * 64;
+    // A warp's tensor-memory lanes are 32 of a row's 128 code bytes (a lane is a byte: an even and an odd
+    // element), its columns 64 of the tile's keys. ldmatrix hands a thread one byte column of four keys;
+    // a key's column holds the converted pair (even, odd), which is what a conversion of the byte gives.
+    // The columns of 16 keys are in the order 0 1 4 5 8 9 12 13, 2 3 6 7 10 11 14 15 (that of the store).
+    const int quarter = warp & 3, hh = (warp - 8) >> 2;
+    const uint32_t tv = tmem + ((uint32_t)(quarter * 32) << 16) + Gm::kColV + hh * 64;
+    const int key = hh * 64 + (lane & 15);
+    const uint32_t row = key * 128 + (((2 * quarter + (lane >> 4)) ^ (key & 7)) * 16);  // lanes 16-31: the second 16 bytes
+    const uint32_t codes0 = smem_u32(smem + Gm::kOffStage + kHalfStage) + row;
+    const uint8_t* sf0 = smem + Gm::kOffSf + quarter * 1024 + hh * 512 + (lane & 3) * 32;
     Cursor cur = start;
     Run run;
     int i = 0;
     bool ok = true;
+    Ring<kStages> ring;
     while (ok && next_run(p, cur, run)) {
-      for (int j = 0; ok && j < run.n; ++j, ++i) {
-        const int st = i % kStages, b = i & 1;
-        ok = warp_wait(&sh.v_full[st], (i / kStages) & 1, abort, wl);
-        if (ok) ok = warp_wait(&sh.sf_ready[b], (i >> 1) & 1, abort, wl);
+      for (int j = 0; ok && j < run.n; ++j, ++i, ring.next()) {
+        const int st = ring.st, b = i & 1;
+        ok = warp_wait(&sh.sf_ready[b], (i >> 1) & 1, abort, wl);  // the scales' warp has waited for the codes too
         if (ok && i >= 1) ok = warp_wait(&sh.vt_free[hh], (i - 1) & 1, abort, wl);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t codes = smem_u32(smem + Gm::kOffStage + st * Gm::kStage + kHalfStage) + lane * 128 + ((c ^ (lane & 7)) * 16);
-        const uint8_t* sf = smem + Gm::kOffSf + b * Gm::kSfBuf + c * 512 + (lane & 3) * 16;
+        const uint32_t codes = codes0 + st * Gm::kStage;
+        const uint8_t* sf = sf0 + b * Gm::kSfBuf;
 #pragma unroll 1
-        for (int kb = 0; kb < 4; ++kb) {  // 32 keys
-          uint32_t w[4], even[8], odd[8];
-          ldmatrix_t8_x2(codes + kb * 32 * 128, w);
+        for (int kb = 0; kb < 4; ++kb) {  // 16 keys
+          uint32_t w[4];
+          ldmatrix_t8_x2(codes + kb * 16 * 128, w);
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {  // 16 keys: bytes of four keys, for two groups
-            const uint4 s4 = *reinterpret_cast<const uint4*>(sf + kb * 128 + x * 64);
-            const uint32_t s01[2] = {s4.x, s4.z}, s23[2] = {s4.y, s4.w};
+          for (int x = 0; x < 2; ++x) {  // 16 bytes: two groups, eight bytes each
+            const uint4 s4 = *reinterpret_cast<const uint4*>(sf + kb * 128 + x * 16);
+            uint32_t o[8];
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-              constexpr uint32_t kLow = 0x0f0f0f0fu;
-              const uint32_t v = w[2 * x + g], v4 = v >> 4;
-              const uint32_t lo = (v & kLow) | (v4 & ~kLow);         // bytes 0, 2: the low nibbles of keys 0 1, 2 3
-              const uint32_t hi = (v4 & kLow) | ((v >> 8) & ~kLow);  // the high nibbles
-              uint32_t a, d;
-              e2m1_bytes02(lo, a, d);
-              even[4 * x + 2 * g] = hmul2_u32(a, s01[g]);
-              even[4 * x + 2 * g + 1] = hmul2_u32(d, s23[g]);
-              e2m1_bytes02(hi, a, d);
-              odd[4 * x + 2 * g] = hmul2_u32(a, s01[g]);
-              odd[4 * x + 2 * g + 1] = hmul2_u32(d, s23[g]);
+              uint32_t v[4];
+              e2m1x8_to_f16(w[2 * x + g], v);
+              const uint32_t s01 = g ? s4.z : s4.x, s23 = g ? s4.w : s4.y;
+              const __half2 h01 = *reinterpret_cast<const __half2*>(&s01), h23 = *reinterpret_cast<const __half2*>(&s23);
+              const __half2 d[4] = {__low2half2(h01), __high2half2(h01), __low2half2(h23), __high2half2(h23)};
+              o[2 * g] = hmul2_u32(v[0], *reinterpret_cast<const uint32_t*>(&d[0]));
+              o[2 * g + 1] = hmul2_u32(v[1], *reinterpret_cast<const uint32_t*>(&d[1]));
+              o[4 + 2 * g] = hmul2_u32(v[2], *reinterpret_cast<const uint32_t*>(&d[2]));
+              o[4 + 2 * g + 1] = hmul2_u32(v[3], *reinterpret_cast<const uint32_t*>(&d[3]));
             }
+            tmem_st_16x256b_x2(tv + ((uint32_t)(16 * x) << 16) + kb * 16, o);
           }
-          tmem_st_16x256b_x2(tv + kb * 16, even);
-          tmem_st_16x256b_x2(tv + (16u << 16) + kb * 16, odd);
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&sh.vt_ready[hh]);
-          mbar_arrive(&sh.v_empty[st]);
+          mbar_arrive(&sh.empty[st]);
           mbar_arrive(&sh.sf_free[b]);
         }
       }
@@ -762,8 +784,18 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const int bar_id = 1 + grp;
     const float vg = __ldg(p.v_scale);
-    // the head_dim element of this thread's tensor-memory lane, less 128 per half (see V columns)
-    const int d_lane = quarter * 32 + (lane < 16 ? 2 * lane : 2 * (lane - 16) + 1);
+    // the key's two rows of P^T (see V columns for the order of the keys): weights in the first kCols
+    // columns of the first row, which meets the even elements, and in the last of the second
+    const int prow = 2 * ((k & ~15) + ((k >> 1) & 1) * 8 + ((k & 15) >> 2) * 2 + (k & 1));
+    auto p_chunk = [&](int odd, int cc) {  // byte offset of the group's chunk cc (8 columns) in a buffer
+      const uint32_t r = prow + odd, chunk = odd * (kCols / 8) + grp * (kGC / 8) + cc;
+      return r * Gm::kPRow + ((chunk ^ (kCols == 16 ? (r >> 1) & 3u : r & 7u)) * 16);
+    };
+    uint32_t p_off[2][kGC / 8];
+#pragma unroll
+    for (int odd = 0; odd < 2; ++odd)
+#pragma unroll
+      for (int cc = 0; cc < kGC / 8; ++cc) p_off[odd][cc] = p_chunk(odd, cc);
     Cursor cur = start;
     Run run;
     int i = 0;
@@ -788,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
         if (ok) ok = warp_wait(&sh.s_full[b], (i >> 1) & 1, abort, wl);
         float x[kGC];
         float tile_sum[2];
-        const uint32_t ts = tmem + lane_off + Gm::col_s(0) + b * kCols + c0;
+        const uint32_t ts = tmem + lane_off + Gm::kColS + b * kCols + c0;
         for (int pass = 0;; ++pass) {
           // weights 2^(S f - m), 0 where the column does not see the key. One that passes 2^15 shows in
           // their sum (no weight is negative; the sum's pipe has room where the maximum's has none).
@@ -879,14 +911,14 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
         if (ok && i >= 2) ok = warp_wait(&sh.pv_done[b], ((i >> 1) - 1) & 1, abort, wl);
 #pragma unroll
         for (int q = 0; q < kGC; q += 2) add2(l[q], l[q + 1], l[q], l[q + 1], x[q], x[q + 1]);
-        if (ok) {  // row k of P^T, the group's 16-byte chunks; the 64-byte swizzle XORs them with bits 1-2 of k
-          uint8_t* prow = smem + Gm::kOffP + b * Gm::kPBuf + k * Gm::kPRow;
+        if (ok) {
+          uint8_t* pb = smem + Gm::kOffP + b * Gm::kPBuf;
 #pragma unroll
           for (int cc = 0; cc < kGC / 8; ++cc) {
-            const uint32_t chunk = (uint32_t)(grp * (kGC / 8) + cc) ^ ((uint32_t)(k >> 1) & 3u);
-            *reinterpret_cast<uint4*>(prow + chunk * 16) =
-                make_uint4(pack_f16x2(x[8 * cc], x[8 * cc + 1]), pack_f16x2(x[8 * cc + 2], x[8 * cc + 3]),
-                           pack_f16x2(x[8 * cc + 4], x[8 * cc + 5]), pack_f16x2(x[8 * cc + 6], x[8 * cc + 7]));
+            const uint4 w = make_uint4(pack_f16x2(x[8 * cc], x[8 * cc + 1]), pack_f16x2(x[8 * cc + 2], x[8 * cc + 3]),
+                                       pack_f16x2(x[8 * cc + 4], x[8 * cc + 5]), pack_f16x2(x[8 * cc + 6], x[8 * cc + 7]));
+            *reinterpret_cast<uint4*>(pb + p_off[0][cc]) = w;
+            *reinterpret_cast<uint4*>(pb + p_off[1][cc]) = w;
           }
           fence_proxy_async_smem();
           tc_fence_before();
@@ -916,12 +948,13 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
         const bool nan = sh.v_nan != 0;
         const int kvh = unit / p.n_tg;
         const int64_t row0 = ((int64_t)run.r * p.T + t_base) * p.num_q_heads + (int64_t)kvh * p.group;
+        const int d = 2 * k;  // this lane's even element
 #pragma unroll 1
-        for (int hh = 0; hh < 2; ++hh) {
-          uint32_t v[kGC];
-          tmem_ld_cols<kGC>(tmem + lane_off + Gm::kColO + hh * kCols + c0, v);
+        for (int q0 = 0; q0 < kGC; q0 += 8) {
+          uint32_t v[8], w[8];
+          tmem_ld_32x32b_x8(tmem + lane_off + Gm::kColO + c0 + q0, v);
+          tmem_ld_32x32b_x8(tmem + lane_off + Gm::kColO + kCols + c0 + q0, w);
           tmem_wait_ld();
-          const int d = hh * 128 + d_lane;
           if (nan) {  // keys that only some columns see, with a NaN V scale
             for (int key = max(seen_by_all + 1, run.t0 * kBN); key < min(run.len, (run.t0 + run.n) * kBN); ++key) {
               const int col = key / p.block_size;
@@ -931,17 +964,19 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
                                        (int64_t)kvh * p.scale_stride_head + d / kFp4Group);
               if ((sb & 0x7f) != 0x7f) continue;
 #pragma unroll
-              for (int q = 0; q < kGC; ++q)
-                if (key - seen_by_all <= sh.tok[c0 + q]) v[q] = 0x7fc00000u;
+              for (int q = 0; q < 8; ++q)
+                if (key - seen_by_all <= sh.tok[c0 + q0 + q]) v[q] = w[q] = 0x7fc00000u;
             }
           }
 #pragma unroll
-          for (int q = 0; q < kGC; ++q) {
-            if (c0 + q >= nq) break;
+          for (int q = 0; q < 8; ++q) {
+            const int c = c0 + q0 + q;
+            if (c >= nq) break;
+            const float x0 = __uint_as_float(v[q]), x1 = __uint_as_float(w[q]);
             if (whole)
-              p.out[(row0 + sh.row_off[c0 + q]) * kFp4D + d] = __float2bfloat16(__uint_as_float(v[q]) * sh.fin[c0 + q]);
+              reinterpret_cast<uint32_t*>(p.out + (row0 + sh.row_off[c]) * kFp4D)[k] = pack_bf16x2(x0 * sh.fin[c], x1 * sh.fin[c]);
             else
-              slot.o[c0 + q][d] = __uint_as_float(v[q]);
+              reinterpret_cast<float2*>(slot.o[c])[k] = make_float2(x0, x1);
           }
         }
         tc_fence_before();
@@ -956,10 +991,7 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
   if (gave_up) {
     // before the tensor memory is freed: wait for the copies of every armed phase and every MMA issued
     if (tid == 0)
-      for (int s = 0; s < kStages; ++s) {
-        drain_armed(&sh.k_full[s], sh.armed[0][s]);
-        drain_armed(&sh.v_full[s], sh.armed[1][s]);
-      }
+      for (int s = 0; s < kStages; ++s) drain_armed(&sh.full[s], sh.armed[s]);
     if ((warp == 1 || warp == 2) && lane == 0) {
       umma_commit(&sh.drain);
       mbar_wait_drain(&sh.drain, 0);
