@@ -313,38 +313,46 @@ def splits_needed(max_seq_len: int, split_tokens: int) -> int:
 # one fp32 scale per tensor
 # ---------------------------------------------------------------------------------------------
 
+# The smallest calls run for two or three microseconds on the device, so the checks below keep to few
+# attribute reads: one test a property, devices as indices, the raw stream.
+_U8, _I32, _F32, _BF16 = torch.uint8, torch.int32, torch.float32, torch.bfloat16
+
+
 def _cache4(k_fp4, v_fp4, k_bscale, v_bscale, k_scale, v_scale):
-    """The checked cache's device and the ABI's (num_blocks, strides) arguments, block_size, heads."""
-    nb, bs, hkv, row = k_fp4.shape
-    assert row == 128 and k_bscale.shape == (nb, bs, hkv, 16), "codes [nb][bs][hkv][128], scales [nb][bs][hkv][16]"
-    assert v_fp4.shape == k_fp4.shape and v_bscale.shape == k_bscale.shape
-    assert k_fp4.dtype == v_fp4.dtype == k_bscale.dtype == v_bscale.dtype == torch.uint8, "the 4-bit cache is uint8 tensors"
-    cs, ss = k_fp4.stride(), k_bscale.stride()
-    assert cs == v_fp4.stride() and ss == v_bscale.stride() and cs[3] == 1 and ss[3] == 1
-    assert k_scale.dtype == torch.float32 and v_scale.dtype == torch.float32
-    dev = k_fp4.device
-    assert dev.type == "cuda" and dev == v_fp4.device == k_bscale.device == v_bscale.device == k_scale.device == v_scale.device
+    """The checked cache's device index, the ABI's (num_blocks, strides), block_size, heads."""
+    shape, cs, ss = k_fp4.shape, k_fp4.stride(), k_bscale.stride()
+    nb, bs, hkv, row = shape
+    assert row == 128 and v_fp4.shape == shape and k_bscale.shape == v_bscale.shape == (nb, bs, hkv, 16), \
+        "codes [nb][bs][hkv][128], scales [nb][bs][hkv][16]"
+    assert v_fp4.stride() == cs and v_bscale.stride() == ss and cs[3] == 1 and ss[3] == 1, "K and V strides must agree"
+    assert k_fp4.dtype is v_fp4.dtype is k_bscale.dtype is v_bscale.dtype is _U8, "the 4-bit cache is uint8 tensors"
+    assert k_scale.dtype is v_scale.dtype is _F32, "k_scale and v_scale are fp32 device scalars"
+    dev = k_fp4.get_device()
+    assert dev >= 0 and dev == v_fp4.get_device() == k_bscale.get_device() == v_bscale.get_device() == \
+        k_scale.get_device() == v_scale.get_device(), "the cache and its scales must be on one CUDA device"
     return dev, (nb, cs[0], cs[1], cs[2], ss[0], ss[1], ss[2]), bs, hkv
 
 
-def _dptr(t, dev):
-    if t is None:
-        return None
-    assert t.device == dev, "tensors of one call must be on one device"
-    return t.data_ptr()
-
-
-def _launch(fn, dev, stream, *args):
-    """fn(*args, stream) with the tensors' device current and, unless given, on its current stream."""
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    if dev.index == torch.cuda.current_device():
-        rc = fn(*args, stream.cuda_stream)
+def _launch(fn, dev, stream, others, *args):
+    """fn(*args, stream) with device `dev` current and, unless one is given, on its current stream; the
+    tensors `others` must be on it."""
+    for t in others:
+        assert t.get_device() == dev, "tensors of one call must be on one device"
+    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        rc = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, stream.cuda_stream)
+            rc = fn(*args, raw)
     if rc != PKV_OK:
         _check(rc)
+
+
+def _err(dev_err, dev):
+    if dev_err is None:
+        return None
+    assert dev_err.dtype is _I32 and dev_err.get_device() == dev, "dev_err: int32 on the cache's device"
+    return dev_err.data_ptr()
 
 
 def kv_cache_write_fp4(k_new, v_new, block_table, seq_lens, query_start_loc, max_q_len, k_fp4, v_fp4, k_bscale,
@@ -352,17 +360,18 @@ def kv_cache_write_fp4(k_new, v_new, block_table, seq_lens, query_start_loc, max
     """Quantize the chunk's new rows k_new / v_new (bf16 [total_q][hkv][256], token stride free) to 4 bits
     and store them into the paged cache at positions seq_lens[r] - q_len + i."""
     dev, cache, bs, hkv = _cache4(k_fp4, v_fp4, k_bscale, v_bscale, k_scale, v_scale)
-    assert k_new.dtype == torch.bfloat16 and v_new.dtype == torch.bfloat16 and k_new.stride() == v_new.stride()
-    assert k_new.shape == v_new.shape and k_new.dim() == 3 and k_new.shape[1] == hkv
-    d = k_new.shape[2]
-    assert k_new.stride(2) == 1 and k_new.stride(1) == d, "new rows: [total][hkv][D], heads contiguous"
-    R = block_table.shape[0]
-    assert seq_lens.shape[0] == R and query_start_loc.shape[0] == R + 1
-    _launch(lib.pkv_kv_cache_write_fp4, dev, stream, _dptr(k_new, dev), _dptr(v_new, dev), k_new.stride(0),
-            _dptr(_i32(block_table), dev), block_table.stride(0), block_table.shape[1], _dptr(_i32(seq_lens), dev),
-            _dptr(_i32(query_start_loc), dev), R, int(max_q_len), k_fp4.data_ptr(), v_fp4.data_ptr(),
+    st = k_new.stride()
+    _, heads, d = k_new.shape
+    assert k_new.dtype is v_new.dtype is _BF16 and v_new.shape == k_new.shape and v_new.stride() == st and \
+        heads == hkv and st[2] == 1 and st[1] == d, "new rows: bf16 [total][hkv][D], heads contiguous, K and V alike"
+    R, cols = block_table.shape
+    assert block_table.dtype is seq_lens.dtype is query_start_loc.dtype is _I32 and seq_lens.shape[0] == R and \
+        query_start_loc.shape[0] == R + 1, "int32 block_table [R][..], seq_lens [R], query_start_loc [R + 1]"
+    _launch(lib.pkv_kv_cache_write_fp4, dev, stream, (k_new, v_new, block_table, seq_lens, query_start_loc),
+            k_new.data_ptr(), v_new.data_ptr(), st[0], block_table.data_ptr(), block_table.stride(0), cols,
+            seq_lens.data_ptr(), query_start_loc.data_ptr(), R, int(max_q_len), k_fp4.data_ptr(), v_fp4.data_ptr(),
             k_bscale.data_ptr(), v_bscale.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *cache, bs, hkv, d,
-            _dptr(dev_err, dev))
+            _err(dev_err, dev))
 
 
 def kv_fp4_dequant_dense(k_fp4, v_fp4, k_bscale, v_bscale, block_table, pos_begin, pos_end, max_tokens, k_scale, v_scale,
@@ -370,15 +379,16 @@ def kv_fp4_dequant_dense(k_fp4, v_fp4, k_bscale, v_bscale, block_table, pos_begi
     """Positions [pos_begin[r], pos_end[r]) of the 4-bit cache -> dense bf16 [R][max_ctx][hkv][256], each at
     its own position."""
     dev, cache, bs, hkv = _cache4(k_fp4, v_fp4, k_bscale, v_bscale, k_scale, v_scale)
-    assert k_dense.is_contiguous() and v_dense.is_contiguous() and k_dense.dtype == v_dense.dtype == torch.bfloat16
-    R, max_ctx = k_dense.shape[:2]
-    assert k_dense.shape == v_dense.shape and k_dense.dim() == 4 and k_dense.shape[2] == hkv
-    assert block_table.shape[0] == R and pos_begin.shape[0] == R and pos_end.shape[0] == R
-    _launch(lib.pkv_kv_fp4_dequant_dense, dev, stream, k_fp4.data_ptr(), v_fp4.data_ptr(), k_bscale.data_ptr(),
-            v_bscale.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *cache, _dptr(_i32(block_table), dev),
-            block_table.stride(0), block_table.shape[1], _dptr(_i32(pos_begin), dev), _dptr(_i32(pos_end), dev), R,
-            int(max_tokens), bs, hkv, k_dense.shape[3], _dptr(k_dense, dev), _dptr(v_dense, dev), max_ctx,
-            _dptr(dev_err, dev))
+    R, max_ctx, heads, d = k_dense.shape
+    assert k_dense.dtype is v_dense.dtype is _BF16 and v_dense.shape == k_dense.shape and heads == hkv and \
+        k_dense.is_contiguous() and v_dense.is_contiguous(), "dense rows: contiguous bf16 [R][max_ctx][hkv][256]"
+    assert block_table.dtype is pos_begin.dtype is pos_end.dtype is _I32 and \
+        block_table.shape[0] == pos_begin.shape[0] == pos_end.shape[0] == R, "int32 block_table [R][..], pos_begin, pos_end [R]"
+    _launch(lib.pkv_kv_fp4_dequant_dense, dev, stream, (block_table, pos_begin, pos_end, k_dense, v_dense),
+            k_fp4.data_ptr(), v_fp4.data_ptr(), k_bscale.data_ptr(), v_bscale.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), *cache, block_table.data_ptr(), block_table.stride(0), block_table.shape[1],
+            pos_begin.data_ptr(), pos_end.data_ptr(), R, int(max_tokens), bs, hkv, d, k_dense.data_ptr(),
+            v_dense.data_ptr(), max_ctx, _err(dev_err, dev))
 
 
 def spec_verify_fp4_workspace_bytes(num_ctas=None) -> int:
@@ -394,11 +404,14 @@ def spec_verify_attn_fp4(q, k_fp4, v_fp4, k_bscale, v_bscale, k_scale, v_scale, 
     [R*T][Hq][256]. workspace: a CUDA byte tensor of spec_verify_fp4_workspace_bytes() bytes, one for each
     stream or graph whose calls may overlap."""
     dev, cache, bs, hkv = _cache4(k_fp4, v_fp4, k_bscale, v_bscale, k_scale, v_scale)
-    assert q.dtype == out.dtype == torch.bfloat16 and q.is_contiguous() and out.is_contiguous()
-    R, T = block_table.shape[0], int(T)
-    assert q.dim() == 3 and q.shape == out.shape and q.shape[0] == R * T and seq_lens.shape[0] == R
-    _launch(lib.pkv_spec_verify_attn_fp4, dev, stream, _dptr(q, dev), k_fp4.data_ptr(), v_fp4.data_ptr(),
-            k_bscale.data_ptr(), v_bscale.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *cache,
-            _dptr(_i32(block_table), dev), block_table.stride(0), block_table.shape[1], _dptr(_i32(seq_lens), dev), R, T,
-            q.shape[1], hkv, q.shape[2], bs, float(softmax_scale), _dptr(out, dev), _dptr(workspace, dev),
-            _ws_bytes(workspace), _dptr(dev_err, dev))
+    R, cols = block_table.shape
+    rows, hq, d = q.shape
+    assert q.dtype is out.dtype is _BF16 and out.shape == q.shape and rows == R * T and q.is_contiguous() and \
+        out.is_contiguous(), "q and out: contiguous bf16 [R*T][Hq][256]"
+    assert block_table.dtype is seq_lens.dtype is _I32 and seq_lens.shape[0] == R, "int32 block_table [R][..], seq_lens [R]"
+    assert workspace.is_contiguous(), "workspace must be a contiguous CUDA tensor"
+    _launch(lib.pkv_spec_verify_attn_fp4, dev, stream, (q, block_table, seq_lens, out, workspace), q.data_ptr(),
+            k_fp4.data_ptr(), v_fp4.data_ptr(), k_bscale.data_ptr(), v_bscale.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), *cache, block_table.data_ptr(), block_table.stride(0), cols, seq_lens.data_ptr(), R,
+            int(T), hq, hkv, d, bs, float(softmax_scale), out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+            _err(dev_err, dev))

@@ -40,6 +40,51 @@ __device__ __forceinline__ uint32_t e4m3_dup_f16(uint32_t byte) {
   return e4m3x2_to_f16x2((uint16_t)((byte & 0xffu) * 0x101u));
 }
 
+// Pair index -> (token, head); the usual pair index fits 32 bits, whose division is an order cheaper.
+__device__ __forceinline__ void split_pair(uint64_t pair, uint32_t heads, uint32_t& tok, uint32_t& head) {
+  tok = (pair >> 32) == 0 ? (uint32_t)pair / heads : (uint32_t)(pair / heads);
+  head = (uint32_t)(pair - (uint64_t)tok * heads);
+}
+
+// Consecutive (token, head) pairs of a request from pair `first` on, token 0 being position pos0: where
+// each lies in the cache. The next block's table entry is read when a block is entered, so that the
+// walk stops for no table load after its first.
+struct PairWalk {
+  const int32_t* table;
+  uint32_t heads, block_size, max_blocks;
+  uint32_t i, h, slot, col;  // token, head, slot in block, block column
+  int32_t blk, blk_next;     // -1: past the table
+  __device__ __forceinline__ int32_t entry(uint32_t c) const { return c < max_blocks ? __ldg(table + c) : -1; }
+  __device__ __forceinline__ PairWalk(const int32_t* t, uint32_t heads_, uint32_t bs, uint32_t mb, uint32_t pos0, uint64_t first)
+      : table(t), heads(heads_), block_size(bs), max_blocks(mb) {
+    split_pair(first, heads, i, h);
+    col = (pos0 + i) / bs;
+    slot = pos0 + i - col * bs;
+    blk = entry(col);
+    blk_next = entry(col + 1);
+  }
+  __device__ __forceinline__ void next() {
+    if (++h < heads) return;
+    h = 0;
+    ++i;
+    if (++slot < block_size) return;
+    slot = 0;
+    ++col;
+    blk = blk_next;
+    blk_next = entry(col + 1);
+  }
+};
+
+// Pairs of a warp: as many as leave kPairWarps warps to the device (twice what it holds at a time), at
+// most kPairsMost. Long walks spread a warp's start (launch, lengths, table: three dependent loads)
+// over more rows; short ones are all that small calls have.
+constexpr int64_t kPairWarps = 152 * 64;
+constexpr int64_t kPairsMost = 16;
+inline int32_t pairs_per_warp(int64_t pairs) {
+  const int64_t per = (pairs + kPairWarps - 1) / kPairWarps;
+  return (int32_t)(per < 1 ? 1 : per > kPairsMost ? kPairsMost : per);
+}
+
 // 32 contiguous bytes, 32-byte aligned, as one access.
 struct alignas(32) Bytes32 {
   uint32_t w[8];

@@ -14,8 +14,8 @@ namespace pkv {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kIter = 4;
+constexpr int kWarps = 4;
+constexpr int64_t kManyPairs = 152 * 64 * 4;
 
 struct ReadArgs {
   const uint8_t* k_fp4;
@@ -38,6 +38,7 @@ struct ReadArgs {
   int* dev_err;
 };
 
+template <int kPairs>
 __global__ void __launch_bounds__(kWarps * 32) kv_fp4_dequant_kernel(const ReadArgs a) {
   const int r = blockIdx.x / a.chunks;
   const int chunk = blockIdx.x - r * a.chunks;
@@ -56,35 +57,34 @@ __global__ void __launch_bounds__(kWarps * 32) kv_fp4_dequant_kernel(const ReadA
   const uint8_t* scales = which ? a.v_bscale : a.k_bscale;
   __nv_bfloat16* dense = which ? a.v_dense : a.k_dense;
   const float g = __ldg(which ? a.v_scale : a.k_scale);
-  const int64_t nrows = (end - begin) * hkv;
-  const int64_t stride = (int64_t)a.chunks * kWarps * kIter;
-  for (int64_t base = ((int64_t)chunk * kWarps + warp) * kIter; base < nrows; base += stride) {
-    uint2 c[kIter];
-    uint32_t sb[kIter];
-    int64_t dst[kIter];
+  const uint64_t nrows = (uint64_t)(end - begin) * hkv;
+  const uint64_t stride = (uint64_t)a.chunks * kWarps * kPairs;
+  const int32_t* table = a.block_table + (int64_t)r * a.bt_stride;
+  for (uint64_t base = ((uint64_t)chunk * kWarps + warp) * kPairs; base < nrows; base += stride) {
+    PairWalk at(table, hkv, a.block_size, a.max_blocks, (uint32_t)begin, base);
+    // the pairs of a request are consecutive rows of the dense tensor
+    __nv_bfloat16* dst = dense + (((int64_t)r * a.max_ctx + begin) * hkv + (int64_t)base) * kFp4D + grp * kFp4Group;
+    uint2 c[kPairs];
+    uint32_t sb[kPairs];
 #pragma unroll
-    for (int u = 0; u < kIter; ++u) {
-      const int64_t row = base + u;
-      dst[u] = -1;
+    for (int u = 0; u < kPairs; ++u) {
       c[u] = make_uint2(0, 0);
       sb[u] = 0;
-      if (row >= nrows) continue;
-      const int h = (int)(row % hkv);
-      const int64_t pos = begin + row / hkv;
-      const int64_t col = pos / a.block_size, slot = pos % a.block_size;
-      dst[u] = (((int64_t)r * a.max_ctx + pos) * hkv + h) * kFp4D + grp * kFp4Group;
-      const int64_t blk = col < a.max_blocks ? (int64_t)__ldg(a.block_table + (int64_t)r * a.bt_stride + col) : -1;
-      if (blk < 0 || blk >= a.num_blocks) {  // reads as zero
-        if (lane == 0) record_error(a.dev_err, kErrDeviceBounds);
-        continue;
+      if (base + u < nrows) {
+        if (at.blk < 0 || at.blk >= a.num_blocks) {  // reads as zero
+          if (lane == 0) record_error(a.dev_err, kErrDeviceBounds);
+        } else {
+          c[u] = __ldg(reinterpret_cast<const uint2*>(codes + (int64_t)at.blk * a.stride_blk +
+                                                      (int64_t)at.slot * a.stride_tok + (int64_t)at.h * a.stride_head + grp * 8));
+          sb[u] = __ldg(scales + (int64_t)at.blk * a.scale_stride_blk + (int64_t)at.slot * a.scale_stride_tok +
+                        (int64_t)at.h * a.scale_stride_head + grp);
+        }
       }
-      c[u] = __ldg(reinterpret_cast<const uint2*>(codes + blk * a.stride_blk + slot * a.stride_tok +
-                                                  (int64_t)h * a.stride_head + grp * 8));
-      sb[u] = __ldg(scales + blk * a.scale_stride_blk + slot * a.scale_stride_tok + (int64_t)h * a.scale_stride_head + grp);
+      at.next();
     }
 #pragma unroll
-    for (int u = 0; u < kIter; ++u) {
-      if (dst[u] < 0) continue;
+    for (int u = 0; u < kPairs; ++u) {
+      if (base + u >= nrows) break;
       const uint32_t s2 = e4m3_dup_f16(sb[u]);
       Bytes32 o;
 #pragma unroll
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv_fp4_dequant_kernel(const ReadA
           o.w[4 * half + i] = pack_bf16x2(__fmul_rn(f.x, g), __fmul_rn(f.y, g));
         }
       }
-      stg_bytes32(dense + dst[u], o);
+      stg_bytes32(dst + (int64_t)u * kFp4D, o);
     }
   }
 }
@@ -138,11 +138,18 @@ extern "C" pkv_status pkv_kv_fp4_dequant_dense(
              scale_stride_blk, scale_stride_tok, scale_stride_head, block_table, bt_stride, max_blocks, pos_begin,
              pos_end, block_size, num_kv_heads, 0, static_cast<__nv_bfloat16*>(k_dense),
              static_cast<__nv_bfloat16*>(v_dense), max_ctx, dev_err};
-  const int64_t rows = (int64_t)max_tokens * num_kv_heads, per_cta = (int64_t)kWarps * kIter;
+  // pairs of a warp: 4 in flight where there are enough for every warp the device holds, else 1
+  const int64_t rows = (int64_t)max_tokens * num_kv_heads;
+  const bool many = rows * num_reqs > kManyPairs;
+  const int64_t per_cta = (int64_t)kWarps * (many ? 4 : 1);
   const int64_t want = (rows + per_cta - 1) / per_cta;
   const int64_t cap = ((1ll << 30) - 1) / num_reqs + 1;
   a.chunks = (int32_t)(want < cap ? want : cap);
   PKV_ARG((int64_t)a.chunks * num_reqs < (1ll << 31), "kv_fp4_dequant_dense: grid too large");
-  kv_fp4_dequant_kernel<<<(unsigned)(a.chunks * num_reqs), kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  const unsigned grid = (unsigned)(a.chunks * num_reqs);
+  if (many)
+    kv_fp4_dequant_kernel<4><<<grid, kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  else
+    kv_fp4_dequant_kernel<1><<<grid, kWarps * 32, 0, static_cast<cudaStream_t>(stream)>>>(a);
   return check_launch("kv_fp4_dequant_dense");
 }

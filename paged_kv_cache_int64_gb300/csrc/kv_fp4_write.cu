@@ -9,10 +9,10 @@
 //
 // One lane holds one group: 32 bytes in (one 256-bit load), 8 bytes of codes and 1 byte of scale
 // out, so nothing crosses lanes; a warp covers a K row and its V row (same token and head) at once.
-// The quotient is q0 = x inv with inv = 1 / d, corrected by its exact remainder: r = x - q0 d is
-// exact in one fma, and q0 + r inv is within 2^-46 of x / d before its one rounding, so the code is
-// that of the correctly rounded quotient at less than half the price of 16 divisions; groups where
-// an intermediate could overflow or underflow take the division itself.
+// The quotient is q0 = x inv with inv = 1 / d, corrected by its remainder: e = q0 d - x is exact in
+// one fma, and q0 - e inv is within 2^-46 of x / d before its one rounding, so the code is that of
+// the correctly rounded quotient at less than half the price of 16 divisions; groups where an
+// intermediate could overflow or underflow take the division itself.
 #include <cuda_bf16.h>
 
 #include "host_common.h"
@@ -22,8 +22,8 @@ namespace pkv {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kIter = 4;  // (token, head) pairs a warp has in flight
+constexpr int kWarps = 4;
+constexpr int kDepth = 2;  // (token, head) pairs a warp has in flight
 
 struct WriteArgs {
   const __nv_bfloat16* k_new;
@@ -42,16 +42,36 @@ struct WriteArgs {
   int64_t scale_stride_blk, scale_stride_tok, scale_stride_head;
   const float* k_scale;
   const float* v_scale;
-  int32_t block_size, num_kv_heads, chunks;
+  int32_t block_size, num_kv_heads, chunks, per;
   int* dev_err;
 };
 
-__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
+// 8 values -> 8 e2m1 codes, to nearest even, magnitudes past 6 as 6 (the hardware conversion).
+__device__ __forceinline__ uint32_t e2m1x8(const float* x) {
   uint32_t r;
-  asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tcvt.u32.u8 %0, b;\n\t}"
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
       : "=r"(r)
-      : "f"(hi), "f"(lo));
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
   return r;
+}
+
+// The division itself, for groups outside the range of the corrected product: 8 elements. By value and
+// out of line: its registers are not the common path's.
+__device__ __noinline__ uint32_t quantize8_slow(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, float d) {
+  const bool zero = !(d >= 0x1p-126f && d <= 3.4028234e38f);
+  const uint32_t w[4] = {w0, w1, w2, w3};
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float v = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    x[i] = copysignf(zero ? 0.0f : __fdiv_rn(v, d), v);
+  }
+  return e2m1x8(x);
 }
 
 // 16 bf16 elements -> 8 bytes of codes and the group's scale byte.
@@ -62,41 +82,33 @@ __device__ __forceinline__ uint2 quantize_group(const Bytes32& in, float g, floa
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = __vmaxu2(m, in.w[i] & 0x7fff7fffu);
   const uint32_t mx = max(m & 0xffffu, m >> 16);
-  if (mx > 0x7f80u) {
-    scale_byte = 0x7fu;
-    return make_uint2(0, 0);
-  }
   const float amax = __uint_as_float(mx << 16);
   uint16_t s2;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(s2) : "f"(0.0f), "f"(__fdiv_rn(amax, g6)));
-  scale_byte = s2 & 0xffu;
-  const uint32_t sh = e4m3_dup_f16(scale_byte);
+  const uint32_t sh = e4m3_dup_f16(s2);
   const float d = __fmul_rn(__low2float(*reinterpret_cast<const __half2*>(&sh)), g);
-  float x[16];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[2 * i] = __uint_as_float(in.w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(in.w[i] & 0xffff0000u);
-  }
-  if (d >= 0x1p-80f && d <= 0x1p100f && amax <= __fmul_rn(16.0f, d)) {
-    const float inv = __fdiv_rn(1.0f, d);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float q0 = __fmul_rn(x[i], inv);
-      x[i] = copysignf(__fmaf_rn(__fmaf_rn(-q0, d, x[i]), inv, q0), x[i]);
+  scale_byte = s2 & 0xffu;
+  if (!(d >= 0x1p-80f && d <= 0x1p100f && amax <= __fmul_rn(16.0f, d))) {
+    if (mx > 0x7f80u) {
+      scale_byte = 0x7fu;
+      return make_uint2(0, 0);
     }
-  } else {
-    const bool zero = !(d >= 0x1p-126f && d <= 3.4028234e38f);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = copysignf(zero ? 0.0f : __fdiv_rn(x[i], d), x[i]);
+    return make_uint2(quantize8_slow(in.w[0], in.w[1], in.w[2], in.w[3], d), quantize8_slow(in.w[4], in.w[5], in.w[6], in.w[7], d));
   }
+  // e = q0 d - x is exact; its sign convention also keeps the sign of a zero
+  const float inv = __fdiv_rn(1.0f, d);
   uint32_t c[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint32_t b[4];
+    float x[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = e2m1x2(x[8 * h + 2 * i], x[8 * h + 2 * i + 1]);
-    c[h] = b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24);
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t w = in.w[4 * h + i / 2];
+      const float v = __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+      const float q0 = __fmul_rn(v, inv);
+      x[i] = __fmaf_rn(-__fmaf_rn(q0, d, -v), inv, q0);
+    }
+    c[h] = e2m1x8(x);
   }
   return make_uint2(c[0], c[1]);
 }
@@ -121,37 +133,40 @@ __global__ void __launch_bounds__(kWarps * 32) kv_fp4_write_kernel(const WriteAr
   const __nv_bfloat16* src = which ? a.v_new : a.k_new;
   uint8_t* codes = which ? a.v_fp4 : a.k_fp4;
   uint8_t* scales = which ? a.v_bscale : a.k_bscale;
-  const int64_t nrows = (int64_t)q_len * hkv;  // (token, head) pairs
-  const int64_t stride = (int64_t)a.chunks * kWarps * kIter;
-  for (int64_t base = ((int64_t)chunk * kWarps + warp) * kIter; base < nrows; base += stride) {
-    Bytes32 raw[kIter];
-    int64_t off[kIter], soff[kIter];
-#pragma unroll
-    for (int u = 0; u < kIter; ++u) {
-      const int64_t row = base + u;
+  const uint64_t nrows = (uint64_t)q_len * hkv;  // (token, head) pairs
+  const uint64_t stride = (uint64_t)a.chunks * kWarps * a.per;
+  const int32_t* table = a.block_table + (int64_t)r * a.bt_stride;
+  for (uint64_t base = ((uint64_t)chunk * kWarps + warp) * a.per; base < nrows; base += stride) {
+    const int n = (int)min((uint64_t)a.per, nrows - base);
+    PairWalk at(table, hkv, a.block_size, a.max_blocks, (uint32_t)(seq_len - q_len), base);
+    Bytes32 raw[kDepth];
+    int64_t off[kDepth], soff[kDepth];
+    auto fetch = [&](int u, bool live) {
       off[u] = -1;
-      if (row >= nrows) continue;
-      const int h = (int)(row % hkv);
-      const int i = (int)(row / hkv);
-      const int64_t pos = (int64_t)seq_len - q_len + i;
-      const int64_t col = pos / a.block_size;
-      const int64_t blk = col < a.max_blocks ? (int64_t)__ldg(a.block_table + (int64_t)r * a.bt_stride + col) : -1;
-      if (blk < 0 || blk >= a.num_blocks) {
-        if (lane == 0) record_error(a.dev_err, kErrDeviceBounds);
-        continue;  // not written
+      if (!live) return;
+      raw[u] = ldg_bytes32(src + (int64_t)(q0 + at.i) * a.new_stride_tok + (int64_t)at.h * kFp4D + grp * kFp4Group);
+      if (at.blk < 0 || at.blk >= a.num_blocks) {
+        if (lane == 0) record_error(a.dev_err, kErrDeviceBounds);  // not written
+      } else {
+        off[u] = (int64_t)at.blk * a.stride_blk + (int64_t)at.slot * a.stride_tok + (int64_t)at.h * a.stride_head + grp * 8;
+        soff[u] = (int64_t)at.blk * a.scale_stride_blk + (int64_t)at.slot * a.scale_stride_tok +
+                  (int64_t)at.h * a.scale_stride_head + grp;
       }
-      const int64_t slot = pos % a.block_size;
-      off[u] = blk * a.stride_blk + slot * a.stride_tok + (int64_t)h * a.stride_head + grp * 8;
-      soff[u] = blk * a.scale_stride_blk + slot * a.scale_stride_tok + (int64_t)h * a.scale_stride_head + grp;
-      raw[u] = ldg_bytes32(src + (int64_t)(q0 + i) * a.new_stride_tok + (int64_t)h * kFp4D + grp * kFp4Group);
-    }
+      at.next();
+    };
 #pragma unroll
-    for (int u = 0; u < kIter; ++u) {
-      if (off[u] < 0) continue;  // warp-uniform: one table entry per pair
-      uint32_t sb;
-      const uint2 c = quantize_group(raw[u], g, g6, sb);
-      *reinterpret_cast<uint2*>(codes + off[u]) = c;
-      scales[soff[u]] = (uint8_t)sb;
+    for (int u = 0; u < kDepth; ++u) fetch(u, u < n);
+    for (int k = 0; k < n; k += kDepth) {
+#pragma unroll
+      for (int u = 0; u < kDepth; ++u) {
+        if (off[u] >= 0) {  // warp-uniform: one table entry a pair
+          uint32_t sb;
+          const uint2 c = quantize_group(raw[u], g, g6, sb);
+          *reinterpret_cast<uint2*>(codes + off[u]) = c;
+          scales[soff[u]] = (uint8_t)sb;
+        }
+        fetch(u, k + kDepth + u < n);
+      }
     }
   }
 }
@@ -192,8 +207,10 @@ extern "C" pkv_status pkv_kv_cache_write_fp4(
   WriteArgs a{static_cast<const __nv_bfloat16*>(k_new), static_cast<const __nv_bfloat16*>(v_new), new_stride_tok,
               block_table, bt_stride, max_blocks, seq_lens, query_start_loc, k_fp4, v_fp4, num_blocks, stride_blk,
               stride_tok, stride_head, k_bscale, v_bscale, scale_stride_blk, scale_stride_tok, scale_stride_head,
-              k_scale, v_scale, block_size, num_kv_heads, 0, dev_err};
-  const int64_t rows = (int64_t)max_q_len * num_kv_heads, per_cta = (int64_t)kWarps * kIter;
+              k_scale, v_scale, block_size, num_kv_heads, 0, 0, dev_err};
+  const int64_t rows = (int64_t)max_q_len * num_kv_heads;
+  a.per = pairs_per_warp(rows * num_reqs);
+  const int64_t per_cta = (int64_t)kWarps * a.per;
   const int64_t want = (rows + per_cta - 1) / per_cta;
   const int64_t cap = ((1ll << 30) - 1) / num_reqs + 1;  // the grid's x extent stays below 2^31
   a.chunks = (int32_t)(want < cap ? want : cap);
