@@ -59,9 +59,8 @@ struct Slot {
   float m[kMaxCols], l[kMaxCols];
 };
 struct Note {
-  int32_t valid, r, unit, unused;
-  int64_t unit_end, total;  // line positions: where the piece's unit ends, the line's tiles
-  int64_t pad[12];
+  int32_t pieces, r, unit;  // pieces: CTAs of the line that hold the unit (0: none begins here and goes on)
+  int32_t pad[29];
 };
 struct CtaWorkspace {
   Slot slot[2];
@@ -111,7 +110,6 @@ struct alignas(16) Shared {
   int v_nan;                                     // a NaN V scale was left out for a key that some columns do not see
   int r0, u0, t00;                               // first tile of the CTA's range
   long long wsum[kThreads / 32];
-  long long total;
   int32_t row_off[kCols];                        // column -> token * Hq + head in group
   int32_t tok[kCols];                            // column -> token
   alignas(16) float f[8][kCols];                 // column factors of the segment (ring: the softmax may be 4 behind)
@@ -143,7 +141,10 @@ struct Params {
   uint64_t wait_limit_ns;
 };
 
-__device__ __forceinline__ int64_t line_begin(int64_t total, int c, int ctas) { return total * c / ctas; }
+__device__ __forceinline__ int64_t line_begin(int64_t total, int c, int ctas) {
+  const uint64_t x = (uint64_t)total * (uint32_t)c;  // (a 32-bit division where it does)
+  return (x >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)ctas) : (int64_t)(x / (uint32_t)ctas);
+}
 
 // The tiles of a CTA, as runs of consecutive tiles of one (request, unit). Every role walks the same runs.
 struct Cursor {
@@ -335,71 +336,84 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
   for (int x = tid; x < 2 * Gm::kPBuf / 16; x += kThreads)
     reinterpret_cast<uint4*>(smem + Gm::kOffP)[x] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
-  // the line's tiles, and zeros for the rows of empty requests (each CTA its share of the requests)
-  long long mine = 0;
-  for (int r = tid; r < p.num_reqs; r += kThreads) {
-    const int len = __ldg(p.seq_lens + r);
-    if (len > 0) mine += ((int64_t)len + kBN - 1) / kBN;
-  }
+  // The CTA's range of the line's tiles. A thread holds a request (kThreads of them at a time).
+  auto tiles_of = [&](int r) -> int {
+    const int len = r < p.num_reqs ? __ldg(p.seq_lens + r) : 0;
+    return len > 0 ? (int)(((int64_t)len + kBN - 1) / kBN) : 0;
+  };
+  auto scan = [&](long long x, long long& sum) -> long long {  // inclusive over the CTA; two barriers
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) sh.wsum[warp] = mine;
-  for (int r = blockIdx.x; r < p.num_reqs; r += gridDim.x) {
-    if (__ldg(p.seq_lens + r) > 0) continue;
-    uint4* o = reinterpret_cast<uint4*>(p.out + (int64_t)r * p.T * p.num_q_heads * kFp4D);
-    const int64_t n = (int64_t)p.T * p.num_q_heads * (kFp4D / 8);
-    for (int64_t i = tid; i < n; i += kThreads) o[i] = make_uint4(0, 0, 0, 0);
-  }
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) sh.wsum[warp] = x;
+    __syncthreads();
+    sum = 0;
+#pragma unroll 8
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const long long y = sh.wsum[w];
+      if (w < warp) x += y;
+      sum += y;
+    }
+    return x;
+  };
   tc_fence_before();
-  __syncthreads();
+  int t_req = tiles_of(tid);
+  long long sum, inc = scan(t_req, sum), total = sum;
+  for (int base = kThreads; base < p.num_reqs; base += kThreads) {
+    scan(tiles_of(base + tid), sum);
+    total += sum;
+  }
   tc_fence_after();
-  long long total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) total += sh.wsum[w];
+  // zeros for the rows of empty requests, each CTA its share of the requests
+  for (int base = 0; base < p.num_reqs; base += kThreads) {
+    const int r = base + tid;
+    const bool empty = r < p.num_reqs && r % (int)gridDim.x == (int)blockIdx.x && (base ? tiles_of(r) : t_req) == 0;
+    if (!__syncthreads_or(empty)) continue;
+    for (int x = base; x < min(base + kThreads, p.num_reqs); ++x) {
+      if (x % (int)gridDim.x != (int)blockIdx.x || tiles_of(x) != 0) continue;
+      uint4* o = reinterpret_cast<uint4*>(p.out + (int64_t)x * p.T * p.num_q_heads * kFp4D);
+      const int64_t n = (int64_t)p.T * p.num_q_heads * (kFp4D / 8);
+      for (int64_t i = tid; i < n; i += kThreads) o[i] = make_uint4(0, 0, 0, 0);
+    }
+  }
   const int64_t line_total = total * p.units;
   const int64_t begin = line_begin(line_total, cta, p.ctas), end = line_begin(line_total, cta + 1, p.ctas);
-  __syncthreads();
   if (begin < end) {  // the requests that hold the range's first and last tile
     long long before = 0;
-    for (int base = 0; base < p.num_reqs; base += kThreads) {
-      const int r = base + tid;
-      const int len = r < p.num_reqs ? __ldg(p.seq_lens + r) : 0;
-      const long long tiles = len > 0 ? ((int64_t)len + kBN - 1) / kBN : 0;
-      long long inc = tiles * p.units;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
+    for (int base = 0;; base += kThreads) {
+      if (base) {
+        t_req = tiles_of(base + tid);
+        inc = scan(t_req, sum);
+      } else if (p.num_reqs > kThreads) {
+        inc = scan(t_req, sum);
       }
-      if (lane == 31) sh.wsum[warp] = inc;
-      __syncthreads();
-      long long sum = 0;
-      for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) inc += sh.wsum[w];
-        sum += sh.wsum[w];
+      const long long at = (before + inc - t_req) * p.units, next = at + (long long)t_req * p.units;
+      if (at <= begin && begin < next) {
+        const int64_t x = begin - at;
+        sh.r0 = base + tid;
+        sh.u0 = p.units == 1 ? 0 : (int)(x / t_req);
+        sh.t00 = (int)(x - (int64_t)sh.u0 * t_req);
       }
-      const long long at = before + inc - tiles * p.units;
-      if (tiles > 0 && at <= begin && begin < at + tiles * p.units) {
-        sh.r0 = r;
-        sh.u0 = (int)((begin - at) / tiles);
-        sh.t00 = (int)((begin - at) % tiles);
-      }
-      if (tiles > 0 && at < end && end <= at + tiles * p.units) {
+      if (at < end && end <= next) {
         // for the merge: does the unit of the last tile begin in this range and go on past it?
-        const int64_t u = (end - 1 - at) / tiles, unit_begin = at + u * tiles;
+        const int64_t u = p.units == 1 ? 0 : (end - 1 - at) / t_req, unit_begin = at + u * t_req, unit_end = unit_begin + t_req;
         Note& note = p.ws[blockIdx.x].note;
-        note.r = r;
+        note.r = base + tid;
         note.unit = p.lines > 1 ? line : (int)u;
-        note.unit_end = unit_begin + tiles;
-        note.total = line_total;
-        note.valid = unit_begin >= begin && unit_begin + tiles > end;
+        // its last CTA: the first whose range ends at or after the unit's end
+        note.pieces = unit_begin >= begin && unit_end > end ? (int)((unit_end * p.ctas + line_total - 1) / line_total) - cta : 0;
       }
       before += sum;
-      __syncthreads();
-      if (before >= end) break;  // CTA-uniform
+      if (before * p.units >= end || base + kThreads >= p.num_reqs) break;  // CTA-uniform
     }
-  } else if (tid == 0) {
-    p.ws[blockIdx.x].note.valid = 0;
+  } else {  // nothing to do (fewer tiles than CTAs): the merge may still pass by
+    if (tid == 0) p.ws[blockIdx.x].note.pieces = 0;
+    if (tid < kMaxCols) p.ws[blockIdx.x].slot[0].l[tid] = 0.0f;
   }
+  __syncthreads();
   const Cursor start{sh.r0, sh.u0, sh.t00, sh.r0 >= 0 ? end - begin : 0};
   const uint32_t tmem = sh.tmem_base;
   volatile int* abort = &sh.abort;
@@ -1009,59 +1023,67 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
 // ------------------------------------------------------------------------------------------
 // merge of the pieces of a unit that several CTAs worked on
 // ------------------------------------------------------------------------------------------
-// Block (b, y): CTA b's note says whether a unit began in its range and went on; one warp a column adds
-// the pieces up: M = max m, out = v_scale sum 2^(m - M) O / sum 2^(m - M) l. Lane = 8 elements.
+// Block (b, y): CTA b's note says whether a unit began in its range and went on; two warps a column (128
+// elements each) add its pieces up: M = max m, out = v_scale sum 2^(m - M) O / sum 2^(m - M) l. The
+// first 16 pieces are loaded before their weights are known; a piece without a key (l = 0: its range
+// is empty, or the column sees none of its keys) may hold anything and counts as nothing.
 __global__ void __launch_bounds__(256)
-    spec_verify_fp4_merge_kernel(const CtaWorkspace* __restrict__ ws, int32_t lines, int32_t ctas, int32_t T, int32_t group,
+    spec_verify_fp4_merge_kernel(const CtaWorkspace* __restrict__ ws, int32_t lines, int32_t T, int32_t group,
                                  int32_t num_q_heads, int32_t tpc, int32_t n_tg, const float* __restrict__ v_scale,
                                  __nv_bfloat16* __restrict__ out) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Note& note = ws[blockIdx.x].note;
-  if (!note.valid) return;
-  const int lane = threadIdx.x & 31, col = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int pieces = note.pieces;
+  if (pieces == 0) return;
+  const int lane = threadIdx.x & 31, half = (threadIdx.x >> 5) & 1, col = blockIdx.y * 4 + (threadIdx.x >> 6);
   const int unit = note.unit, t_base = (unit % n_tg) * tpc;
   if (col >= min(tpc, T - t_base) * group) return;
-  const int line = blockIdx.x % lines, c = blockIdx.x / lines;
-  const int64_t total = note.total;
-  // pieces c .. last: the smallest `last` whose range ends at or after the unit's end
-  const int pieces = (int)((note.unit_end * ctas + total - 1) / total) - c;
-  float M = -INFINITY, L = 0.0f;
-  float acc[8] = {};
-  auto piece = [&](int i) -> const Slot& { return ws[(int64_t)(c + i) * lines + line].slot[i == 0 ? 1 : 0]; };
-  auto has = [&](int i) {  // a range may be empty when there are fewer tiles than CTAs
-    return i < pieces && line_begin(total, c + i, ctas) < line_begin(total, c + i + 1, ctas);
-  };
-  for (int base = 0; base < pieces; base += 32) {
-    const bool live = has(base + lane) && piece(base + lane).l[col] != 0.0f;
-    float m = live ? piece(base + lane).m[col] : -INFINITY;
+  // piece i > 0 is slot 0 of the i-th CTA after this one in the line
+  const CtaWorkspace* first = ws + blockIdx.x;
+  auto slot = [&](int i) -> const Slot& { return i == 0 ? first->slot[1] : first[(int64_t)i * lines].slot[0]; };
+  constexpr int kBatch = 16;
+  float4 o[kBatch];
+  auto load = [&](int base) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    M = fmaxf(M, m);
-  }
-  for (int base = 0; base < pieces; base += 32) {
-    const float l = has(base + lane) ? piece(base + lane).l[col] : 0.0f;
-    const float w = l != 0.0f ? exp2f(piece(base + lane).m[col] - M) : 0.0f;
+    for (int i = 0; i < kBatch; ++i)
+      o[i] = base + i < pieces ? __ldg(reinterpret_cast<const float4*>(slot(base + i).o[col]) + half * 32 + lane)
+                               : make_float4(0, 0, 0, 0);
+  };
+  load(0);
+  const float l0 = lane < pieces ? slot(lane).l[col] : 0.0f, m0 = lane < pieces ? slot(lane).m[col] : 0.0f;
+  float M = l0 != 0.0f ? m0 : -INFINITY;
+  for (int i = 32 + lane; i < pieces; i += 32)
+    if (slot(i).l[col] != 0.0f) M = fmaxf(M, slot(i).m[col]);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+  float4 acc = make_float4(0, 0, 0, 0);
+  float L = 0.0f;
+  for (int base = 0; base < pieces; base += 32) {  // lane = piece
+    const float l = base == 0 ? l0 : base + lane < pieces ? slot(base + lane).l[col] : 0.0f;
+    const float m = base == 0 ? m0 : base + lane < pieces ? slot(base + lane).m[col] : 0.0f;
+    const float w = l != 0.0f ? exp2f(m - M) : 0.0f;
     float wl = w * l;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) wl += __shfl_xor_sync(0xffffffffu, wl, o);
+    for (int x = 16; x > 0; x >>= 1) wl += __shfl_xor_sync(0xffffffffu, wl, x);
     L += wl;
-    const int n = min(32, pieces - base);
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      if (wi == 0.0f) continue;
-      const float4* src = reinterpret_cast<const float4*>(piece(base + i).o[col]) + lane * 2;
-      const float4 a = __ldg(src), b = __ldg(src + 1);
-      acc[0] += wi * a.x; acc[1] += wi * a.y; acc[2] += wi * a.z; acc[3] += wi * a.w;
-      acc[4] += wi * b.x; acc[5] += wi * b.y; acc[6] += wi * b.z; acc[7] += wi * b.w;
+    for (int b = base; b < min(base + 32, pieces); b += kBatch) {
+      if (b > 0) load(b);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, b - base + i);
+        const bool live = wi != 0.0f;
+        acc.x += live ? wi * o[i].x : 0.0f;
+        acc.y += live ? wi * o[i].y : 0.0f;
+        acc.z += live ? wi * o[i].z : 0.0f;
+        acc.w += live ? wi * o[i].w : 0.0f;
+      }
     }
   }
   const float f = L == 0.0f ? 0.0f : __ldg(v_scale) / L;
   const int t = t_base + col / group;
   const int64_t row = ((int64_t)note.r * T + t) * num_q_heads + (int64_t)(unit / n_tg) * group + col % group;
-  reinterpret_cast<uint4*>(out + row * kFp4D)[lane] =
-      make_uint4(pack_bf16x2(acc[0] * f, acc[1] * f), pack_bf16x2(acc[2] * f, acc[3] * f),
-                 pack_bf16x2(acc[4] * f, acc[5] * f), pack_bf16x2(acc[6] * f, acc[7] * f));
+  reinterpret_cast<uint2*>(out + row * kFp4D)[half * 32 + lane] =
+      make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
 }
 
 int gcd_int(int a, int b) {
@@ -1086,7 +1108,7 @@ pkv_status launch(const Params& p, cudaStream_t st) {
   pkv_status s = check_launch("spec_verify_attn_fp4");
   if (s != PKV_OK) return s;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, (unsigned)(kCols / 8));
+  cfg.gridDim = dim3(grid, (unsigned)(kCols / 4));
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -1094,7 +1116,7 @@ pkv_status launch(const Params& p, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, spec_verify_fp4_merge_kernel, (const CtaWorkspace*)p.ws, p.lines, p.ctas, p.T, p.group,
+  cudaLaunchKernelEx(&cfg, spec_verify_fp4_merge_kernel, (const CtaWorkspace*)p.ws, p.lines, p.T, p.group,
                      p.num_q_heads, p.tpc, p.n_tg, p.v_scale, p.out);
   return check_launch("spec_verify_attn_fp4 (merge)");
 }
