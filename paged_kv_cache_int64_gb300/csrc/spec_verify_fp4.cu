@@ -206,10 +206,22 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 // A wait whose threads sleep in the barrier test, in few instructions (the roles' loops share the
-// instruction cache): gives up after limit_ns, or when another thread of the CTA has.
+// instruction cache): gives up after limit_ns, or when another thread of the CTA has. With a bound below
+// the sleep (a test of this path) the barrier is polled instead.
 __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
   uint64_t t0 = 0;
-  while (!mbar_try_wait_suspend(bar, parity)) {
+  while (true) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p, s;\n\t"
+        "setp.ge.u64 s, %4, %3;\n\t"
+        "@s mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "@!s mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity), "n"(kSuspendHintNs), "l"(limit_ns)
+        : "memory");
+    if (done) return true;
     if (*abort) return false;
     const uint64_t t = globaltimer_ns();
     if (t0 == 0) {
@@ -219,7 +231,6 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
       return false;
     }
   }
-  return true;
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t wl) {
   return __all_sync(0xffffffffu, wait_bar(bar, parity, abort, wl));
@@ -1006,7 +1017,7 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
     // before the tensor memory is freed: wait for the copies of every armed phase and every MMA issued
     if (tid == 0)
       for (int s = 0; s < kStages; ++s) drain_armed(&sh.full[s], sh.armed[s]);
-    if ((warp == 1 || warp == 2) && lane == 0) {
+    if ((warp == 1 || warp == 2) && elect_one()) {  // (the lane that issued)
       umma_commit(&sh.drain);
       mbar_wait_drain(&sh.drain, 0);
     }

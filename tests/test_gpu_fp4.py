@@ -458,6 +458,23 @@ def test_attend_on_two_streams(pkv):
         check(F.bf16_to_f32(bf16_to_u16(o)).astype(np.float64), want, tol)
 
 
+@pytest.mark.parametrize("T,lens", [(8, [3000, 900, 64]), (1, [20000, 0, 5]), (4, [90] * 40)])
+def test_attend_gives_up_reports_timeout_and_recovers(pkv, ws, T, lens):
+    """With a bound of one nanosecond the CTAs give up at their first wait that is not already satisfied,
+    with their copies in flight: the call reports the timeout, and the next one is as before."""
+    b = Batch(lens, 2, 16, seed=T)
+    q = queries(b.rng, len(lens) * T, 8)
+    ref = attend(pkv, b, q, T, 1 / 16, ws)
+    caches, scales, bt, sl = b.device()
+    qd = u16_to_bf16(q).to(DEV)
+    err, out = dev_err(), torch.zeros_like(qd)
+    pkv.lib.pkv_testing_set_wait_limit_ns(1)
+    pkv.spec_verify_attn_fp4(qd, *caches, *scales, bt, sl, T, 1 / 16, out, ws, dev_err=err)
+    torch.cuda.synchronize()
+    assert err.item() == pkv.PKV_ERR_TIMEOUT
+    assert np.array_equal(ref, attend(pkv, b, q, T, 1 / 16, ws))
+
+
 # ------------------------------------------------------------------------------------------------
 # together
 # ------------------------------------------------------------------------------------------------
