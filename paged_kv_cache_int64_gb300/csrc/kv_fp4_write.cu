@@ -46,20 +46,6 @@ struct WriteArgs {
   int* dev_err;
 };
 
-// 8 values -> 8 e2m1 codes, to nearest even, magnitudes past 6 as 6 (the hardware conversion).
-__device__ __forceinline__ uint32_t e2m1x8(const float* x) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
-      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
-      : "=r"(r)
-      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
-  return r;
-}
-
 // The division itself, for groups outside the range of the corrected product: 8 elements. By value and
 // out of line: its registers are not the common path's.
 __device__ __noinline__ uint32_t quantize8_slow(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, float d) {
@@ -71,7 +57,7 @@ __device__ __noinline__ uint32_t quantize8_slow(uint32_t w0, uint32_t w1, uint32
     const float v = __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
     x[i] = copysignf(zero ? 0.0f : __fdiv_rn(v, d), v);
   }
-  return e2m1x8(x);
+  return e2m1x8_rn(x);
 }
 
 // 16 bf16 elements -> 8 bytes of codes and the group's scale byte.
@@ -108,7 +94,7 @@ __device__ __forceinline__ uint2 quantize_group(const Bytes32& in, float g, floa
       const float q0 = __fmul_rn(v, inv);
       x[i] = __fmaf_rn(-__fmaf_rn(q0, d, -v), inv, q0);
     }
-    c[h] = e2m1x8(x);
+    c[h] = e2m1x8_rn(x);
   }
   return make_uint2(c[0], c[1]);
 }

@@ -48,6 +48,13 @@ constexpr int kScaleTile = kBN * kFp4Groups;   // 2 KB
 constexpr int kHalfStage = kCodeTile + kScaleTile;
 constexpr int kMaxCols = 32;
 constexpr uint32_t kTmemCols = 512;
+// Q as a sum of kTerms e2m1 rows, digits of base 8: a block of 16 elements whose largest magnitude lies
+// in [2^E, 2^(E+1)) has the scales 2^E, 2^(E-3), ..., each term the last one's remainder rounded to
+// halves (which are e2m1 values up to 2), so what is left is at most 2^(E + 1 - 3 kTerms). Five terms:
+// elements down to 2^-6 of the block's largest keep all of bf16's bits, smaller ones an absolute error
+// of 2^(E-14). Rows are brought to [2^8, 2^9) first; e4m3 ends at 2^-9, so blocks that are 2^-5 of the
+// row's largest or less are kept to 2^-11, 2^-19 of it.
+constexpr int kTerms = 5;
 constexpr float kUnset = -3e38f;          // running maximum of a column that has seen no key
 constexpr float kStart = 8.0f;            // a new maximum's weight is 2^8; the maximum moves when a thread's
 constexpr float kMove = 32768.0f;         // weights of one key add up to more than this (fp16 ends at 65,504)
@@ -72,36 +79,40 @@ template <int kCols>
 struct Geo {
   static constexpr int kGC = kCols / 2;          // columns of a softmax warpgroup
   static constexpr int kStages = kCols == 16 ? 4 : 3;
-  static constexpr int kQChunk = kCols * 128;    // fp16 [kCols rows][64]
-  static constexpr int kQBuf = 4 * kQChunk;
+  static constexpr int kQTerm = kCols * 128;     // codes of one term of Q: [kCols rows][128 B], 128-byte swizzle
+  static constexpr int kQsTerm = 4 * 512;        // its scales: [4 steps of 64 elements][32 lanes][16 B]
+  static constexpr int kQBuf = kTerms * (kQTerm + kQsTerm);
   static constexpr int kPRow = kCols * 4;        // bytes of a row of P^T: 2 kCols columns
   static constexpr uint32_t kPLayout = kCols == 16 ? kLayoutSW64 : kLayoutSW128;
   static constexpr int kPBuf = 2 * kBN * kPRow;
   static constexpr int kOffQ = 0;
   static constexpr int kOffP = kOffQ + 2 * kQBuf;
-  static constexpr int kOffSf = kOffP + 2 * kPBuf;          // V scales, fp16 [4 quarters][32 key quads][4 groups][4 keys]
+  static constexpr int kOffSf = kOffP + kPBuf;   // V scales, fp16 [4 quarters][32 key quads][4 groups][4 keys]
   static constexpr int kSfBuf = kBN * kFp4Groups * 2;
-  static constexpr int kOffStage = kOffSf + 2 * kSfBuf;
+  static constexpr int kOffKs = kOffSf + 2 * kSfBuf;        // K scales: [4 steps][32 lanes][4 keys lane + 32 x][4 groups]
+  static constexpr int kOffStage = kOffKs + 2 * kScaleTile;
   static constexpr int kStage = 2 * kHalfStage;             // K codes, K scales, V codes, V scales
   static constexpr int kTiles = kOffStage + kStages * kStage;
-  static constexpr uint32_t kColK = 0;                      // two K tiles, 128 columns each
-  static constexpr uint32_t kColV = 256;                    // the V tile: a column a key
-  static constexpr uint32_t kColS = 384;                    // two S^T
-  static constexpr uint32_t kColO = 384 + 2 * kCols;        // O^T of the even elements, then of the odd ones
-  static_assert(kColO + 2 * kCols <= kTmemCols, "tensor memory");
-  static_assert(kOffStage % 1024 == 0 && kHalfStage % 1024 == 0 && kOffP % 1024 == 0, "swizzle atoms");
+  // tensor memory; the scale factors in blocks of 4 columns (one step of 64 elements)
+  static constexpr uint32_t kColV = 0;                      // two V tiles: a column a key
+  static constexpr uint32_t kColS = 256;                    // two S^T
+  static constexpr uint32_t kColO = kColS + 2 * kCols;      // O^T of the even elements, then of the odd ones
+  static constexpr uint32_t kColKs = kColO + 2 * kCols;     // two tiles' K scales
+  static constexpr uint32_t kColQs = kColKs + 32;           // Q scales of every term
+  static_assert(kColQs + 16 * kTerms <= kTmemCols && kColKs % 4 == 0, "tensor memory");
+  static_assert(kQBuf % 1024 == 0 && kOffP % 1024 == 0 && kOffStage % 1024 == 0 && kHalfStage % 1024 == 0, "swizzle atoms");
 };
 
 template <int kCols>
 struct alignas(16) Shared {
   static constexpr int kStages = Geo<kCols>::kStages;
   uint64_t full[kStages], empty[kStages];        // codes and scales of a tile
-  uint64_t q_ready[4], q_free[2];                // Q of run s (buffer s % 2; barrier s % 4: the K rows may be 3 runs ahead of the softmax)
-  uint64_t kt_ready[2], kt_free[2];              // K in tensor memory
-  uint64_t s_full[2], s_free[2];                 // S^T
+  uint64_t q_ready[4], q_free[2];                // Q of run s (buffer s % 2; barrier s % 4: Q may be 3 runs ahead of the softmax)
+  uint64_t ks_ready[2];                          // K scales of a tile laid out
+  uint64_t s_full[2], s_free[2];                 // S^T; s_full also frees the K scales
   uint64_t sf_ready[2], sf_free[2];              // transposed V scales
-  uint64_t vt_ready[2], vt_free[2];              // V in tensor memory, per half of the keys
-  uint64_t p_full[2], pv_done[2];                // P^T written; PV of the tile complete
+  uint64_t vt_ready[2];                          // V tile in tensor memory
+  uint64_t p_full, pv_done[2];                   // P^T written; PV of the tile complete (frees V tile and P^T)
   uint64_t drain;
   uint32_t armed[kStages];
   uint32_t bad[kStages];                         // key segments in a bad block
@@ -199,6 +210,25 @@ __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
+}
+// kind::mxf4nvf4: e2m1 operands with an e4m3 scale per 16 elements (K = 64), fp32 accumulator, A and B in
+// shared memory, the scales in tensor memory (blocks of 4 columns: row r's four scales in lane r % 32,
+// column r / 32). Instruction descriptor: bits 7-9 and 10-12 the operand types (1: e2m1), 17-22 N >> 3,
+// 23 the scale type (0: e4m3), 27-28 M >> 7.
+constexpr uint32_t idesc_fp4(int N) { return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 27); }
+__device__ __forceinline__ void umma_fp4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t sfa, uint32_t sfb,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+// A block of scales, 32 lanes x 16 bytes, from shared memory to the four quarters of tensor memory; runs
+// in order with the MMAs that the same lane issues after it.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t t, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(t), "l"(desc) : "memory");
 }
 // One arrival for the warp, after every lane's preceding accesses.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
@@ -314,24 +344,22 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&sh.full[s], 1);
-      mbar_init(&sh.empty[s], 4 + 8 + 1);  // K rows, V columns, V scales
+      mbar_init(&sh.empty[s], 1 + 8 + 1);  // QK (K codes), V columns, scales
       sh.armed[s] = 0;
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&sh.q_ready[b], 4);
       mbar_init(&sh.q_ready[2 + b], 4);
       mbar_init(&sh.q_free[b], 1);
-      mbar_init(&sh.kt_ready[b], 4);
-      mbar_init(&sh.kt_free[b], 1);
+      mbar_init(&sh.ks_ready[b], 1);
       mbar_init(&sh.s_full[b], 1);
       mbar_init(&sh.s_free[b], 4 * live_groups);
       mbar_init(&sh.sf_ready[b], 1);
       mbar_init(&sh.sf_free[b], 8);
-      mbar_init(&sh.vt_ready[b], 4);
-      mbar_init(&sh.vt_free[b], 1);
-      mbar_init(&sh.p_full[b], 4 * live_groups);
+      mbar_init(&sh.vt_ready[b], 8);
       mbar_init(&sh.pv_done[b], 1);
     }
+    mbar_init(&sh.p_full, 4 * live_groups);
     mbar_init(&sh.drain, 2);
     sh.abort = 0;
     sh.v_nan = 0;
@@ -344,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
     sh.row_off[tid] = t * p.num_q_heads + (tid - t * p.group);
   }
   // P^T: its zero half stays zero, the softmax writes the other
-  for (int x = tid; x < 2 * Gm::kPBuf / 16; x += kThreads)
+  for (int x = tid; x < Gm::kPBuf / 16; x += kThreads)
     reinterpret_cast<uint4*>(smem + Gm::kOffP)[x] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   // The CTA's range of the line's tiles. A thread holds a request (kThreads of them at a time).
@@ -515,34 +543,52 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------------------ QK issuer
-    // The whole warp walks the tiles and one elected lane issues: with a warp-uniform address stream the
-    // MMAs follow one another at the tensor core's own rate (9.5 clocks each with 16 columns, 16.4 with
-    // 32); from inside a `lane == 0` branch each takes 45 and more.
-    constexpr uint32_t id = idesc_f16(128, kCols, false, false, false);
-    const uint64_t q_desc = smem_desc(smem_u32(smem + Gm::kOffQ), 16, 1024);
+    // S^T = sum over the terms of K Q_term^T, all steps into one accumulator. The whole warp walks the
+    // tiles and one elected lane issues: with a warp-uniform address stream the MMAs follow one another
+    // at the tensor core's own rate; from inside a `lane == 0` branch each takes 45 clocks and more.
+    constexpr uint32_t id = idesc_fp4(kCols);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+    const uint64_t q_desc = smem_desc(smem_u32(smem + Gm::kOffQ), 16, 1024);
+    const uint64_t qs_desc = smem_desc(smem_u32(smem + Gm::kOffQ + kTerms * Gm::kQTerm), 16, 128, 0);
+    const uint64_t k_desc = smem_desc(smem_u32(smem + Gm::kOffStage), 16, 1024);
+    const uint64_t ks_desc = smem_desc(smem_u32(smem + Gm::kOffKs), 16, 128, 0);
     Cursor cur = start;
     Run run;
     int i = 0;
     bool ok = true;
+    Ring<kStages> ring;
     for (int s = 0; ok && next_run(p, cur, run); ++s) {
       ok = warp_wait(&sh.q_ready[s & 3], (s >> 2) & 1, abort, wl);
-      const uint64_t qd = q_desc + (uint64_t)((s & 1) * (Gm::kQBuf >> 4));
-      for (int j = 0; ok && j < run.n; ++j, ++i) {
+      // the last run's MMAs are done with the Q scales in tensor memory
+      if (ok && i > 0) ok = warp_wait(&sh.s_full[(i - 1) & 1], ((i - 1) >> 1) & 1, abort, wl);
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t q_off = (uint64_t)((s & 1) * (Gm::kQBuf >> 4));
+      if (elect_one()) {
+#pragma unroll 1
+        for (int x = 0; x < 4 * kTerms; ++x) tmem_cp_scales(tm + Gm::kColQs + 4 * x, qs_desc + q_off + (uint64_t)(x * 32));
+      }
+      __syncwarp();
+      for (int j = 0; ok && j < run.n; ++j, ++i, ring.next()) {
         const int b = i & 1;
         if (i >= 2) ok = warp_wait(&sh.s_free[b], ((i >> 1) - 1) & 1, abort, wl);
-        if (ok) ok = warp_wait(&sh.kt_ready[b], (i >> 1) & 1, abort, wl);
+        if (ok) ok = warp_wait(&sh.ks_ready[b], (i >> 1) & 1, abort, wl);
+        if (ok) ok = warp_wait(&sh.full[ring.st], ring.ph, abort, wl);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tm + Gm::kColS + b * kCols, a = tm + Gm::kColK + b * 128;
+        const uint32_t d = tm + Gm::kColS + b * kCols, sfa = tm + Gm::kColKs + b * 16;
+        const uint64_t kd = k_desc + (uint64_t)(ring.st * (Gm::kStage >> 4)), ksd = ks_desc + (uint64_t)(b * (kScaleTile >> 4));
         if (elect_one()) {
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) tmem_cp_scales(sfa + 4 * ks, ksd + (uint64_t)(ks * 32));
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c)
+          for (int t = 0; t < kTerms; ++t)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              umma_f16_ts(d, a + c * 32 + ks * 8, qd + (uint64_t)(c * (Gm::kQChunk >> 4) + ks * 2), id, (c | ks) ? 1u : 0u);
+              umma_fp4_ss(d, kd + (uint64_t)(ks * 2), q_desc + q_off + (uint64_t)(t * (Gm::kQTerm >> 4) + ks * 2), id,
+                          sfa + 4 * ks, tm + Gm::kColQs + 16 * t + 4 * ks, (t | ks) ? 1u : 0u);
           umma_commit(&sh.s_full[b]);
-          umma_commit(&sh.kt_free[b]);
+          umma_commit(&sh.empty[ring.st]);
           if (j == run.n - 1) umma_commit(&sh.q_free[s & 1]);
         }
         __syncwarp();
@@ -551,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
   } else if (warp == 2) {
     // ------------------------------------------------------------------------------ PV issuer
     constexpr uint32_t id = idesc_f16(128, 2 * kCols, false, false, true);
-    const uint64_t p_desc = smem_desc(smem_u32(smem + Gm::kOffP), 0, 8 * Gm::kPRow, Gm::kPLayout);
+    const uint64_t pd = smem_desc(smem_u32(smem + Gm::kOffP), 0, 8 * Gm::kPRow, Gm::kPLayout);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     Cursor cur = start;
     Run run;
@@ -560,35 +606,31 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
     while (ok && next_run(p, cur, run)) {
       for (int j = 0; ok && j < run.n; ++j, ++i) {
         const int b = i & 1;
-        ok = warp_wait(&sh.p_full[b], (i >> 1) & 1, abort, wl);
-        const uint64_t pd = p_desc + (uint64_t)(b * (Gm::kPBuf >> 4));
-        for (int hh = 0; ok && hh < 2; ++hh) {
-          ok = warp_wait(&sh.vt_ready[hh], i & 1, abort, wl);
-          if (!ok) break;
-          tc_fence_after();
-          // 64 keys: 8 steps of 8 keys, 16 rows of P^T (an even and an odd one a key)
-          const uint32_t a = tm + Gm::kColV + hh * 64;
-          const uint64_t pdh = pd + (uint64_t)(hh * (128 * Gm::kPRow >> 4));
-          if (elect_one()) {
+        ok = warp_wait(&sh.vt_ready[b], (i >> 1) & 1, abort, wl);
+        if (ok) ok = warp_wait(&sh.p_full, i & 1, abort, wl);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t a = tm + Gm::kColV + b * 128;
+        if (elect_one()) {
+          // 16 steps of 8 keys, 16 rows of P^T (an even and an odd one a key)
 #pragma unroll 1
-            for (int c = 0; c < 2; ++c)
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                umma_f16_ts(tm + Gm::kColO, a + c * 32 + ks * 8, pdh + (uint64_t)((4 * c + ks) * (16 * Gm::kPRow >> 4)), id,
-                            (j | hh | c | ks) ? 1u : 0u);
-            umma_commit(&sh.vt_free[hh]);
-            if (hh == 1) umma_commit(&sh.pv_done[b]);
-          }
-          __syncwarp();
+            for (int ks = 0; ks < 4; ++ks)
+              umma_f16_ts(tm + Gm::kColO, a + c * 32 + ks * 8, pd + (uint64_t)((4 * c + ks) * (16 * Gm::kPRow >> 4)), id,
+                          (j | c | ks) ? 1u : 0u);
+          umma_commit(&sh.pv_done[b]);
         }
+        __syncwarp();
       }
     }
   } else if (warp == 3) {
-    // ------------------------------------------------------------------------------ V scales
-    // lane = four keys: their 4 x 16 e4m3 bytes as fp16, [quarter of the row][key quad][group][key].
-    // Keys past the request or in a bad block get 0. A NaN scale of a key that some columns of the CTA
-    // do not see would reach them as 0 * NaN: it is left out here and put into the columns that see
-    // the key by the epilogue.
+    // ------------------------------------------------------------------------------ scales
+    // K: the four scale words of a key go to the blocks of the four steps, lane = key % 32. V: lane = four
+    // keys, their 4 x 16 e4m3 bytes as fp16, [quarter of the row][key quad][group][key]. Keys past the
+    // request or in a bad block get 0. A NaN V scale of a key that some columns of the CTA do not see
+    // would reach them as 0 * NaN: it is left out here and put into the columns that see the key by the
+    // epilogue.
     Cursor cur = start;
     Run run;
     int i = 0;
@@ -599,8 +641,30 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
       const int seen_by_all = run.len - p.T + (unit % p.n_tg) * p.tpc;  // the last such key
       for (int j = 0; ok && j < run.n; ++j, ++i, ring.next()) {
         const int st = ring.st, b = i & 1;
+        ok = warp_wait(&sh.full[st], ring.ph, abort, wl);
+        if (ok && i >= 2) ok = warp_wait(&sh.s_full[b], ((i >> 1) - 1) & 1, abort, wl);  // tile i - 2's scales are read
+        if (!ok) break;
+        const int key0 = (run.t0 + j) * kBN;
+        const uint32_t bad = sh.bad[st];
+        const bool plain = bad == 0 && key0 + kBN <= run.len;  // every key is live
+        auto dead = [&](int k) { return key0 + k >= run.len || ((bad >> (k / G)) & 1u); };
+        {
+          const uint4* src = reinterpret_cast<const uint4*>(smem + Gm::kOffStage + st * Gm::kStage + kCodeTile);
+          uint4 v[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            v[x] = src[lane + 32 * x];
+            if (!plain && dead(lane + 32 * x)) v[x] = make_uint4(0, 0, 0, 0);
+          }
+          uint4* dst = reinterpret_cast<uint4*>(smem + Gm::kOffKs + b * kScaleTile) + lane;
+          dst[0] = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
+          dst[32] = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
+          dst[64] = make_uint4(v[0].z, v[1].z, v[2].z, v[3].z);
+          dst[96] = make_uint4(v[0].w, v[1].w, v[2].w, v[3].w);
+          fence_proxy_async_smem();
+          warp_arrive(&sh.ks_ready[b], lane);
+        }
         ok = i < 2 || warp_wait(&sh.sf_free[b], ((i >> 1) - 1) & 1, abort, wl);
-        if (ok) ok = warp_wait(&sh.full[st], ring.ph, abort, wl);
         if (!ok) break;
         const uint4* src = reinterpret_cast<const uint4*>(smem + Gm::kOffStage + st * Gm::kStage + kHalfStage + kCodeTile);
         uint32_t w[4][4];
@@ -609,22 +673,17 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
           const uint4 v = src[lane * 4 + k];
           w[k][0] = v.x; w[k][1] = v.y; w[k][2] = v.z; w[k][3] = v.w;
         }
-        const int key0 = (run.t0 + j) * kBN;
-        const uint32_t bad = sh.bad[st];
-        if (bad || key0 + kBN > run.len || key0 + kBN - 1 > seen_by_all) {
+        if (!plain || key0 + kBN - 1 > seen_by_all) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int key = key0 + lane * 4 + k;
-            const bool dead = key >= run.len || ((bad >> ((lane * 4 + k) / G)) & 1u);
+            const bool gone = dead(lane * 4 + k), partly = key0 + lane * 4 + k > seen_by_all;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              if (dead) w[k][q] = 0;
-              if (key > seen_by_all) {
-                const uint32_t nan = __vcmpeq4(w[k][q] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                if (nan) {
-                  w[k][q] &= ~nan;
-                  sh.v_nan = 1;
-                }
+              if (gone) w[k][q] = 0;
+              const uint32_t nan = partly ? __vcmpeq4(w[k][q] & 0x7f7f7f7fu, 0x7f7f7f7fu) : 0u;
+              if (nan) {
+                w[k][q] &= ~nan;
+                sh.v_nan = 1;
               }
             }
           }
@@ -648,98 +707,72 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
       }
     }
   } else if (warp < 8) {
-    // ------------------------------------------------------------------------------ K rows
-    const int k = (warp & 3) * 32 + lane;  // the key row of a tile
-    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    // ------------------------------------------------------------------------------ Q
+    // The terms of Q for a run, a run ahead of its use. A warp takes a row, a lane 8 of its elements (two
+    // lanes share a block of 16).
     const float kg = __ldg(p.k_scale);
     Cursor cur = start;
     Run run;
-    int i = 0;
     bool ok = true;
-    Ring<kStages> ring;
     for (int s = 0; ok && next_run(p, cur, run); ++s) {
       const int unit = p.lines > 1 ? line : run.u;
       const int t_base = (unit % p.n_tg) * p.tpc;
       const int nq = min(p.tpc, p.T - t_base) * p.group;
+      const __nv_bfloat16* base = p.q + (((int64_t)run.r * p.T + t_base) * p.num_q_heads +
+                                         (int64_t)(unit / p.n_tg) * p.group) * kFp4D;
       if (s >= 2) ok = warp_wait(&sh.q_free[s & 1], ((s >> 1) - 1) & 1, abort, wl);
       if (!ok) break;
-      // Q: four threads a row, 64 elements (one swizzled chunk) each
-      {
-        const __nv_bfloat16* base = p.q + (((int64_t)run.r * p.T + t_base) * p.num_q_heads +
-                                           (int64_t)(unit / p.n_tg) * p.group) * kFp4D;
-        for (int row = k >> 2; row < kCols; row += 32) {
-          const int c = k & 3;
-          uint4 v[8];
-          const uint4* src = reinterpret_cast<const uint4*>(base + (int64_t)(row < nq ? sh.row_off[row] : 0) * kFp4D + c * 64);
-#pragma unroll
-          for (int x = 0; x < 8; ++x) v[x] = row < nq ? __ldg(src + x) : make_uint4(0, 0, 0, 0);
-          uint32_t mx = 0;
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            mx = __vmaxu2(mx, v[x].x & 0x7fff7fffu);
-            mx = __vmaxu2(mx, v[x].y & 0x7fff7fffu);
-            mx = __vmaxu2(mx, v[x].z & 0x7fff7fffu);
-            mx = __vmaxu2(mx, v[x].w & 0x7fff7fffu);
-          }
-          mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const int e = (int)(max(mx & 0xffffu, mx >> 16) >> 7);  // the row's largest exponent, biased
-          // rows are brought to [1, 2) by a power of two; rows with an infinity or NaN stay as they are
-          const int shift = e == 255 ? 0 : min(max(127 - e, -126), 126);
-          const float up = __int_as_float((127 + shift) << 23);
-          uint8_t* dst = smem + Gm::kOffQ + (s & 1) * Gm::kQBuf + c * Gm::kQChunk + row * 128;
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            uint32_t* wv = reinterpret_cast<uint32_t*>(&v[x]);
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-              wv[y] = pack_f16x2(__uint_as_float(wv[y] << 16) * up, __uint_as_float(wv[y] & 0xffff0000u) * up);
-            *reinterpret_cast<uint4*>(dst + ((x ^ (row & 7)) * 16)) = v[x];
-          }
-          if (c == 0) sh.f[s & 7][row] = row < nq ? p.scale_log2 * __int_as_float((127 - shift) << 23) * kg : 0.0f;
-        }
-        fence_proxy_async_smem();
-        warp_arrive(&sh.q_ready[s & 3], lane);
-      }
-      for (int j = 0; ok && j < run.n; ++j, ++i, ring.next()) {
-        const int st = ring.st, b = i & 1;
-        ok = warp_wait(&sh.full[st], ring.ph, abort, wl);
-        if (ok && i >= 2) ok = warp_wait(&sh.kt_free[b], ((i >> 1) - 1) & 1, abort, wl);
-        if (!ok) break;
-        tc_fence_after();
-        const uint8_t* stage = smem + Gm::kOffStage + st * Gm::kStage;
-        uint4 sc = *reinterpret_cast<const uint4*>(stage + kCodeTile + k * 16);
-        const uint32_t bad = sh.bad[st];
-        if (bad && ((bad >> (k / G)) & 1u)) sc = make_uint4(0, 0, 0, 0);
+      uint8_t* codes = smem + Gm::kOffQ + (s & 1) * Gm::kQBuf;
+      uint8_t* scales = codes + kTerms * Gm::kQTerm;
 #pragma unroll 1
-        for (int c2 = 0; c2 < 4; ++c2) {  // 64 elements: four groups, 32 tensor-memory columns
+      for (int row = warp - 4; row < kCols; row += 4) {
+        const uint4 raw = row < nq ? __ldg(reinterpret_cast<const uint4*>(base + (int64_t)sh.row_off[row] * kFp4D) + lane)
+                                   : make_uint4(0, 0, 0, 0);
+        const uint32_t rw[4] = {raw.x, raw.y, raw.z, raw.w};
+        uint32_t mx = 0;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint4 v = *reinterpret_cast<const uint4*>(stage + k * 128 + (((2 * c2 + h) ^ (k & 7)) * 16));
-            const uint32_t s2 = e4m3x2_to_f16x2((uint16_t)(h ? sc.x >> 16 : sc.x));
-            const __half2 sh2 = *reinterpret_cast<const __half2*>(&s2);
-            const __half2 lo = __low2half2(sh2), hi = __high2half2(sh2);
-            const uint32_t slo = *reinterpret_cast<const uint32_t*>(&lo), shi = *reinterpret_cast<const uint32_t*>(&hi);
-            uint32_t o[16], x[4];
-            const uint32_t cw[4] = {v.x, v.y, v.z, v.w};
+        for (int x = 0; x < 4; ++x) mx = __vmaxu2(mx, rw[x] & 0x7fff7fffu);
+        mx = max(mx & 0xffffu, mx >> 16);
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));  // of the block
+        uint32_t mr = mx;
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              e2m1x8_to_f16(cw[y], x);
+        for (int o = 2; o < 32; o <<= 1) mr = max(mr, __shfl_xor_sync(0xffffffffu, mr, o));
+        const int shift = min(135 - (int)(mr >> 7), 126);  // the row's largest to [2^8, 2^9)
+        const float up = __int_as_float((127 + shift) << 23);
+        int e = max((int)(__float_as_uint(__uint_as_float(mx << 16) * up) >> 23) - 127, -9);
+        float y[8];
+        const float inv = __int_as_float((127 - e) << 23);
 #pragma unroll
-              for (int z = 0; z < 4; ++z) o[4 * y + z] = hmul2_u32(x[z], y < 2 ? slo : shi);
-            }
-            tmem_st_32x32b_x16(tmem + lane_off + Gm::kColK + b * 128 + 32 * c2 + 16 * h, o);
+        for (int x = 0; x < 4; ++x) {
+          y[2 * x] = __uint_as_float(rw[x] << 16) * up * inv;
+          y[2 * x + 1] = __uint_as_float(rw[x] & 0xffff0000u) * up * inv;
+        }
+        uint8_t* dst = codes + row * 128 + (((lane >> 2) ^ (row & 7)) * 16) + (lane & 3) * 4;
+        uint8_t* sdst = scales + (lane >> 3) * 512 + row * 16 + ((lane >> 1) & 3);
+#pragma unroll 1
+        for (int t = 0; t < kTerms; ++t) {
+          *reinterpret_cast<uint32_t*>(dst) = e2m1x8_rn(y);
+          if ((lane & 1) == 0) *sdst = (uint8_t)(e >= -6 ? (e + 7) << 3 : 1 << (e + 9));
+          const int down = min(3, e + 9);
+          const float next = __int_as_float((127 + down) << 23);
+          e -= down;
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            constexpr float kHalves = 6291456.0f;  // 1.5 * 2^22: adding it leaves a multiple of one half
+            const float v = __fadd_rn(__fadd_rn(y[x], kHalves), -kHalves);
+            y[x] = (y[x] - v) * next;
           }
-          sc = make_uint4(sc.y, sc.z, sc.w, 0);
+          dst += Gm::kQTerm;
+          sdst += Gm::kQsTerm;
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sh.kt_ready[b]);
-          mbar_arrive(&sh.empty[st]);
-        }
+        // rows with an infinity or NaN: a NaN factor makes their scores, and so the row, NaN
+        if (lane == 0)
+          sh.f[s & 7][row] = row >= nq        ? 0.0f
+                             : mr >= 0x7f80u ? __int_as_float(0x7fc00000)
+                                             : p.scale_log2 * __int_as_float((127 - shift) << 23) * kg;
       }
+      fence_proxy_async_smem();
+      warp_arrive(&sh.q_ready[s & 3], lane);
     }
   } else if (warp < 16) {
     // ------------------------------------------------------------------------------ V columns
@@ -748,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
     // a key's column holds the converted pair (even, odd), which is what a conversion of the byte gives.
     // The columns of 16 keys are in the order 0 1 4 5 8 9 12 13, 2 3 6 7 10 11 14 15 (that of the store).
     const int quarter = warp & 3, hh = (warp - 8) >> 2;
-    const uint32_t tv = tmem + ((uint32_t)(quarter * 32) << 16) + Gm::kColV + hh * 64;
+    const uint32_t tv0 = tmem + ((uint32_t)(quarter * 32) << 16) + Gm::kColV + hh * 64;
     const int key = hh * 64 + (lane & 15);
     const uint32_t row = key * 128 + (((2 * quarter + (lane >> 4)) ^ (key & 7)) * 16);  // lanes 16-31: the second 16 bytes
     const uint32_t codes0 = smem_u32(smem + Gm::kOffStage + kHalfStage) + row;
@@ -762,10 +795,10 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
       for (int j = 0; ok && j < run.n; ++j, ++i, ring.next()) {
         const int st = ring.st, b = i & 1;
         ok = warp_wait(&sh.sf_ready[b], (i >> 1) & 1, abort, wl);  // the scales' warp has waited for the codes too
-        if (ok && i >= 1) ok = warp_wait(&sh.vt_free[hh], (i - 1) & 1, abort, wl);
+        if (ok && i >= 2) ok = warp_wait(&sh.pv_done[b], ((i >> 1) - 1) & 1, abort, wl);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t codes = codes0 + st * Gm::kStage;
+        const uint32_t codes = codes0 + st * Gm::kStage, tv = tv0 + b * 128;
         const uint8_t* sf = sf0 + b * Gm::kSfBuf;
 #pragma unroll 1
         for (int kb = 0; kb < 4; ++kb) {  // 16 keys
@@ -794,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&sh.vt_ready[hh]);
+          mbar_arrive(&sh.vt_ready[b]);
           mbar_arrive(&sh.empty[st]);
           mbar_arrive(&sh.sf_free[b]);
         }
@@ -933,11 +966,11 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
         }
         tc_fence_before();
         if (ok) warp_arrive(&sh.s_free[b], lane);
-        if (ok && i >= 2) ok = warp_wait(&sh.pv_done[b], ((i >> 1) - 1) & 1, abort, wl);
+        if (ok && i >= 1) ok = warp_wait(&sh.pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, abort, wl);  // P^T is read
 #pragma unroll
         for (int q = 0; q < kGC; q += 2) add2(l[q], l[q + 1], l[q], l[q + 1], x[q], x[q + 1]);
         if (ok) {
-          uint8_t* pb = smem + Gm::kOffP + b * Gm::kPBuf;
+          uint8_t* pb = smem + Gm::kOffP;
 #pragma unroll
           for (int cc = 0; cc < kGC / 8; ++cc) {
             const uint4 w = make_uint4(pack_f16x2(x[8 * cc], x[8 * cc + 1]), pack_f16x2(x[8 * cc + 2], x[8 * cc + 3]),
@@ -947,7 +980,7 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
           }
           fence_proxy_async_smem();
           tc_fence_before();
-          warp_arrive(&sh.p_full[b], lane);
+          warp_arrive(&sh.p_full, lane);
         }
       }
       // the segment's sums and O

@@ -93,15 +93,28 @@ def attention(q_u16, k, v, seq_len, T, group, softmax_scale):
             p /= p.sum()
             out[t, h] = p @ vv
             size = softmax_scale * (np.abs(kk) @ np.abs(q[t, h])).max()
-            tol[t, h] = allowed(out[t, h], p @ np.abs(vv), np.abs(vv).max(), n, size)
+            lost = softmax_scale * (np.abs(kk) @ q_error(q[t, h])).max()
+            tol[t, h] = allowed(out[t, h], p @ np.abs(vv), np.abs(vv).max(), n, size, lost)
     return out, tol
 
 
-def allowed(out, mag, vmax, n, size):
+def q_error(q):
+    """What the five-term form of a query row may leave of each element: 2^-14 of the largest magnitude of
+    its block of 16 (the last of five base-8 digits, the first of which counts in halves of the block's
+    power of two, is off by at most half a unit: 2^(E - 1 - 1 - 12) for a block in [2^E, 2^(E+1))), and no
+    less than 2^-19 of the row's (a digit's scale is at least 2^-9 in a row brought to [2^8, 2^9))."""
+    a = np.abs(q)
+    block = np.repeat(a.reshape(D // G, G).max(-1), G)
+    return np.maximum(2.0 ** -14 * block, 2.0 ** -19 * a.max())
+
+
+def allowed(out, mag, vmax, n, size, lost):
     """Allowed |error| of one bf16 output row: half a step of the output (2^-8 of its value); half a step
     of the fp16 probabilities (2^-11 of each, so of mag = sum_j p_j |v_j|); for probabilities below
     fp16's normal range half a quantum, 2^-25, against a row sum of at least 2^8 (n of them, times
-    the largest |v|); fp32 scores of 256 products (256 * 2^-24 of size = max_j scale * sum_d |q_d k_jd|),
-    which move numerator and denominator; fp32 sums over n keys in steps of 16 (2^-23 each)."""
-    return (2.0 ** -8 * np.abs(out) + (2.0 ** -11 + 2 * 256 * 2.0 ** -24 * size + (n / 16 + 16) * 2.0 ** -23) * mag +
+    the largest |v|); scores of 256 products summed in fp32 (256 * 2^-24 of size = max_j scale * sum_d
+    |q_d k_jd|) from a query row that is off by at most q_error (lost = max_j scale * sum_d q_error_d
+    |k_jd|), which move numerator and denominator; fp32 sums over n keys in steps of 16 (2^-23 each)."""
+    return (2.0 ** -8 * np.abs(out) +
+            (2.0 ** -11 + 2 * (256 * 2.0 ** -24 * size + lost) + (n / 16 + 16) * 2.0 ** -23) * mag +
             n * 2.0 ** -33 * vmax + 1e-30)
