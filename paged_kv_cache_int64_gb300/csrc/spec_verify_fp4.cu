@@ -30,8 +30,9 @@
 // at most one piece that began before it and one that ends after it, so two slots of workspace. The
 // pipeline runs on from one request to the next.
 //
-// Roles (24 warps): 0 TMA producer; 1 QK issuer; 2 PV issuer; 3 V scales; 4-7 K rows; 8-15 V columns;
-// 16-23 softmax, two warpgroups of kCols / 2 columns each.
+// Roles: warps 0 and 6 TMA producers of K and V; 1 QK issuer; 2 PV issuer; 3 V scales; 4-5 Q; 7 K scales;
+// 8-15 V columns;
+// from 16 on the softmax, a warpgroup for 8 columns.
 #include <cuda_bf16.h>
 
 #include "host_common.h"
@@ -42,19 +43,19 @@ namespace pkv {
 namespace {
 
 constexpr int kBN = 128;                  // keys of a tile
-constexpr int kThreads = 768;
 constexpr int kCodeTile = kBN * kFp4RowBytes;  // 16 KB
 constexpr int kScaleTile = kBN * kFp4Groups;   // 2 KB
-constexpr int kHalfStage = kCodeTile + kScaleTile;
+constexpr int kStage = kCodeTile + kScaleTile;
 constexpr int kMaxCols = 32;
 constexpr uint32_t kTmemCols = 512;
-// Q as a sum of kTerms e2m1 rows, digits of base 8: a block of 16 elements whose largest magnitude lies
-// in [2^E, 2^(E+1)) has the scales 2^E, 2^(E-3), ..., each term the last one's remainder rounded to
-// halves (which are e2m1 values up to 2), so what is left is at most 2^(E + 1 - 3 kTerms). Five terms:
-// elements down to 2^-6 of the block's largest keep all of bf16's bits, smaller ones an absolute error
-// of 2^(E-14). Rows are brought to [2^8, 2^9) first; e4m3 ends at 2^-9, so blocks that are 2^-5 of the
-// row's largest or less are kept to 2^-11, 2^-19 of it.
-constexpr int kTerms = 5;
+// Q as a sum of four e2m1 rows, digits of base 8: a block of 16 elements whose largest magnitude lies in
+// [2^E, 2^(E+1)) has the scales 2^E, 2^(E-3), 2^(E-6), 2^(E-9), each term the last one's remainder rounded
+// to halves (which are e2m1 values up to 2), so what is left is at most 2^(E-11): a quarter of half a
+// bf16 step of the block's largest element, whose own rounding already moves the scores by more. Rows are
+// brought to [2^8, 2^9) first; e4m3 ends at 2^-9, so blocks of 2^-8 of the row's largest or less are kept
+// to 2^-11, 2^-19 of it. Two terms stand side by side as columns of one product (the instruction takes
+// 40 clocks for 16 or 32 columns and 49 for 64), and the softmax adds their scores.
+constexpr int kTerms = 4;
 constexpr float kUnset = -3e38f;          // running maximum of a column that has seen no key
 constexpr float kStart = 8.0f;            // a new maximum's weight is 2^8; the maximum moves when a thread's
 constexpr float kMove = 32768.0f;         // weights of one key add up to more than this (fp16 ends at 65,504)
@@ -75,57 +76,68 @@ struct CtaWorkspace {
 };
 static_assert(sizeof(CtaWorkspace) % 16 == 0, "workspace of a CTA");
 
+#ifndef PKV_GC32
+#define PKV_GC32 16
+#endif
 template <int kCols>
 struct Geo {
-  static constexpr int kGC = kCols / 2;          // columns of a softmax warpgroup
-  static constexpr int kStages = kCols == 16 ? 4 : 3;
+  static constexpr int kGC = kCols == 16 ? 8 : PKV_GC32;  // columns of a softmax warpgroup
+  static constexpr int kGroups = kCols / kGC;
+  static constexpr int kThreads = 512 + 128 * kGroups;
+  // K codes are held until QK has read them, V codes until they are converted, which waits for the PV two
+  // tiles back
+  static constexpr int kKStages = kCols == 16 ? 4 : 3;
+  static constexpr int kVStages = 4;
   static constexpr int kQTerm = kCols * 128;     // codes of one term of Q: [kCols rows][128 B], 128-byte swizzle
-  static constexpr int kQsTerm = 4 * 512;        // its scales: [4 steps of 64 elements][32 lanes][16 B]
-  static constexpr int kQBuf = kTerms * (kQTerm + kQsTerm);
+  static constexpr int kQsPair = 4 * 512;        // scales of two terms: [4 steps of 64 elements][32 lanes][16 B]
+  static constexpr int kQBuf = kTerms * kQTerm + kTerms / 2 * kQsPair;
   static constexpr int kPRow = kCols * 4;        // bytes of a row of P^T: 2 kCols columns
   static constexpr uint32_t kPLayout = kCols == 16 ? kLayoutSW64 : kLayoutSW128;
   static constexpr int kPBuf = 2 * kBN * kPRow;
+  static constexpr int kPBufs = kCols == 16 ? 2 : 1;
   static constexpr int kOffQ = 0;
   static constexpr int kOffP = kOffQ + 2 * kQBuf;
-  static constexpr int kOffSf = kOffP + kPBuf;   // V scales, fp16 [4 quarters][32 key quads][4 groups][4 keys]
+  static constexpr int kOffSf = kOffP + kPBufs * kPBuf;     // V scales, fp16 [4 quarters][32 key quads][4 groups][4 keys]
   static constexpr int kSfBuf = kBN * kFp4Groups * 2;
   static constexpr int kOffKs = kOffSf + 2 * kSfBuf;        // K scales: [4 steps][32 lanes][4 keys lane + 32 x][4 groups]
-  static constexpr int kOffStage = kOffKs + 2 * kScaleTile;
-  static constexpr int kStage = 2 * kHalfStage;             // K codes, K scales, V codes, V scales
-  static constexpr int kTiles = kOffStage + kStages * kStage;
+  static constexpr int kOffK = kOffKs + 2 * kScaleTile;     // stages: codes, then scales
+  static constexpr int kOffV = kOffK + kKStages * kStage;
+  static constexpr int kTiles = kOffV + kVStages * kStage;
   // tensor memory; the scale factors in blocks of 4 columns (one step of 64 elements)
   static constexpr uint32_t kColV = 0;                      // two V tiles: a column a key
-  static constexpr uint32_t kColS = 256;                    // two S^T
-  static constexpr uint32_t kColO = kColS + 2 * kCols;      // O^T of the even elements, then of the odd ones
+  static constexpr uint32_t kColS = 256;                    // two S^T, the two terms' sums side by side
+  static constexpr uint32_t kColO = kColS + 4 * kCols;      // O^T of the even elements, then of the odd ones
   static constexpr uint32_t kColKs = kColO + 2 * kCols;     // two tiles' K scales
-  static constexpr uint32_t kColQs = kColKs + 32;           // Q scales of every term
-  static_assert(kColQs + 16 * kTerms <= kTmemCols && kColKs % 4 == 0, "tensor memory");
-  static_assert(kQBuf % 1024 == 0 && kOffP % 1024 == 0 && kOffStage % 1024 == 0 && kHalfStage % 1024 == 0, "swizzle atoms");
+  static constexpr uint32_t kColQs = kColKs + 32;           // Q scales of the pairs of terms
+  static_assert(kColQs + 8 * kTerms <= kTmemCols && kColKs % 4 == 0, "tensor memory");
+  static_assert(kOffQ == 0 && kQBuf % 1024 == 0 && kOffP % 1024 == 0 && kOffK % 1024 == 0 && kStage % 1024 == 0, "swizzle atoms");
 };
 
 template <int kCols>
 struct alignas(16) Shared {
-  static constexpr int kStages = Geo<kCols>::kStages;
-  uint64_t full[kStages], empty[kStages];        // codes and scales of a tile
+  static constexpr int kKStages = Geo<kCols>::kKStages, kVStages = Geo<kCols>::kVStages;
+  uint64_t k_full[kKStages], k_empty[kKStages];  // codes and scales of a tile's K
+  uint64_t v_full[kVStages], v_empty[kVStages];  // ... of its V
+  uint64_t q_first;                              // every warp's share of the first run's Q
   uint64_t q_ready[4], q_free[2];                // Q of run s (buffer s % 2; barrier s % 4: Q may be 3 runs ahead of the softmax)
   uint64_t ks_ready[2];                          // K scales of a tile laid out
-  uint64_t s_full[2], s_free[2];                 // S^T; s_full also frees the K scales
-  uint64_t sf_ready[2], sf_free[2];              // transposed V scales
+  uint64_t s_full[2], s_free[2];                 // S^T; s_free also means that the K scales are read
+  uint64_t sf_ready[2];                          // transposed V scales (and the V tile's place in tensor memory free)
   uint64_t vt_ready[2];                          // V tile in tensor memory
-  uint64_t p_full, pv_done[2];                   // P^T written; PV of the tile complete (frees V tile and P^T)
+  uint64_t p_full[2], pv_done[2];                // P^T written; PV of the tile complete (frees V tile and P^T)
   uint64_t drain;
-  uint32_t armed[kStages];
-  uint32_t bad[kStages];                         // key segments in a bad block
+  uint32_t k_armed[kKStages], v_armed[kVStages];
+  uint32_t k_bad[kKStages], v_bad[kVStages];     // key segments in a bad block
   uint32_t tmem_base;
   int abort;
   int v_nan;                                     // a NaN V scale was left out for a key that some columns do not see
   int r0, u0, t00;                               // first tile of the CTA's range
-  long long wsum[kThreads / 32];
+  long long wsum[Geo<kCols>::kThreads / 32];
   int32_t row_off[kCols];                        // column -> token * Hq + head in group
   int32_t tok[kCols];                            // column -> token
   alignas(16) float f[8][kCols];                 // column factors of the segment (ring: the softmax may be 4 behind)
   alignas(16) float m[kCols];                    // running maxima, log2, negated
-  float red[2][4][kCols / 2];
+  float red[Geo<kCols>::kGroups][4][Geo<kCols>::kGC];
   float fin[kCols];
 };
 
@@ -235,11 +247,12 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
 }
-// A wait whose threads sleep in the barrier test, in few instructions (the roles' loops share the
-// instruction cache): gives up after limit_ns, or when another thread of the CTA has. With a bound below
-// the sleep (a test of this path) the barrier is polled instead.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+// A warp waits for a barrier's phase: false when limit_ns has passed, or when another warp of the CTA has
+// given up. A satisfied wait is one test (56 clocks; 86 with a sleep's bound); the rest is out of line
+// and sleeps in the test, or with a bound below the sleep (a test of this path) polls.
+__device__ __noinline__ bool warp_wait_long(uint32_t bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
   uint64_t t0 = 0;
+  bool got = true;
   while (true) {
     uint32_t done;
     asm volatile(
@@ -249,21 +262,30 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatil
         "@!s mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity), "n"(kSuspendHintNs), "l"(limit_ns)
+        : "r"(bar), "r"(parity), "n"(kSuspendHintNs), "l"(limit_ns)
         : "memory");
-    if (done) return true;
-    if (*abort) return false;
+    if (done) break;
     const uint64_t t = globaltimer_ns();
-    if (t0 == 0) {
-      t0 = t;
-    } else if (t - t0 > limit_ns) {
+    if (t0 == 0) t0 = t;
+    if (*abort || t - t0 > limit_ns) {
       *abort = 1;
-      return false;
+      got = false;
+      break;
     }
   }
+  return __all_sync(0xffffffffu, got);
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t wl) {
-  return __all_sync(0xffffffffu, wait_bar(bar, parity, abort, wl));
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  if (__all_sync(0xffffffffu, done)) return true;
+  return warp_wait_long(smem_u32(bar), parity, abort, wl);
 }
 // Stage and parity of the tile ring.
 template <int kStages>
@@ -324,10 +346,60 @@ __device__ __forceinline__ void tmem_st_16x256b_x2(uint32_t a, const uint32_t (&
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
+// A query row's terms and their scales into a Q buffer, and its factor: by one warp, a lane 8 elements (two
+// lanes share a block of 16).
 template <int kCols>
-__global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __grid_constant__ Params p) {
+__device__ __noinline__ void quantize_q_row(uint4 raw, int row, uint8_t* buf, float* f, float scale_log2, float kg) {
   using Gm = Geo<kCols>;
-  constexpr int kGC = Gm::kGC, kStages = Gm::kStages;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rw[4] = {raw.x, raw.y, raw.z, raw.w};
+  uint32_t mx = 0;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) mx = __vmaxu2(mx, rw[x] & 0x7fff7fffu);
+  mx = max(mx & 0xffffu, mx >> 16);
+  mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));  // of the block
+  const uint32_t mr = __reduce_max_sync(0xffffffffu, mx);
+  const int shift = min(135 - (int)(mr >> 7), 126);  // the row's largest to [2^8, 2^9)
+  const float up = __int_as_float((127 + shift) << 23);
+  int e = max((int)(__float_as_uint(__uint_as_float(mx << 16) * up) >> 23) - 127, -9);
+  const float inv = __int_as_float((127 - e) << 23);
+  float y[8];
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    y[2 * x] = __uint_as_float(rw[x] << 16) * up * inv;
+    y[2 * x + 1] = __uint_as_float(rw[x] & 0xffff0000u) * up * inv;
+  }
+  uint8_t* dst = buf + row * 128 + (((lane >> 2) ^ (row & 7)) * 16) + (lane & 3) * 4;
+  // row n = row + kCols (t % 2) of the pair t / 2: lane n % 32, word n / 32 of the step's block
+  uint8_t* sdst = buf + kTerms * Gm::kQTerm + (lane >> 3) * 512 + row * 16 + ((lane >> 1) & 3);
+#pragma unroll
+  for (int t = 0; t < kTerms; ++t) {
+    *reinterpret_cast<uint32_t*>(dst + t * Gm::kQTerm) = e2m1x8_rn(y);
+    if ((lane & 1) == 0)
+      sdst[(t >> 1) * Gm::kQsPair + (t & 1) * (kCols == 16 ? 256 : 4)] = (uint8_t)(e >= -6 ? (e + 7) << 3 : 1 << (e + 9));
+    if (t == kTerms - 1) break;
+    const int down = min(3, e + 9);
+    const float next = __int_as_float((127 + down) << 23);
+    e -= down;
+#pragma unroll
+    for (int x = 0; x < 8; x += 2) {
+      constexpr float kHalves = 6291456.0f;  // 1.5 * 2^22: adding it leaves a multiple of one half
+      float v0, v1;
+      add2(v0, v1, y[x], y[x + 1], kHalves, kHalves);
+      add2(v0, v1, v0, v1, -kHalves, -kHalves);
+      add2(y[x], y[x + 1], y[x], y[x + 1], -v0, -v1);
+      mul2(y[x], y[x + 1], y[x], y[x + 1], next, next);
+    }
+  }
+  // rows with an infinity or NaN: a NaN factor makes their scores, and so the row, NaN
+  if (lane == 0)
+    f[row] = mr >= 0x7f80u ? __int_as_float(0x7fc00000) : scale_log2 * __int_as_float((127 - shift) << 23) * kg;
+}
+
+template <int kCols>
+__global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kernel(const __grid_constant__ Params p) {
+  using Gm = Geo<kCols>;
+  constexpr int kGC = Gm::kGC, kThreads = Gm::kThreads, kKStages = Gm::kKStages, kVStages = Gm::kVStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Shared<kCols>& sh = *reinterpret_cast<Shared<kCols>*>(smem + Gm::kTiles);
@@ -340,27 +412,32 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
     tmem_alloc(&sh.tmem_base, kTmemCols);
     tmem_relinquish();
   }
-  const int live_groups = nq_max > kGC ? 2 : 1;  // softmax warpgroups with a live column
+  const int live_groups = (nq_max + kGC - 1) / kGC;  // softmax warpgroups with a live column
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&sh.full[s], 1);
-      mbar_init(&sh.empty[s], 1 + 8 + 1);  // QK (K codes), V columns, scales
-      sh.armed[s] = 0;
+    for (int s = 0; s < kKStages; ++s) {
+      mbar_init(&sh.k_full[s], 1);
+      mbar_init(&sh.k_empty[s], 2);  // QK, K scales
+      sh.k_armed[s] = 0;
+    }
+    for (int s = 0; s < kVStages; ++s) {
+      mbar_init(&sh.v_full[s], 1);
+      mbar_init(&sh.v_empty[s], 9);  // V columns, V scales
+      sh.v_armed[s] = 0;
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&sh.q_ready[b], 4);
-      mbar_init(&sh.q_ready[2 + b], 4);
+      mbar_init(&sh.q_ready[b], 2);
+      mbar_init(&sh.q_ready[2 + b], 2);
       mbar_init(&sh.q_free[b], 1);
       mbar_init(&sh.ks_ready[b], 1);
       mbar_init(&sh.s_full[b], 1);
       mbar_init(&sh.s_free[b], 4 * live_groups);
       mbar_init(&sh.sf_ready[b], 1);
-      mbar_init(&sh.sf_free[b], 8);
       mbar_init(&sh.vt_ready[b], 8);
       mbar_init(&sh.pv_done[b], 1);
+      mbar_init(&sh.p_full[b], 4 * live_groups);
     }
-    mbar_init(&sh.p_full, 4 * live_groups);
     mbar_init(&sh.drain, 2);
+    mbar_init(&sh.q_first, kThreads / 32 - 2);
     sh.abort = 0;
     sh.v_nan = 0;
     sh.r0 = -1;
@@ -371,9 +448,8 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
     sh.tok[tid] = t;
     sh.row_off[tid] = t * p.num_q_heads + (tid - t * p.group);
   }
-  // P^T: its zero half stays zero, the softmax writes the other
-  for (int x = tid; x < Gm::kPBuf / 16; x += kThreads)
-    reinterpret_cast<uint4*>(smem + Gm::kOffP)[x] = make_uint4(0, 0, 0, 0);
+  // Q: rows past the live ones count for nothing, but have to be numbers; P^T: its zero half stays zero
+  for (int x = tid; x < Gm::kOffSf / 16; x += kThreads) reinterpret_cast<uint4*>(smem)[x] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   // The CTA's range of the line's tiles. A thread holds a request (kThreads of them at a time).
   auto tiles_of = [&](int r) -> int {
@@ -455,14 +531,36 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
   __syncthreads();
   const Cursor start{sh.r0, sh.u0, sh.t00, sh.r0 >= 0 ? end - begin : 0};
   const uint32_t tmem = sh.tmem_base;
-  volatile int* abort = &sh.abort;
+  volatile int* const abort = &sh.abort;
   const uint64_t wl = p.wait_limit_ns;
   const int G = p.seg;
   CtaWorkspace& ws = p.ws[blockIdx.x];
 
-  if (warp == 0) {
-    // ------------------------------------------------------------------------------ producer
-    // Lane = key segment (G keys, inside one block). Each lane walks its segment's place in the table a
+  auto q_rows = [&](const Run& run, int unit) {  // the unit's first query row
+    return reinterpret_cast<const uint4*>(p.q) +
+           (((int64_t)run.r * p.T + (unit % p.n_tg) * p.tpc) * p.num_q_heads + (int64_t)(unit / p.n_tg) * p.group) * (kFp4D / 8);
+  };
+  if (warp != 0 && warp != 6) {
+    Cursor cur = start;
+    Run run;
+    if (next_run(p, cur, run)) {
+      const int unit = p.lines > 1 ? line : run.u;
+      const int nq = min(p.tpc, p.T - (unit % p.n_tg) * p.tpc) * p.group;
+      const uint4* base = q_rows(run, unit);
+      const float kg = __ldg(p.k_scale);
+      const int at = warp - (warp > 6 ? 2 : 1);  // 0 .. kThreads / 32 - 3
+      if (at == 0 && lane >= nq && lane < kCols) sh.f[0][lane] = 0.0f;
+#pragma unroll 1
+      for (int row = at; row < nq; row += kThreads / 32 - 2)
+        quantize_q_row<kCols>(__ldg(base + (int64_t)sh.row_off[row] * (kFp4D / 8) + lane), row, smem + Gm::kOffQ, sh.f[0], p.scale_log2, kg);
+      fence_proxy_async_smem();
+      warp_arrive(&sh.q_first, lane);
+    }
+  }
+
+  if (warp == 0 || warp == 6) {
+    // ------------------------------------------------------------------------------ producers
+    // Warp 0 K, warp 6 V, each through its own ring. Lane = key segment (G keys, inside one block). Each lane walks its segment's place in the table a
     // tile ahead of the copies, without divisions inside a run; one elected lane issues the tile's
     // copies. Few instructions a tile: this code runs once in a tile, so it is fetched anew each time.
     const int nseg = kBN / G;
@@ -496,67 +594,76 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
       if (lane >= nseg || key >= run.len) return -1;
       return col < p.max_blocks ? __ldg(table + col) : -2;
     };
+    const bool is_k = warp == 0;
+    uint64_t* const fulls = is_k ? sh.k_full : sh.v_full;
+    uint64_t* const empties = is_k ? sh.k_empty : sh.v_empty;
+    uint32_t* const bads = is_k ? sh.k_bad : sh.v_bad;
+    uint32_t* const armed = is_k ? sh.k_armed : sh.v_armed;
+    const int stages = is_k ? kKStages : kVStages;
+    uint8_t* const base = smem + (is_k ? Gm::kOffK : Gm::kOffV);
+    const CUtensorMap* const maps = &p.map[is_k ? 0 : 4];
     int blk = look_up();
-    Ring<kStages> ring;
-    for (int i = 0; more; ++i, ring.next()) {
+    int st = 0;
+    uint32_t ph = 1;  // parity of the stage's last release (none before its first use)
+    bool first = true;
+    while (more) {
       const int c_slot = slot, c_kvh = kvh;
       int c_blk = blk;
       blk = look_up();
-      uint64_t* full = &sh.full[ring.st];
-      if (i >= kStages && !warp_wait(&sh.empty[ring.st], ring.ph ^ 1, abort, wl)) break;
+      uint64_t* full = &fulls[st];
+      if (!first && !warp_wait(&empties[st], ph, abort, wl)) break;
       if ((int64_t)c_blk >= p.num_blocks) c_blk = -2;
       const uint32_t bad = __ballot_sync(0xffffffffu, c_blk < -1);
       const uint32_t live = __ballot_sync(0xffffffffu, c_blk >= 0);
       // one block holds the tile (segment 0 is live then, or bad)
       const bool big = p.big_ok && __shfl_sync(0xffffffffu, c_blk >= 0 && c_slot + kBN <= p.block_size, 0);
-      uint8_t* stage = smem + Gm::kOffStage + ring.st * Gm::kStage;
+      uint8_t* stage = base + st * kStage;
       if (bad && lane == 0) record_error(p.dev_err, kErrDeviceBounds);
       if (lane == 0) {
-        sh.bad[ring.st] = bad;
+        bads[st] = bad;
         const uint32_t rows = big ? (uint32_t)kBN : (uint32_t)(__popc(live) * G);
-        mbar_arm_tx(full, rows * 2u * (uint32_t)(kFp4RowBytes + kFp4Groups), &sh.armed[ring.st]);
+        mbar_arm_tx(full, rows * (uint32_t)(kFp4RowBytes + kFp4Groups), &armed[st]);
       }
       __syncwarp();
       if (big) {
         const int b0 = __shfl_sync(0xffffffffu, c_blk, 0), s0 = __shfl_sync(0xffffffffu, c_slot, 0);
         if (elect_one()) {
-          tma_load_4d(stage, &p.map[2], full, 0, c_kvh, s0, b0);
-          tma_load_4d(stage + kCodeTile, &p.map[3], full, 0, c_kvh, s0, b0);
-          tma_load_4d(stage + kHalfStage, &p.map[6], full, 0, c_kvh, s0, b0);
-          tma_load_4d(stage + kHalfStage + kCodeTile, &p.map[7], full, 0, c_kvh, s0, b0);
+          tma_load_4d(stage, maps + 2, full, 0, c_kvh, s0, b0);
+          tma_load_4d(stage + kCodeTile, maps + 3, full, 0, c_kvh, s0, b0);
         }
       } else {
 #pragma unroll 1
         for (int g = 0; g < nseg; ++g) {
           const int b = __shfl_sync(0xffffffffu, c_blk, g), s = __shfl_sync(0xffffffffu, c_slot, g);
           if (b >= 0 && elect_one()) {
-            uint8_t* dst = stage + g * G * kFp4RowBytes;
-            uint8_t* dst_s = stage + kCodeTile + g * G * kFp4Groups;
-            tma_load_4d(dst, &p.map[0], full, 0, c_kvh, s, b);
-            tma_load_4d(dst_s, &p.map[1], full, 0, c_kvh, s, b);
-            tma_load_4d(dst + kHalfStage, &p.map[4], full, 0, c_kvh, s, b);
-            tma_load_4d(dst_s + kHalfStage, &p.map[5], full, 0, c_kvh, s, b);
+            tma_load_4d(stage + g * G * kFp4RowBytes, maps, full, 0, c_kvh, s, b);
+            tma_load_4d(stage + kCodeTile + g * G * kFp4Groups, maps + 1, full, 0, c_kvh, s, b);
           }
         }
       }
       __syncwarp();
+      if (++st == stages) {
+        st = 0;
+        ph ^= 1;
+        first = false;
+      }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------------------ QK issuer
-    // S^T = sum over the terms of K Q_term^T, all steps into one accumulator. The whole warp walks the
+    // S^T = sum over the terms of K Q_term^T, two terms' columns side by side. The whole warp walks the
     // tiles and one elected lane issues: with a warp-uniform address stream the MMAs follow one another
     // at the tensor core's own rate; from inside a `lane == 0` branch each takes 45 clocks and more.
-    constexpr uint32_t id = idesc_fp4(kCols);
+    constexpr uint32_t id = idesc_fp4(2 * kCols);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t q_desc = smem_desc(smem_u32(smem + Gm::kOffQ), 16, 1024);
     const uint64_t qs_desc = smem_desc(smem_u32(smem + Gm::kOffQ + kTerms * Gm::kQTerm), 16, 128, 0);
-    const uint64_t k_desc = smem_desc(smem_u32(smem + Gm::kOffStage), 16, 1024);
+    const uint64_t k_desc = smem_desc(smem_u32(smem + Gm::kOffK), 16, 1024);
     const uint64_t ks_desc = smem_desc(smem_u32(smem + Gm::kOffKs), 16, 128, 0);
     Cursor cur = start;
     Run run;
     int i = 0;
     bool ok = true;
-    Ring<kStages> ring;
+    Ring<kKStages> ring;
     for (int s = 0; ok && next_run(p, cur, run); ++s) {
       ok = warp_wait(&sh.q_ready[s & 3], (s >> 2) & 1, abort, wl);
       // the last run's MMAs are done with the Q scales in tensor memory
@@ -566,29 +673,28 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
       const uint64_t q_off = (uint64_t)((s & 1) * (Gm::kQBuf >> 4));
       if (elect_one()) {
 #pragma unroll 1
-        for (int x = 0; x < 4 * kTerms; ++x) tmem_cp_scales(tm + Gm::kColQs + 4 * x, qs_desc + q_off + (uint64_t)(x * 32));
+        for (int x = 0; x < 2 * kTerms; ++x) tmem_cp_scales(tm + Gm::kColQs + 4 * x, qs_desc + q_off + (uint64_t)(x * 32));
       }
       __syncwarp();
       for (int j = 0; ok && j < run.n; ++j, ++i, ring.next()) {
         const int b = i & 1;
-        if (i >= 2) ok = warp_wait(&sh.s_free[b], ((i >> 1) - 1) & 1, abort, wl);
-        if (ok) ok = warp_wait(&sh.ks_ready[b], (i >> 1) & 1, abort, wl);
-        if (ok) ok = warp_wait(&sh.full[ring.st], ring.ph, abort, wl);
+        // the K scales' warp has waited for the codes and for the softmax to be through with S^T_{i-2}
+        ok = warp_wait(&sh.ks_ready[b], (i >> 1) & 1, abort, wl);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tm + Gm::kColS + b * kCols, sfa = tm + Gm::kColKs + b * 16;
-        const uint64_t kd = k_desc + (uint64_t)(ring.st * (Gm::kStage >> 4)), ksd = ks_desc + (uint64_t)(b * (kScaleTile >> 4));
+        const uint32_t d = tm + Gm::kColS + b * 2 * kCols, sfa = tm + Gm::kColKs + b * 16;
+        const uint64_t kd = k_desc + (uint64_t)(ring.st * (kStage >> 4)), ksd = ks_desc + (uint64_t)(b * (kScaleTile >> 4));
         if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) tmem_cp_scales(sfa + 4 * ks, ksd + (uint64_t)(ks * 32));
-#pragma unroll 1
-          for (int t = 0; t < kTerms; ++t)
+#pragma unroll
+          for (int t = 0; t < kTerms / 2; ++t)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              umma_fp4_ss(d, kd + (uint64_t)(ks * 2), q_desc + q_off + (uint64_t)(t * (Gm::kQTerm >> 4) + ks * 2), id,
+              umma_fp4_ss(d, kd + (uint64_t)(ks * 2), q_desc + q_off + (uint64_t)(t * (2 * Gm::kQTerm >> 4) + ks * 2), id,
                           sfa + 4 * ks, tm + Gm::kColQs + 16 * t + 4 * ks, (t | ks) ? 1u : 0u);
           umma_commit(&sh.s_full[b]);
-          umma_commit(&sh.empty[ring.st]);
+          umma_commit(&sh.k_empty[ring.st]);
           if (j == run.n - 1) umma_commit(&sh.q_free[s & 1]);
         }
         __syncwarp();
@@ -597,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
   } else if (warp == 2) {
     // ------------------------------------------------------------------------------ PV issuer
     constexpr uint32_t id = idesc_f16(128, 2 * kCols, false, false, true);
-    const uint64_t pd = smem_desc(smem_u32(smem + Gm::kOffP), 0, 8 * Gm::kPRow, Gm::kPLayout);
+    const uint64_t p_desc = smem_desc(smem_u32(smem + Gm::kOffP), 0, 8 * Gm::kPRow, Gm::kPLayout);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     Cursor cur = start;
     Run run;
@@ -607,10 +713,11 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
       for (int j = 0; ok && j < run.n; ++j, ++i) {
         const int b = i & 1;
         ok = warp_wait(&sh.vt_ready[b], (i >> 1) & 1, abort, wl);
-        if (ok) ok = warp_wait(&sh.p_full, i & 1, abort, wl);
+        if (ok) ok = warp_wait(&sh.p_full[b], (i >> 1) & 1, abort, wl);
         if (!ok) break;
         tc_fence_after();
         const uint32_t a = tm + Gm::kColV + b * 128;
+        const uint64_t pd = p_desc + (uint64_t)((Gm::kPBufs == 2 ? b : 0) * (Gm::kPBuf >> 4));
         if (elect_one()) {
           // 16 steps of 8 keys, 16 rows of P^T (an even and an odd one a key)
 #pragma unroll 1
@@ -625,61 +732,42 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
       }
     }
   } else if (warp == 3) {
-    // ------------------------------------------------------------------------------ scales
-    // K: the four scale words of a key go to the blocks of the four steps, lane = key % 32. V: lane = four
-    // keys, their 4 x 16 e4m3 bytes as fp16, [quarter of the row][key quad][group][key]. Keys past the
-    // request or in a bad block get 0. A NaN V scale of a key that some columns of the CTA do not see
-    // would reach them as 0 * NaN: it is left out here and put into the columns that see the key by the
-    // epilogue.
+    // ------------------------------------------------------------------------------ V scales
+    // Lane = four keys: their 4 x 16 e4m3 bytes as fp16, [quarter of the row][key quad][group][key]. Keys
+    // past the request or in a bad block get 0. A NaN scale of a key that some columns of the CTA do not
+    // see would reach them as 0 * NaN: it is left out here and put into the columns that see the key by
+    // the epilogue.
     Cursor cur = start;
     Run run;
     int i = 0;
     bool ok = true;
-    Ring<kStages> ring;
+    Ring<kVStages> ring;
     while (ok && next_run(p, cur, run)) {
       const int unit = p.lines > 1 ? line : run.u;
       const int seen_by_all = run.len - p.T + (unit % p.n_tg) * p.tpc;  // the last such key
       for (int j = 0; ok && j < run.n; ++j, ++i, ring.next()) {
         const int st = ring.st, b = i & 1;
-        ok = warp_wait(&sh.full[st], ring.ph, abort, wl);
-        if (ok && i >= 2) ok = warp_wait(&sh.s_full[b], ((i >> 1) - 1) & 1, abort, wl);  // tile i - 2's scales are read
+        ok = warp_wait(&sh.v_full[st], ring.ph, abort, wl);
+        // PV_{i-2} is done: its V tile was converted (with these scales' last contents) and is read
+        if (ok && i >= 2) ok = warp_wait(&sh.pv_done[b], ((i >> 1) - 1) & 1, abort, wl);
         if (!ok) break;
-        const int key0 = (run.t0 + j) * kBN;
-        const uint32_t bad = sh.bad[st];
-        const bool plain = bad == 0 && key0 + kBN <= run.len;  // every key is live
-        auto dead = [&](int k) { return key0 + k >= run.len || ((bad >> (k / G)) & 1u); };
-        {
-          const uint4* src = reinterpret_cast<const uint4*>(smem + Gm::kOffStage + st * Gm::kStage + kCodeTile);
-          uint4 v[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            v[x] = src[lane + 32 * x];
-            if (!plain && dead(lane + 32 * x)) v[x] = make_uint4(0, 0, 0, 0);
-          }
-          uint4* dst = reinterpret_cast<uint4*>(smem + Gm::kOffKs + b * kScaleTile) + lane;
-          dst[0] = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
-          dst[32] = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
-          dst[64] = make_uint4(v[0].z, v[1].z, v[2].z, v[3].z);
-          dst[96] = make_uint4(v[0].w, v[1].w, v[2].w, v[3].w);
-          fence_proxy_async_smem();
-          warp_arrive(&sh.ks_ready[b], lane);
-        }
-        ok = i < 2 || warp_wait(&sh.sf_free[b], ((i >> 1) - 1) & 1, abort, wl);
-        if (!ok) break;
-        const uint4* src = reinterpret_cast<const uint4*>(smem + Gm::kOffStage + st * Gm::kStage + kHalfStage + kCodeTile);
+        const uint4* src = reinterpret_cast<const uint4*>(smem + Gm::kOffV + st * kStage + kCodeTile);
         uint32_t w[4][4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const uint4 v = src[lane * 4 + k];
           w[k][0] = v.x; w[k][1] = v.y; w[k][2] = v.z; w[k][3] = v.w;
         }
-        if (!plain || key0 + kBN - 1 > seen_by_all) {
+        const int key0 = (run.t0 + j) * kBN;
+        const uint32_t bad = sh.v_bad[st];
+        if (bad || key0 + kBN > run.len || key0 + kBN - 1 > seen_by_all) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const bool gone = dead(lane * 4 + k), partly = key0 + lane * 4 + k > seen_by_all;
+            const int key = lane * 4 + k;
+            const bool dead = key0 + key >= run.len || ((bad >> (key / G)) & 1u), partly = key0 + key > seen_by_all;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              if (gone) w[k][q] = 0;
+              if (dead) w[k][q] = 0;
               const uint32_t nan = partly ? __vcmpeq4(w[k][q] & 0x7f7f7f7fu, 0x7f7f7f7fu) : 0u;
               if (nan) {
                 w[k][q] &= ~nan;
@@ -701,78 +789,81 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
         }
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&sh.empty[st]);
+          mbar_arrive(&sh.v_empty[st]);
           mbar_arrive(&sh.sf_ready[b]);
         }
       }
     }
-  } else if (warp < 8) {
+  } else if (warp == 7) {
+    // ------------------------------------------------------------------------------ K scales
+    // The four scale words of a key go to the blocks of the four steps of 64 elements, lane = key % 32.
+    // Keys past the request or in a bad block get 0 (their codes are whatever the stage held).
+    Cursor cur = start;
+    Run run;
+    int i = 0;
+    bool ok = true;
+    Ring<kKStages> ring;
+    while (ok && next_run(p, cur, run)) {
+      for (int j = 0; ok && j < run.n; ++j, ++i, ring.next()) {
+        const int st = ring.st, b = i & 1;
+        ok = warp_wait(&sh.k_full[st], ring.ph, abort, wl);
+        // S^T_{i-2} has been read, so QK_{i-2} is done with its scales, and QK_i may overwrite S^T
+        if (ok && i >= 2) ok = warp_wait(&sh.s_free[b], ((i >> 1) - 1) & 1, abort, wl);
+        if (!ok) break;
+        const uint4* src = reinterpret_cast<const uint4*>(smem + Gm::kOffK + st * kStage + kCodeTile) + lane;
+        uint4 v[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) v[x] = src[32 * x];
+        const int key0 = (run.t0 + j) * kBN + lane;
+        const uint32_t bad = sh.k_bad[st];
+        if (bad || key0 - lane + kBN > run.len) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (key0 + 32 * x >= run.len || ((bad >> ((lane + 32 * x) / G)) & 1u)) v[x] = make_uint4(0, 0, 0, 0);
+        }
+        uint4* dst = reinterpret_cast<uint4*>(smem + Gm::kOffKs + b * kScaleTile) + lane;
+        dst[0] = make_uint4(v[0].x, v[1].x, v[2].x, v[3].x);
+        dst[32] = make_uint4(v[0].y, v[1].y, v[2].y, v[3].y);
+        dst[64] = make_uint4(v[0].z, v[1].z, v[2].z, v[3].z);
+        dst[96] = make_uint4(v[0].w, v[1].w, v[2].w, v[3].w);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sh.ks_ready[b]);
+          mbar_arrive(&sh.k_empty[st]);
+        }
+      }
+    }
+  } else if (warp < 6) {
     // ------------------------------------------------------------------------------ Q
-    // The terms of Q for a run, a run ahead of its use. A warp takes a row, a lane 8 of its elements (two
-    // lanes share a block of 16).
+    // The terms of Q for a run, a run ahead of its use; a warp takes every other row and has the next one's
+    // load in flight. The first run's rows were spread over all warps but the producers.
     const float kg = __ldg(p.k_scale);
     Cursor cur = start;
     Run run;
     bool ok = true;
     for (int s = 0; ok && next_run(p, cur, run); ++s) {
-      const int unit = p.lines > 1 ? line : run.u;
-      const int t_base = (unit % p.n_tg) * p.tpc;
-      const int nq = min(p.tpc, p.T - t_base) * p.group;
-      const __nv_bfloat16* base = p.q + (((int64_t)run.r * p.T + t_base) * p.num_q_heads +
-                                         (int64_t)(unit / p.n_tg) * p.group) * kFp4D;
-      if (s >= 2) ok = warp_wait(&sh.q_free[s & 1], ((s >> 1) - 1) & 1, abort, wl);
-      if (!ok) break;
-      uint8_t* codes = smem + Gm::kOffQ + (s & 1) * Gm::kQBuf;
-      uint8_t* scales = codes + kTerms * Gm::kQTerm;
+      if (s == 0) {
+        ok = warp_wait(&sh.q_first, 0, abort, wl);
+      } else {
+        const int unit = p.lines > 1 ? line : run.u;
+        const int t_base = (unit % p.n_tg) * p.tpc;
+        const int nq = min(p.tpc, p.T - t_base) * p.group;
+        const uint4* base = q_rows(run, unit);
+        auto fetch = [&](int row) { return row < nq ? __ldg(base + (int64_t)sh.row_off[row] * (kFp4D / 8) + lane) : make_uint4(0, 0, 0, 0); };
+        if (s >= 2) ok = warp_wait(&sh.q_free[s & 1], ((s >> 1) - 1) & 1, abort, wl);
+        if (!ok) break;
+        if (warp == 4 && lane >= nq && lane < kCols) sh.f[s & 7][lane] = 0.0f;
+        uint4 raw = fetch(warp - 4);
 #pragma unroll 1
-      for (int row = warp - 4; row < kCols; row += 4) {
-        const uint4 raw = row < nq ? __ldg(reinterpret_cast<const uint4*>(base + (int64_t)sh.row_off[row] * kFp4D) + lane)
-                                   : make_uint4(0, 0, 0, 0);
-        const uint32_t rw[4] = {raw.x, raw.y, raw.z, raw.w};
-        uint32_t mx = 0;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) mx = __vmaxu2(mx, rw[x] & 0x7fff7fffu);
-        mx = max(mx & 0xffffu, mx >> 16);
-        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));  // of the block
-        uint32_t mr = mx;
-#pragma unroll
-        for (int o = 2; o < 32; o <<= 1) mr = max(mr, __shfl_xor_sync(0xffffffffu, mr, o));
-        const int shift = min(135 - (int)(mr >> 7), 126);  // the row's largest to [2^8, 2^9)
-        const float up = __int_as_float((127 + shift) << 23);
-        int e = max((int)(__float_as_uint(__uint_as_float(mx << 16) * up) >> 23) - 127, -9);
-        float y[8];
-        const float inv = __int_as_float((127 - e) << 23);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          y[2 * x] = __uint_as_float(rw[x] << 16) * up * inv;
-          y[2 * x + 1] = __uint_as_float(rw[x] & 0xffff0000u) * up * inv;
+        for (int row = warp - 4; row < nq; row += 2) {
+          const uint4 next = fetch(row + 2);
+          quantize_q_row<kCols>(raw, row, smem + Gm::kOffQ + (s & 1) * Gm::kQBuf, sh.f[s & 7], p.scale_log2, kg);
+          raw = next;
         }
-        uint8_t* dst = codes + row * 128 + (((lane >> 2) ^ (row & 7)) * 16) + (lane & 3) * 4;
-        uint8_t* sdst = scales + (lane >> 3) * 512 + row * 16 + ((lane >> 1) & 3);
-#pragma unroll 1
-        for (int t = 0; t < kTerms; ++t) {
-          *reinterpret_cast<uint32_t*>(dst) = e2m1x8_rn(y);
-          if ((lane & 1) == 0) *sdst = (uint8_t)(e >= -6 ? (e + 7) << 3 : 1 << (e + 9));
-          const int down = min(3, e + 9);
-          const float next = __int_as_float((127 + down) << 23);
-          e -= down;
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            constexpr float kHalves = 6291456.0f;  // 1.5 * 2^22: adding it leaves a multiple of one half
-            const float v = __fadd_rn(__fadd_rn(y[x], kHalves), -kHalves);
-            y[x] = (y[x] - v) * next;
-          }
-          dst += Gm::kQTerm;
-          sdst += Gm::kQsTerm;
-        }
-        // rows with an infinity or NaN: a NaN factor makes their scores, and so the row, NaN
-        if (lane == 0)
-          sh.f[s & 7][row] = row >= nq        ? 0.0f
-                             : mr >= 0x7f80u ? __int_as_float(0x7fc00000)
-                                             : p.scale_log2 * __int_as_float((127 - shift) << 23) * kg;
+        fence_proxy_async_smem();
       }
-      fence_proxy_async_smem();
-      warp_arrive(&sh.q_ready[s & 3], lane);
+      if (ok) warp_arrive(&sh.q_ready[s & 3], lane);
     }
   } else if (warp < 16) {
     // ------------------------------------------------------------------------------ V columns
@@ -784,35 +875,42 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
     const uint32_t tv0 = tmem + ((uint32_t)(quarter * 32) << 16) + Gm::kColV + hh * 64;
     const int key = hh * 64 + (lane & 15);
     const uint32_t row = key * 128 + (((2 * quarter + (lane >> 4)) ^ (key & 7)) * 16);  // lanes 16-31: the second 16 bytes
-    const uint32_t codes0 = smem_u32(smem + Gm::kOffStage + kHalfStage) + row;
+    const uint32_t codes0 = smem_u32(smem + Gm::kOffV) + row;
     const uint8_t* sf0 = smem + Gm::kOffSf + quarter * 1024 + hh * 512 + (lane & 3) * 32;
     Cursor cur = start;
     Run run;
     int i = 0;
     bool ok = true;
-    Ring<kStages> ring;
+    Ring<kVStages> ring;
     while (ok && next_run(p, cur, run)) {
       for (int j = 0; ok && j < run.n; ++j, ++i, ring.next()) {
         const int st = ring.st, b = i & 1;
-        ok = warp_wait(&sh.sf_ready[b], (i >> 1) & 1, abort, wl);  // the scales' warp has waited for the codes too
-        if (ok && i >= 2) ok = warp_wait(&sh.pv_done[b], ((i >> 1) - 1) & 1, abort, wl);
+        // the scales' warp has waited for the codes and for the PV that read this V tile's place
+        ok = warp_wait(&sh.sf_ready[b], (i >> 1) & 1, abort, wl);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t codes = codes0 + st * Gm::kStage, tv = tv0 + b * 128;
+        const uint32_t codes = codes0 + st * kStage, tv = tv0 + b * 128;
         const uint8_t* sf = sf0 + b * Gm::kSfBuf;
+        // 16 keys a step; the next step's codes and scales are read before this one's are converted
+        uint32_t w[4], w2[4];
+        uint4 s4[2], s42[2];
+        ldmatrix_t8_x2(codes, w);
+        s4[0] = *reinterpret_cast<const uint4*>(sf);
+        s4[1] = *reinterpret_cast<const uint4*>(sf + 16);
 #pragma unroll 1
-        for (int kb = 0; kb < 4; ++kb) {  // 16 keys
-          uint32_t w[4];
-          ldmatrix_t8_x2(codes + kb * 16 * 128, w);
+        for (int kb = 0; kb < 4; ++kb) {
+          const int nb = kb < 3 ? kb + 1 : 3;
+          ldmatrix_t8_x2(codes + nb * 16 * 128, w2);
+          s42[0] = *reinterpret_cast<const uint4*>(sf + nb * 128);
+          s42[1] = *reinterpret_cast<const uint4*>(sf + nb * 128 + 16);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {  // 16 bytes: two groups, eight bytes each
-            const uint4 s4 = *reinterpret_cast<const uint4*>(sf + kb * 128 + x * 16);
             uint32_t o[8];
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
               uint32_t v[4];
               e2m1x8_to_f16(w[2 * x + g], v);
-              const uint32_t s01 = g ? s4.z : s4.x, s23 = g ? s4.w : s4.y;
+              const uint32_t s01 = g ? s4[x].z : s4[x].x, s23 = g ? s4[x].w : s4[x].y;
               const __half2 h01 = *reinterpret_cast<const __half2*>(&s01), h23 = *reinterpret_cast<const __half2*>(&s23);
               const __half2 d[4] = {__low2half2(h01), __high2half2(h01), __low2half2(h23), __high2half2(h23)};
               o[2 * g] = hmul2_u32(v[0], *reinterpret_cast<const uint32_t*>(&d[0]));
@@ -822,14 +920,17 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
             }
             tmem_st_16x256b_x2(tv + ((uint32_t)(16 * x) << 16) + kb * 16, o);
           }
+#pragma unroll
+          for (int x = 0; x < 4; ++x) w[x] = w2[x];
+          s4[0] = s42[0];
+          s4[1] = s42[1];
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&sh.vt_ready[b]);
-          mbar_arrive(&sh.empty[st]);
-          mbar_arrive(&sh.sf_free[b]);
+          mbar_arrive(&sh.v_empty[st]);
         }
       }
     }
@@ -845,15 +946,27 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
     // the key's two rows of P^T (see V columns for the order of the keys): weights in the first kCols
     // columns of the first row, which meets the even elements, and in the last of the second
     const int prow = 2 * ((k & ~15) + ((k >> 1) & 1) * 8 + ((k & 15) >> 2) * 2 + (k & 1));
-    auto p_chunk = [&](int odd, int cc) {  // byte offset of the group's chunk cc (8 columns) in a buffer
-      const uint32_t r = prow + odd, chunk = odd * (kCols / 8) + grp * (kGC / 8) + cc;
-      return r * Gm::kPRow + ((chunk ^ (kCols == 16 ? (r >> 1) & 3u : r & 7u)) * 16);
-    };
-    uint32_t p_off[2][kGC / 8];
+    uint32_t p_off[2][kGC / 8];  // byte offsets of the group's chunks of 8 columns in the two rows
 #pragma unroll
     for (int odd = 0; odd < 2; ++odd)
 #pragma unroll
-      for (int cc = 0; cc < kGC / 8; ++cc) p_off[odd][cc] = p_chunk(odd, cc);
+      for (int cc = 0; cc < kGC / 8; ++cc) {
+        const uint32_t r = prow + odd, chunk = odd * (kCols / 8) + grp * (kGC / 8) + cc;
+        p_off[odd][cc] = r * Gm::kPRow + ((chunk ^ (kCols == 16 ? (r >> 1) & 3u : r & 7u)) * 16);
+      }
+    auto load_scores = [&](uint32_t t, float (&x)[kGC]) {  // the two halves of the terms, added
+#pragma unroll
+      for (int q = 0; q < kGC; q += 8) {
+        uint32_t u[8], v[8];
+        tmem_ld_32x32b_x8(t + q, u);
+        tmem_ld_32x32b_x8(t + kCols + q, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int y = 0; y < 8; y += 2)
+          add2(x[q + y], x[q + y + 1], __uint_as_float(u[y]), __uint_as_float(u[y + 1]), __uint_as_float(v[y]),
+               __uint_as_float(v[y + 1]));
+      }
+    };
     Cursor cur = start;
     Run run;
     int i = 0;
@@ -878,22 +991,20 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
         if (ok) ok = warp_wait(&sh.s_full[b], (i >> 1) & 1, abort, wl);
         float x[kGC];
         float tile_sum[2];
-        const uint32_t ts = tmem + lane_off + Gm::kColS + b * kCols + c0;
+        const uint32_t ts = tmem + lane_off + Gm::kColS + b * 2 * kCols + c0;
         for (int pass = 0;; ++pass) {
           // weights 2^(S f - m), 0 where the column does not see the key. One that passes 2^15 shows in
           // their sum (no weight is negative; the sum's pipe has room where the maximum's has none).
           bool over = false;
           if (ok) {
             tc_fence_after();
-            uint32_t v[kGC];
-            tmem_ld_cols<kGC>(ts, v);
-            tmem_wait_ld();
+            load_scores(ts, x);
 #pragma unroll
             for (int q = 0; q < kGC; q += 4) {
               const float4 f4 = *reinterpret_cast<const float4*>(f + q);
               const float4 m4 = *reinterpret_cast<const float4*>(m + q);
-              fma2(x[q], x[q + 1], __uint_as_float(v[q]), __uint_as_float(v[q + 1]), f4.x, f4.y, m4.x, m4.y);
-              fma2(x[q + 2], x[q + 3], __uint_as_float(v[q + 2]), __uint_as_float(v[q + 3]), f4.z, f4.w, m4.z, m4.w);
+              fma2(x[q], x[q + 1], x[q], x[q + 1], f4.x, f4.y, m4.x, m4.y);
+              fma2(x[q + 2], x[q + 3], x[q + 2], x[q + 3], f4.z, f4.w, m4.z, m4.w);
             }
             if (masked) {
 #pragma unroll
@@ -916,12 +1027,10 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
           // some column's maximum moves (always so in a run's first tile): exact maxima of this tile
           float alpha = 1.0f, m_new = 0.0f;
           if (ok) {
-            uint32_t v[kGC];
-            tmem_ld_cols<kGC>(ts, v);
-            tmem_wait_ld();
+            load_scores(ts, x);
 #pragma unroll
             for (int q = 0; q < kGC; ++q) {
-              x[q] = __uint_as_float(v[q]) * f[q];
+              x[q] *= f[q];
               if (masked && past > sh.tok[c0 + q]) x[q] = -INFINITY;
             }
           }
@@ -966,11 +1075,14 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
         }
         tc_fence_before();
         if (ok) warp_arrive(&sh.s_free[b], lane);
-        if (ok && i >= 1) ok = warp_wait(&sh.pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, abort, wl);  // P^T is read
+        {  // the P^T buffer has been read
+          const int last = i - Gm::kPBufs;
+          if (ok && last >= 0) ok = warp_wait(&sh.pv_done[last & 1], (last >> 1) & 1, abort, wl);
+        }
 #pragma unroll
         for (int q = 0; q < kGC; q += 2) add2(l[q], l[q + 1], l[q], l[q + 1], x[q], x[q + 1]);
         if (ok) {
-          uint8_t* pb = smem + Gm::kOffP;
+          uint8_t* pb = smem + Gm::kOffP + (Gm::kPBufs == 2 ? b : 0) * Gm::kPBuf;
 #pragma unroll
           for (int cc = 0; cc < kGC / 8; ++cc) {
             const uint4 w = make_uint4(pack_f16x2(x[8 * cc], x[8 * cc + 1]), pack_f16x2(x[8 * cc + 2], x[8 * cc + 3]),
@@ -980,7 +1092,7 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
           }
           fence_proxy_async_smem();
           tc_fence_before();
-          warp_arrive(&sh.p_full, lane);
+          warp_arrive(&sh.p_full[b], lane);
         }
       }
       // the segment's sums and O
@@ -1008,10 +1120,10 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
         const int64_t row0 = ((int64_t)run.r * p.T + t_base) * p.num_q_heads + (int64_t)kvh * p.group;
         const int d = 2 * k;  // this lane's even element
 #pragma unroll 1
-        for (int q0 = 0; q0 < kGC; q0 += 8) {
+        for (int cq = c0; cq < c0 + kGC; cq += 8) {
           uint32_t v[8], w[8];
-          tmem_ld_32x32b_x8(tmem + lane_off + Gm::kColO + c0 + q0, v);
-          tmem_ld_32x32b_x8(tmem + lane_off + Gm::kColO + kCols + c0 + q0, w);
+          tmem_ld_32x32b_x8(tmem + lane_off + Gm::kColO + cq, v);
+          tmem_ld_32x32b_x8(tmem + lane_off + Gm::kColO + kCols + cq, w);
           tmem_wait_ld();
           if (nan) {  // keys that only some columns see, with a NaN V scale
             for (int key = max(seen_by_all + 1, run.t0 * kBN); key < min(run.len, (run.t0 + run.n) * kBN); ++key) {
@@ -1023,12 +1135,12 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
               if ((sb & 0x7f) != 0x7f) continue;
 #pragma unroll
               for (int q = 0; q < 8; ++q)
-                if (key - seen_by_all <= sh.tok[c0 + q0 + q]) v[q] = w[q] = 0x7fc00000u;
+                if (key - seen_by_all <= sh.tok[cq + q]) v[q] = w[q] = 0x7fc00000u;
             }
           }
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
-            const int c = c0 + q0 + q;
+            const int c = cq + q;
             if (c >= nq) break;
             const float x0 = __uint_as_float(v[q]), x1 = __uint_as_float(w[q]);
             if (whole)
@@ -1049,7 +1161,10 @@ __global__ void __launch_bounds__(kThreads, 1) spec_verify_fp4_kernel(const __gr
   if (gave_up) {
     // before the tensor memory is freed: wait for the copies of every armed phase and every MMA issued
     if (tid == 0)
-      for (int s = 0; s < kStages; ++s) drain_armed(&sh.full[s], sh.armed[s]);
+    {
+      for (int s = 0; s < kKStages; ++s) drain_armed(&sh.k_full[s], sh.k_armed[s]);
+      for (int s = 0; s < kVStages; ++s) drain_armed(&sh.v_full[s], sh.v_armed[s]);
+    }
     if ((warp == 1 || warp == 2) && elect_one()) {  // (the lane that issued)
       umma_commit(&sh.drain);
       mbar_wait_drain(&sh.drain, 0);
@@ -1148,7 +1263,7 @@ pkv_status launch(const Params& p, cudaStream_t st) {
     cudaFuncSetAttribute(spec_verify_fp4_kernel<kCols>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   });
   const unsigned grid = (unsigned)(p.ctas * p.lines);
-  spec_verify_fp4_kernel<kCols><<<grid, kThreads, kSmem, st>>>(p);
+  spec_verify_fp4_kernel<kCols><<<grid, Geo<kCols>::kThreads, kSmem, st>>>(p);
   pkv_status s = check_launch("spec_verify_attn_fp4");
   if (s != PKV_OK) return s;
   cudaLaunchConfig_t cfg = {};

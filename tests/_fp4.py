@@ -99,13 +99,13 @@ def attention(q_u16, k, v, seq_len, T, group, softmax_scale):
 
 
 def q_error(q):
-    """What the five-term form of a query row may leave of each element: 2^-14 of the largest magnitude of
-    its block of 16 (the last of five base-8 digits, the first of which counts in halves of the block's
-    power of two, is off by at most half a unit: 2^(E - 1 - 1 - 12) for a block in [2^E, 2^(E+1))), and no
+    """What the four-term form of a query row may leave of each element: 2^-11 of the largest magnitude of
+    its block of 16 (the last of four base-8 digits, the first of which counts in halves of the block's
+    power of two, is off by at most half a unit: 2^(E - 1 - 1 - 9) for a block in [2^E, 2^(E+1))), and no
     less than 2^-19 of the row's (a digit's scale is at least 2^-9 in a row brought to [2^8, 2^9))."""
     a = np.abs(q)
     block = np.repeat(a.reshape(D // G, G).max(-1), G)
-    return np.maximum(2.0 ** -14 * block, 2.0 ** -19 * a.max())
+    return np.maximum(2.0 ** -11 * block, 2.0 ** -19 * a.max())
 
 
 def allowed(out, mag, vmax, n, size, lost):
