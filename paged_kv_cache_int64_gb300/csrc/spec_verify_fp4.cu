@@ -122,7 +122,7 @@ struct alignas(16) Shared {
   uint64_t q_ready[4], q_free[2];                // Q of run s (buffer s % 2; barrier s % 4: Q may be 3 runs ahead of the softmax)
   uint64_t ks_ready[2];                          // K scales of a tile laid out
   uint64_t s_full[2], s_free[2];                 // S^T; s_free also means that the K scales are read
-  uint64_t sf_ready[2];                          // transposed V scales (and the V tile's place in tensor memory free)
+  uint64_t sf_ready[2], sf_free[2];              // transposed V scales
   uint64_t vt_ready[2];                          // V tile in tensor memory
   uint64_t p_full[2], pv_done[2];                // P^T written; PV of the tile complete (frees V tile and P^T)
   uint64_t drain;
@@ -432,6 +432,7 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
       mbar_init(&sh.s_full[b], 1);
       mbar_init(&sh.s_free[b], 4 * live_groups);
       mbar_init(&sh.sf_ready[b], 1);
+      mbar_init(&sh.sf_free[b], 8);
       mbar_init(&sh.vt_ready[b], 8);
       mbar_init(&sh.pv_done[b], 1);
       mbar_init(&sh.p_full[b], 4 * live_groups);
@@ -748,8 +749,7 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
       for (int j = 0; ok && j < run.n; ++j, ++i, ring.next()) {
         const int st = ring.st, b = i & 1;
         ok = warp_wait(&sh.v_full[st], ring.ph, abort, wl);
-        // PV_{i-2} is done: its V tile was converted (with these scales' last contents) and is read
-        if (ok && i >= 2) ok = warp_wait(&sh.pv_done[b], ((i >> 1) - 1) & 1, abort, wl);
+        if (ok && i >= 2) ok = warp_wait(&sh.sf_free[b], ((i >> 1) - 1) & 1, abort, wl);
         if (!ok) break;
         const uint4* src = reinterpret_cast<const uint4*>(smem + Gm::kOffV + st * kStage + kCodeTile);
         uint32_t w[4][4];
@@ -885,45 +885,45 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
     while (ok && next_run(p, cur, run)) {
       for (int j = 0; ok && j < run.n; ++j, ++i, ring.next()) {
         const int st = ring.st, b = i & 1;
-        // the scales' warp has waited for the codes and for the PV that read this V tile's place
-        ok = warp_wait(&sh.sf_ready[b], (i >> 1) & 1, abort, wl);
+        ok = warp_wait(&sh.sf_ready[b], (i >> 1) & 1, abort, wl);  // the scales' warp has waited for the codes
+        if (ok && i >= 2) ok = warp_wait(&sh.pv_done[b], ((i >> 1) - 1) & 1, abort, wl);  // the V tile's place is read
         if (!ok) break;
         tc_fence_after();
         const uint32_t codes = codes0 + st * kStage, tv = tv0 + b * 128;
         const uint8_t* sf = sf0 + b * Gm::kSfBuf;
         // 16 keys a step; the next step's codes and scales are read before this one's are converted
-        uint32_t w[4], w2[4];
-        uint4 s4[2], s42[2];
-        ldmatrix_t8_x2(codes, w);
-        s4[0] = *reinterpret_cast<const uint4*>(sf);
-        s4[1] = *reinterpret_cast<const uint4*>(sf + 16);
+        uint32_t w[2][4];
+        uint4 s4[2][2];
+        auto read = [&](int kb, int to) {
+          ldmatrix_t8_x2(codes + kb * 16 * 128, w[to]);
+          s4[to][0] = *reinterpret_cast<const uint4*>(sf + kb * 128);
+          s4[to][1] = *reinterpret_cast<const uint4*>(sf + kb * 128 + 16);
+        };
+        read(0, 0);
 #pragma unroll 1
-        for (int kb = 0; kb < 4; ++kb) {
-          const int nb = kb < 3 ? kb + 1 : 3;
-          ldmatrix_t8_x2(codes + nb * 16 * 128, w2);
-          s42[0] = *reinterpret_cast<const uint4*>(sf + nb * 128);
-          s42[1] = *reinterpret_cast<const uint4*>(sf + nb * 128 + 16);
+        for (int kb2 = 0; kb2 < 4; kb2 += 2) {
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {  // 16 bytes: two groups, eight bytes each
-            uint32_t o[8];
+          for (int h = 0; h < 2; ++h) {
+            const int kb = kb2 + h;
+            read(h ? (kb2 + 2) & 3 : kb + 1, h ^ 1);  // (the last one's is not used)
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              uint32_t v[4];
-              e2m1x8_to_f16(w[2 * x + g], v);
-              const uint32_t s01 = g ? s4[x].z : s4[x].x, s23 = g ? s4[x].w : s4[x].y;
-              const __half2 h01 = *reinterpret_cast<const __half2*>(&s01), h23 = *reinterpret_cast<const __half2*>(&s23);
-              const __half2 d[4] = {__low2half2(h01), __high2half2(h01), __low2half2(h23), __high2half2(h23)};
-              o[2 * g] = hmul2_u32(v[0], *reinterpret_cast<const uint32_t*>(&d[0]));
-              o[2 * g + 1] = hmul2_u32(v[1], *reinterpret_cast<const uint32_t*>(&d[1]));
-              o[4 + 2 * g] = hmul2_u32(v[2], *reinterpret_cast<const uint32_t*>(&d[2]));
-              o[4 + 2 * g + 1] = hmul2_u32(v[3], *reinterpret_cast<const uint32_t*>(&d[3]));
+            for (int x = 0; x < 2; ++x) {  // 16 bytes: two groups, eight bytes each
+              uint32_t o[8];
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {
+                uint32_t v[4];
+                e2m1x8_to_f16(w[h][2 * x + g], v);
+                const uint32_t s01 = g ? s4[h][x].z : s4[h][x].x, s23 = g ? s4[h][x].w : s4[h][x].y;
+                const __half2 h01 = *reinterpret_cast<const __half2*>(&s01), h23 = *reinterpret_cast<const __half2*>(&s23);
+                const __half2 d[4] = {__low2half2(h01), __high2half2(h01), __low2half2(h23), __high2half2(h23)};
+                o[2 * g] = hmul2_u32(v[0], *reinterpret_cast<const uint32_t*>(&d[0]));
+                o[2 * g + 1] = hmul2_u32(v[1], *reinterpret_cast<const uint32_t*>(&d[1]));
+                o[4 + 2 * g] = hmul2_u32(v[2], *reinterpret_cast<const uint32_t*>(&d[2]));
+                o[4 + 2 * g + 1] = hmul2_u32(v[3], *reinterpret_cast<const uint32_t*>(&d[3]));
+              }
+              tmem_st_16x256b_x2(tv + ((uint32_t)(16 * x) << 16) + kb * 16, o);
             }
-            tmem_st_16x256b_x2(tv + ((uint32_t)(16 * x) << 16) + kb * 16, o);
           }
-#pragma unroll
-          for (int x = 0; x < 4; ++x) w[x] = w2[x];
-          s4[0] = s42[0];
-          s4[1] = s42[1];
         }
         tmem_wait_st();
         tc_fence_before();
@@ -931,6 +931,7 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
         if (lane == 0) {
           mbar_arrive(&sh.vt_ready[b]);
           mbar_arrive(&sh.v_empty[st]);
+          mbar_arrive(&sh.sf_free[b]);
         }
       }
     }
