@@ -947,13 +947,15 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
     // the key's two rows of P^T (see V columns for the order of the keys): weights in the first kCols
     // columns of the first row, which meets the even elements, and in the last of the second
     const int prow = 2 * ((k & ~15) + ((k >> 1) & 1) * 8 + ((k & 15) >> 2) * 2 + (k & 1));
-    uint32_t p_off[2][kGC / 8];  // byte offsets of the group's chunks of 8 columns in the two rows
+    // byte offsets of the group's chunks of 8 columns in the two rows; both get the same weights, and every
+    // other pair of keys writes its second row first, so that a store's 8 lanes meet 8 bank groups
+    uint32_t p_off[2][kGC / 8];
 #pragma unroll
-    for (int odd = 0; odd < 2; ++odd)
+    for (int x = 0; x < 2; ++x)
 #pragma unroll
       for (int cc = 0; cc < kGC / 8; ++cc) {
-        const uint32_t r = prow + odd, chunk = odd * (kCols / 8) + grp * (kGC / 8) + cc;
-        p_off[odd][cc] = r * Gm::kPRow + ((chunk ^ (kCols == 16 ? (r >> 1) & 3u : r & 7u)) * 16);
+        const uint32_t odd = x ^ ((k >> 1) & 1), r = prow + odd, chunk = odd * (kCols / 8) + grp * (kGC / 8) + cc;
+        p_off[x][cc] = r * Gm::kPRow + ((chunk ^ (kCols == 16 ? (r >> 1) & 3u : r & 7u)) * 16);
       }
     auto load_scores = [&](uint32_t t, float (&x)[kGC]) {  // the two halves of the terms, added
 #pragma unroll
