@@ -5,6 +5,9 @@
 //
 // One lane holds one group: 8 bytes of codes and a scale byte in, 32 bytes out (one 256-bit store);
 // a warp covers the K row and the V row of one (position, head), four of them in flight.
+//
+// Bound by memory, four fifths of it the stores. Measured: 2.6 million pairs of rows 589 us, 5.8 TB/s in and
+// out (0.85 of the measured copy rate); 188,416 pairs 43 us (48 with a cold L2); the smallest calls 2.2 us.
 #include <cuda_bf16.h>
 
 #include "host_common.h"
@@ -138,7 +141,8 @@ extern "C" pkv_status pkv_kv_fp4_dequant_dense(
              scale_stride_blk, scale_stride_tok, scale_stride_head, block_table, bt_stride, max_blocks, pos_begin,
              pos_end, block_size, num_kv_heads, 0, static_cast<__nv_bfloat16*>(k_dense),
              static_cast<__nv_bfloat16*>(v_dense), max_ctx, dev_err};
-  // pairs of a warp: 4 in flight where there are enough for every warp the device holds, else 1
+  // pairs of a warp: 4 in flight where there are enough for every warp the device holds (2.6 million pairs:
+  // 590 us against 1,028 with one), else 1 (256 pairs: 2.1 us against 2.9 with four)
   const int64_t rows = (int64_t)max_tokens * num_kv_heads;
   const bool many = rows * num_reqs > kManyPairs;
   const int64_t per_cta = (int64_t)kWarps * (many ? 4 : 1);

