@@ -90,8 +90,8 @@ PKV_API int32_t pkv_abi_version(void);
 /*
  * testing_set_wait_limit_ns - a testing hook with no counterpart on the pages: the next attention
  * kernel launched by the calling host thread (pkv_paged_prefill_attn, pkv_paged_prefill_attn_fp8,
- * pkv_spec_verify_attn_partial, pkv_spec_verify_attn_partial_fp8) bounds each of its internal
- * waits by ns nanoseconds instead of the default one second; later launches use the default
+ * pkv_spec_verify_attn_partial, pkv_spec_verify_attn_partial_fp8, pkv_spec_verify_attn_fp4) bounds
+ * each of its internal waits by ns nanoseconds instead of the default one second; later launches use the default
  * again. ns = 0 keeps the default. With a bound far below the time a copy or an MMA takes, the
  * launch's CTAs give up at their first wait that is not already satisfied: each records
  * PKV_ERR_TIMEOUT in dev_err, waits (with its own bound) for the copies and MMAs it has in flight,
@@ -384,7 +384,9 @@ PKV_API pkv_status pkv_spec_verify_attn_noalloc(const void* q, const int8_t* k_c
  *   stride_tok, stride_head. Scales: k_bscale / v_bscale uint8 [num_blocks][block_size][num_kv_heads]
  *   [16], byte strides scale_stride_blk, scale_stride_tok, scale_stride_head. Bases 16-byte aligned,
  *   strides positive multiples of 16; every block-id x stride product is formed in 64 bits.
- * k_scale / v_scale: device pointers to one fp32 each, positive, finite and normal.
+ * k_scale / v_scale: device pointers to one fp32 each, positive, finite and normal. A scale byte's top
+ * bit is 0, as the write leaves it (the read-back takes it as the sign; what the attention gives for such
+ * a row is not specified).
  *
  * kv_cache_write_fp4 - quantize a chunk's new K and V rows and store them through the block table.
  *   Rows, positions, query_start_loc and max_q_len as for pkv_kv_cache_write (new rows 32-byte
@@ -436,16 +438,19 @@ PKV_API pkv_status pkv_kv_fp4_dequant_dense(const uint8_t* k_fp4, const uint8_t*
  * device (no split to choose, so a captured graph stays balanced as the sequences grow).
  *   q, out bf16 [num_reqs*T][num_q_heads][256], tokens and positions as for
  *   pkv_spec_verify_attn_partial: token t of request r sits at position seq_lens[r] - T + t and attends
- *   the keys up to it. out = softmax(softmax_scale q . k) v with fp32 scores, sums and accumulation;
- *   the probabilities meet V in fp16. A token before position 0 (seq_lens[r] < T, an empty request
- *   included) attends nothing and gives zeros.
+ *   the keys up to it. out = softmax(softmax_scale q . k) v with fp32 scores, sums and accumulation, on
+ *   the exact stored k and v. Two roundings are its own: the probabilities meet V in fp16, and a query
+ *   row meets K as a sum of four e2m1 rows with a scale per 16 elements, which leaves each element
+ *   within max(2^-11 of its 16's largest, 2^-19 of its row's largest) of q (a row whose largest is
+ *   below 2^-118: 2^-137 at most). A query row with an infinity or a NaN gives NaN. A token before position 0 (seq_lens[r] < T, an empty request included) attends
+ *   nothing and gives zeros. out must not overlap q.
  * Keys in a block whose id is out of range, or past the table, read as zero (k = v = 0) and
  * PKV_ERR_DEVICE_BOUNDS is recorded.
  * workspace: caller-owned device memory, 16-byte aligned, contents scratch; calls that may overlap on
  * the GPU (two streams, two graphs) need one each. pkv_spec_verify_fp4_workspace_bytes(n) bytes let n
  * CTAs run: pass the device's SM count; a smaller one (at least that of n = 1) runs on fewer SMs.
- * Requirements: num_q_heads / num_kv_heads <= 32; block_size a multiple of 8; q, out, caches, scale
- * caches and their strides 16-byte aligned.
+ * Requirements: num_q_heads / num_kv_heads <= 32; block_size a multiple of 8; max_blocks * block_size at
+ * most 2^31 - 128; q, out, caches, scale caches and their strides 16-byte aligned.
  */
 PKV_API size_t pkv_spec_verify_fp4_workspace_bytes(int32_t num_ctas);
 PKV_API pkv_status pkv_spec_verify_attn_fp4(const void* q, const uint8_t* k_fp4, const uint8_t* v_fp4,

@@ -333,6 +333,16 @@ def _cache4(k_fp4, v_fp4, k_bscale, v_bscale, k_scale, v_scale):
     return dev, (nb, cs[0], cs[1], cs[2], ss[0], ss[1], ss[2]), bs, hkv
 
 
+def _table(block_table, *vectors):
+    """The checked block table's requests, columns and row stride; vectors: its int32 companions."""
+    R, cols = block_table.shape
+    row, col = block_table.stride()
+    assert block_table.dtype is _I32 and (col == 1 or cols == 1), "int32 block_table [R][..], columns contiguous"
+    for t in vectors:
+        assert t.dtype is _I32 and t.dim() == 1 and t.is_contiguous(), "int32 vectors, contiguous, beside the block table"
+    return R, cols, row
+
+
 def _launch(fn, dev, stream, others, *args):
     """fn(*args, stream) with device `dev` current and, unless one is given, on its current stream; the
     tensors `others` must be on it."""
@@ -364,11 +374,10 @@ def kv_cache_write_fp4(k_new, v_new, block_table, seq_lens, query_start_loc, max
     _, heads, d = k_new.shape
     assert k_new.dtype is v_new.dtype is _BF16 and v_new.shape == k_new.shape and v_new.stride() == st and \
         heads == hkv and st[2] == 1 and st[1] == d, "new rows: bf16 [total][hkv][D], heads contiguous, K and V alike"
-    R, cols = block_table.shape
-    assert block_table.dtype is seq_lens.dtype is query_start_loc.dtype is _I32 and seq_lens.shape[0] == R and \
-        query_start_loc.shape[0] == R + 1, "int32 block_table [R][..], seq_lens [R], query_start_loc [R + 1]"
+    R, cols, row = _table(block_table, seq_lens, query_start_loc)
+    assert seq_lens.shape[0] == R and query_start_loc.shape[0] == R + 1, "seq_lens [R], query_start_loc [R + 1]"
     _launch(lib.pkv_kv_cache_write_fp4, dev, stream, (k_new, v_new, block_table, seq_lens, query_start_loc),
-            k_new.data_ptr(), v_new.data_ptr(), st[0], block_table.data_ptr(), block_table.stride(0), cols,
+            k_new.data_ptr(), v_new.data_ptr(), st[0], block_table.data_ptr(), row, cols,
             seq_lens.data_ptr(), query_start_loc.data_ptr(), R, int(max_q_len), k_fp4.data_ptr(), v_fp4.data_ptr(),
             k_bscale.data_ptr(), v_bscale.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *cache, bs, hkv, d,
             _err(dev_err, dev))
@@ -382,13 +391,12 @@ def kv_fp4_dequant_dense(k_fp4, v_fp4, k_bscale, v_bscale, block_table, pos_begi
     R, max_ctx, heads, d = k_dense.shape
     assert k_dense.dtype is v_dense.dtype is _BF16 and v_dense.shape == k_dense.shape and heads == hkv and \
         k_dense.is_contiguous() and v_dense.is_contiguous(), "dense rows: contiguous bf16 [R][max_ctx][hkv][256]"
-    assert block_table.dtype is pos_begin.dtype is pos_end.dtype is _I32 and \
-        block_table.shape[0] == pos_begin.shape[0] == pos_end.shape[0] == R, "int32 block_table [R][..], pos_begin, pos_end [R]"
+    reqs, cols, row = _table(block_table, pos_begin, pos_end)
+    assert reqs == pos_begin.shape[0] == pos_end.shape[0] == R, "block_table [R][..], pos_begin, pos_end [R]"
     _launch(lib.pkv_kv_fp4_dequant_dense, dev, stream, (block_table, pos_begin, pos_end, k_dense, v_dense),
             k_fp4.data_ptr(), v_fp4.data_ptr(), k_bscale.data_ptr(), v_bscale.data_ptr(), k_scale.data_ptr(),
-            v_scale.data_ptr(), *cache, block_table.data_ptr(), block_table.stride(0), block_table.shape[1],
-            pos_begin.data_ptr(), pos_end.data_ptr(), R, int(max_tokens), bs, hkv, d, k_dense.data_ptr(),
-            v_dense.data_ptr(), max_ctx, _err(dev_err, dev))
+            v_scale.data_ptr(), *cache, block_table.data_ptr(), row, cols, pos_begin.data_ptr(), pos_end.data_ptr(), R,
+            int(max_tokens), bs, hkv, d, k_dense.data_ptr(), v_dense.data_ptr(), max_ctx, _err(dev_err, dev))
 
 
 def spec_verify_fp4_workspace_bytes(num_ctas=None) -> int:
@@ -404,14 +412,14 @@ def spec_verify_attn_fp4(q, k_fp4, v_fp4, k_bscale, v_bscale, k_scale, v_scale, 
     [R*T][Hq][256]. workspace: a CUDA byte tensor of spec_verify_fp4_workspace_bytes() bytes, one for each
     stream or graph whose calls may overlap."""
     dev, cache, bs, hkv = _cache4(k_fp4, v_fp4, k_bscale, v_bscale, k_scale, v_scale)
-    R, cols = block_table.shape
+    R, cols, row = _table(block_table, seq_lens)
     rows, hq, d = q.shape
     assert q.dtype is out.dtype is _BF16 and out.shape == q.shape and rows == R * T and q.is_contiguous() and \
         out.is_contiguous(), "q and out: contiguous bf16 [R*T][Hq][256]"
-    assert block_table.dtype is seq_lens.dtype is _I32 and seq_lens.shape[0] == R, "int32 block_table [R][..], seq_lens [R]"
+    assert seq_lens.shape[0] == R, "seq_lens [R]"
     assert workspace.is_contiguous(), "workspace must be a contiguous CUDA tensor"
     _launch(lib.pkv_spec_verify_attn_fp4, dev, stream, (q, block_table, seq_lens, out, workspace), q.data_ptr(),
             k_fp4.data_ptr(), v_fp4.data_ptr(), k_bscale.data_ptr(), v_bscale.data_ptr(), k_scale.data_ptr(),
-            v_scale.data_ptr(), *cache, block_table.data_ptr(), block_table.stride(0), cols, seq_lens.data_ptr(), R,
+            v_scale.data_ptr(), *cache, block_table.data_ptr(), row, cols, seq_lens.data_ptr(), R,
             int(T), hq, hkv, d, bs, float(softmax_scale), out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
             _err(dev_err, dev))

@@ -1315,6 +1315,9 @@ extern "C" pkv_status pkv_spec_verify_attn_fp4(
   const int group = num_q_heads / num_kv_heads;
   PKV_UNSUP(group <= kMaxCols, "%s: num_q_heads / num_kv_heads must be at most %d (got %d)", name, kMaxCols, group);
   PKV_UNSUP(block_size % 8 == 0, "%s: block_size must be a multiple of 8", name);
+  // (positions of a whole last tile stay below 2^31)
+  PKV_UNSUP((int64_t)max_blocks * block_size <= (1ll << 31) - kBN, "%s: the table's columns reach past 2^31 - %d positions",
+            name, kBN);
   PKV_ARG(stride_blk > 0 && stride_tok > 0 && stride_head > 0 && scale_stride_blk > 0 && scale_stride_tok > 0 &&
               scale_stride_head > 0,
           "%s: strides must be positive", name);

@@ -115,6 +115,7 @@ def test_read_refuses(pkv, kw, status):
     (dict(bs=20), 2),                        # block_size not a multiple of 8
     (dict(q=72), 1), (dict(out=72), 1), (dict(ws=72), 1), (dict(wsb=1024), 1),
     (dict(scale=0.0), 1), (dict(scale=float("nan")), 1), (dict(R=1 << 30, T=1 << 20), 1),
+    (dict(mb=1 << 27, bts=1 << 27), 2),      # table columns past 2^31 - 128 positions
 ])
 def test_attend_refuses(pkv, kw, status):
     assert _attend(pkv, **kw) == status and pkv.lib.pkv_last_error()

@@ -433,6 +433,107 @@ def test_attend_same_bits_again_and_for_other_blocks(pkv, ws):
     assert np.array_equal(first, attend(pkv, c, q, 3, 1 / 16, ws))
 
 
+@pytest.mark.parametrize("T,hkv,group", [(1, 100, 2), (64, 4, 32), (33, 3, 5)])
+def test_attend_more_rows_than_ctas(pkv, ws, T, hkv, group):
+    """Column groups that do not fill the SMs evenly, and more of them than SMs: one line of all of them."""
+    run_attend(pkv, ws, [150, 70], T, hkv, group, 16, seed=hkv)
+
+
+def test_attend_every_code_and_scale(pkv, ws):
+    """Keys and values of random codes under every scale that is not negative or NaN, subnormal ones and
+    zero among them."""
+    b = Batch([508], 1, 16, seed=97)
+    blk, slot = b.where(0, np.arange(508))
+    for w in ("k", "v"):
+        b.codes[w][blk, slot] = b.rng.integers(0, 256, (508, 1, 128))
+        b.sb[w][blk, slot] = ((np.arange(508)[:, None, None] + 8 * np.arange(16)) % 127).astype(np.uint8)
+    for T, scale in ((1, 1e-3), (8, 1e-3), (8, 0.2)):
+        q = queries(b.rng, T, 4)
+        check(attend(pkv, b, q, T, scale, ws), *reference(b, q, T, 4, scale))
+
+
+def test_attend_query_rows_of_zero_and_infinity(pkv, ws):
+    """A zero row weighs its keys alike; a row with an infinity is NaN and leaves the others as they are."""
+    b = Batch([500], 2, 16, seed=98)
+    q = queries(b.rng, 3, 8)
+    q[1, 2], q[2, 5] = 0, 0x8000
+    q[0, 1], q[0, 6] = 1, 0x0080  # the smallest subnormal, the smallest normal number
+    want = attend(pkv, b, q, 3, 1 / 16, ws)
+    check(want, *reference(b, q, 3, 4, 1 / 16))
+    bad = q.copy()
+    bad[1, 0, 17], bad[2, 7, 255] = 0x7F80, 0xFF80
+    got = attend(pkv, b, bad, 3, 1 / 16, ws)
+    assert np.isnan(got[1, 0]).all() and np.isnan(got[2, 7]).all()
+    got[1, 0], got[2, 7] = want[1, 0], want[2, 7]
+    check(got, *reference(b, q, 3, 4, 1 / 16))
+
+
+def test_attend_requests_that_share_blocks(pkv, ws):
+    """The same blocks in two requests' tables, and twice in one."""
+    b = Batch([300, 300, 300], 2, 16, seed=99)
+    b.bt[1, :10] = b.bt[0, :10]
+    b.bt[2, 1:12] = b.bt[2, 0]
+    q = queries(b.rng, 3 * 2, 8)
+    check(attend(pkv, b, q, 2, 1 / 16, ws), *reference(b, q, 2, 4, 1 / 16))
+
+
+def test_attend_graphs_that_take_turns_with_a_workspace(pkv, ws):
+    """Two graphs over the same workspace and tables, one after the other on a stream, with an eager call of
+    another shape between them; the lengths change between the rounds."""
+    b = Batch([900, 2000, 40], 2, 16, seed=103)
+    caches, scales, bt, sl = b.device()
+    calls = []
+    for T, group in ((1, 4), (8, 4), (3, 2)):
+        q = queries(b.rng, 3 * T, 2 * group)
+        calls.append((T, group, q, u16_to_bf16(q).to(DEV)))
+    outs = [torch.empty_like(c[3]) for c in calls]
+
+    def call(i):
+        T, _, _, qd = calls[i]
+        pkv.spec_verify_attn_fp4(qd, *caches, *scales, bt, sl, T, 1 / 16, outs[i], ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for i in range(3):
+            call(i)
+    torch.cuda.synchronize()
+    graphs = []
+    for i in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            call(i)
+    for lens in ([900, 2000, 40], [1, 1500, 39], [0, 8, 0]):
+        sl.copy_(torch.tensor(lens, dtype=torch.int32))
+        for o in outs:
+            o.fill_(float("nan"))
+        graphs[0].replay()
+        call(2)
+        graphs[1].replay()
+        torch.cuda.synchronize()
+        b.lens = lens
+        for (T, group, q, _), o in zip(calls, outs):
+            check(F.bf16_to_f32(bf16_to_u16(o)).astype(np.float64), *reference(b, q, T, group, 1 / 16))
+
+
+def test_refuses_strided_index_tensors(pkv, ws):
+    b = Batch([40, 40], 1, 16, seed=104)
+    caches, scales, bt, sl = b.device()
+    q = torch.zeros(2, 4, 256, dtype=torch.bfloat16, device=DEV)
+    dense = [torch.zeros(2, 64, 1, 256, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    new = [torch.zeros(2, 1, 256, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    qsl = torch.tensor([0, 1, 2], dtype=torch.int32, device=DEV)
+    wide = sl.repeat_interleave(2)[::2]
+    for table, lens in ((bt.t().contiguous().t(), sl), (bt, wide), (bt, sl.long())):
+        with pytest.raises(AssertionError):
+            pkv.spec_verify_attn_fp4(q, *caches, *scales, table, lens, 1, 1 / 16, torch.empty_like(q), ws)
+        with pytest.raises(AssertionError):
+            pkv.kv_fp4_dequant_dense(*caches, table, lens, lens, 40, *scales, *dense)
+        with pytest.raises(AssertionError):
+            pkv.kv_cache_write_fp4(*new, table, lens, qsl, 1, *caches, *scales)
+    torch.cuda.synchronize()
+
+
 @pytest.mark.parametrize("ctas", [1, 2, 7, 100])
 def test_attend_small_workspace(pkv, ctas):
     small = torch.empty(pkv.spec_verify_fp4_workspace_bytes(ctas), dtype=torch.uint8, device=DEV)
