@@ -89,17 +89,6 @@ struct PairWalk {
   }
 };
 
-// Pairs of a warp: as many as leave kPairWarps warps to the device (twice what it holds at a time), at
-// most kPairsMost. Long walks spread a warp's start (launch, lengths, table: three dependent loads)
-// over more rows; short ones are all that small calls have. The write of 570,184 pairs: 143 us, 357
-// with one pair a warp; of 8,192 pairs: 5.7 us, 8.1 with 16.
-constexpr int64_t kPairWarps = 152 * 64;
-constexpr int64_t kPairsMost = 16;
-inline int32_t pairs_per_warp(int64_t pairs) {
-  const int64_t per = (pairs + kPairWarps - 1) / kPairWarps;
-  return (int32_t)(per < 1 ? 1 : per > kPairsMost ? kPairsMost : per);
-}
-
 // 32 contiguous bytes, 32-byte aligned, as one access.
 struct alignas(32) Bytes32 {
   uint32_t w[8];

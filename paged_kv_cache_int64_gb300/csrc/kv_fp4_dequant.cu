@@ -6,8 +6,8 @@
 // One lane holds one group: 8 bytes of codes and a scale byte in, 32 bytes out (one 256-bit store);
 // a warp covers the K row and the V row of one (position, head), four of them in flight.
 //
-// Bound by memory, four fifths of it the stores. Measured: 2.6 million pairs of rows 589 us, 5.8 TB/s in and
-// out (0.85 of the measured copy rate); 188,416 pairs 43 us (48 with a cold L2); the smallest calls 2.2 us.
+// Bound by memory, four fifths of it the stores. Measured: 2.6 million pairs of rows 553 us, 6.2 TB/s in and
+// out (0.91 of the measured copy rate); 188,416 pairs 42 us (46 with a cold L2); the smallest calls 2.0 us.
 #include <cuda_bf16.h>
 
 #include "host_common.h"
@@ -18,6 +18,7 @@ namespace pkv {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kCtas = 16;  // of an SM: all the warps it holds, 32 registers (553 us below; 589 without the bound)
 constexpr int64_t kManyPairs = 152 * 64 * 4;
 
 struct ReadArgs {
@@ -42,7 +43,7 @@ struct ReadArgs {
 };
 
 template <int kPairs>
-__global__ void __launch_bounds__(kWarps * 32) kv_fp4_dequant_kernel(const ReadArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, kCtas) kv_fp4_dequant_kernel(const ReadArgs a) {
   const int r = blockIdx.x / a.chunks;
   const int chunk = blockIdx.x - r * a.chunks;
   const int lane = threadIdx.x & 31;
@@ -142,7 +143,8 @@ extern "C" pkv_status pkv_kv_fp4_dequant_dense(
              pos_end, block_size, num_kv_heads, 0, static_cast<__nv_bfloat16*>(k_dense),
              static_cast<__nv_bfloat16*>(v_dense), max_ctx, dev_err};
   // pairs of a warp: 4 in flight where there are enough for every warp the device holds (2.6 million pairs:
-  // 590 us against 1,028 with one), else 1 (256 pairs: 2.1 us against 2.9 with four)
+  // 590 us against 1,028 with one, before all warps were resident; three 609, five 593 against 553 since), else 1
+  // (256 pairs: 2.1 us against 2.9 with four)
   const int64_t rows = (int64_t)max_tokens * num_kv_heads;
   const bool many = rows * num_reqs > kManyPairs;
   const int64_t per_cta = (int64_t)kWarps * (many ? 4 : 1);

@@ -14,8 +14,8 @@
 // the correctly rounded quotient at less than half the price of 16 divisions; groups where an
 // intermediate could overflow or underflow take the division itself.
 //
-// Measured (pairs of a K and a V row of 256): 570,184 pairs 143 us, 5.2 TB/s in and out; 8,192 pairs 5.7
-// us; the smallest calls 2.2 to 2.6 us, launch and three dependent loads. Large calls are bound by the
+// Measured (pairs of a K and a V row of 256): 570,184 pairs 137 us, 5.5 TB/s in and out; 8,192 pairs 4.6
+// us; the smallest calls 2.2 to 2.5 us, launch and three dependent loads. Large calls are bound by the
 // instructions of the conversion, small ones by latency.
 #include <cuda_bf16.h>
 
@@ -28,6 +28,20 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kDepth = 2;  // (token, head) pairs a warp has in flight
+// CTAs of an SM: 64 registers, one more warp of four to a scheduler than without the bound (570,184 pairs:
+// 137 us against 143; three pairs in flight instead 146, ten CTAs 141)
+constexpr int kCtas = 8;
+
+// Pairs of a warp: as many as leave the device the warps that it holds, at most 16. Long walks spread a
+// warp's start (launch, lengths, table: three dependent loads) over more rows; short ones are all that
+// small calls have (570,184 pairs: 137 us with 16, 139 with 12, 357 with one; 8,192 pairs: 4.6 us with
+// two, 5.5 with one, 8.1 with 16).
+constexpr int64_t kDeviceWarps = 152 * kCtas * kWarps;
+constexpr int64_t kPairsMost = 16;
+int32_t pairs_per_warp(int64_t pairs) {
+  const int64_t per = (pairs + kDeviceWarps - 1) / kDeviceWarps;
+  return (int32_t)(per < 1 ? 1 : per > kPairsMost ? kPairsMost : per);
+}
 
 struct WriteArgs {
   const __nv_bfloat16* k_new;
@@ -103,7 +117,7 @@ __device__ __forceinline__ uint2 quantize_group(const Bytes32& in, float g, floa
   return make_uint2(c[0], c[1]);
 }
 
-__global__ void __launch_bounds__(kWarps * 32) kv_fp4_write_kernel(const WriteArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, kCtas) kv_fp4_write_kernel(const WriteArgs a) {
   const int r = blockIdx.x / a.chunks;
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
