@@ -32,9 +32,9 @@
 // Roles: warps 0 and 6 TMA producers of K and V; 1 QK issuer; 2 PV issuer; 3 V scales; 4-5 Q; 7 K scales;
 // 8-15 V columns; 16-23 softmax, a warpgroup for half the columns.
 //
-// Measured (4 KV heads, 16 query heads): one token, 32 requests of up to 16,384 keys 81 us (3.2
-// TB/s of cache); one token, one request of 262,144 keys 65 us (4.6 TB/s); eight tokens, 32 requests of
-// up to 40,960 keys 195 us (3.8 TB/s); one token, one request of 1,024 keys 15.7 us. No unit is above a
+// Measured (4 KV heads, 16 query heads): one token, 32 requests of up to 16,384 keys 68 us (3.9
+// TB/s of cache); one token, one request of 262,144 keys 64 us (4.7 TB/s); eight tokens, 32 requests of
+// up to 40,960 keys 195 us (3.8 TB/s); one token, one request of 1,024 keys 15 us. No unit is above a
 // half (issue slots 48 %, tensor pipe 22 %): a tile passes through scores, exponentials, vote, weights and
 // back in about 1,800 (kCols 16) or 2,300 clocks (32) of latencies, of which the double buffers overlap
 // two tiles.
@@ -636,13 +636,29 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
           tma_load_4d(stage + kCodeTile, maps + 3, full, 0, c_kvh, s0, b0);
         }
       } else {
+        // segments in batches: their places by shuffles first, then one lane issues the batch's copies, 65
+        // clocks each (a segment at a time: 136; one token, 32 requests of up to 16,384 keys in pages of 16: 68 us
+        // against 81)
+        constexpr int kBatch = 8;
 #pragma unroll 1
-        for (int g = 0; g < nseg; ++g) {
-          const int b = __shfl_sync(0xffffffffu, c_blk, g), s = __shfl_sync(0xffffffffu, c_slot, g);
-          if (b >= 0 && elect_one()) {
-            tma_load_4d(stage + g * G * kFp4RowBytes, maps, full, 0, c_kvh, s, b);
-            tma_load_4d(stage + kCodeTile + g * G * kFp4Groups, maps + 1, full, 0, c_kvh, s, b);
+        for (int g0 = 0; g0 < nseg; g0 += kBatch) {
+          int sb[kBatch], ss[kBatch];
+#pragma unroll
+          for (int g = 0; g < kBatch; ++g) {
+            sb[g] = __shfl_sync(0xffffffffu, c_blk, g0 + g);
+            ss[g] = __shfl_sync(0xffffffffu, c_slot, g0 + g);
           }
+          uint8_t* const codes = stage + g0 * G * kFp4RowBytes;
+          uint8_t* const scales = stage + kCodeTile + g0 * G * kFp4Groups;
+          if (elect_one()) {
+#pragma unroll
+            for (int g = 0; g < kBatch; ++g)
+              if (sb[g] >= 0) {  // (-1 past the tile's segments)
+                tma_load_4d(codes + g * G * kFp4RowBytes, maps, full, 0, c_kvh, ss[g], sb[g]);
+                tma_load_4d(scales + g * G * kFp4Groups, maps + 1, full, 0, c_kvh, ss[g], sb[g]);
+              }
+          }
+          __syncwarp();
         }
       }
       __syncwarp();
@@ -1330,8 +1346,8 @@ extern "C" pkv_status pkv_spec_verify_attn_fp4(
   PKV_ARG(workspace_bytes >= (int64_t)sizeof(CtaWorkspace), "%s: the workspace needs at least %zu bytes", name,
           sizeof(CtaWorkspace));
   Params p{};
-  // columns of a CTA: 16 when a KV head's query rows fit (half the padding, and half the softmax: 81 us
-  // against 86 with 32 for one token over 32 requests of up to 16,384, 65 against 76 over one of 262,144),
+  // columns of a CTA: 16 when a KV head's query rows fit (half the padding, and half the softmax: one
+  // token over 32 requests of up to 16,384: 81 us against 86 with 32, over one of 262,144: 65 against 76),
   // else 32, the tokens spread over column groups that read the same keys
   const bool narrow = (int64_t)T * group <= 16;
   p.tpc = T < kMaxCols / group ? T : kMaxCols / group;
