@@ -33,11 +33,12 @@
 // 8-15 V columns; 16-23 softmax, a warpgroup for half the columns.
 //
 // Measured (4 KV heads, 16 query heads): one token, 32 requests of up to 16,384 keys 68 us (3.9
-// TB/s of cache); one token, one request of 262,144 keys 64 us (4.7 TB/s); eight tokens, 32 requests of
-// up to 40,960 keys 195 us (3.8 TB/s); one token, one request of 1,024 keys 15 us. No unit is above a
+// TB/s of cache); one token, one request of 262,144 keys 62 us (4.9 TB/s); eight tokens, 32 requests of
+// up to 40,960 keys 195 us (3.8 TB/s); one token, one request of 1,024 keys 14.3 us. No unit is above a
 // half (issue slots 48 %, tensor pipe 22 %): a tile passes through scores, exponentials, vote, weights and
 // back in about 1,800 (kCols 16) or 2,300 clocks (32) of latencies, of which the double buffers overlap
-// two tiles.
+// two tiles. About 13 us of every call are none of its tiles': 3 until the range is known, 2 to 3 until the
+// first tile has come, 2 through it, then the launch of the merge and its two or three turns of loads.
 #include <cuda_bf16.h>
 
 #include "host_common.h"
@@ -65,21 +66,24 @@ constexpr float kUnset = -3e38f;          // running maximum of a column that ha
 constexpr float kStart = 8.0f;            // a new maximum's weight is 2^8; the maximum moves when a thread's
 constexpr float kMove = 32768.0f;         // weights of one key add up to more than this (fp16 ends at 65,504)
 
-// Workspace of a CTA: two slots (0: the piece that began before it, 1: the piece that goes on after
-// it) of O [kMaxCols][256], m and l [kMaxCols], and a note for the merge.
-struct Slot {
-  float o[kMaxCols][kFp4D];
-  float m[kMaxCols], l[kMaxCols];
-};
+// Workspace of n CTAs: their notes for the merge, [n]; the sums and maxima (log2) of two slots of each (0: the
+// piece that began before it, 1: the piece that goes on after it), [n][2][kMaxCols]; the slots' O, [n][2][live
+// columns][256]. Close together: with a CTA's whole share in one place the merge's loads met a page each.
 struct Note {
-  int32_t pieces, r, unit;  // pieces: CTAs of the line that hold the unit (0: none begins here and goes on)
-  int32_t pad[29];
+  int32_t pieces, r, unit, pad;  // pieces: CTAs of the line that hold the unit (0: none begins here and goes on)
 };
-struct CtaWorkspace {
-  Slot slot[2];
-  Note note;
+constexpr size_t kWorkspaceOfCta = sizeof(Note) + 2 * kMaxCols * (sizeof(float2) + kFp4D * sizeof(float));
+static_assert(sizeof(Note) == 16 && kWorkspaceOfCta % 16 == 0, "workspace of a CTA");
+struct Workspace {
+  Note* notes;
+  float2* lm;
+  float* o;
+  __host__ __device__ Workspace(void* base, int n) {
+    notes = static_cast<Note*>(base);
+    lm = reinterpret_cast<float2*>(notes + n);
+    o = reinterpret_cast<float*>(lm + (size_t)n * 2 * kMaxCols);
+  }
 };
-static_assert(sizeof(CtaWorkspace) % 16 == 0, "workspace of a CTA");
 
 template <int kCols>
 struct Geo {
@@ -161,7 +165,7 @@ struct Params {
   int32_t lines, units, ctas;      // lines; units of a request in a line; CTAs of a line
   float scale_log2;
   __nv_bfloat16* out;
-  CtaWorkspace* ws;
+  void* ws;
   int* dev_err;
   uint64_t wait_limit_ns;
 };
@@ -408,6 +412,7 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int line = blockIdx.x % p.lines, cta = blockIdx.x / p.lines;
   const int nq_max = p.tpc * p.group;
+  const Workspace ws(p.ws, (int)gridDim.x);
 
   // ------------------------------------------------------------------ barriers, tensor memory, range
   if (warp == 2) {
@@ -518,7 +523,7 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
       if (at < end && end <= next) {
         // for the merge: does the unit of the last tile begin in this range and go on past it?
         const int64_t u = p.units == 1 ? 0 : (end - 1 - at) / t_req, unit_begin = at + u * t_req, unit_end = unit_begin + t_req;
-        Note& note = p.ws[blockIdx.x].note;
+        Note& note = ws.notes[blockIdx.x];
         note.r = base + tid;
         note.unit = p.lines > 1 ? line : (int)u;
         // its last CTA: the first whose range ends at or after the unit's end
@@ -528,8 +533,8 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
       if (before * p.units >= end || base + kThreads >= p.num_reqs) break;  // CTA-uniform
     }
   } else {  // nothing to do (fewer tiles than CTAs): the merge may still pass by
-    if (tid == 0) p.ws[blockIdx.x].note.pieces = 0;
-    if (tid < kMaxCols) p.ws[blockIdx.x].slot[0].l[tid] = 0.0f;
+    if (tid == 0) ws.notes[blockIdx.x].pieces = 0;
+    if (tid < kMaxCols) ws.lm[(size_t)blockIdx.x * 2 * kMaxCols + tid].x = 0.0f;
   }
   __syncthreads();
   const Cursor start{sh.r0, sh.u0, sh.t00, sh.r0 >= 0 ? end - begin : 0};
@@ -537,7 +542,6 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
   volatile int* const abort = &sh.abort;
   const uint64_t wl = p.wait_limit_ns;
   const int G = p.seg;
-  CtaWorkspace& ws = p.ws[blockIdx.x];
 
   auto q_rows = [&](const Run& run, int unit) {  // the unit's first query row
     return reinterpret_cast<const uint4*>(p.q) +
@@ -1120,7 +1124,7 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
       // the segment's sums and O
       if (ok) ok = warp_wait(&sh.pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, abort, wl);
       const bool whole = run.n == run.tiles;
-      Slot& slot = ws.slot[run.t0 > 0 ? 0 : 1];
+      const size_t slot = (size_t)blockIdx.x * 2 + (run.t0 > 0 ? 0 : 1);
       {
         const float part = reduce_columns<kGC, false>(l, lane);
         if (lane < kGC) sh.red[grp][quarter][lane] = part;
@@ -1130,8 +1134,7 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
         const float sum = sh.red[grp][0][lane] + sh.red[grp][1][lane] + sh.red[grp][2][lane] + sh.red[grp][3][lane];
         sh.fin[c0 + lane] = whole ? (sum == 0.0f ? 0.0f : vg / sum) : 1.0f;
         if (!whole && ok) {
-          slot.m[c0 + lane] = -m[lane];
-          slot.l[c0 + lane] = sum;
+          ws.lm[slot * kMaxCols + c0 + lane] = make_float2(sum, -m[lane]);
         }
       }
       group_sync(bar_id);
@@ -1168,7 +1171,7 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
             if (whole)
               reinterpret_cast<uint32_t*>(p.out + (row0 + sh.row_off[c]) * kFp4D)[k] = pack_bf16x2(x0 * sh.fin[c], x1 * sh.fin[c]);
             else
-              reinterpret_cast<float2*>(slot.o[c])[k] = make_float2(x0, x1);
+              reinterpret_cast<float2*>(ws.o + (slot * nq_max + c) * kFp4D)[k] = make_float2(x0, x1);
           }
         }
         tc_fence_before();
@@ -1203,67 +1206,101 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
 // ------------------------------------------------------------------------------------------
 // merge of the pieces of a unit that several CTAs worked on
 // ------------------------------------------------------------------------------------------
-// Block (b, y): CTA b's note says whether a unit began in its range and went on; two warps a column (128
-// elements each) add its pieces up: M = max m, out = v_scale sum 2^(m - M) O / sum 2^(m - M) l. The
-// first 16 pieces are loaded before their weights are known; a piece without a key (l = 0: its range
-// is empty, or the column sees none of its keys) may hold anything and counts as nothing.
-__global__ void __launch_bounds__(256)
-    spec_verify_fp4_merge_kernel(const CtaWorkspace* __restrict__ ws, int32_t lines, int32_t T, int32_t group,
-                                 int32_t num_q_heads, int32_t tpc, int32_t n_tg, const float* __restrict__ v_scale,
+// Block (b, y): CTA b's note says whether a unit began in its range and went on; kP * kH warps a column, each
+// every kP-th piece and one of kH parts of the row, add its pieces up: M = max m, out = v_scale sum 2^(m - M) O
+// / sum 2^(m - M) l. The first pieces are loaded before their weights are known; a piece without a key
+// (l = 0: its range is empty, or the column sees none of its keys) may hold anything and counts as
+// nothing.
+template <int kP, int kH>
+__global__ void __launch_bounds__(256, 4)
+    spec_verify_fp4_merge_kernel(const Workspace ws, int32_t lines, int32_t T, int32_t group, int32_t num_q_heads,
+                                 int32_t tpc, int32_t n_tg, const float* __restrict__ v_scale,
                                  __nv_bfloat16* __restrict__ out) {
+  constexpr int kCol = 8 / (kP * kH), kF = 2 / kH, kBatch = 4;  // columns; float4 a lane; pieces in flight
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Note& note = ws[blockIdx.x].note;
-  const int pieces = note.pieces;
+  const int4 note = __ldg(reinterpret_cast<const int4*>(ws.notes + blockIdx.x));
+  const int pieces = note.x, unit = note.z;
   if (pieces == 0) return;
-  const int lane = threadIdx.x & 31, half = (threadIdx.x >> 5) & 1, col = blockIdx.y * 4 + (threadIdx.x >> 6);
-  const int unit = note.unit, t_base = (unit % n_tg) * tpc;
-  if (col >= min(tpc, T - t_base) * group) return;
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) % (kP * kH), c = (threadIdx.x >> 5) / (kP * kH);
+  const int first = kH == 2 ? 0 : w, part_of_row = kH == 2 ? w : 0;
+  const int cols = tpc * group, y = blockIdx.y * kCol + c, col = min(y, cols - 1);
   // piece i > 0 is slot 0 of the i-th CTA after this one in the line
-  const CtaWorkspace* first = ws + blockIdx.x;
-  auto slot = [&](int i) -> const Slot& { return i == 0 ? first->slot[1] : first[(int64_t)i * lines].slot[0]; };
-  constexpr int kBatch = 16;
-  float4 o[kBatch];
+  auto slot = [&](int i) -> size_t { return i == 0 ? (size_t)blockIdx.x * 2 + 1 : ((size_t)blockIdx.x + (size_t)i * lines) * 2; };
+  auto load_lm = [&](int i) { return i < pieces ? __ldg(ws.lm + slot(i) * kMaxCols + col) : make_float2(0, 0); };
+  float4 o[kBatch][kF];
   auto load = [&](int base) {
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i)
-      o[i] = base + i < pieces ? __ldg(reinterpret_cast<const float4*>(slot(base + i).o[col]) + half * 32 + lane)
-                               : make_float4(0, 0, 0, 0);
+    for (int i = 0; i < kBatch; ++i) {
+      const int at = base + first + kP * i;
+      const float4* src = reinterpret_cast<const float4*>(ws.o + (slot(at) * cols + col) * kFp4D) + part_of_row * 32 + lane;
+#pragma unroll
+      for (int h = 0; h < kF; ++h) o[i][h] = at < pieces ? __ldg(src + 32 * h) : make_float4(0, 0, 0, 0);
+    }
   };
+  const float2 lm0 = load_lm(lane);
   load(0);
-  const float l0 = lane < pieces ? slot(lane).l[col] : 0.0f, m0 = lane < pieces ? slot(lane).m[col] : 0.0f;
-  float M = l0 != 0.0f ? m0 : -INFINITY;
-  for (int i = 32 + lane; i < pieces; i += 32)
-    if (slot(i).l[col] != 0.0f) M = fmaxf(M, slot(i).m[col]);
+  float M = lm0.x != 0.0f ? lm0.y : -INFINITY;
+  for (int i = 32 + lane; i < pieces; i += 32) {
+    const float2 lm = load_lm(i);
+    if (lm.x != 0.0f) M = fmaxf(M, lm.y);
+  }
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-  float4 acc = make_float4(0, 0, 0, 0);
+  float4 acc[kF];
+#pragma unroll
+  for (int h = 0; h < kF; ++h) acc[h] = make_float4(0, 0, 0, 0);
   float L = 0.0f;
   for (int base = 0; base < pieces; base += 32) {  // lane = piece
-    const float l = base == 0 ? l0 : base + lane < pieces ? slot(base + lane).l[col] : 0.0f;
-    const float m = base == 0 ? m0 : base + lane < pieces ? slot(base + lane).m[col] : 0.0f;
-    const float w = l != 0.0f ? exp2f(m - M) : 0.0f;
-    float wl = w * l;
+    const float2 lm = base == 0 ? lm0 : load_lm(base + lane);
+    const float weight = lm.x != 0.0f ? exp2f(lm.y - M) : 0.0f;
+    const uint32_t live = __ballot_sync(0xffffffffu, lm.x != 0.0f);
+    float wl = weight * lm.x;
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) wl += __shfl_xor_sync(0xffffffffu, wl, x);
     L += wl;
-    for (int b = base; b < min(base + 32, pieces); b += kBatch) {
+    for (int b = base; b < min(base + 32, pieces); b += kP * kBatch) {
       if (b > 0) load(b);
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const float wi = __shfl_sync(0xffffffffu, w, b - base + i);
-        const bool live = wi != 0.0f;
-        acc.x += live ? wi * o[i].x : 0.0f;
-        acc.y += live ? wi * o[i].y : 0.0f;
-        acc.z += live ? wi * o[i].z : 0.0f;
-        acc.w += live ? wi * o[i].w : 0.0f;
+        const int at = b - base + first + kP * i;
+        const float wi = __shfl_sync(0xffffffffu, weight, at);
+        const bool counts = (live >> at) & 1u;
+#pragma unroll
+        for (int h = 0; h < kF; ++h) {
+          acc[h].x += counts ? wi * o[i][h].x : 0.0f;
+          acc[h].y += counts ? wi * o[i][h].y : 0.0f;
+          acc[h].z += counts ? wi * o[i][h].z : 0.0f;
+          acc[h].w += counts ? wi * o[i][h].w : 0.0f;
+        }
       }
     }
   }
+  float4 sum = acc[0];
+  int e = part_of_row * 32 + lane;  // this thread's four elements
+  if constexpr (kP > 1) {
+    static_assert(kP == 4 && kH == 1, "a warp finishes a quarter of the row, half its lanes at work");
+    __shared__ float4 part[kCol][kP][64];
+    part[c][w][lane] = acc[0];
+    part[c][w][32 + lane] = acc[1];
+    __syncthreads();
+    if (lane >= 16) return;
+    e = w * 16 + lane;
+    sum = part[c][0][e];
+#pragma unroll
+    for (int x = 1; x < kP; ++x) {
+      const float4 v = part[c][x][e];
+      sum.x += v.x;
+      sum.y += v.y;
+      sum.z += v.z;
+      sum.w += v.w;
+    }
+  }
+  const int t_base = (unit % n_tg) * tpc;
+  if (y >= min(tpc, T - t_base) * group) return;
   const float f = L == 0.0f ? 0.0f : __ldg(v_scale) / L;
   const int t = t_base + col / group;
-  const int64_t row = ((int64_t)note.r * T + t) * num_q_heads + (int64_t)(unit / n_tg) * group + col % group;
-  reinterpret_cast<uint2*>(out + row * kFp4D)[half * 32 + lane] =
-      make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+  const int64_t row = ((int64_t)note.y * T + t) * num_q_heads + (int64_t)(unit / n_tg) * group + col % group;
+  reinterpret_cast<uint2*>(out + row * kFp4D)[e] = make_uint2(pack_bf16x2(sum.x * f, sum.y * f), pack_bf16x2(sum.z * f, sum.w * f));
 }
 
 int gcd_int(int a, int b) {
@@ -1288,7 +1325,12 @@ pkv_status launch(const Params& p, cudaStream_t st) {
   pkv_status s = check_launch("spec_verify_attn_fp4");
   if (s != PKV_OK) return s;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, (unsigned)(kCols / 4));
+  // Four warps over a column's pieces where units have more than four of them on average (one token over
+  // 262,144 keys, 38 pieces: 62 us the whole call, 64 with two over the row's halves; over 1,024 keys, 8 pieces: 14.3
+  // and 15.7); else two over the halves, since the blocks, nearly all of them with work, then go through the
+  // SMs in several turns (eight tokens over 32 requests of up to 40,960: 195 us; 199 with four over the pieces).
+  const bool many = grid > 4ll * p.num_reqs * p.lines * p.units;
+  cfg.gridDim = dim3(grid, (unsigned)((p.tpc * p.group * (many ? 4 : 2) + 7) / 8));
   cfg.blockDim = dim3(256);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -1296,8 +1338,8 @@ pkv_status launch(const Params& p, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, spec_verify_fp4_merge_kernel, (const CtaWorkspace*)p.ws, p.lines, p.T, p.group,
-                     p.num_q_heads, p.tpc, p.n_tg, p.v_scale, p.out);
+  cudaLaunchKernelEx(&cfg, many ? spec_verify_fp4_merge_kernel<4, 1> : spec_verify_fp4_merge_kernel<1, 2>,
+                     Workspace(p.ws, (int)grid), p.lines, p.T, p.group, p.num_q_heads, p.tpc, p.n_tg, p.v_scale, p.out);
   return check_launch("spec_verify_attn_fp4 (merge)");
 }
 
@@ -1306,7 +1348,7 @@ pkv_status launch(const Params& p, cudaStream_t st) {
 }  // namespace pkv
 
 extern "C" size_t pkv_spec_verify_fp4_workspace_bytes(int32_t num_ctas) {
-  return num_ctas > 0 ? (size_t)num_ctas * sizeof(pkv::CtaWorkspace) : 0;
+  return num_ctas > 0 ? (size_t)num_ctas * pkv::kWorkspaceOfCta : 0;
 }
 
 extern "C" pkv_status pkv_spec_verify_attn_fp4(
@@ -1343,8 +1385,7 @@ extern "C" pkv_status pkv_spec_verify_attn_fp4(
               scale_stride_head % 16 == 0,
           "%s: q, out, workspace, caches, scale caches and their strides must be 16-byte aligned", name);
   PKV_ARG(softmax_scale > 0.0f, "%s: softmax_scale must be positive", name);
-  PKV_ARG(workspace_bytes >= (int64_t)sizeof(CtaWorkspace), "%s: the workspace needs at least %zu bytes", name,
-          sizeof(CtaWorkspace));
+  PKV_ARG(workspace_bytes >= (int64_t)kWorkspaceOfCta, "%s: the workspace needs at least %zu bytes", name, kWorkspaceOfCta);
   Params p{};
   // columns of a CTA: 16 when a KV head's query rows fit (half the padding, and half the softmax: one
   // token over 32 requests of up to 16,384: 81 us against 86 with 32, over one of 262,144: 65 against 76),
@@ -1357,7 +1398,7 @@ extern "C" pkv_status pkv_spec_verify_attn_fp4(
   // one line per unit (the heads of a request side by side) where that keeps nine tenths of the SMs busy,
   // (eight tokens over 32 requests of up to 40,960: 196 us against 218 in one line, whose CTAs read a page's
   // heads at different times), else one line with the units one after the other and no SM idle
-  int64_t ctas = workspace_bytes / (int64_t)sizeof(CtaWorkspace);
+  int64_t ctas = workspace_bytes / (int64_t)kWorkspaceOfCta;
   if (ctas > num_sms()) ctas = num_sms();
   const bool side = units <= ctas && ctas / units * units * 10 >= ctas * 9;
   p.lines = side ? (int)units : 1;
@@ -1400,7 +1441,7 @@ extern "C" pkv_status pkv_spec_verify_attn_fp4(
   p.num_q_heads = num_q_heads;
   p.scale_log2 = softmax_scale * 1.4426950408889634f;
   p.out = static_cast<__nv_bfloat16*>(out);
-  p.ws = static_cast<CtaWorkspace*>(workspace);
+  p.ws = workspace;
   p.dev_err = dev_err;
   p.wait_limit_ns = take_wait_limit_ns();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
