@@ -579,7 +579,8 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
     int j = 0, key = 0, col = 0, slot = 0, kvh = 0;  // of the tile that is looked up
     const int32_t* table = nullptr;
     bool more = true;
-    // moves on to the next tile and reads its table entry: -1 past the request, -2 past the table
+    bool need = false;  // the segment has a key of the request
+    // moves on to the next tile and reads its table entry (-1 past the table, as for any bad block)
     auto look_up = [&]() -> int {
       if (++j < run.n) {
         key += kBN;
@@ -591,7 +592,10 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
         }
       } else {
         more = next_run(p, cur, run);
-        if (!more) return -1;
+        if (!more) {
+          need = false;
+          return -1;
+        }
         j = 0;
         kvh = (p.lines > 1 ? line : run.u) / p.n_tg;
         key = run.t0 * kBN + lane * G;
@@ -599,8 +603,8 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
         slot = key - col * p.block_size;
         table = p.block_table + (int64_t)run.r * p.bt_stride;
       }
-      if (lane >= nseg || key >= run.len) return -1;
-      return col < p.max_blocks ? __ldg(table + col) : -2;
+      need = lane < nseg && key < run.len;
+      return need && col < p.max_blocks ? __ldg(table + col) : -1;
     };
     const bool is_k = warp == 0;
     uint64_t* const fulls = is_k ? sh.k_full : sh.v_full;
@@ -616,12 +620,13 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
     bool first = true;
     while (more) {
       const int c_slot = slot, c_kvh = kvh;
+      const bool c_need = need;
       int c_blk = blk;
       blk = look_up();
       uint64_t* full = &fulls[st];
       if (!first && !warp_wait(&empties[st], ph, abort, wl)) break;
-      if ((int64_t)c_blk >= p.num_blocks) c_blk = -2;
-      const uint32_t bad = __ballot_sync(0xffffffffu, c_blk < -1);
+      if ((int64_t)c_blk >= p.num_blocks) c_blk = -1;
+      const uint32_t bad = __ballot_sync(0xffffffffu, c_need && c_blk < 0);
       const uint32_t live = __ballot_sync(0xffffffffu, c_blk >= 0);
       // one block holds the tile (segment 0 is live then, or bad)
       const bool big = p.big_ok && __shfl_sync(0xffffffffu, c_blk >= 0 && c_slot + kBN <= p.block_size, 0);
@@ -657,7 +662,7 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
           if (elect_one()) {
 #pragma unroll
             for (int g = 0; g < kBatch; ++g)
-              if (sb[g] >= 0) {  // (-1 past the tile's segments)
+              if (sb[g] >= 0) {  // (negative past the tile's segments, and for a bad block)
                 tma_load_4d(codes + g * G * kFp4RowBytes, maps, full, 0, c_kvh, ss[g], sb[g]);
                 tma_load_4d(scales + g * G * kFp4Groups, maps + 1, full, 0, c_kvh, ss[g], sb[g]);
               }

@@ -433,6 +433,21 @@ def test_attend_same_bits_again_and_for_other_blocks(pkv, ws):
     assert np.array_equal(first, attend(pkv, c, q, 3, 1 / 16, ws))
 
 
+@pytest.mark.parametrize("entry", [-1, -2, -(1 << 31), (1 << 31) - 1])
+def test_attend_every_bad_table_entry(pkv, ws, entry):
+    """Also -1, which tables are padded with: below seq_len it is a bad block like any other, read as zero."""
+    b, zero = Batch([900, 300], 2, 16, seed=83), Batch([900, 300], 2, 16, seed=83)
+    bad = b.bt.copy()
+    for r, j in ((0, 0), (0, 20), (0, 56), (1, 18)):
+        bad[r, j] = entry
+        for w in ("k", "v"):
+            zero.codes[w][zero.bt[r, j]] = 0
+            zero.sb[w][zero.bt[r, j]] = 0
+    q = queries(b.rng, 2 * 2, 8)
+    got = attend(pkv, b, q, 2, 1 / 16, ws, expect_err=pkv.PKV_ERR_DEVICE_BOUNDS, bt=bad)
+    check(got, *reference(zero, q, 2, 4, 1 / 16))
+
+
 @pytest.mark.parametrize("T,hkv,group", [(1, 100, 2), (64, 4, 32), (33, 3, 5)])
 def test_attend_more_rows_than_ctas(pkv, ws, T, hkv, group):
     """Column groups that do not fill the SMs evenly, and more of them than SMs: one line of all of them."""
