@@ -343,17 +343,19 @@ def _table(block_table, *vectors):
     return R, cols, row
 
 
-def _launch(fn, dev, stream, others, *args):
-    """fn(*args, stream) with device `dev` current and, unless one is given, on its current stream; the
-    tensors `others` must be on it."""
+def _raw_stream(dev, stream):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _launch(fn, dev, others, args):
+    """fn(*args) with device `dev` current; the tensors `others` must be on it."""
     for t in others:
         assert t.get_device() == dev, "tensors of one call must be on one device"
-    raw = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-    if dev == torch.cuda.current_device():
-        rc = fn(*args, raw)
+    if dev == torch._C._cuda_getDevice():
+        rc = fn(*args)
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, raw)
+            rc = fn(*args)
     if rc != PKV_OK:
         _check(rc)
 
@@ -376,11 +378,11 @@ def kv_cache_write_fp4(k_new, v_new, block_table, seq_lens, query_start_loc, max
         heads == hkv and st[2] == 1 and st[1] == d, "new rows: bf16 [total][hkv][D], heads contiguous, K and V alike"
     R, cols, row = _table(block_table, seq_lens, query_start_loc)
     assert seq_lens.shape[0] == R and query_start_loc.shape[0] == R + 1, "seq_lens [R], query_start_loc [R + 1]"
-    _launch(lib.pkv_kv_cache_write_fp4, dev, stream, (k_new, v_new, block_table, seq_lens, query_start_loc),
-            k_new.data_ptr(), v_new.data_ptr(), st[0], block_table.data_ptr(), row, cols,
-            seq_lens.data_ptr(), query_start_loc.data_ptr(), R, int(max_q_len), k_fp4.data_ptr(), v_fp4.data_ptr(),
-            k_bscale.data_ptr(), v_bscale.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *cache, bs, hkv, d,
-            _err(dev_err, dev))
+    _launch(lib.pkv_kv_cache_write_fp4, dev, (k_new, v_new, block_table, seq_lens, query_start_loc),
+            (k_new.data_ptr(), v_new.data_ptr(), st[0], block_table.data_ptr(), row, cols,
+             seq_lens.data_ptr(), query_start_loc.data_ptr(), R, int(max_q_len), k_fp4.data_ptr(), v_fp4.data_ptr(),
+             k_bscale.data_ptr(), v_bscale.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *cache, bs, hkv, d,
+             _err(dev_err, dev), _raw_stream(dev, stream)))
 
 
 def kv_fp4_dequant_dense(k_fp4, v_fp4, k_bscale, v_bscale, block_table, pos_begin, pos_end, max_tokens, k_scale, v_scale,
@@ -393,10 +395,11 @@ def kv_fp4_dequant_dense(k_fp4, v_fp4, k_bscale, v_bscale, block_table, pos_begi
         k_dense.is_contiguous() and v_dense.is_contiguous(), "dense rows: contiguous bf16 [R][max_ctx][hkv][256]"
     reqs, cols, row = _table(block_table, pos_begin, pos_end)
     assert reqs == pos_begin.shape[0] == pos_end.shape[0] == R, "block_table [R][..], pos_begin, pos_end [R]"
-    _launch(lib.pkv_kv_fp4_dequant_dense, dev, stream, (block_table, pos_begin, pos_end, k_dense, v_dense),
-            k_fp4.data_ptr(), v_fp4.data_ptr(), k_bscale.data_ptr(), v_bscale.data_ptr(), k_scale.data_ptr(),
-            v_scale.data_ptr(), *cache, block_table.data_ptr(), row, cols, pos_begin.data_ptr(), pos_end.data_ptr(), R,
-            int(max_tokens), bs, hkv, d, k_dense.data_ptr(), v_dense.data_ptr(), max_ctx, _err(dev_err, dev))
+    _launch(lib.pkv_kv_fp4_dequant_dense, dev, (block_table, pos_begin, pos_end, k_dense, v_dense),
+            (k_fp4.data_ptr(), v_fp4.data_ptr(), k_bscale.data_ptr(), v_bscale.data_ptr(), k_scale.data_ptr(),
+             v_scale.data_ptr(), *cache, block_table.data_ptr(), row, cols, pos_begin.data_ptr(), pos_end.data_ptr(), R,
+             int(max_tokens), bs, hkv, d, k_dense.data_ptr(), v_dense.data_ptr(), max_ctx, _err(dev_err, dev),
+             _raw_stream(dev, stream)))
 
 
 def spec_verify_fp4_workspace_bytes(num_ctas=None) -> int:
@@ -418,8 +421,8 @@ def spec_verify_attn_fp4(q, k_fp4, v_fp4, k_bscale, v_bscale, k_scale, v_scale, 
         out.is_contiguous(), "q and out: contiguous bf16 [R*T][Hq][256]"
     assert seq_lens.shape[0] == R, "seq_lens [R]"
     assert workspace.is_contiguous(), "workspace must be a contiguous CUDA tensor"
-    _launch(lib.pkv_spec_verify_attn_fp4, dev, stream, (q, block_table, seq_lens, out, workspace), q.data_ptr(),
-            k_fp4.data_ptr(), v_fp4.data_ptr(), k_bscale.data_ptr(), v_bscale.data_ptr(), k_scale.data_ptr(),
-            v_scale.data_ptr(), *cache, block_table.data_ptr(), row, cols, seq_lens.data_ptr(), R,
-            int(T), hq, hkv, d, bs, float(softmax_scale), out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
-            _err(dev_err, dev))
+    _launch(lib.pkv_spec_verify_attn_fp4, dev, (q, block_table, seq_lens, out, workspace),
+            (q.data_ptr(), k_fp4.data_ptr(), v_fp4.data_ptr(), k_bscale.data_ptr(), v_bscale.data_ptr(),
+             k_scale.data_ptr(), v_scale.data_ptr(), *cache, block_table.data_ptr(), row, cols, seq_lens.data_ptr(), R,
+             int(T), hq, hkv, d, bs, float(softmax_scale), out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+             _err(dev_err, dev), _raw_stream(dev, stream)))

@@ -1397,7 +1397,7 @@ extern "C" pkv_status pkv_spec_verify_attn_fp4(
   // else 32, the tokens spread over column groups that read the same keys
   const bool narrow = (int64_t)T * group <= 16;
   p.tpc = T < kMaxCols / group ? T : kMaxCols / group;
-  p.n_tg = (T + p.tpc - 1) / p.tpc;
+  p.n_tg = (int32_t)(((int64_t)T + p.tpc - 1) / p.tpc);
   const int64_t units = (int64_t)num_kv_heads * p.n_tg;
   PKV_ARG(units < (1ll << 31) && (int64_t)num_reqs * T * num_q_heads < (1ll << 40), "%s: too many query rows", name);
   // one line per unit (the heads of a request side by side) where that keeps nine tenths of the SMs busy,
