@@ -440,10 +440,11 @@ PKV_API pkv_status pkv_kv_fp4_dequant_dense(const uint8_t* k_fp4, const uint8_t*
  *   pkv_spec_verify_attn_partial: token t of request r sits at position seq_lens[r] - T + t and attends
  *   the keys up to it. out = softmax(softmax_scale q . k) v with fp32 scores, sums and accumulation, on
  *   the exact stored k and v. Two roundings are its own: the probabilities meet V in fp16, and a query
- *   row meets K as a sum of four e2m1 rows with a scale per 16 elements, which leaves each element
- *   within max(2^-11 of its 16's largest, 2^-19 of its row's largest) of q (a row whose largest is
- *   below 2^-118: 2^-137 at most). A query row with an infinity or a NaN gives NaN. A token before position 0 (seq_lens[r] < T, an empty request included) attends
- *   nothing and gives zeros. out must not overlap q.
+ *   row meets K as a sum of six e2m1 rows with a scale per 16 elements: elements down to 2^-9 of their
+ *   16's largest magnitude and 2^-11 of their row's are exact, smaller ones within max(2^-17 of their
+ *   16's largest, 2^-19 of their row's largest) of q (a row whose largest is below 2^-118: 2^-137 at most).
+ *   A query row with an infinity or a NaN gives NaN. A token before position 0 (seq_lens[r] < T, an
+ *   empty request included) attends nothing and gives zeros. out must not overlap q.
  * Keys in a block whose id is out of range, or past the table, read as zero (k = v = 0) and
  * PKV_ERR_DEVICE_BOUNDS is recorded.
  * workspace: caller-owned device memory, 16-byte aligned, contents scratch; calls that may overlap on

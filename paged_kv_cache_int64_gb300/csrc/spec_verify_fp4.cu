@@ -9,7 +9,7 @@
 // A tile of 128 keys is 36 KB, 0.83 us (1,590 clocks) of an SM's share of the measured copy rate, and holds
 // 65,536 codes. What the design follows from:
 //   - K needs no widening: QK runs on the stored codes and scales (kind::mxf4nvf4), with a query row as a
-//     sum of four e2m1 rows under block scales (kTerms). Widening K to fp16 in registers as well took the
+//     sum of six e2m1 rows under block scales (kTerms). Widening K to fp16 in registers as well took the
 //     issue slots that V needs (eight tokens over up to 40,960 keys: 235 us against 210).
 //   - V has to be transposed (M is head_dim) and its scales vary along both axes, so it is widened, to fp16,
 //     which holds e2m1 * e4m3 exactly (6 significant bits). ldmatrix.m16n16.trans.b8 hands a thread one
@@ -54,14 +54,17 @@ constexpr int kScaleTile = kBN * kFp4Groups;   // 2 KB
 constexpr int kStage = kCodeTile + kScaleTile;
 constexpr int kMaxCols = 32;
 constexpr uint32_t kTmemCols = 512;
-// Q as a sum of four e2m1 rows, digits of base 8: a block of 16 elements whose largest magnitude lies in
-// [2^E, 2^(E+1)) has the scales 2^E, 2^(E-3), 2^(E-6), 2^(E-9), each term the last one's remainder rounded
-// to halves (which are e2m1 values up to 2), so what is left is at most 2^(E-11): a quarter of half a
-// bf16 step of the block's largest element, whose own rounding already moves the scores by more. Rows are
-// brought to [2^8, 2^9) first; e4m3 ends at 2^-9, so blocks of 2^-8 of the row's largest or less are kept
-// to 2^-11, 2^-19 of it. Two terms stand side by side as columns of one product (the instruction takes
-// 40 clocks for 16 or 32 columns and 49 for 64), and the softmax adds their scores.
-constexpr int kTerms = 4;
+// Q as a sum of six e2m1 rows, digits of base 8: a block of 16 elements whose largest magnitude lies in
+// [2^E, 2^(E+1)) has the scales 2^E, 2^(E-3), ... 2^(E-15), each term the last one's remainder rounded to
+// halves (which are e2m1 values up to 2). What is kept are multiples of 2^(E-16): a bf16 element has 8
+// bits, so all of them down to 2^-9 of the block's largest, and 2^-17 of the largest is the most that a smaller
+// one is off by. (Four terms keep 8 bits down to 2^-3: with one channel of 16 a hundred times the others,
+// and K's small there, outputs were off by 5 % and more. They took 195 us where six take 208, eight tokens over
+// up to 40,960 keys; one token measured the same.) Rows are brought to [2^8, 2^9) first; e4m3 ends at 2^-9, so that
+// no block keeps less than 2^-10 there, 2^-18 of the row's power of two. Terms stand side by side as
+// columns of one product (kSide; the instruction takes 40 clocks for 16 or 32 columns and 49 for 64), and
+// the softmax adds their scores.
+constexpr int kTerms = 6;
 constexpr float kUnset = -3e38f;          // running maximum of a column that has seen no key
 constexpr float kStart = 8.0f;            // a new maximum's weight is 2^8; the maximum moves when a thread's
 constexpr float kMove = 32768.0f;         // weights of one key add up to more than this (fp16 ends at 65,504)
@@ -93,10 +96,12 @@ struct Geo {
   // K codes are held until QK has read them, V codes until they are converted, which waits for the PV two
   // tiles back
   static constexpr int kKStages = kCols == 16 ? 4 : 3;
-  static constexpr int kVStages = 4;
+  static constexpr int kVStages = kCols == 16 ? 4 : 3;
+  static constexpr int kSide = kCols == 16 ? 3 : 2;  // terms side by side
+  static constexpr int kTurns = kTerms / kSide;      // products of a step of K
   static constexpr int kQTerm = kCols * 128;     // codes of one term of Q: [kCols rows][128 B], 128-byte swizzle
-  static constexpr int kQsPair = 4 * 512;        // scales of two terms: [4 steps of 64 elements][32 lanes][16 B]
-  static constexpr int kQBuf = kTerms * kQTerm + kTerms / 2 * kQsPair;
+  static constexpr int kQsTurn = 4 * 512;        // scales of kSide terms: [4 steps of 64 elements][32 lanes][16 B]
+  static constexpr int kQBuf = kTerms * kQTerm + kTurns * kQsTurn;
   static constexpr int kPRow = kCols * 4;        // bytes of a row of P^T: 2 kCols columns
   static constexpr uint32_t kPLayout = kCols == 16 ? kLayoutSW64 : kLayoutSW128;
   static constexpr int kPBuf = 2 * kBN * kPRow;
@@ -111,11 +116,13 @@ struct Geo {
   static constexpr int kTiles = kOffV + kVStages * kStage;
   // tensor memory; the scale factors in blocks of 4 columns (one step of 64 elements)
   static constexpr uint32_t kColV = 0;                      // two V tiles: a column a key
-  static constexpr uint32_t kColS = 256;                    // two S^T, the two terms' sums side by side
-  static constexpr uint32_t kColO = kColS + 4 * kCols;      // O^T of the even elements, then of the odd ones
-  static constexpr uint32_t kColKs = kColO + 2 * kCols;     // two tiles' K scales
-  static constexpr uint32_t kColQs = kColKs + 32;           // Q scales of the pairs of terms
-  static_assert(kColQs + 8 * kTerms <= kTmemCols && kColKs % 4 == 0, "tensor memory");
+  static constexpr uint32_t kColS = 256;                    // two S^T, the sums of kSide terms side by side
+  static constexpr uint32_t kSBuf = 64;
+  static constexpr uint32_t kColO = kColS + 2 * kSBuf;      // O^T of the even elements, then of the odd ones
+  static constexpr uint32_t kColKs = kColO + 2 * kCols;     // a tile's K scales
+  static constexpr uint32_t kColQs = kColKs + 16;           // Q scales of the turns
+  static_assert(kTerms % kSide == 0 && kSide * kCols <= (int)kSBuf, "terms side by side");
+  static_assert(kColQs + 16 * kTurns <= kTmemCols && kColKs % 4 == 0, "tensor memory");
   static_assert(kOffQ == 0 && kQBuf % 1024 == 0 && kOffP % 1024 == 0 && kOffK % 1024 == 0 && kStage % 1024 == 0, "swizzle atoms");
 };
 
@@ -376,13 +383,14 @@ __device__ __noinline__ void quantize_q_row(uint4 raw, int row, uint8_t* buf, fl
     y[2 * x + 1] = __uint_as_float(rw[x] & 0xffff0000u) * up * inv;
   }
   uint8_t* dst = buf + row * 128 + (((lane >> 2) ^ (row & 7)) * 16) + (lane & 3) * 4;
-  // row n = row + kCols (t % 2) of the pair t / 2: lane n % 32, word n / 32 of the step's block
+  // row n = row + kCols (t % kSide) of the turn t / kSide: lane n % 32, word n / 32 of the step's block
   uint8_t* sdst = buf + kTerms * Gm::kQTerm + (lane >> 3) * 512 + row * 16 + ((lane >> 1) & 3);
 #pragma unroll
   for (int t = 0; t < kTerms; ++t) {
     *reinterpret_cast<uint32_t*>(dst + t * Gm::kQTerm) = e2m1x8_rn(y);
+    const int n0 = t % Gm::kSide * kCols;
     if ((lane & 1) == 0)
-      sdst[(t >> 1) * Gm::kQsPair + (t & 1) * (kCols == 16 ? 256 : 4)] = (uint8_t)(e >= -6 ? (e + 7) << 3 : 1 << (e + 9));
+      sdst[t / Gm::kSide * Gm::kQsTurn + n0 % 32 * 16 + n0 / 32 * 4] = (uint8_t)(e >= -6 ? (e + 7) << 3 : 1 << (e + 9));
     if (t == kTerms - 1) break;
     const int down = min(3, e + 9);
     const float next = __int_as_float((127 + down) << 23);
@@ -679,10 +687,10 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------------------ QK issuer
-    // S^T = sum over the terms of K Q_term^T, two terms' columns side by side. The whole warp walks the
+    // S^T = sum over the terms of K Q_term^T, kSide terms' columns side by side. The whole warp walks the
     // tiles and one elected lane issues: with a warp-uniform address stream the MMAs follow one another
     // at the tensor core's own rate; from inside a `lane == 0` branch each takes 45 clocks and more.
-    constexpr uint32_t id = idesc_fp4(2 * kCols);
+    constexpr uint32_t id = idesc_fp4(Gm::kSide * kCols);
     const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
     const uint64_t q_desc = smem_desc(smem_u32(smem + Gm::kOffQ), 16, 1024);
     const uint64_t qs_desc = smem_desc(smem_u32(smem + Gm::kOffQ + kTerms * Gm::kQTerm), 16, 128, 0);
@@ -695,32 +703,34 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
     Ring<kKStages> ring;
     for (int s = 0; ok && next_run(p, cur, run); ++s) {
       ok = warp_wait(&sh.q_ready[s & 3], (s >> 2) & 1, abort, wl);
-      // the last run's MMAs are done with the Q scales in tensor memory
+      // the last run's MMAs are done with the scales in tensor memory
       if (ok && i > 0) ok = warp_wait(&sh.s_full[(i - 1) & 1], ((i - 1) >> 1) & 1, abort, wl);
       if (!ok) break;
       tc_fence_after();
       const uint64_t q_off = (uint64_t)((s & 1) * (Gm::kQBuf >> 4));
       if (elect_one()) {
 #pragma unroll 1
-        for (int x = 0; x < 2 * kTerms; ++x) tmem_cp_scales(tm + Gm::kColQs + 4 * x, qs_desc + q_off + (uint64_t)(x * 32));
+        for (int x = 0; x < 4 * Gm::kTurns; ++x) tmem_cp_scales(tm + Gm::kColQs + 4 * x, qs_desc + q_off + (uint64_t)(x * 32));
       }
       __syncwarp();
       for (int j = 0; ok && j < run.n; ++j, ++i, ring.next()) {
         const int b = i & 1;
+        // the last tile's MMAs are done with the K scales in tensor memory (long before the next ones are here)
+        if (j > 0) ok = warp_wait(&sh.s_full[b ^ 1], ((i - 1) >> 1) & 1, abort, wl);
         // the K scales' warp has waited for the codes and for the softmax to be through with S^T_{i-2}
-        ok = warp_wait(&sh.ks_ready[b], (i >> 1) & 1, abort, wl);
+        if (ok) ok = warp_wait(&sh.ks_ready[b], (i >> 1) & 1, abort, wl);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t d = tm + Gm::kColS + b * 2 * kCols, sfa = tm + Gm::kColKs + b * 16;
+        const uint32_t d = tm + Gm::kColS + b * Gm::kSBuf, sfa = tm + Gm::kColKs;
         const uint64_t kd = k_desc + (uint64_t)(ring.st * (kStage >> 4)), ksd = ks_desc + (uint64_t)(b * (kScaleTile >> 4));
         if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks) tmem_cp_scales(sfa + 4 * ks, ksd + (uint64_t)(ks * 32));
 #pragma unroll
-          for (int t = 0; t < kTerms / 2; ++t)
+          for (int t = 0; t < Gm::kTurns; ++t)
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              umma_fp4_ss(d, kd + (uint64_t)(ks * 2), q_desc + q_off + (uint64_t)(t * (2 * Gm::kQTerm >> 4) + ks * 2), id,
+              umma_fp4_ss(d, kd + (uint64_t)(ks * 2), q_desc + q_off + (uint64_t)(t * (Gm::kSide * Gm::kQTerm >> 4) + ks * 2), id,
                           sfa + 4 * ks, tm + Gm::kColQs + 16 * t + 4 * ks, (t | ks) ? 1u : 0u);
           umma_commit(&sh.s_full[b]);
           umma_commit(&sh.k_empty[ring.st]);
@@ -985,17 +995,21 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
         const uint32_t odd = x ^ ((k >> 1) & 1), r = prow + odd, chunk = odd * (kCols / 8) + grp * (kGC / 8) + cc;
         p_off[x][cc] = r * Gm::kPRow + ((chunk ^ (kCols == 16 ? (r >> 1) & 3u : r & 7u)) * 16);
       }
-    auto load_scores = [&](uint32_t t, float (&x)[kGC]) {  // the two halves of the terms, added
+    auto load_scores = [&](uint32_t t, float (&x)[kGC]) {  // the terms side by side, added
 #pragma unroll
       for (int q = 0; q < kGC; q += 8) {
-        uint32_t u[8], v[8];
-        tmem_ld_32x32b_x8(t + q, u);
-        tmem_ld_32x32b_x8(t + kCols + q, v);
+        uint32_t u[Gm::kSide][8];
+#pragma unroll
+        for (int h = 0; h < Gm::kSide; ++h) tmem_ld_32x32b_x8(t + h * kCols + q, u[h]);
         tmem_wait_ld();
 #pragma unroll
-        for (int y = 0; y < 8; y += 2)
-          add2(x[q + y], x[q + y + 1], __uint_as_float(u[y]), __uint_as_float(u[y + 1]), __uint_as_float(v[y]),
-               __uint_as_float(v[y + 1]));
+        for (int y = 0; y < 8; y += 2) {
+          add2(x[q + y], x[q + y + 1], __uint_as_float(u[0][y]), __uint_as_float(u[0][y + 1]), __uint_as_float(u[1][y]),
+               __uint_as_float(u[1][y + 1]));
+#pragma unroll
+          for (int h = 2; h < Gm::kSide; ++h)
+            add2(x[q + y], x[q + y + 1], x[q + y], x[q + y + 1], __uint_as_float(u[h][y]), __uint_as_float(u[h][y + 1]));
+        }
       }
     };
     Cursor cur = start;
@@ -1022,7 +1036,7 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
         if (ok) ok = warp_wait(&sh.s_full[b], (i >> 1) & 1, abort, wl);
         float x[kGC];
         float tile_sum[2];
-        const uint32_t ts = tmem + lane_off + Gm::kColS + b * 2 * kCols + c0;
+        const uint32_t ts = tmem + lane_off + Gm::kColS + b * Gm::kSBuf + c0;
         for (int pass = 0;; ++pass) {
           // weights 2^(S f - m), 0 where the column does not see the key. One that passes 2^15 shows in
           // their sum (no weight is negative; the sum's pipe has room where the maximum's has none).

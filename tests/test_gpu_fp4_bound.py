@@ -1,0 +1,58 @@
+"""Attention over the 4-bit cache held to the sharp bound of tests/_fp4_bound.py."""
+import numpy as np
+import pytest
+
+import _fp4 as F
+import _fp4_bound as B
+from test_gpu_fp4 import Batch, attend, check, pkv, rows_u16, ws  # noqa: F401  (fixtures)
+
+pytestmark = pytest.mark.gpu
+
+
+def even_batch(lens, hkv, bs, seed, channel=None, **kw):
+    """A Batch whose rows are alike in size: normal elements, K's times `channel`."""
+    b = Batch(lens, hkv, bs, seed=seed, fill=False, **kw)
+    for r, n in enumerate(lens):
+        if not n:
+            continue
+        blk, slot = b.where(r, np.arange(n))
+        for w, g in (("k", b.kg), ("v", b.vg)):
+            x = rows_u16(b.rng, n, hkv, spread=False)
+            if w == "k" and channel is not None:
+                x = F.f32_to_bf16(F.bf16_to_f32(x) * channel)
+            # rows of the tensor's size, whatever its scale
+            b.codes[w][blk, slot], b.sb[w][blk, slot] = F.quantize(x, 0.013)
+    return b
+
+
+def reference(b, q, T, group, scale):
+    parts = []
+    for r, n in enumerate(b.lens):
+        k, v = (b.value(w, r) if n else np.zeros((0, b.hkv, 256)) for w in ("k", "v"))
+        parts.append(B.attention(q[r * T:(r + 1) * T], k, v, n, T, group, scale))
+    return np.concatenate([p[0] for p in parts]), np.concatenate([p[1] for p in parts])
+
+
+def even_queries(rng, n, hq):
+    return F.f32_to_bf16(rng.standard_normal((n, hq, 256)).astype(np.float32))
+
+
+def outliers(rng, q_u16, big):
+    """One element of each 16 `big` times the others, the same channels in every row, and K's factors."""
+    at = rng.integers(0, 16, 16) + 16 * np.arange(16)
+    f = F.bf16_to_f32(q_u16)
+    f[..., at] *= big
+    channel = np.ones(256, dtype=np.float32)
+    channel[at] = 1 / big
+    return F.f32_to_bf16(f), channel
+
+
+@pytest.mark.parametrize("T,group", [(1, 4), (4, 4), (8, 4), (3, 7)])
+@pytest.mark.parametrize("big", [1, 30, 100, 1000])
+def test_attend_outlier_channels(pkv, ws, T, group, big):
+    """A query row's small elements count beside large ones of the same 16 that meet small channels of K."""
+    rng = np.random.default_rng(1000 * T + big)
+    lens, hkv = [1500, 300], 2
+    q, channel = outliers(rng, even_queries(rng, len(lens) * T, hkv * group), big)
+    b = even_batch(lens, hkv, 16, seed=big, channel=channel, kg=0.013)
+    check(attend(pkv, b, q, T, 0.25, ws), *reference(b, q, T, group, 0.25))
