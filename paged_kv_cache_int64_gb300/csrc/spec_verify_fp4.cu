@@ -151,7 +151,7 @@ struct alignas(16) Shared {
   alignas(16) float f[8][kCols];                 // column factors of the segment (ring: the softmax may be 4 behind)
   alignas(16) float m[kCols];                    // running maxima, log2, negated
   float red[Geo<kCols>::kGroups][4][Geo<kCols>::kGC];
-  float fin[kCols];
+  float fin[kCols];                              // 1 / sum, 0 for a column without a key
 };
 
 struct Params {
@@ -981,7 +981,6 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
     const int k = quarter * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const int bar_id = 1 + grp;
-    const float vg = __ldg(p.v_scale);
     // the key's two rows of P^T (see V columns for the order of the keys): weights in the first kCols
     // columns of the first row, which meets the even elements, and in the last of the second
     const int prow = 2 * ((k & ~15) + ((k >> 1) & 1) * 8 + ((k & 15) >> 2) * 2 + (k & 1));
@@ -1151,7 +1150,7 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
       group_sync(bar_id);
       if (quarter == 0 && lane < kGC) {
         const float sum = sh.red[grp][0][lane] + sh.red[grp][1][lane] + sh.red[grp][2][lane] + sh.red[grp][3][lane];
-        sh.fin[c0 + lane] = whole ? (sum == 0.0f ? 0.0f : vg / sum) : 1.0f;
+        sh.fin[c0 + lane] = sum == 0.0f ? 0.0f : 1.0f / sum;
         if (!whole && ok) {
           ws.lm[slot * kMaxCols + c0 + lane] = make_float2(sum, -m[lane]);
         }
@@ -1160,6 +1159,7 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
       if (ok) {
         tc_fence_after();
         const bool nan = sh.v_nan != 0;
+        const float vg = __ldg(p.v_scale);
         const int kvh = unit / p.n_tg;
         const int64_t row0 = ((int64_t)run.r * p.T + t_base) * p.num_q_heads + (int64_t)kvh * p.group;
         const int d = 2 * k;  // this lane's even element
@@ -1188,7 +1188,9 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
             if (c >= nq) break;
             const float x0 = __uint_as_float(v[q]), x1 = __uint_as_float(w[q]);
             if (whole)
-              reinterpret_cast<uint32_t*>(p.out + (row0 + sh.row_off[c]) * kFp4D)[k] = pack_bf16x2(x0 * sh.fin[c], x1 * sh.fin[c]);
+              // v_scale last: 1 / sum is normal, v_scale / sum need not be
+              reinterpret_cast<uint32_t*>(p.out + (row0 + sh.row_off[c]) * kFp4D)[k] =
+                  pack_bf16x2(x0 * sh.fin[c] * vg, x1 * sh.fin[c] * vg);
             else
               reinterpret_cast<float2*>(ws.o + (slot * nq_max + c) * kFp4D)[k] = make_float2(x0, x1);
           }
@@ -1226,8 +1228,8 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
 // merge of the pieces of a unit that several CTAs worked on
 // ------------------------------------------------------------------------------------------
 // Block (b, y): CTA b's note says whether a unit began in its range and went on; kP * kH warps a column, each
-// every kP-th piece and one of kH parts of the row, add its pieces up: M = max m, out = v_scale sum 2^(m - M) O
-// / sum 2^(m - M) l. The first pieces are loaded before their weights are known; a piece without a key
+// every kP-th piece and one of kH parts of the row, add its pieces up: M = max m, out = v_scale (sum 2^(m - M) O
+// / sum 2^(m - M) l). The first pieces are loaded before their weights are known; a piece without a key
 // (l = 0: its range is empty, or the column sees none of its keys) may hold anything and counts as
 // nothing.
 template <int kP, int kH>
@@ -1316,10 +1318,11 @@ __global__ void __launch_bounds__(256, 4)
   }
   const int t_base = (unit % n_tg) * tpc;
   if (y >= min(tpc, T - t_base) * group) return;
-  const float f = L == 0.0f ? 0.0f : __ldg(v_scale) / L;
+  const float f = L == 0.0f ? 0.0f : 1.0f / L, vg = __ldg(v_scale);  // (v_scale / L need not be normal)
   const int t = t_base + col / group;
   const int64_t row = ((int64_t)note.y * T + t) * num_q_heads + (int64_t)(unit / n_tg) * group + col % group;
-  reinterpret_cast<uint2*>(out + row * kFp4D)[e] = make_uint2(pack_bf16x2(sum.x * f, sum.y * f), pack_bf16x2(sum.z * f, sum.w * f));
+  reinterpret_cast<uint2*>(out + row * kFp4D)[e] =
+      make_uint2(pack_bf16x2(sum.x * f * vg, sum.y * f * vg), pack_bf16x2(sum.z * f * vg, sum.w * f * vg));
 }
 
 int gcd_int(int a, int b) {

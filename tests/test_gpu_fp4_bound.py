@@ -56,3 +56,12 @@ def test_attend_outlier_channels(pkv, ws, T, group, big):
     q, channel = outliers(rng, even_queries(rng, len(lens) * T, hkv * group), big)
     b = even_batch(lens, hkv, 16, seed=big, channel=channel, kg=0.013)
     check(attend(pkv, b, q, T, 0.25, ws), *reference(b, q, T, group, 0.25))
+
+
+@pytest.mark.parametrize("vg", [2.0 ** -126, 2.0 ** -120, 3e-30, 1e30, 2.0 ** 110])
+@pytest.mark.parametrize("lens,T", [([1000, 40], 1), ([5, 300], 4), ([70000], 1)])
+def test_attend_value_scales(pkv, ws, vg, lens, T):
+    """The tensor's scale of V anywhere in its range, in units that one CTA holds and in merged ones."""
+    b = even_batch(lens, 2, 16, seed=T, vg=vg)
+    q = even_queries(b.rng, len(lens) * T, 4)
+    check(*(x / vg for x in (attend(pkv, b, q, T, 1 / 64, ws), *reference(b, q, T, 2, 1 / 64))))  # (check's own floor is 1e-30)
