@@ -359,10 +359,21 @@ __device__ __forceinline__ void tmem_st_16x256b_x2(uint32_t a, const uint32_t (&
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
 }
+// What the scores of all rows share of their factor, softmax_scale log2(e) k_scale = m 2^e: with the exponents
+// apart no part of the product leaves fp32's range where the whole (2^-shift of the row joins it) does not.
+struct Factor {
+  float m;
+  int e;
+  __device__ __forceinline__ Factor(float scale_log2, float kg) {
+    int a, b;
+    m = frexpf(scale_log2, &a) * frexpf(kg, &b);
+    e = a + b;
+  }
+};
 // A query row's terms and their scales into a Q buffer, and its factor: by one warp, a lane 8 elements (two
 // lanes share a block of 16).
 template <int kCols>
-__device__ __noinline__ void quantize_q_row(uint4 raw, int row, uint8_t* buf, float* f, float scale_log2, float kg) {
+__device__ __noinline__ void quantize_q_row(uint4 raw, int row, uint8_t* buf, float* f, Factor shared) {
   using Gm = Geo<kCols>;
   const int lane = threadIdx.x & 31;
   const uint32_t rw[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -407,7 +418,7 @@ __device__ __noinline__ void quantize_q_row(uint4 raw, int row, uint8_t* buf, fl
   }
   // rows with an infinity or NaN: a NaN factor makes their scores, and so the row, NaN
   if (lane == 0)
-    f[row] = mr >= 0x7f80u ? __int_as_float(0x7fc00000) : scale_log2 * __int_as_float((127 - shift) << 23) * kg;
+    f[row] = mr >= 0x7f80u ? __int_as_float(0x7fc00000) : ldexpf(shared.m, shared.e - shift);
 }
 
 template <int kCols>
@@ -562,12 +573,12 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
       const int unit = p.lines > 1 ? line : run.u;
       const int nq = min(p.tpc, p.T - (unit % p.n_tg) * p.tpc) * p.group;
       const uint4* base = q_rows(run, unit);
-      const float kg = __ldg(p.k_scale);
+      const Factor factor(p.scale_log2, __ldg(p.k_scale));
       const int at = warp - (warp > 6 ? 2 : 1);  // 0 .. kThreads / 32 - 3
       if (at == 0 && lane >= nq && lane < kCols) sh.f[0][lane] = 0.0f;
 #pragma unroll 1
       for (int row = at; row < nq; row += kThreads / 32 - 2)
-        quantize_q_row<kCols>(__ldg(base + (int64_t)sh.row_off[row] * (kFp4D / 8) + lane), row, smem + Gm::kOffQ, sh.f[0], p.scale_log2, kg);
+        quantize_q_row<kCols>(__ldg(base + (int64_t)sh.row_off[row] * (kFp4D / 8) + lane), row, smem + Gm::kOffQ, sh.f[0], factor);
       fence_proxy_async_smem();
       warp_arrive(&sh.q_first, lane);
     }
@@ -876,7 +887,7 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
     // ------------------------------------------------------------------------------ Q
     // The terms of Q for a run, a run ahead of its use; a warp takes every other row and has the next one's
     // load in flight. The first run's rows were spread over all warps but the producers.
-    const float kg = __ldg(p.k_scale);
+    const Factor factor(p.scale_log2, __ldg(p.k_scale));
     Cursor cur = start;
     Run run;
     bool ok = true;
@@ -896,7 +907,7 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
 #pragma unroll 1
         for (int row = warp - 4; row < nq; row += 2) {
           const uint4 next = fetch(row + 2);
-          quantize_q_row<kCols>(raw, row, smem + Gm::kOffQ + (s & 1) * Gm::kQBuf, sh.f[s & 7], p.scale_log2, kg);
+          quantize_q_row<kCols>(raw, row, smem + Gm::kOffQ + (s & 1) * Gm::kQBuf, sh.f[s & 7], factor);
           raw = next;
         }
         fence_proxy_async_smem();

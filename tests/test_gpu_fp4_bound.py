@@ -65,3 +65,12 @@ def test_attend_value_scales(pkv, ws, vg, lens, T):
     b = even_batch(lens, 2, 16, seed=T, vg=vg)
     q = even_queries(b.rng, len(lens) * T, 4)
     check(*(x / vg for x in (attend(pkv, b, q, T, 1 / 64, ws), *reference(b, q, T, 2, 1 / 64))))  # (check's own floor is 1e-30)
+
+
+@pytest.mark.parametrize("qscale,kg,scale,size", [(2.0 ** -112, 2.0 ** 125, 2.0 ** -20, 1), (2.0 ** 124, 2.0 ** -126, 2.0 ** 11, 2.0 ** -14),
+                                                  (2.0 ** 124, 2.0 ** -126, 2.0 ** -6, 1), (2.0 ** -120, 2.0 ** 120, 1 / 64, 1)])
+def test_attend_scales_far_apart(pkv, ws, qscale, kg, scale, size):
+    """Query rows, K's scale and softmax_scale whose product is ordinary and whose parts are not."""
+    b = even_batch([900, 60], 2, 16, seed=5, kg=kg, channel=np.float32(size))
+    q = F.f32_to_bf16(F.bf16_to_f32(even_queries(b.rng, 2 * 2, 4)) * np.float32(qscale))
+    check(attend(pkv, b, q, 2, scale, ws), *reference(b, q, 2, 2, scale))
