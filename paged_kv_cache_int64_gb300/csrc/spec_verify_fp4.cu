@@ -1250,7 +1250,9 @@ __global__ void __launch_bounds__(256, 4)
                                  __nv_bfloat16* __restrict__ out) {
   constexpr int kCol = 8 / (kP * kH), kF = 2 / kH, kBatch = 4;  // columns; float4 a lane; pieces in flight
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int4 note = __ldg(reinterpret_cast<const int4*>(ws.notes + blockIdx.x));
+  // The workspace is the preceding grid's output, so it takes plain loads, which stay behind the wait; the
+  // read-only path is for what no grid writes while this one is there.
+  const int4 note = *reinterpret_cast<const int4*>(ws.notes + blockIdx.x);
   const int pieces = note.x, unit = note.z;
   if (pieces == 0) return;
   const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) % (kP * kH), c = (threadIdx.x >> 5) / (kP * kH);
@@ -1258,7 +1260,7 @@ __global__ void __launch_bounds__(256, 4)
   const int cols = tpc * group, y = blockIdx.y * kCol + c, col = min(y, cols - 1);
   // piece i > 0 is slot 0 of the i-th CTA after this one in the line
   auto slot = [&](int i) -> size_t { return i == 0 ? (size_t)blockIdx.x * 2 + 1 : ((size_t)blockIdx.x + (size_t)i * lines) * 2; };
-  auto load_lm = [&](int i) { return i < pieces ? __ldg(ws.lm + slot(i) * kMaxCols + col) : make_float2(0, 0); };
+  auto load_lm = [&](int i) { return i < pieces ? ws.lm[slot(i) * kMaxCols + col] : make_float2(0, 0); };
   float4 o[kBatch][kF];
   auto load = [&](int base) {
 #pragma unroll
@@ -1266,7 +1268,7 @@ __global__ void __launch_bounds__(256, 4)
       const int at = base + first + kP * i;
       const float4* src = reinterpret_cast<const float4*>(ws.o + (slot(at) * cols + col) * kFp4D) + part_of_row * 32 + lane;
 #pragma unroll
-      for (int h = 0; h < kF; ++h) o[i][h] = at < pieces ? __ldg(src + 32 * h) : make_float4(0, 0, 0, 0);
+      for (int h = 0; h < kF; ++h) o[i][h] = at < pieces ? src[32 * h] : make_float4(0, 0, 0, 0);
     }
   };
   const float2 lm0 = load_lm(lane);

@@ -1,5 +1,8 @@
 """The bound of tests/_fp4_bound.py sees what it is to see: coarser query rows, a lost tile or piece, a mask off
 by one; and a query row's digits are as exact as the header says."""
+import os
+import re
+
 import numpy as np
 import pytest
 
@@ -87,3 +90,22 @@ def test_bound_sees_lost_keys(n):
             w = np.ones(n)
             w[lo:hi] = weight
             assert _exceeds(with_weights(w), want, tol), (lo, hi, weight)
+
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "paged_kv_cache_int64_gb300", "csrc")
+
+
+def code(name):
+    """A source file without its comments."""
+    with open(os.path.join(CSRC, name)) as f:
+        return re.sub(r"//[^\n]*|/\*.*?\*/", "", f.read(), flags=re.S)
+
+
+def test_merge_reads_the_workspace_by_plain_loads():
+    """The read-only path promises data that no grid writes while the reading one is resident; the merge is
+    launched beside the grid that writes its workspace."""
+    text = code("spec_verify_fp4.cu")
+    merge = text[text.index("spec_verify_fp4_merge_kernel("):]
+    merge = merge[:merge.index("\n}")]
+    assert "ws.lm" in merge and "ws.notes" in merge and "ws.o" in merge
+    assert re.findall(r"__ld\w+\(([^)]*)\)", merge) == ["v_scale"]

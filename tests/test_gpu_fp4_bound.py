@@ -1,9 +1,11 @@
 """Attention over the 4-bit cache held to the sharp bound of tests/_fp4_bound.py."""
 import numpy as np
 import pytest
+import torch
 
 import _fp4 as F
 import _fp4_bound as B
+from _devsetup import DEV, u16_to_bf16
 from test_gpu_fp4 import Batch, attend, check, pkv, rows_u16, ws  # noqa: F401  (fixtures)
 
 pytestmark = pytest.mark.gpu
@@ -74,3 +76,30 @@ def test_attend_scales_far_apart(pkv, ws, qscale, kg, scale, size):
     b = even_batch([900, 60], 2, 16, seed=5, kg=kg, channel=np.float32(size))
     q = F.f32_to_bf16(F.bf16_to_f32(even_queries(b.rng, 2 * 2, 4)) * np.float32(qscale))
     check(attend(pkv, b, q, 2, scale, ws), *reference(b, q, 2, 2, scale))
+
+
+def test_attend_calls_that_follow_one_another(pkv, ws):
+    """Calls of other shapes and lengths one after the other on a stream, one workspace, no wait between them: each
+    merge reads what its own call left there, so each gives the bits that it gives alone."""
+    b = even_batch([6000, 700, 3000, 50], 2, 16, seed=7)
+    caches, scales, bt, _ = b.device()
+    calls = []
+    for T, group, lens in ((1, 4, [6000, 700, 3000, 50]), (8, 4, [130, 0, 2999, 8]), (1, 2, [6000, 1, 1, 1]), (3, 7, [257, 600, 5, 50]),
+                           (2, 8, [0, 0, 2900, 0])):
+        qd = u16_to_bf16(even_queries(b.rng, 4 * T, 2 * group)).to(DEV)
+        calls.append((qd, torch.tensor(lens, dtype=torch.int32, device=DEV), T, torch.empty_like(qd)))
+
+    def call(i, out):
+        qd, sl, T, _ = calls[i]
+        pkv.spec_verify_attn_fp4(qd, *caches, *scales, bt, sl, T, 1 / 64, out, ws)
+
+    for i, c in enumerate(calls):
+        call(i, c[3])
+        torch.cuda.synchronize()
+    order = np.random.default_rng(8).integers(0, len(calls), 300)
+    outs = [torch.empty_like(calls[i][3]) for i in order]
+    for i, out in zip(order, outs):
+        call(i, out)
+    torch.cuda.synchronize()
+    for i, out in zip(order, outs):
+        assert torch.equal(out.view(torch.int16), calls[i][3].view(torch.int16))
