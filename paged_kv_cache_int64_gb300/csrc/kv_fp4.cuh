@@ -55,37 +55,49 @@ __device__ __forceinline__ uint32_t e4m3_dup_f16(uint32_t byte) {
 }
 
 // Pair index -> (token, head); the usual pair index fits 32 bits, whose division is an order cheaper.
-__device__ __forceinline__ void split_pair(uint64_t pair, uint32_t heads, uint32_t& tok, uint32_t& head) {
+__host__ __device__ __forceinline__ void split_pair(uint64_t pair, uint32_t heads, uint32_t& tok, uint32_t& head) {
   tok = (pair >> 32) == 0 ? (uint32_t)pair / heads : (uint32_t)(pair / heads);
   head = (uint32_t)(pair - (uint64_t)tok * heads);
 }
 
-// Consecutive (token, head) pairs of a request from pair `first` on, token 0 being position pos0: where
-// each lies in the cache. The next block's table entry is read when a block is entered, so that the
-// walk stops for no table load after its first.
+// Consecutive (token, head) pairs of a request from pair `first` on, token 0 being position pos0 and `end` the
+// position after the last: where each lies in the cache. The next block's table entry is read when a block
+// is entered, so that the walk stops for no table load after its first, and only if that block holds a
+// position of the request. (For the host too, where it is tested.)
 struct PairWalk {
   const int32_t* table;
-  uint32_t heads, block_size, max_blocks;
+  uint32_t heads, block_size, max_blocks, end;
   uint32_t i, h, slot, col;  // token, head, slot in block, block column
-  int32_t blk, blk_next;     // -1: past the table
-  __device__ __forceinline__ int32_t entry(uint32_t c) const { return c < max_blocks ? __ldg(table + c) : -1; }
-  __device__ __forceinline__ PairWalk(const int32_t* t, uint32_t heads_, uint32_t bs, uint32_t mb, uint32_t pos0, uint64_t first)
-      : table(t), heads(heads_), block_size(bs), max_blocks(mb) {
+  uint32_t next_pos;         // the next block's first position
+  int32_t blk, blk_next;     // -1: past the table, or the request
+  __host__ __device__ __forceinline__ int32_t entry(uint32_t c) const {
+    if (c >= max_blocks) return -1;
+#ifdef __CUDA_ARCH__
+    return __ldg(table + c);
+#else
+    return table[c];
+#endif
+  }
+  __host__ __device__ __forceinline__ PairWalk(const int32_t* t, uint32_t heads_, uint32_t bs, uint32_t mb, uint32_t pos0,
+                                               uint32_t end_, uint64_t first)
+      : table(t), heads(heads_), block_size(bs), max_blocks(mb), end(end_) {
     split_pair(first, heads, i, h);
     col = (pos0 + i) / bs;
     slot = pos0 + i - col * bs;
+    next_pos = col * bs + bs;
     blk = entry(col);
-    blk_next = entry(col + 1);
+    blk_next = next_pos < end ? entry(col + 1) : -1;
   }
-  __device__ __forceinline__ void next() {
+  __host__ __device__ __forceinline__ void next() {
     if (++h < heads) return;
     h = 0;
     ++i;
     if (++slot < block_size) return;
     slot = 0;
     ++col;
+    next_pos += block_size;
     blk = blk_next;
-    blk_next = entry(col + 1);
+    blk_next = next_pos < end ? entry(col + 1) : -1;
   }
 };
 

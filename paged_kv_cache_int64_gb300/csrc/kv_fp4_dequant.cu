@@ -4,10 +4,12 @@
 // The first product is exact (6 significant bits); the second is one fp32 rounding.
 //
 // One lane holds one group: 8 bytes of codes and a scale byte in, 32 bytes out (one 256-bit store);
-// a warp covers the K row and the V row of one (position, head), four of them in flight.
+// a warp covers the K row and the V row of one (position, head), four of them in flight. Their places are found
+// side by side, a lane each, and handed round: with a walk from one pair to the next, 2.6 million pairs
+// took 554 us.
 //
-// Bound by memory, four fifths of it the stores. Measured: 2.6 million pairs of rows 553 us, 6.2 TB/s in and
-// out (0.91 of the measured copy rate); 188,416 pairs 42 us (46 with a cold L2); the smallest calls 2.0 us.
+// Bound by memory, four fifths of it the stores. Measured: 2.6 million pairs of rows 536 us, 6.4 TB/s in and
+// out (0.94 of the measured copy rate); 188,416 pairs 41 us (46 with a cold L2); the smallest calls 2.1 us.
 #include <cuda_bf16.h>
 
 #include "host_common.h"
@@ -18,7 +20,7 @@ namespace pkv {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kCtas = 16;  // of an SM: all the warps it holds, 32 registers (553 us below; 589 without the bound)
+constexpr int kCtas = 16;  // of an SM: all the warps it holds, 32 registers (2.6 million pairs 535 us; 545 without the bound)
 constexpr int64_t kManyPairs = 152 * 64 * 4;
 
 struct ReadArgs {
@@ -65,7 +67,20 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) kv_fp4_dequant_kernel(cons
   const uint64_t stride = (uint64_t)a.chunks * kWarps * kPairs;
   const int32_t* table = a.block_table + (int64_t)r * a.bt_stride;
   for (uint64_t base = ((uint64_t)chunk * kWarps + warp) * kPairs; base < nrows; base += stride) {
-    PairWalk at(table, hkv, a.block_size, a.max_blocks, (uint32_t)begin, base);
+    // lane u finds pair u's place (no table entry past the request's last is read); a warp-uniform offset then
+    int64_t off = -1, soff = 0;
+    if (lane < kPairs && base + lane < nrows) {
+      uint32_t tok, head;
+      split_pair(base + lane, hkv, tok, head);
+      const uint32_t pos = (uint32_t)begin + tok, col = pos / (uint32_t)a.block_size, slot = pos - col * a.block_size;
+      const int64_t blk = col < (uint32_t)a.max_blocks ? __ldg(table + col) : -1;
+      if (blk < 0 || blk >= a.num_blocks) {  // reads as zero
+        record_error(a.dev_err, kErrDeviceBounds);
+      } else {
+        off = blk * a.stride_blk + (int64_t)slot * a.stride_tok + (int64_t)head * a.stride_head;
+        soff = blk * a.scale_stride_blk + (int64_t)slot * a.scale_stride_tok + (int64_t)head * a.scale_stride_head;
+      }
+    }
     // the pairs of a request are consecutive rows of the dense tensor
     __nv_bfloat16* dst = dense + (((int64_t)r * a.max_ctx + begin) * hkv + (int64_t)base) * kFp4D + grp * kFp4Group;
     uint2 c[kPairs];
@@ -74,17 +89,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) kv_fp4_dequant_kernel(cons
     for (int u = 0; u < kPairs; ++u) {
       c[u] = make_uint2(0, 0);
       sb[u] = 0;
-      if (base + u < nrows) {
-        if (at.blk < 0 || at.blk >= a.num_blocks) {  // reads as zero
-          if (lane == 0) record_error(a.dev_err, kErrDeviceBounds);
-        } else {
-          c[u] = __ldg(reinterpret_cast<const uint2*>(codes + (int64_t)at.blk * a.stride_blk +
-                                                      (int64_t)at.slot * a.stride_tok + (int64_t)at.h * a.stride_head + grp * 8));
-          sb[u] = __ldg(scales + (int64_t)at.blk * a.scale_stride_blk + (int64_t)at.slot * a.scale_stride_tok +
-                        (int64_t)at.h * a.scale_stride_head + grp);
-        }
+      const int64_t o = __shfl_sync(0xffffffffu, off, u), so = __shfl_sync(0xffffffffu, soff, u);
+      if (o >= 0) {
+        c[u] = __ldg(reinterpret_cast<const uint2*>(codes + o + grp * 8));
+        sb[u] = __ldg(scales + so + grp);
       }
-      at.next();
     }
 #pragma unroll
     for (int u = 0; u < kPairs; ++u) {
@@ -143,8 +152,8 @@ extern "C" pkv_status pkv_kv_fp4_dequant_dense(
              pos_end, block_size, num_kv_heads, 0, static_cast<__nv_bfloat16*>(k_dense),
              static_cast<__nv_bfloat16*>(v_dense), max_ctx, dev_err};
   // pairs of a warp: 4 in flight where there are enough for every warp the device holds (2.6 million pairs:
-  // 590 us against 1,028 with one, before all warps were resident; three 609, five 593 against 553 since), else 1
-  // (256 pairs: 2.1 us against 2.9 with four)
+  // 535 us against 1,072 with one, 562 with three, 587 with five), else 1 (256 pairs: 2.1 us against 2.8 with
+  // four)
   const int64_t rows = (int64_t)max_tokens * num_kv_heads;
   const bool many = rows * num_reqs > kManyPairs;
   const int64_t per_cta = (int64_t)kWarps * (many ? 4 : 1);

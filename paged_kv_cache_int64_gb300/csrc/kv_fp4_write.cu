@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas) kv_fp4_write_kernel(const 
   const int32_t* table = a.block_table + (int64_t)r * a.bt_stride;
   for (uint64_t base = ((uint64_t)chunk * kWarps + warp) * a.per; base < nrows; base += stride) {
     const int n = (int)min((uint64_t)a.per, nrows - base);
-    PairWalk at(table, hkv, a.block_size, a.max_blocks, (uint32_t)(seq_len - q_len), base);
+    PairWalk at(table, hkv, a.block_size, a.max_blocks, (uint32_t)(seq_len - q_len), (uint32_t)seq_len, base);
     Bytes32 raw[kDepth];
     int64_t off[kDepth], soff[kDepth];
     auto fetch = [&](int u, bool live) {
