@@ -21,7 +21,6 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kCtas = 16;  // of an SM: all the warps it holds, 32 registers (2.6 million pairs 535 us; 545 without the bound)
-constexpr int64_t kManyPairs = 152 * 64 * 4;
 
 struct ReadArgs {
   const uint8_t* k_fp4;
@@ -155,7 +154,7 @@ extern "C" pkv_status pkv_kv_fp4_dequant_dense(
   // 535 us against 1,072 with one, 562 with three, 587 with five), else 1 (256 pairs: 2.1 us against 2.8 with
   // four)
   const int64_t rows = (int64_t)max_tokens * num_kv_heads;
-  const bool many = rows * num_reqs > kManyPairs;
+  const bool many = rows * num_reqs > (int64_t)num_sms() * kCtas * kWarps * 4;
   const int64_t per_cta = (int64_t)kWarps * (many ? 4 : 1);
   const int64_t want = (rows + per_cta - 1) / per_cta;
   const int64_t cap = ((1ll << 30) - 1) / num_reqs + 1;

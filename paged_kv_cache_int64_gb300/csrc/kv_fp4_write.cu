@@ -36,10 +36,10 @@ constexpr int kCtas = 8;
 // warp's start (launch, lengths, table: three dependent loads) over more rows; short ones are all that
 // small calls have (570,184 pairs: 137 us with 16, 139 with 12, 357 with one; 8,192 pairs: 4.6 us with
 // two, 5.5 with one, 8.1 with 16).
-constexpr int64_t kDeviceWarps = 152 * kCtas * kWarps;
 constexpr int64_t kPairsMost = 16;
 int32_t pairs_per_warp(int64_t pairs) {
-  const int64_t per = (pairs + kDeviceWarps - 1) / kDeviceWarps;
+  const int64_t device_warps = (int64_t)num_sms() * kCtas * kWarps;
+  const int64_t per = (pairs + device_warps - 1) / device_warps;
   return (int32_t)(per < 1 ? 1 : per > kPairsMost ? kPairsMost : per);
 }
 

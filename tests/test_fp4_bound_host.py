@@ -109,3 +109,10 @@ def test_merge_reads_the_workspace_by_plain_loads():
     merge = merge[:merge.index("\n}")]
     assert "ws.lm" in merge and "ws.notes" in merge and "ws.o" in merge
     assert re.findall(r"__ld\w+\(([^)]*)\)", merge) == ["v_scale"]
+
+
+@pytest.mark.parametrize("name", ["kv_fp4_write.cu", "kv_fp4_dequant.cu", "spec_verify_fp4.cu"])
+def test_rules_take_the_device_s_sm_count(name):
+    """What depends on how many warps or CTAs the device holds asks the device."""
+    text = code(name)
+    assert "num_sms()" in text and not re.search(r"\b1(32|4[48]|5[26]|60)\b", text)
