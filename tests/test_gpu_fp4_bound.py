@@ -103,3 +103,64 @@ def test_attend_calls_that_follow_one_another(pkv, ws):
     torch.cuda.synchronize()
     for i, out in zip(order, outs):
         assert torch.equal(out.view(torch.int16), calls[i][3].view(torch.int16))
+
+
+def run_even(pkv, ws, lens, T, hkv, group, bs, seed=1, scale=1 / 64, **kw):
+    """Rows of equal norms under a small scale: every key carries weight, and the bound is a fraction of what a
+    key tile, a merged piece or the newest key adds (tests/test_fp4_bound_host.py)."""
+    b = even_batch(lens, hkv, bs, seed, **kw)
+    q = even_queries(b.rng, len(lens) * T, hkv * group)
+    check(attend(pkv, b, q, T, scale, ws), *reference(b, q, T, group, scale))
+
+
+@pytest.mark.parametrize("T,hkv,group", [(1, 4, 4), (1, 1, 1), (1, 2, 32), (1, 3, 7), (2, 8, 1), (3, 2, 7), (8, 4, 4), (8, 4, 6),
+                                         (5, 1, 16), (17, 1, 3), (40, 2, 1), (1, 5, 12), (64, 4, 32)])
+def test_attend_even_geometries(pkv, ws, T, hkv, group):
+    run_even(pkv, ws, [130, 700, 64], T, hkv, group, 16, seed=T + hkv)
+
+
+@pytest.mark.parametrize("n", [1, 2, 16, 17, 127, 128, 129, 256, 257, 640, 1025, 4000])
+@pytest.mark.parametrize("T", [1, 8])
+def test_attend_even_lengths(pkv, ws, n, T):
+    run_even(pkv, ws, [n], T, 2, 4, 32, seed=n)
+
+
+@pytest.mark.parametrize("bs", [8, 16, 24, 48, 64, 120, 128, 136, 256, 880])
+@pytest.mark.parametrize("layout", ["nbhd", "nhbd", "padded"])
+def test_attend_even_pages(pkv, ws, bs, layout):
+    run_even(pkv, ws, [901, 129], 4, 2, 2, bs, seed=bs, layout=layout)
+
+
+@pytest.mark.parametrize("T", [1, 8])
+def test_attend_even_ragged_batch(pkv, ws, T):
+    rng = np.random.default_rng(77)
+    lens = [int(x) for x in np.exp(rng.uniform(np.log(20), np.log(4000), 37))]
+    run_even(pkv, ws, lens + [9000, 0, 1], T, 4, 4, 16, seed=7)
+
+
+@pytest.mark.parametrize("lens,T,hkv,group", [([40000, 3], 1, 2, 2), ([20008], 8, 4, 6), ([100000], 1, 1, 4), ([9000, 9000], 8, 2, 4)])
+def test_attend_even_long_contexts(pkv, ws, lens, T, hkv, group):
+    """Units that many CTAs share: each one's piece counts once."""
+    run_even(pkv, ws, lens, T, hkv, group, 880, seed=41)
+
+
+@pytest.mark.parametrize("ctas", [1, 2, 7, 31, 100])
+def test_attend_even_small_workspace(pkv, ctas):
+    small = torch.empty(pkv.spec_verify_fp4_workspace_bytes(ctas), dtype=torch.uint8, device=DEV)
+    run_even(pkv, small, [700, 20, 1300, 0, 5000], 3, 2, 4, 16, seed=ctas)
+
+
+@pytest.mark.parametrize("T,hkv,group", [(1, 2, 4), (4, 2, 4)])
+def test_attend_even_growing_scores(pkv, ws, T, hkv, group):
+    """Scores that rise along the keys by 40 and fall again, so that the maximum moves and O is rescaled in most tiles;
+    the keys near the top share the weight."""
+    n = 5000
+    b = even_batch([n], hkv, 16, seed=52)
+    blk, slot = b.where(0, np.arange(n))
+    f = F.bf16_to_f32(rows_u16(b.rng, n, hkv, spread=False))
+    f[..., 0] = (3 * np.sin(np.linspace(-1.5, 5.0, n, dtype=np.float32)))[:, None]
+    b.codes["k"][blk, slot], b.sb["k"][blk, slot] = F.quantize(F.f32_to_bf16(f), 0.013)
+    q = F.bf16_to_f32(even_queries(b.rng, T, hkv * group))
+    q[..., 0] = 60.0
+    q = F.f32_to_bf16(q)
+    check(attend(pkv, b, q, T, 1 / 8, ws), *reference(b, q, T, group, 1 / 8))
