@@ -369,6 +369,11 @@ struct Factor {
     m = frexpf(scale_log2, &a) * frexpf(kg, &b);
     e = a + b;
   }
+  // m 2^(e - shift) in two steps: the first stays normal (m is at least 1/4)
+  __device__ __forceinline__ float row(int shift) const {
+    const int t = min(max(e - shift, -240), 240), h = t >> 1;
+    return m * __int_as_float((127 + h) << 23) * __int_as_float((127 + t - h) << 23);
+  }
 };
 // A query row's terms and their scales into a Q buffer, and its factor: by one warp, a lane 8 elements (two
 // lanes share a block of 16).
@@ -418,7 +423,7 @@ __device__ __noinline__ void quantize_q_row(uint4 raw, int row, uint8_t* buf, fl
   }
   // rows with an infinity or NaN: a NaN factor makes their scores, and so the row, NaN
   if (lane == 0)
-    f[row] = mr >= 0x7f80u ? __int_as_float(0x7fc00000) : ldexpf(shared.m, shared.e - shift);
+    f[row] = mr >= 0x7f80u ? __int_as_float(0x7fc00000) : shared.row(shift);
 }
 
 template <int kCols>
