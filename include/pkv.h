@@ -83,7 +83,8 @@ typedef enum pkv_kv_dtype {
 /* Message of the last failed call on this host thread ("" if none). Never NULL. */
 PKV_API const char* pkv_last_error(void);
 
-/* ABI version of this header (incremented on any signature change). */
+/* ABI version of this header (incremented on any signature change; a call that is only added, such as those of the
+ * 4-bit cache, leaves it: look its symbol up). */
 #define PKV_ABI_VERSION 7
 PKV_API int32_t pkv_abi_version(void);
 

@@ -10,7 +10,7 @@
 // 65,536 codes. What the design follows from:
 //   - K needs no widening: QK runs on the stored codes and scales (kind::mxf4nvf4), with a query row as a
 //     sum of six e2m1 rows under block scales (kTerms). Widening K to fp16 in registers as well took the
-//     issue slots that V needs (eight tokens over up to 40,960 keys: 235 us against 210).
+//     issue slots that V needs (eight tokens over up to 40,960 keys, with four terms: 235 us against 210).
 //   - V has to be transposed (M is head_dim) and its scales vary along both axes, so it is widened, to fp16,
 //     which holds e2m1 * e4m3 exactly (6 significant bits). ldmatrix.m16n16.trans.b8 hands a thread one
 //     byte column of four keys, the conversion of a byte gives the (even, odd) elements of one key, and
@@ -32,14 +32,17 @@
 // Roles: warps 0 and 6 TMA producers of K and V; 1 QK issuer; 2 PV issuer; 3 V scales; 4-5 Q; 7 K scales;
 // 8-15 V columns; 16-23 softmax, a warpgroup for half the columns.
 //
-// Measured (4 KV heads, 16 query heads): one token, 32 requests of up to 16,384 keys 68 us (3.9
-// TB/s of cache); one token, one request of 262,144 keys 62 us (4.9 TB/s); eight tokens, 32 requests of
-// up to 40,960 keys 195 us (3.8 TB/s); one token, one request of 1,024 keys 14.3 us. No unit is above a
-// half (issue slots 48 %, tensor pipe 22 %): a tile passes through scores, exponentials, vote, weights and
-// back in about 1,800 (kCols 16) or 2,300 clocks (32) of latencies, of which the double buffers overlap
-// two tiles. About 13 us of every call are none of its tiles': 3 until the range is known, 2 to 3 until the
-// first tile has come, 2 through it, then the launch of the merge and its two or three turns of loads.
+// Measured (4 KV heads, 16 query heads): one token, 32 requests of up to 16,384 keys 67 us (3.9
+// TB/s of cache); one token, one request of 262,144 keys 63 us (4.8 TB/s); eight tokens, 32 requests of
+// up to 40,960 keys 209 us (3.6 TB/s); one token, one request of 1,024 keys 15.0 us. No unit is above a
+// half (issue slots 46 %, tensor pipe 23 %): a tile passes through scores, exponentials, vote, weights and
+// back in about 1,800 (kCols 16) or 2,500 clocks (32) of latencies, of which the double buffers overlap
+// two tiles. With 32 columns the 80 registers that 24 warps leave spill (180 bytes stored, 300 loaded). About 14 us
+// of every call are none of its tiles': 3 until the range is known, 2 to 3 until the first tile has
+// come, 2 through it, then the launch of the merge and its two or three turns of loads.
 #include <cuda_bf16.h>
+
+#include <numeric>
 
 #include "host_common.h"
 #include "kv_fp4.cuh"
@@ -670,8 +673,8 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
         }
       } else {
         // segments in batches: their places by shuffles first, then one lane issues the batch's copies, 65
-        // clocks each (a segment at a time: 136; one token, 32 requests of up to 16,384 keys in pages of 16: 68 us
-        // against 81)
+        // clocks each (a segment at a time: 136; one token, 32 requests of up to 16,384 keys in pages of 16: 67 us
+        // against 79)
         constexpr int kBatch = 8;
 #pragma unroll 1
         for (int g0 = 0; g0 < nseg; g0 += kBatch) {
@@ -1343,15 +1346,6 @@ __global__ void __launch_bounds__(256, 4)
       make_uint2(pack_bf16x2(sum.x * f * vg, sum.y * f * vg), pack_bf16x2(sum.z * f * vg, sum.w * f * vg));
 }
 
-int gcd_int(int a, int b) {
-  while (b) {
-    const int t = a % b;
-    a = b;
-    b = t;
-  }
-  return a;
-}
-
 template <int kCols>
 pkv_status launch(const Params& p, cudaStream_t st) {
   constexpr int kSmem = 1024 + Geo<kCols>::kTiles + (int)sizeof(Shared<kCols>);
@@ -1366,9 +1360,9 @@ pkv_status launch(const Params& p, cudaStream_t st) {
   if (s != PKV_OK) return s;
   cudaLaunchConfig_t cfg = {};
   // Four warps over a column's pieces where units have more than four of them on average (one token over
-  // 262,144 keys, 38 pieces: 62 us the whole call, 64 with two over the row's halves; over 1,024 keys, 8 pieces: 14.3
-  // and 15.7); else two over the halves, since the blocks, nearly all of them with work, then go through the
-  // SMs in several turns (eight tokens over 32 requests of up to 40,960: 195 us; 199 with four over the pieces).
+  // 262,144 keys, 38 pieces: 62.6 us the whole call, 65 with two over the row's halves; over 1,024 keys, 8 pieces: 15.0
+  // and 15.9); else two over the halves, since the blocks, nearly all of them with work, then go through the
+  // SMs in several turns (eight tokens over 32 requests of up to 40,960: 209 us; 213 with four over the pieces).
   const bool many = grid > 4ll * p.num_reqs * p.lines * p.units;
   cfg.gridDim = dim3(grid, (unsigned)((p.tpc * p.group * (many ? 4 : 2) + 7) / 8));
   cfg.blockDim = dim3(256);
@@ -1428,7 +1422,7 @@ extern "C" pkv_status pkv_spec_verify_attn_fp4(
   PKV_ARG(workspace_bytes >= (int64_t)kWorkspaceOfCta, "%s: the workspace needs at least %zu bytes", name, kWorkspaceOfCta);
   Params p{};
   // columns of a CTA: 16 when a KV head's query rows fit (half the padding, and half the softmax: one
-  // token over 32 requests of up to 16,384: 81 us against 86 with 32, over one of 262,144: 65 against 76),
+  // token over 32 requests of up to 16,384: 67 us against 79 with 32, over one of 262,144: 63 against 78),
   // else 32, the tokens spread over column groups that read the same keys
   const bool narrow = (int64_t)T * group <= 16;
   p.tpc = T < kMaxCols / group ? T : kMaxCols / group;
@@ -1436,7 +1430,7 @@ extern "C" pkv_status pkv_spec_verify_attn_fp4(
   const int64_t units = (int64_t)num_kv_heads * p.n_tg;
   PKV_ARG(units < (1ll << 31) && (int64_t)num_reqs * T * num_q_heads < (1ll << 40), "%s: too many query rows", name);
   // one line per unit (the heads of a request side by side) where that keeps nine tenths of the SMs busy,
-  // (eight tokens over 32 requests of up to 40,960: 196 us against 218 in one line, whose CTAs read a page's
+  // (eight tokens over 32 requests of up to 40,960: 209 us against 235 in one line, whose CTAs read a page's
   // heads at different times), else one line with the units one after the other and no SM idle
   int64_t ctas = workspace_bytes / (int64_t)kWorkspaceOfCta;
   if (ctas > num_sms()) ctas = num_sms();
@@ -1444,7 +1438,7 @@ extern "C" pkv_status pkv_spec_verify_attn_fp4(
   p.lines = side ? (int)units : 1;
   p.units = side ? 1 : (int)units;
   p.ctas = (int)(ctas / p.lines);
-  const int G = gcd_int(block_size, kBN);
+  const int G = std::gcd(block_size, kBN);
   const uint64_t cdims[4] = {(uint64_t)kFp4RowBytes, (uint64_t)num_kv_heads, (uint64_t)block_size, (uint64_t)num_blocks};
   const uint64_t cstr[3] = {(uint64_t)stride_head, (uint64_t)stride_tok, (uint64_t)stride_blk};
   const uint64_t sdims[4] = {(uint64_t)kFp4Groups, (uint64_t)num_kv_heads, (uint64_t)block_size, (uint64_t)num_blocks};
