@@ -1189,7 +1189,9 @@ __global__ void __launch_bounds__(Geo<kCols>::kThreads, 1) spec_verify_fp4_kerne
           tmem_ld_32x32b_x8(tmem + lane_off + Gm::kColO + kCols + cq, w);
           tmem_wait_ld();
           if (nan) {  // keys that only some columns see, with a NaN V scale
-            for (int key = max(seen_by_all + 1, run.t0 * kBN); key < min(run.len, (run.t0 + run.n) * kBN); ++key) {
+            // (no column sees the keys from seen_by_all + tpc on)
+            const int last = min(min(run.len, seen_by_all + p.tpc), (run.t0 + run.n) * kBN);
+            for (int key = max(seen_by_all + 1, run.t0 * kBN); key < last; ++key) {
               const int col = key / p.block_size;
               const int64_t blk = col < p.max_blocks ? (int64_t)__ldg(p.block_table + (int64_t)run.r * p.bt_stride + col) : -1;
               if (blk < 0 || blk >= p.num_blocks) continue;

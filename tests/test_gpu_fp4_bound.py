@@ -164,3 +164,26 @@ def test_attend_even_growing_scores(pkv, ws, T, hkv, group):
     q[..., 0] = 60.0
     q = F.f32_to_bf16(q)
     check(attend(pkv, b, q, T, 1 / 8, ws), *reference(b, q, T, group, 1 / 8))
+
+
+def test_attend_nan_value_scale_under_many_tokens(pkv, ws):
+    """A NaN V scale among many tokens of a request reaches the tokens from its key on, and costs a look at the few
+    keys that a CTA's columns differ in: with a look at all that follow, 5 ms a unit, the waits of 2 ms ran out."""
+    T, hkv, key = 6000, 4, 2999
+    b = even_batch([T], hkv, 16, seed=53)
+    blk, slot = b.where(0, np.array([key]))
+    b.sb["v"][blk, slot, 1, 3] = 0x7F
+    q = even_queries(b.rng, T, hkv)
+    pkv.lib.pkv_testing_set_wait_limit_ns(2_000_000)
+    got = attend(pkv, b, q, T, 1 / 64, ws)
+    nan = np.isnan(got)
+    assert nan[key:, 1, 48:64].all()
+    nan[key:, 1, 48:64] = False
+    assert not nan.any()
+    b.sb["v"][blk, slot, 1, 3] = 0
+    k, v = b.value("k", 0), b.value("v", 0)
+    for t in (0, 1, 31, 32, 127, 128, key - 1, key, key + 1, key + 31, 4095, T - 1):
+        for h in range(hkv):
+            want, tol = B._rows(F.bf16_to_f32(q[t:t + 1, h]).astype(np.float64), k[:t + 1, h], v[:t + 1, h], 1 / 64)
+            keep = np.r_[0:48, 64:256] if h == 1 else np.arange(256)
+            check(got[t:t + 1, h][:, keep], want[:, keep], tol[:, keep])
