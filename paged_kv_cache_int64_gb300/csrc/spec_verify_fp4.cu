@@ -37,7 +37,7 @@
 // up to 40,960 keys 209 us (3.6 TB/s); one token, one request of 1,024 keys 15.0 us. No unit is above a
 // half (issue slots 46 %, tensor pipe 23 %): a tile passes through scores, exponentials, vote, weights and
 // back in about 1,800 (kCols 16) or 2,500 clocks (32) of latencies, of which the double buffers overlap
-// two tiles. With 32 columns the 80 registers that 24 warps leave spill (180 bytes stored, 300 loaded). About 14 us
+// two tiles. With 32 columns the 80 registers that 24 warps leave spill (172 bytes stored, 292 loaded). About 14 us
 // of every call are none of its tiles': 3 until the range is known, 2 to 3 until the first tile has
 // come, 2 through it, then the launch of the merge and its two or three turns of loads.
 #include <cuda_bf16.h>

@@ -31,7 +31,8 @@ def q_unit(q):
     """The step in which a query row's elements are kept: those that are multiples of it exactly, the others
     within half of it. The first of six base-8 digits counts in halves of the power of two of the
     block of 16's largest magnitude, the last in 2^-16 of it; a digit's scale is at least 2^-9 in a row brought to
-    [2^8, 2^9), where a step is 2^-18 of the row's power of two (2^-136 in rows that cannot be brought there)."""
+    [2^8, 2^9), where a step is 2^-18 of the row's power of two (2^-136 in rows that cannot be brought there).
+    (_fp4.q_error allows more: what four digits would leave.)"""
     a = np.abs(q)
     block = np.repeat(a.reshape(*a.shape[:-1], F.D // F.G, F.G).max(-1), F.G, axis=-1)
     return np.maximum(2.0 ** -16 * _power(block), np.maximum(2.0 ** -18 * _power(a.max(-1, keepdims=True)), 2.0 ** -136))
