@@ -77,8 +77,11 @@ typedef enum pkv_kv_dtype {
   PKV_KV_BF16 = 0, /* bf16 rows */
   PKV_KV_INT8 = 1, /* int8 per (token, head) row with an fp32 scale per row [P91 review:
                       "int8_per_token_head"] */
-  PKV_KV_FP8 = 2   /* OCP e4m3 bytes with one fp32 scale per tensor [P91 review: k_descale] */
+  PKV_KV_FP8 = 2,  /* OCP e4m3 bytes with one fp32 scale per tensor [P91 review: k_descale] */
+  PKV_KV_FP4 = 3   /* the 4-bit cache below: e2m1 codes with an e4m3 scale per 16 (pkv_kv_cache_compact) */
 } pkv_kv_dtype;
+
+typedef enum pkv_prob_dtype { PKV_PROB_F32 = 0, PKV_PROB_BF16 = 1, PKV_PROB_F16 = 2 } pkv_prob_dtype;
 
 /* Message of the last failed call on this host thread ("" if none). Never NULL. */
 PKV_API const char* pkv_last_error(void);
@@ -465,6 +468,123 @@ PKV_API pkv_status pkv_spec_verify_attn_fp4(const void* q, const uint8_t* k_fp4,
                                             int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                             int32_t block_size, float softmax_scale, void* out, void* workspace,
                                             int64_t workspace_bytes, int32_t* dev_err, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * After the verify attention: which drafts stay, and which keys (csrc/spec_verify_accept.cu,
+ * kv_attn_weights.cu, kv_evict_select.cu, kv_cache_compact.cu)
+ *
+ * spec_verify_accept - verification of drafted tokens against the target's probabilities from given
+ * random numbers; the emitted tokens have the target's distribution.
+ *   Request r's verify ran T tokens: the last committed one and num_drafts[r] <= T - 1 drafts (num_drafts
+ *   null: T - 1 each). target_probs[r][t] (T rows) are the target's probabilities of the token after query
+ *   token t; draft t (draft_ids[r][t], T - 1 a request) is proposed for that place, draft_probs[r][t] (T - 1
+ *   rows) what it was drawn from. Rows are `vocab` contiguous values of prob_dtype (draft and target alike),
+ *   element strides of requests and tokens given; ids, u_accept [num_reqs][T-1] and u_sample [num_reqs]
+ *   contiguous.
+ *   Draft t with token x is accepted when every draft before it was and
+ *     u_accept[r][t] * q(x) < p(x), exactly (q = draft_probs[r][t], p = target_probs[r][t]);
+ *   draft_probs null: q(x) = 1 and q is 0 elsewhere (drafts that no distribution proposed). At the first
+ *   draft that is not accepted the next token is drawn from max(p - q, 0), after the last draft from p:
+ *     the smallest i with w(0) + ... + w(i) > u_sample[r] * (w(0) + ... + w(vocab - 1)),
+ *   each probability taken as the nearest multiple of 2^-58 (exact from 2^-34 up) and the rest exact. Where
+ *   max(p - q, 0) is 0 everywhere, w = p. A one-hot target row decodes greedily.
+ *   out_tokens [num_reqs][T]: the accepted drafts, the drawn token, then -1; num_out [num_reqs]: how many of
+ *   these are tokens (the count of query tokens whose keys stay, q_valid of kv_attn_weights).
+ * Probabilities are in [0, 1] (values outside are clamped, NaN counts as 0), a row's sum below 64; u in
+ * [0, 1) (clamped to it, NaN as 0). A draft id outside [0, vocab) is not accepted and leaves p whole, a row
+ * without a positive value gives token 0, num_drafts outside [0, T - 1] is clamped: each sets
+ * PKV_ERR_DEVICE_BOUNDS. vocab at most 2^30. No workspace.
+ */
+PKV_API pkv_status pkv_spec_verify_accept(const void* target_probs, int64_t target_stride_req,
+                                          int64_t target_stride_tok, const void* draft_probs,
+                                          int64_t draft_stride_req, int64_t draft_stride_tok, int32_t prob_dtype,
+                                          const int32_t* draft_ids, const float* u_accept, const float* u_sample,
+                                          const int32_t* num_drafts, int32_t num_reqs, int32_t T, int32_t vocab,
+                                          int32_t* out_tokens, int32_t* num_out, int32_t* dev_err, void* stream);
+
+/*
+ * kv_attn_weights - the attention weight that each cached key collects from the step's queries:
+ *   weights[r][h][pos] = (pos < prev_lens[r] ? prev[r][h][pos] : 0)
+ *                        + sum over t < q_valid[r], query heads of KV head h, of exp(s - lse)
+ *   for every pos < seq_lens[r]; s = softmax_scale q . k as for pkv_spec_verify_attn_partial (token t at
+ *   position seq_lens[r] - T + t attends the keys up to it; a token before position 0 attends nothing and
+ *   adds nothing), lse the log-sum-exp of that query's scores. fp32 throughout, on the exact stored k.
+ *   q bf16 [num_reqs*T][num_q_heads][256]; the K cache by kv_dtype: bf16, int8 with k_scale fp32
+ *   [num_blocks][block_size][num_kv_heads] (strides scale_stride_*), e4m3 with k_scale one device fp32.
+ *   part_lse (nullable): the split log-sum-exps that a verify call left for the same q, cache and lengths,
+ *   [max_splits][num_reqs*T][num_q_heads] with its split_tokens. Without it they are computed first, which
+ *   reads K twice.
+ *   q_valid (nullable: T each): the first tokens that count, such as num_out of spec_verify_accept; the
+ *   rejected drafts add nothing. Values outside [0, T] are clamped.
+ *   prev (nullable): earlier weights, laid out as weights, which may be the same buffer; prev_lens (nullable:
+ *   seq_lens): positions from prev_lens[r] on take nothing from prev, as for keys that are new.
+ *   weights fp32, element strides w_stride_req and w_stride_head, positions contiguous, max_ctx of them;
+ *   positions from seq_lens[r] on are left as they were.
+ * Keys in a bad block, or past the table, read as zero and set PKV_ERR_DEVICE_BOUNDS; so does a seq_lens[r]
+ * past max_ctx or the table (positions past them are left out).
+ * workspace: caller-owned, 16-byte aligned, contents scratch; calls that may overlap on the GPU need one
+ * each. pkv_kv_attn_weights_workspace_bytes(num_reqs * T, num_q_heads, n) bytes let n CTAs run: pass the
+ * device's SM count; a smaller n runs on fewer SMs.
+ * Requirements: num_q_heads / num_kv_heads <= 128; block_size a multiple of 8; max_blocks * block_size at
+ * most 2^31 - 128; q, the cache and its strides 16-byte aligned.
+ */
+PKV_API size_t pkv_kv_attn_weights_workspace_bytes(int32_t num_rows, int32_t num_q_heads, int32_t num_ctas);
+PKV_API pkv_status pkv_kv_attn_weights(const void* q, const void* k_cache, int32_t kv_dtype, const float* k_scale,
+                                       int64_t num_blocks, int64_t stride_blk, int64_t stride_tok,
+                                       int64_t stride_head, int64_t scale_stride_blk, int64_t scale_stride_tok,
+                                       const int32_t* block_table, int64_t bt_stride, int32_t max_blocks,
+                                       const int32_t* seq_lens, const int32_t* q_valid, int32_t num_reqs, int32_t T,
+                                       int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                       int32_t block_size, float softmax_scale, const float* part_lse,
+                                       int32_t split_tokens, int32_t max_splits, const float* prev,
+                                       const int32_t* prev_lens, float* weights, int64_t w_stride_req,
+                                       int64_t w_stride_head, int64_t max_ctx, void* workspace,
+                                       int64_t workspace_bytes, int32_t* dev_err, void* stream);
+
+/*
+ * kv_evict_select - the positions of a cache that stay within a budget, for each (request, KV head):
+ *   seq_lens[r] <= budget: all of them. Else the first `sinks`, the last `recent`, and of those in between
+ *   the budget - sinks - recent with the highest scores (equal scores: the lowest position first; NaN below
+ *   every number).
+ *   scores fp32 [num_reqs][num_kv_heads][max_ctx] (element strides, positions contiguous), such as the
+ *   weights of kv_attn_weights. keep int32 [num_reqs][num_kv_heads][budget]: the positions, ascending, in the
+ *   first new_lens[r] = min(seq_lens[r], budget) entries; the others are left as they were.
+ * sinks + recent <= budget. seq_lens[r] outside [0, max_ctx] is clamped and sets PKV_ERR_DEVICE_BOUNDS.
+ */
+PKV_API pkv_status pkv_kv_evict_select(const float* scores, int64_t stride_req, int64_t stride_head, int64_t max_ctx,
+                                       const int32_t* seq_lens, int32_t num_reqs, int32_t num_kv_heads, int32_t sinks,
+                                       int32_t recent, int32_t budget, int32_t* keep, int32_t* new_lens,
+                                       int32_t* dev_err, void* stream);
+
+/*
+ * kv_cache_compact - row j of (request r, KV head h) := row keep[r][h][j], j < new_lens[r], in the K cache, the
+ * V cache, their scale caches (int8: fp32 [num_blocks][block_size][num_kv_heads]; 4-bit: 16 bytes a row) and the
+ * weights (nullable, fp32 [num_reqs][num_kv_heads][max_ctx], moved in place). Row contents are copied bit for bit.
+ *   keep int32 [num_reqs][num_kv_heads][budget], ascending, as kv_evict_select leaves it.
+ *   Rows are read through src_table and written through dst_table (int32, rows of src_blocks / dst_blocks
+ *   entries). The same table moves the rows in place; entry i of dst_table may also be a block that no row of
+ *   any request is read from (where blocks are shared with other requests). Other overlaps of the two are not
+ *   allowed, nor two requests that write the same block.
+ *   Strides in elements of the cache's storage (bf16; bytes else), scale strides in fp32 (int8) or bytes
+ *   (4-bit). The later calls read the cache with seq_lens = new_lens: keys carry their rotary position in
+ *   themselves, and order does not matter to attention.
+ * An entry of keep below its own index, not above the one before it, past the table or past max_ctx, and rows
+ * in a bad block: the row is not moved and PKV_ERR_DEVICE_BOUNDS is set; so does new_lens[r] outside
+ * [0, budget], which is clamped.
+ * workspace: pkv_kv_cache_compact_workspace_bytes bytes, 4-byte aligned, contents scratch; calls that may
+ * overlap on the GPU need one each. Caches and strides 16-byte aligned (4-bit scales too).
+ */
+PKV_API size_t pkv_kv_cache_compact_workspace_bytes(int32_t num_reqs, int32_t num_kv_heads, int32_t budget);
+PKV_API pkv_status pkv_kv_cache_compact(void* k_cache, void* v_cache, int32_t kv_dtype, int64_t num_blocks,
+                                        int64_t stride_blk, int64_t stride_tok, int64_t stride_head, void* k_scale,
+                                        void* v_scale, int64_t scale_stride_blk, int64_t scale_stride_tok,
+                                        int64_t scale_stride_head, const int32_t* src_table, int64_t src_stride,
+                                        int32_t src_blocks, const int32_t* dst_table, int64_t dst_stride,
+                                        int32_t dst_blocks, const int32_t* keep, const int32_t* new_lens,
+                                        int32_t num_reqs, int32_t num_kv_heads, int32_t budget, int32_t block_size,
+                                        int32_t head_dim, float* weights, int64_t w_stride_req, int64_t w_stride_head,
+                                        int64_t max_ctx, void* workspace, int64_t workspace_bytes, int32_t* dev_err,
+                                        void* stream);
 
 #ifdef __cplusplus
 }

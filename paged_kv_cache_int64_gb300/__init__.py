@@ -22,11 +22,13 @@ __all__ = [
     "library_path", "kv_cache_write", "kv_int8_stats_quant", "paged_prefill_attn_fp8", "kv_fp8_dequant_dense", "paged_prefill_attn", "paged_prefill_workspace_bytes", "spec_verify_workspace_bytes", "spec_verify_pick_split",
     "spec_verify_attn_partial", "spec_verify_attn_partial_fp8", "spec_verify_combine", "EXPORTED_SYMBOLS",
     "kv_cache_write_fp4", "kv_fp4_dequant_dense", "spec_verify_attn_fp4", "spec_verify_fp4_workspace_bytes",
+    "PKV_KV_FP4", "spec_verify_accept", "kv_attn_weights", "kv_attn_weights_workspace_bytes", "kv_evict_select",
+    "kv_cache_compact", "kv_cache_compact_workspace_bytes",
 ]
 
 PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA, PKV_ERR_DEVICE_BOUNDS, PKV_ERR_TIMEOUT = range(6)
 PKV_QK_BF16, PKV_QK_INT8 = 0, 1
-PKV_KV_BF16, PKV_KV_INT8, PKV_KV_FP8 = 0, 1, 2
+PKV_KV_BF16, PKV_KV_INT8, PKV_KV_FP8, PKV_KV_FP4 = 0, 1, 2, 3
 
 EXPORTED_SYMBOLS = (
     "pkv_last_error", "pkv_abi_version", "pkv_kv_int8_stats_quant", "pkv_kv_fp8_dequant_dense",
@@ -35,7 +37,9 @@ EXPORTED_SYMBOLS = (
     "pkv_spec_verify_attn_noalloc", "pkv_kv_cache_write", "pkv_paged_prefill_attn_fp8",
     "pkv_paged_prefill_workspace_bytes", "pkv_testing_set_wait_limit_ns", "pkv_spec_verify_pick_split",
     "pkv_kv_cache_write_fp4", "pkv_kv_fp4_dequant_dense", "pkv_spec_verify_fp4_workspace_bytes",
-    "pkv_spec_verify_attn_fp4",
+    "pkv_spec_verify_attn_fp4", "pkv_spec_verify_accept", "pkv_kv_attn_weights",
+    "pkv_kv_attn_weights_workspace_bytes", "pkv_kv_evict_select", "pkv_kv_cache_compact",
+    "pkv_kv_cache_compact_workspace_bytes",
 )
 
 library_path = _build.LIB
@@ -92,6 +96,17 @@ def _load():
                                            i32, i32, f32, vp, vp, i64, vp, vp]
     L.pkv_spec_verify_fp4_workspace_bytes.argtypes = [i32]
     L.pkv_spec_verify_fp4_workspace_bytes.restype = sz
+    L.pkv_spec_verify_accept.argtypes = [vp, i64, i64, vp, i64, i64, i32, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp]
+    L.pkv_kv_attn_weights.argtypes = [vp, vp, i32, vp, *[i64] * 6, vp, i64, i32, vp, vp, *[i32] * 6, f32, vp, i32, i32,
+                                      vp, vp, vp, i64, i64, i64, vp, i64, vp, vp]
+    L.pkv_kv_evict_select.argtypes = [vp, i64, i64, i64, vp, *[i32] * 5, vp, vp, vp, vp]
+    L.pkv_kv_cache_compact.argtypes = [vp, vp, i32, *[i64] * 4, vp, vp, i64, i64, i64, vp, i64, i32, vp, i64, i32, vp, vp,
+                                       *[i32] * 5, vp, i64, i64, i64, vp, i64, vp, vp]
+    for name in ("pkv_kv_attn_weights_workspace_bytes", "pkv_kv_cache_compact_workspace_bytes"):
+        getattr(L, name).argtypes = [i32, i32, i32]
+        getattr(L, name).restype = sz
+    for name in ("pkv_spec_verify_accept", "pkv_kv_attn_weights", "pkv_kv_evict_select", "pkv_kv_cache_compact"):
+        getattr(L, name).restype = i32
     for name in ("pkv_kv_cache_write_fp4", "pkv_kv_fp4_dequant_dense", "pkv_spec_verify_attn_fp4"):
         getattr(L, name).restype = i32
     for name in ("pkv_paged_prefill_attn_fp8", "pkv_kv_cache_write", "pkv_kv_int8_stats_quant", "pkv_kv_fp8_dequant_dense", "pkv_paged_prefill_attn",
@@ -426,3 +441,159 @@ def spec_verify_attn_fp4(q, k_fp4, v_fp4, k_bscale, v_bscale, k_scale, v_scale, 
              k_scale.data_ptr(), v_scale.data_ptr(), *cache, block_table.data_ptr(), row, cols, seq_lens.data_ptr(), R,
              int(T), hq, hkv, d, bs, float(softmax_scale), out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
              _err(dev_err, dev), _raw_stream(dev, stream)))
+
+
+# ---------------------------------------------------------------------------------------------
+# after the verify attention: which drafts stay, and which keys
+# ---------------------------------------------------------------------------------------------
+
+_PROBS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_KV_TYPES = {PKV_KV_BF16: torch.bfloat16, PKV_KV_INT8: torch.int8, PKV_KV_FP8: torch.uint8, PKV_KV_FP4: torch.uint8}
+
+
+def _flat(t, dtype, *shape):
+    """t's pointer; t: contiguous, of that type and shape."""
+    assert t.dtype is dtype and t.shape == shape and t.is_contiguous(), f"expected contiguous {dtype} {list(shape)}"
+    return t.data_ptr()
+
+
+def _maybe(t):
+    return None if t is None else t.data_ptr()
+
+
+def spec_verify_accept(target_probs, draft_probs, draft_ids, u_accept, u_sample, out_tokens, num_out, num_drafts=None,
+                       dev_err=None, stream=None):
+    """Verify drafted tokens against the target's probabilities [R][T][vocab] (fp32, bf16 or fp16, rows contiguous):
+    draft_ids int32 [R][T-1] drawn from draft_probs [R][T-1][vocab] (None: proposed by no distribution), uniform
+    numbers u_accept [R][T-1] and u_sample [R] fp32; num_drafts int32 [R] (None: T-1 each). out_tokens int32 [R][T]:
+    the accepted drafts, the token drawn after them, -1; num_out int32 [R]: how many are tokens."""
+    R, T, V = target_probs.shape
+    ts = target_probs.stride()
+    dev = target_probs.get_device()
+    kind = _PROBS.get(target_probs.dtype)
+    assert kind is not None and (ts[2] == 1 or V == 1), "target_probs: fp32, bf16 or fp16 [R][T][vocab], rows contiguous"
+    assert dev >= 0, "target_probs must be a CUDA tensor"
+    others = [draft_ids, u_accept, u_sample, out_tokens, num_out]
+    ds = (0, 0)
+    if draft_probs is not None:
+        ds = draft_probs.stride()
+        assert draft_probs.dtype is target_probs.dtype and draft_probs.shape == (R, T - 1, V) and (ds[2] == 1 or V == 1), \
+            "draft_probs: [R][T-1][vocab], of target_probs' type, rows contiguous"
+        others.append(draft_probs)
+    if num_drafts is not None:
+        _flat(num_drafts, _I32, R)
+        others.append(num_drafts)
+    _launch(lib.pkv_spec_verify_accept, dev, others,
+            (target_probs.data_ptr(), ts[0], ts[1], _maybe(draft_probs), ds[0], ds[1], kind, _flat(draft_ids, _I32, R, T - 1),
+             _flat(u_accept, _F32, R, T - 1), _flat(u_sample, _F32, R), _maybe(num_drafts), R, T, V,
+             _flat(out_tokens, _I32, R, T), _flat(num_out, _I32, R), _err(dev_err, dev), _raw_stream(dev, stream)))
+
+
+def kv_attn_weights_workspace_bytes(num_rows, num_q_heads, num_ctas=None) -> int:
+    """bytes of kv_attn_weights' workspace for num_rows = R*T query rows on num_ctas CTAs (default: the current
+    device's SM count)."""
+    if num_ctas is None:
+        num_ctas = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
+    return int(lib.pkv_kv_attn_weights_workspace_bytes(int(num_rows), int(num_q_heads), int(num_ctas)))
+
+
+def kv_attn_weights(q, k_cache, block_table, seq_lens, T, softmax_scale, weights, workspace, kv_dtype=PKV_KV_BF16,
+                    k_scale=None, prev=None, prev_lens=None, q_valid=None, part_lse=None, split_tokens=0, dev_err=None,
+                    stream=None):
+    """weights[r][h][pos] (fp32 [R][hkv][max_ctx]) = prev's (positions < prev_lens[r]) + the attention weight that the key
+    collects from tokens t < q_valid[r] of the step's T, all query heads of its KV head; q bf16 [R*T][Hq][256]. k_cache:
+    bf16, int8 (k_scale fp32 [nb][bs][hkv]) or uint8 e4m3 (k_scale a device scalar), by kv_dtype. part_lse [S][R*T][Hq] with
+    its split_tokens: what a verify call left for the same queries (None: computed first)."""
+    nb, bs, hkv, d, sb, st, sh = _cache_strides(k_cache)
+    dev = k_cache.get_device()
+    assert dev >= 0 and k_cache.dtype is {PKV_KV_BF16: _BF16, PKV_KV_INT8: torch.int8, PKV_KV_FP8: _U8}[kv_dtype], \
+        "k_cache: a CUDA tensor of kv_dtype"
+    R, cols, row = _table(block_table, seq_lens)
+    rows, hq, dq = q.shape
+    assert q.dtype is _BF16 and rows == R * T and dq == d and q.is_contiguous(), "q: contiguous bf16 [R*T][Hq][256]"
+    ws = weights.stride()
+    max_ctx = weights.shape[2]
+    assert weights.dtype is _F32 and weights.shape == (R, hkv, max_ctx) and (ws[2] == 1 or max_ctx == 1), \
+        "weights: fp32 [R][hkv][max_ctx], positions contiguous"
+    assert seq_lens.shape[0] == R, "seq_lens [R]"
+    assert workspace.is_contiguous(), "workspace must be a contiguous CUDA tensor"
+    others = [q, block_table, seq_lens, weights, workspace]
+    ssb = sst = splits = 0
+    if kv_dtype == PKV_KV_INT8:
+        assert k_scale.dtype is _F32 and k_scale.shape == (nb, bs, hkv) and (k_scale.stride(2) == 1 or hkv == 1), \
+            "k_scale: fp32 [nb][bs][hkv], heads contiguous"
+        ssb, sst = k_scale.stride(0), k_scale.stride(1)
+    elif kv_dtype == PKV_KV_FP8:
+        assert k_scale.dtype is _F32 and k_scale.numel() == 1, "k_scale: an fp32 device scalar"
+    if kv_dtype != PKV_KV_BF16:
+        others.append(k_scale)
+    if prev is not None:
+        assert prev.dtype is _F32 and prev.shape == weights.shape and prev.stride() == ws, "prev: laid out as weights"
+        others.append(prev)
+    for t in (prev_lens, q_valid):
+        if t is not None:
+            _flat(t, _I32, R)
+            others.append(t)
+    if part_lse is not None:
+        splits = part_lse.shape[0]
+        _flat(part_lse, _F32, splits, rows, hq)
+        others.append(part_lse)
+    _launch(lib.pkv_kv_attn_weights, dev, others,
+            (q.data_ptr(), k_cache.data_ptr(), kv_dtype, None if kv_dtype == PKV_KV_BF16 else k_scale.data_ptr(), nb, sb, st,
+             sh, ssb, sst, block_table.data_ptr(), row, cols, seq_lens.data_ptr(), _maybe(q_valid), R, int(T), hq, hkv, d, bs,
+             float(softmax_scale), _maybe(part_lse), int(split_tokens), splits, _maybe(prev), _maybe(prev_lens),
+             weights.data_ptr(), ws[0], ws[1], max_ctx, workspace.data_ptr(), workspace.nbytes, _err(dev_err, dev),
+             _raw_stream(dev, stream)))
+
+
+def kv_evict_select(scores, seq_lens, sinks, recent, budget, keep, new_lens, dev_err=None, stream=None):
+    """keep int32 [R][hkv][budget] := the positions of each (request, KV head) that stay, ascending: the first `sinks`,
+    the last `recent`, the highest of scores (fp32 [R][hkv][max_ctx]) in between; new_lens int32 [R] := how many."""
+    R, hkv, max_ctx = scores.shape
+    ss = scores.stride()
+    dev = scores.get_device()
+    assert dev >= 0 and scores.dtype is _F32 and (ss[2] == 1 or max_ctx == 1), "scores: fp32 [R][hkv][max_ctx] on the GPU, positions contiguous"
+    _launch(lib.pkv_kv_evict_select, dev, (seq_lens, keep, new_lens),
+            (scores.data_ptr(), ss[0], ss[1], max_ctx, _flat(seq_lens, _I32, R), R, hkv, int(sinks), int(recent), int(budget),
+             _flat(keep, _I32, R, hkv, int(budget)), _flat(new_lens, _I32, R), _err(dev_err, dev), _raw_stream(dev, stream)))
+
+
+def kv_cache_compact_workspace_bytes(num_reqs, num_kv_heads, budget) -> int:
+    return int(lib.pkv_kv_cache_compact_workspace_bytes(int(num_reqs), int(num_kv_heads), int(budget)))
+
+
+def kv_cache_compact(k_cache, v_cache, src_table, dst_table, keep, new_lens, workspace, kv_dtype=PKV_KV_BF16, k_scale=None,
+                     v_scale=None, weights=None, dev_err=None, stream=None):
+    """Row j of (r, h) := row keep[r][h][j] (int32 [R][hkv][budget], ascending), j < new_lens[r], in K, V, the scale
+    caches (int8: fp32 [nb][bs][hkv]; 4-bit: uint8 [nb][bs][hkv][16]) and weights (fp32 [R][hkv][max_ctx]). Read through
+    src_table, written through dst_table: the same table, or other blocks."""
+    nb, bs, hkv, d, sb, st, sh = _cache_strides(k_cache)
+    dev = k_cache.get_device()
+    assert dev >= 0 and k_cache.dtype is v_cache.dtype is _KV_TYPES[kv_dtype], "caches: CUDA tensors of kv_dtype"
+    assert v_cache.shape == k_cache.shape and v_cache.stride() == k_cache.stride(), "K and V strides must agree"
+    R, cols, row = _table(src_table, new_lens)
+    reqs, dcols, drow = _table(dst_table)
+    budget = keep.shape[2]
+    assert reqs == R == new_lens.shape[0], "src_table, dst_table, new_lens: the same requests"
+    assert workspace.is_contiguous(), "workspace must be a contiguous CUDA tensor"
+    others = [v_cache, src_table, dst_table, keep, new_lens, workspace]
+    scale = (None, None, 0, 0, 0)
+    if kv_dtype in (PKV_KV_INT8, PKV_KV_FP4):
+        want = (nb, bs, hkv) if kv_dtype == PKV_KV_INT8 else (nb, bs, hkv, 16)
+        ss = k_scale.stride()
+        assert k_scale.dtype is v_scale.dtype is (_F32 if kv_dtype == PKV_KV_INT8 else _U8) and k_scale.shape == v_scale.shape == want \
+            and v_scale.stride() == ss and ss[3:] in ((), (1,)), "scale caches: fp32 [nb][bs][hkv] (int8) or uint8 [nb][bs][hkv][16] (4-bit)"
+        scale = (k_scale.data_ptr(), v_scale.data_ptr(), ss[0], ss[1], ss[2])
+        others += [k_scale, v_scale]
+    w = (None, 0, 0, 0)
+    if weights is not None:
+        max_ctx = weights.shape[2]
+        assert weights.dtype is _F32 and weights.shape == (R, hkv, max_ctx) and (weights.stride(2) == 1 or max_ctx == 1), \
+            "weights: fp32 [R][hkv][max_ctx], positions contiguous"
+        w = (weights.data_ptr(), weights.stride(0), weights.stride(1), max_ctx)
+        others.append(weights)
+    _launch(lib.pkv_kv_cache_compact, dev, others,
+            (k_cache.data_ptr(), v_cache.data_ptr(), kv_dtype, nb, sb, st, sh, *scale, src_table.data_ptr(), row, cols,
+             dst_table.data_ptr(), drow, dcols, _flat(keep, _I32, R, hkv, budget), new_lens.data_ptr(), R, hkv, budget, bs,
+             d * 2 if kv_dtype == PKV_KV_FP4 else d, *w, workspace.data_ptr(), workspace.nbytes, _err(dev_err, dev),
+             _raw_stream(dev, stream)))
