@@ -1,152 +1,20 @@
-// kv_attn_weights.cu - pkv_kv_attn_weights: the attention weight that each cached key collects.
-//
-//   weights[r][h][pos] = prev + sum over the counted tokens t and the query heads of KV head h of exp(s - lse),
-// s = softmax_scale q . k, lse the query row's log-sum-exp (of the verify partials, or computed here first).
-#include <cuda_bf16.h>
-#include <cuda_fp8.h>
-
-#include "host_common.h"
-#include "sm103.cuh"
+// kv_attn_weights.cu - pkv_kv_attn_weights: the attention weight that each cached key collects (checks, tensor maps and
+// passes; the kernel is in kv_attn_weights.cuh).
+#include "kv_attn_weights.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr int kD = 256;
-constexpr int kMaxCols = 128;  // query columns of one pass
+constexpr size_t kStatBytes = 2 * kWMaxCols * sizeof(float2);  // a CTA's
 
-struct WeightParams {
-  const __nv_bfloat16* q;
-  const uint8_t* k;
-  const float* k_scale;
-  int64_t num_blocks, stride_blk, stride_tok, stride_head, s_stride_blk, s_stride_tok;  // elements
-  const int32_t* block_table;
-  int64_t bt_stride;
-  int32_t max_blocks;
-  const int32_t* seq_lens;
-  const int32_t* q_valid;
-  int32_t num_reqs, T, num_q_heads, num_kv_heads, block_size;
-  float softmax_scale;
-  const float* part_lse;
-  int32_t split_tokens, max_splits;
-  const float* prev;
-  const int32_t* prev_lens;
-  float* weights;
-  int64_t w_stride_req, w_stride_head, max_ctx;
-  float* lse;  // workspace
-  int* dev_err;
-};
-
-__device__ __forceinline__ int keys_of(const WeightParams& p, int len) {
-  return (int)max((int64_t)0, min((int64_t)len, (int64_t)p.max_blocks * p.block_size));
-}
-
-// The warp's dot product of a query row with the key at `pos`, times the key's scale; lane l has 8 elements.
-template <int kFmt>
-__device__ float score(const WeightParams& p, int r, int h, int pos, const float (&q)[8], int lane) {
-  const int col = pos / p.block_size;
-  const int blk = __ldg(p.block_table + (int64_t)r * p.bt_stride + col);
-  if (blk < 0 || blk >= p.num_blocks) {
-    if (lane == 0) record_error(p.dev_err, kErrDeviceBounds);
-    return 0.0f;
-  }
-  const int slot = pos - col * p.block_size;
-  const int64_t at = blk * p.stride_blk + slot * p.stride_tok + h * p.stride_head + lane * 8;
-  float s = 0.0f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    float k;
-    if (kFmt == PKV_KV_BF16) k = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.k)[at + e]);
-    if (kFmt == PKV_KV_INT8) k = (float)reinterpret_cast<const int8_t*>(p.k)[at + e];
-    if (kFmt == PKV_KV_FP8) k = (float)reinterpret_cast<const __nv_fp8_e4m3*>(p.k)[at + e];
-    s = fmaf(q[e], k, s);
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (kFmt == PKV_KV_INT8) s *= __ldg(p.k_scale + blk * p.s_stride_blk + slot * p.s_stride_tok + h);
-  if (kFmt == PKV_KV_FP8) s *= __ldg(p.k_scale);
-  return s * p.softmax_scale;
-}
-
-__device__ __forceinline__ void load_q(const WeightParams& p, int64_t row, float (&q)[8], int lane) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) q[e] = __bfloat162float(p.q[row * kD + lane * 8 + e]);
-}
-
-template <int kFmt>
-__global__ void lse_kernel(const WeightParams p) {
-  const int64_t row = blockIdx.x;  // (r * T + t) * Hq + head
-  const int head = (int)(row % p.num_q_heads), rt = (int)(row / p.num_q_heads), r = rt / p.T, t = rt % p.T;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  const int len = p.seq_lens[r], n = min(keys_of(p, len), len - p.T + t + 1);
-  __shared__ float s_m[32], s_l[32];
-  float m = -INFINITY, l = 0.0f;
-  if (p.part_lse) {
-    if (warp == 0) {
-      const int splits = len > 0 ? min((len - 1) / p.split_tokens + 1, p.max_splits) : 0;
-      const int64_t rows = (int64_t)p.num_reqs * p.T * p.num_q_heads;
-      for (int s = 0; s < splits; ++s) {
-        const float x = p.part_lse[s * rows + row];
-        const float m2 = fmaxf(m, x);
-        if (m2 != -INFINITY) l = l * expf(m - m2) + expf(x - m2);
-        m = m2;
-      }
-    }
-  } else {
-    float q[8];
-    load_q(p, row, q, lane);
-    for (int pos = warp; pos < n; pos += warps) {
-      const float x = score<kFmt>(p, r, head / (p.num_q_heads / p.num_kv_heads), pos, q, lane);
-      const float m2 = fmaxf(m, x);
-      if (m2 != -INFINITY) l = l * expf(m - m2) + expf(x - m2);
-      m = m2;
-    }
-  }
-  s_m[warp] = m;
-  s_l[warp] = l;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    float mm = -INFINITY, ll = 0.0f;
-    for (int w = 0; w < warps; ++w) mm = fmaxf(mm, s_m[w]);
-    for (int w = 0; w < warps; ++w)
-      if (s_l[w] != 0.0f) ll += s_l[w] * expf(s_m[w] - mm);
-    p.lse[row] = ll == 0.0f ? -INFINITY : mm + logf(ll);
-  }
-}
-
-template <int kFmt>
-__global__ void weights_kernel(const WeightParams p) {
-  const int r = blockIdx.y, h = blockIdx.z;
-  const int lane = threadIdx.x & 31;
-  const int group = p.num_q_heads / p.num_kv_heads;
-  const int len = p.seq_lens[r], n = keys_of(p, len);
-  const int valid = p.q_valid ? max(0, min(p.q_valid[r], p.T)) : p.T;
-  if (blockIdx.x == 0 && threadIdx.x == 0 && h == 0 && (len < 0 || len > n || n > p.max_ctx)) record_error(p.dev_err, kErrDeviceBounds);
-  const int n_out = (int)min((int64_t)n, p.max_ctx);
-  const int prev_len = p.prev && p.prev_lens ? p.prev_lens[r] : p.prev ? n : 0;
-  for (int pos = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); pos < n_out; pos += gridDim.x * (blockDim.x >> 5)) {
-    float sum = 0.0f;
-    for (int t = max(0, pos - (len - p.T)); t < valid; ++t)
-      for (int g = 0; g < group; ++g) {
-        const int64_t row = ((int64_t)r * p.T + t) * p.num_q_heads + h * group + g;
-        const float lse = p.lse[row];
-        if (lse == -INFINITY) continue;
-        float q[8];
-        load_q(p, row, q, lane);
-        sum += expf(score<kFmt>(p, r, h, pos, q, lane) - lse);
-      }
-    if (lane == 0) {
-      const int64_t at = (int64_t)r * p.w_stride_req + (int64_t)h * p.w_stride_head + pos;
-      p.weights[at] = pos < prev_len ? p.prev[at] + sum : sum;
-    }
-  }
-}
+size_t lse_bytes(int64_t rows) { return ((size_t)rows * 4 + 255) & ~(size_t)255; }
 
 }  // namespace
 }  // namespace pkv
 
 extern "C" size_t pkv_kv_attn_weights_workspace_bytes(int32_t num_rows, int32_t num_q_heads, int32_t num_ctas) {
   if (num_rows <= 0 || num_q_heads <= 0 || num_ctas <= 0) return 0;
-  return ((size_t)num_rows * (size_t)num_q_heads * 4 + 255) & ~(size_t)255;
+  return pkv::lse_bytes((int64_t)num_rows * num_q_heads) + (size_t)num_ctas * pkv::kStatBytes;
 }
 
 extern "C" pkv_status pkv_kv_attn_weights(const void* q, const void* k_cache, int32_t kv_dtype, const float* k_scale,
@@ -162,7 +30,7 @@ extern "C" pkv_status pkv_kv_attn_weights(const void* q, const void* k_cache, in
   using namespace pkv;
   clear_error();
   const char* name = "kv_attn_weights";
-  PKV_UNSUP(head_dim == kD, "%s: head_dim must be 256 (got %d)", name, head_dim);
+  PKV_UNSUP(head_dim == kWD, "%s: head_dim must be 256 (got %d)", name, head_dim);
   PKV_ARG(kv_dtype >= PKV_KV_BF16 && kv_dtype <= PKV_KV_FP8, "%s: kv_dtype must be bf16, int8 or fp8 (got %d)", name, kv_dtype);
   if (num_reqs == 0) return PKV_OK;
   PKV_ARG(q && k_cache && block_table && seq_lens && weights && workspace && (kv_dtype == PKV_KV_BF16 || k_scale),
@@ -172,11 +40,11 @@ extern "C" pkv_status pkv_kv_attn_weights(const void* q, const void* k_cache, in
               (!part_lse || (split_tokens > 0 && max_splits > 0)),
           "%s: bad size argument", name);
   PKV_UNSUP(num_q_heads % num_kv_heads == 0, "%s: num_q_heads %% num_kv_heads != 0", name);
-  PKV_UNSUP(num_q_heads / num_kv_heads <= kMaxCols, "%s: num_q_heads / num_kv_heads must be at most %d (got %d)", name, kMaxCols,
-            num_q_heads / num_kv_heads);
+  const int group = num_q_heads / num_kv_heads;
+  PKV_UNSUP(group <= kWMaxCols, "%s: num_q_heads / num_kv_heads must be at most %d (got %d)", name, kWMaxCols, group);
   PKV_UNSUP(block_size % 8 == 0, "%s: block_size must be a multiple of 8", name);
   PKV_UNSUP((int64_t)max_blocks * block_size <= INT32_MAX - 127, "%s: max_blocks * block_size must be at most 2^31 - 128", name);
-  PKV_UNSUP((int64_t)num_reqs * T * num_q_heads <= INT32_MAX, "%s: too many query rows", name);
+  PKV_UNSUP((int64_t)num_reqs * T <= INT32_MAX / num_q_heads, "%s: too many query rows", name);
   const int64_t es = kv_dtype == PKV_KV_BF16 ? 2 : 1;
   PKV_ARG(stride_blk > 0 && stride_tok > 0 && stride_head > 0, "%s: strides must be positive", name);
   PKV_ARG(aligned16(q) && aligned16(k_cache) && stride_blk * es % 16 == 0 && stride_tok * es % 16 == 0 && stride_head * es % 16 == 0,
@@ -187,26 +55,62 @@ extern "C" pkv_status pkv_kv_attn_weights(const void* q, const void* k_cache, in
   PKV_ARG(kv_dtype != PKV_KV_INT8 || (scale_stride_blk > 0 && scale_stride_tok >= num_kv_heads),
           "%s: scale strides must be positive, with scale_stride_tok >= num_kv_heads", name);
   PKV_ARG(softmax_scale > 0.0f && softmax_scale <= 3.4e38f, "%s: softmax_scale must be positive and finite", name);
-  const int64_t need = (int64_t)pkv_kv_attn_weights_workspace_bytes(num_reqs * T, num_q_heads, 1);
-  PKV_ARG(aligned16(workspace) && workspace_bytes >= need, "%s: workspace must be 16-byte aligned and hold %lld bytes (got %lld)",
-          name, (long long)need, (long long)workspace_bytes);
-  WeightParams p{static_cast<const __nv_bfloat16*>(q), static_cast<const uint8_t*>(k_cache), k_scale, num_blocks, stride_blk,
-                 stride_tok, stride_head, scale_stride_blk, scale_stride_tok, block_table, bt_stride, max_blocks, seq_lens,
-                 q_valid, num_reqs, T, num_q_heads, num_kv_heads, block_size, softmax_scale, part_lse, split_tokens,
-                 max_splits, prev, prev_lens, weights, w_stride_req, w_stride_head, max_ctx,
-                 static_cast<float*>(workspace), dev_err};
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const unsigned rows = (unsigned)num_reqs * T * num_q_heads;
-  const dim3 grid(1024, num_reqs, num_kv_heads);
-  if (kv_dtype == PKV_KV_BF16) {
-    lse_kernel<PKV_KV_BF16><<<rows, 256, 0, st>>>(p);
-    weights_kernel<PKV_KV_BF16><<<grid, 256, 0, st>>>(p);
-  } else if (kv_dtype == PKV_KV_INT8) {
-    lse_kernel<PKV_KV_INT8><<<rows, 256, 0, st>>>(p);
-    weights_kernel<PKV_KV_INT8><<<grid, 256, 0, st>>>(p);
-  } else {
-    lse_kernel<PKV_KV_FP8><<<rows, 256, 0, st>>>(p);
-    weights_kernel<PKV_KV_FP8><<<grid, 256, 0, st>>>(p);
+  const size_t lse = lse_bytes((int64_t)num_reqs * T * num_q_heads);
+  PKV_ARG(aligned16(workspace) && workspace_bytes >= (int64_t)(lse + kStatBytes),
+          "%s: workspace must be 16-byte aligned and hold %lld bytes at least (got %lld)", name, (long long)(lse + kStatBytes),
+          (long long)workspace_bytes);
+
+  WeightParams p{};
+  int seg = kWTile;
+  while (block_size % seg) seg >>= 1;  // gcd with 128: 8 at least
+  p.seg = seg;
+  p.big_ok = block_size >= kWTile;
+  {
+    const uint64_t dims[4] = {(uint64_t)kWD, (uint64_t)num_kv_heads, (uint64_t)block_size, (uint64_t)num_blocks};
+    const uint64_t strides[3] = {(uint64_t)(stride_head * es), (uint64_t)(stride_tok * es), (uint64_t)(stride_blk * es)};
+    const CUtensorMapDataType type = kv_dtype == PKV_KV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    uint32_t box[4] = {(uint32_t)(128 / es), 1, (uint32_t)seg, 1};
+    pkv_status s = encode_tiled(&p.kmap, type, 4, k_cache, dims, strides, box, "k_cache");
+    if (s != PKV_OK) return s;
+    if (p.big_ok) {
+      box[2] = kWTile;
+      s = encode_tiled(&p.kmap_big, type, 4, k_cache, dims, strides, box, "k_cache");
+      if (s != PKV_OK) return s;
+    }
   }
-  return check_launch(name);
+  p.k_scale = k_scale;
+  p.num_blocks = num_blocks;
+  p.s_stride_blk = scale_stride_blk, p.s_stride_tok = scale_stride_tok;
+  p.block_table = block_table, p.bt_stride = bt_stride, p.max_blocks = max_blocks;
+  p.seq_lens = seq_lens, p.q_valid = q_valid;
+  p.num_reqs = num_reqs, p.T = T, p.group = group, p.num_q_heads = num_q_heads, p.num_kv_heads = num_kv_heads;
+  p.block_size = block_size;
+  p.scale_log2 = softmax_scale * 1.4426950408889634f;
+  p.part_lse = part_lse, p.split_tokens = split_tokens, p.max_splits = max_splits;
+  p.prev = prev, p.prev_lens = prev_lens;
+  p.weights = weights, p.w_stride_req = w_stride_req, p.w_stride_head = w_stride_head, p.max_ctx = max_ctx;
+  p.lse2 = static_cast<float*>(workspace);
+  p.stat = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + lse);
+  p.dev_err = dev_err;
+  p.wait_limit_ns = take_wait_limit_ns();
+  const int64_t room = (workspace_bytes - (int64_t)lse) / (int64_t)kStatBytes;
+  const int ctas = (int)(room < num_sms() ? room : num_sms());
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // more query columns than one pass takes: tokens in passes, each on top of the one before
+  const int most = kWMaxCols / group;
+  for (int t = 0; t < T; t += most) {
+    p.t_base = t;
+    p.tpc = T - t < most ? T - t : most;
+    const uint64_t dims[3] = {(uint64_t)kWD, (uint64_t)num_q_heads, (uint64_t)num_reqs * (uint64_t)T};
+    const uint64_t strides[2] = {(uint64_t)kWD * 2, (uint64_t)num_q_heads * kWD * 2};
+    const uint32_t box[3] = {64, (uint32_t)group, (uint32_t)p.tpc};
+    pkv_status s = encode_tiled(&p.qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, dims, strides, box, "q");
+    if (s != PKV_OK) return s;
+    s = kv_dtype == PKV_KV_BF16 ? run_attn_weights_bf16(p, ctas, st)
+        : kv_dtype == PKV_KV_INT8 ? run_attn_weights_int8(p, ctas, st) : run_attn_weights_fp8(p, ctas, st);
+    if (s != PKV_OK) return s;
+    p.prev = weights;
+    p.prev_lens = nullptr;
+  }
+  return PKV_OK;
 }

@@ -1,0 +1,721 @@
+// kv_attn_weights.cuh - the kernel of pkv_kv_attn_weights: scores of a step's queries against every cached key on the
+// tensor cores, reduced either to each query row's log-sum-exp (kStats) or to each key's collected weight.
+//
+// S^T = K Q^T with the 128 keys of a tile on the MMA's M axis and the query columns (tokens x query heads of the KV
+// head, kN at most) on N, fp32 in tensor memory: a key is a TMEM lane, so a thread has one key's scores and adds its
+// exponentials up by itself; no sum crosses threads. The weights need one log-sum-exp a column, from the verify's
+// partials or from a first launch of the same kernel, where a thread keeps one sum a column and the references are per
+// warp (moved only when a score passes its reference by 2^64, so that a tile has no exchange between threads).
+//
+// The K cache is what is read: bf16 tiles go to the tensor core as TMA leaves them (128-byte swizzle); int8 and e4m3
+// rows are widened to bf16 in registers (every code is a bf16 value) and stored to tensor memory as the A operand, so
+// that the queries stay the bf16 that they are.
+//
+// The tiles of all (request, KV head, 128 keys) are one list, cut into equal ranges, one a CTA, from the lengths on the
+// device. Roles: warp 0 K producer, warp 1 MMA issuer, warp 2 tensor memory, warp 3 Q producer, warps 4-11 two
+// reducing warpgroups (tiles in turn; with kN = 128 the log-sum-exp's take half of the columns each), warps 12 on the
+// widening ones (tiles in turn where there are two).
+#pragma once
+#include <cuda_bf16.h>
+
+#include "host_common.h"
+#include "sm103.cuh"
+
+namespace pkv {
+
+constexpr int kWD = 256;
+constexpr int kWTile = 128;     // keys of a tile
+constexpr int kWMaxCols = 128;  // query columns of a pass
+constexpr int kWBadRing = 16;   // tiles whose bad segments are remembered: more than are ever under way
+
+struct WeightParams {
+  CUtensorMap qmap;   // bf16 [R*T][Hq][256]: dims {256, Hq, R*T}, box {64, group, tpc}
+  CUtensorMap kmap;   // dims {256, Hkv, bs, nb}, box {128 bytes, 1, seg, 1}
+  CUtensorMap kmap_big;  // box {128 bytes, 1, 128, 1}: a whole tile inside one block
+  int32_t big_ok, seg;
+  const float* k_scale;
+  int64_t num_blocks, s_stride_blk, s_stride_tok;
+  const int32_t* block_table;
+  int64_t bt_stride;
+  int32_t max_blocks;
+  const int32_t* seq_lens;
+  const int32_t* q_valid;
+  int32_t num_reqs, T, group, num_q_heads, num_kv_heads, block_size;
+  int32_t t_base, tpc;  // tokens of this pass: t_base .. t_base + tpc - 1
+  float scale_log2;
+  const float* part_lse;
+  int32_t split_tokens, max_splits;
+  const float* prev;
+  const int32_t* prev_lens;
+  float* weights;
+  int64_t w_stride_req, w_stride_head, max_ctx;
+  float2* stat;   // workspace: [CTAs][2][kWMaxCols] (reference, sum) of the units that a CTA has a part of
+  float* lse2;    // workspace: [R*T*Hq], base 2, of the units that one CTA has whole
+  int* dev_err;
+  uint64_t wait_limit_ns;
+};
+
+template <int kFmt, int kN>
+struct WGeo {
+  static constexpr bool kWide = kFmt == PKV_KV_BF16;   // no widening
+  static constexpr int kConv = kWide ? 0 : kN == 128 ? 1 : 2;  // widening warpgroups
+  static constexpr int kThreads = 384 + 128 * kConv;
+  static constexpr int kRowBytes = kWide ? 512 : 256;
+  static constexpr int kChunks = kRowBytes / 128;      // 128-byte columns of a K tile
+  static constexpr int kChunk = kWTile * 128;
+  static constexpr int kStage = kChunks * kChunk;      // 64 or 32 KB
+  static constexpr int kStages = kWide ? (kN == 128 ? 2 : 3) : 4;
+  static constexpr int kQChunk = kN * 128;             // bf16 [kN rows][64]
+  static constexpr int kQBytes = 4 * kQChunk;
+  static constexpr int kQBufs = (!kWide && kN == 32) ? 2 : 1;
+  static constexpr int kOffK = kQBufs * kQBytes;
+  static constexpr int kTiles = kOffK + kStages * kStage;
+  static constexpr int kHalf = kN == 128 ? 64 : kN;    // columns of a warp's sums
+  static constexpr uint32_t kColA = 0;                 // widened K: 2 x 128 columns
+  static constexpr uint32_t kColS = kWide ? 0 : 256;   // 2 x kN columns
+  static constexpr uint32_t kTmemCols = kWide ? (2 * kN <= 64 ? 64 : 256) : 512;
+};
+
+template <int kFmt, int kN>
+struct alignas(16) WShared {
+  using G = WGeo<kFmt, kN>;
+  uint64_t q_full[2], q_free[2];
+  uint64_t k_full[G::kStages], k_free[G::kStages];
+  uint64_t a_ready[2], a_free[2];
+  uint64_t s_full[2], s_free[2];
+  uint64_t drain;
+  uint32_t armed_k[G::kStages], armed_q[2];
+  uint32_t bad[kWBadRing];
+  uint32_t tmem_base;
+  int abort;
+  int start_r, start_h, start_tile, ctas;
+  long long first, last;  // this CTA's tiles in the list
+  long long total;
+  alignas(16) float col[2][kN];              // per reducing group: minus the column's log-sum-exp (weights)
+  alignas(16) float ref[8][G::kHalf];        // per reducing warp: the columns' references (log-sum-exps)
+  alignas(16) float2 part[2][8][G::kHalf];   // per unit parity and warp: (reference, sum)
+};
+
+// A place in the list of tiles.
+struct WWalk {
+  int r, h, tile, tiles, n;
+  __device__ __forceinline__ void length(const WeightParams& p) {
+    const int64_t most = (int64_t)p.max_blocks * p.block_size;
+    n = (int)max((int64_t)0, min((int64_t)__ldg(p.seq_lens + r), most));
+    tiles = (n + kWTile - 1) / kWTile;
+  }
+  __device__ __forceinline__ void start(const WeightParams& p, int r0, int h0, int t0) {
+    r = r0, h = h0, tile = t0;
+    if (r < p.num_reqs) length(p);
+  }
+  // to the next tile; r = num_reqs past the last
+  __device__ __forceinline__ void next(const WeightParams& p) {
+    if (++tile < tiles) return;
+    tile = 0;
+    if (++h < p.num_kv_heads) return;
+    h = 0;
+    for (++r; r < p.num_reqs; ++r) {
+      length(p);
+      if (tiles) return;
+    }
+  }
+};
+
+__device__ __forceinline__ bool w_elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+__device__ __forceinline__ void w_bar(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+
+__device__ __forceinline__ uint32_t bf16x2_sub(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// 4 int8 codes -> 4 bf16 integers, exact: a code is its low seven bits minus 128 where its sign bit is set, and bf16
+// bits 0x4300 | x are 128 + x for x < 128, 0x4380 is 256.
+__device__ __forceinline__ void widen4_int8(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t a = __byte_perm(w, 0, 0x4140), b = __byte_perm(w, 0, 0x4342);  // a byte in each half
+  lo = bf16x2_sub((a & 0x007f007fu) | 0x43004300u, (a & 0x00800080u) | 0x43004300u);
+  hi = bf16x2_sub((b & 0x007f007fu) | 0x43004300u, (b & 0x00800080u) | 0x43004300u);
+}
+// 4 e4m3 codes -> 4 bf16 values, exact: the code's exponent and mantissa at bf16's low exponent bits are the value
+// times 2^-120. NaN codes (0x7f) come out as 480 and are told apart by the caller.
+__device__ __forceinline__ void widen4_e4m3(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);  // a byte in each half's upper byte
+  lo = bf16x2_mul((a & 0x80008000u) | ((a >> 4) & 0x07f007f0u), 0x7b807b80u);
+  hi = bf16x2_mul((b & 0x80008000u) | ((b >> 4) & 0x07f007f0u), 0x7b807b80u);
+}
+
+// Sums over the warp's lanes of kC (16 or 32 at a time) columns: lane l gets column l's (kC = 16: l & 15's).
+template <int kC>
+__device__ __forceinline__ float w_reduce(float (&v)[kC], int lane) {
+#pragma unroll
+  for (int o = kC / 2; o >= 1; o >>= 1) {
+    const bool upper = (lane & o) != 0;
+#pragma unroll
+    for (int q = 0; q < o; ++q) {
+      const float keep = upper ? v[q + o] : v[q];
+      const float send = upper ? v[q] : v[q + o];
+      v[q] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+  float x = v[0];
+#pragma unroll
+  for (int o = kC; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+// The list's owner of tile x when `ctas` CTAs share `total` tiles as [c total / ctas, (c + 1) total / ctas).
+__device__ __forceinline__ int w_owner(long long x, long long total, int ctas) { return (int)(((x + 1) * ctas - 1) / total); }
+
+template <int kFmt, int kN, bool kStats>
+__global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_kernel(const __grid_constant__ WeightParams p) {
+  using G = WGeo<kFmt, kN>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  WShared<kFmt, kN>& sh = *reinterpret_cast<WShared<kFmt, kN>*>(smem + G::kTiles);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t wl = p.wait_limit_ns;
+  // every tile's scores are read by one reducing group, or by both where each has half of the columns
+  constexpr bool kBoth = kStats && kN == 128;
+
+  if (warp == 0) {
+    // the list's length and this CTA's range of it
+    const int64_t most = (int64_t)p.max_blocks * p.block_size;
+    long long total = 0;
+    bool odd = false;
+    for (int r = lane; r < p.num_reqs; r += 32) {
+      const int len = __ldg(p.seq_lens + r);
+      const int n = (int)max((int64_t)0, min((int64_t)len, most));
+      odd |= len < 0 || len > most || (!kStats && len > p.max_ctx);
+      total += (n + kWTile - 1) / kWTile;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    total *= p.num_kv_heads;
+    odd = __any_sync(0xffffffffu, odd);
+    // a tile each, where there are fewer tiles than CTAs (so that none between a unit's CTAs is without a part)
+    const int ctas = (int)min((long long)gridDim.x, max(total, 1ll));
+    const bool idle = blockIdx.x >= ctas;
+    const long long first = idle ? total : total * blockIdx.x / ctas, last = idle ? total : total * (blockIdx.x + 1) / ctas;
+    int at_r = p.num_reqs, at_h = 0, at_t = 0;
+    long long before = 0;  // tiles of the requests before
+    if (first < last)
+      for (int r0 = 0; r0 < p.num_reqs; r0 += 32) {
+        const int r = r0 + lane;
+        long long mine = 0;
+        int tiles = 0;
+        if (r < p.num_reqs) {
+          const int n = (int)max((int64_t)0, min((int64_t)__ldg(p.seq_lens + r), most));
+          tiles = (n + kWTile - 1) / kWTile;
+          mine = (long long)tiles * p.num_kv_heads;
+        }
+        long long run = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, run, o);
+          if (lane >= o) run += y;
+        }
+        run += before;
+        const uint32_t past = __ballot_sync(0xffffffffu, run > first);
+        if (past) {
+          const int l = __ffs(past) - 1;
+          const int in = (int)__shfl_sync(0xffffffffu, first - (run - mine), l);
+          tiles = __shfl_sync(0xffffffffu, tiles, l);
+          at_r = r0 + l;
+          at_h = in / tiles;
+          at_t = in - at_h * tiles;
+          break;
+        }
+        before = __shfl_sync(0xffffffffu, run, 31);
+      }
+    if (lane == 0) {
+      sh.first = first, sh.last = last, sh.total = total, sh.ctas = ctas;
+      sh.start_r = at_r, sh.start_h = at_h, sh.start_tile = at_t;
+      if (odd && blockIdx.x == 0) record_error(p.dev_err, kErrDeviceBounds);
+    }
+  } else if (warp == 1 && lane == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.q_full[i], 1);
+      mbar_init(&sh.q_free[i], 1);
+      mbar_init(&sh.a_ready[i], 128);
+      mbar_init(&sh.a_free[i], 1);
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.s_free[i], kBoth ? 256 : 128);
+      sh.armed_q[i] = 0;
+    }
+    for (int i = 0; i < G::kStages; ++i) {
+      mbar_init(&sh.k_full[i], 1);
+      mbar_init(&sh.k_free[i], G::kWide ? 1 : 128);
+      sh.armed_k[i] = 0;
+    }
+    mbar_init(&sh.drain, 1);
+    sh.abort = 0;
+    fence_mbar_init();
+  } else if (warp == 2) {
+    tmem_alloc(&sh.tmem_base, G::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem_base;
+  volatile int* abort = &sh.abort;
+  const int count = (int)(sh.last - sh.first);
+  WWalk at;
+  at.start(p, sh.start_r, sh.start_h, sh.start_tile);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------------------------ K producer
+    // the table entries of a tile's segments, a lane each, are looked up a tile ahead
+    const int nseg = kWTile / p.seg;
+    auto look_up = [&](const WWalk& w, int& slot) -> int {
+      const int pos = w.tile * kWTile + lane * p.seg;
+      slot = 0;
+      if (lane >= nseg || pos >= w.n) return -1;
+      const int col = pos / p.block_size;
+      slot = pos - col * p.block_size;
+      const int blk = __ldg(p.block_table + (int64_t)w.r * p.bt_stride + col);
+      return blk < 0 || (int64_t)blk >= p.num_blocks ? -2 : blk;
+    };
+    int slot = 0, blk = -1, st = 0, round = 0;
+    if (count) blk = look_up(at, slot);
+    for (int i = 0; i < count; ++i) {
+      uint8_t* stage = smem + G::kOffK + st * G::kStage;
+      const int h = at.h, my_blk = blk, my_slot = slot;
+      at.next(p);
+      if (i + 1 < count) blk = look_up(at, slot);
+      bool ok = true;
+      if (lane == 0 && round) ok = mbar_wait_suspend(&sh.k_free[st], (round - 1) & 1, abort, wl);
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      const uint32_t bad = __ballot_sync(0xffffffffu, my_blk == -2);
+      const uint32_t loaded = __popc(__ballot_sync(0xffffffffu, my_blk >= 0));
+      const int blk0 = __shfl_sync(0xffffffffu, my_blk, 0), slot0 = __shfl_sync(0xffffffffu, my_slot, 0);
+      const bool big = p.big_ok && blk0 >= 0 && slot0 + kWTile <= p.block_size;  // the tile lies in one block
+      if (lane == 0) {
+        if (bad) record_error(p.dev_err, kErrDeviceBounds);
+        sh.bad[i & (kWBadRing - 1)] = bad;
+        mbar_arm_tx(&sh.k_full[st], (big ? (uint32_t)kWTile : loaded * (uint32_t)p.seg) * (uint32_t)G::kRowBytes, &sh.armed_k[st]);
+      }
+      __syncwarp();
+      constexpr int kInner = G::kWide ? 64 : 128;  // elements of a 128-byte column
+      if (big) {
+        if (w_elect()) {
+#pragma unroll
+          for (int c = 0; c < G::kChunks; ++c)
+            tma_load_4d(stage + c * G::kChunk, &p.kmap_big, &sh.k_full[st], c * kInner, h, slot0, blk0);
+        }
+      } else if (my_blk >= 0) {
+#pragma unroll
+        for (int c = 0; c < G::kChunks; ++c)
+          tma_load_4d(stage + c * G::kChunk + lane * p.seg * 128, &p.kmap, &sh.k_full[st], c * kInner, h, my_slot, my_blk);
+      }
+      __syncwarp();
+      if (++st == G::kStages) st = 0, ++round;
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------------------------------ Q producer
+    int units = 0;
+    for (int i = 0; i < count; ++i, at.next(p)) {
+      if (i && at.tile) continue;
+      const int b = units % G::kQBufs, round = units / G::kQBufs;
+      bool ok = true;
+      if (lane == 0) {
+        if (round) ok = mbar_wait_suspend(&sh.q_free[b], (round - 1) & 1, abort, wl);
+        if (ok) {
+          mbar_arm_tx(&sh.q_full[b], 512u * (uint32_t)(p.tpc * p.group), &sh.armed_q[b]);
+          for (int c = 0; c < 4; ++c)
+            tma_load_3d(smem + b * G::kQBytes + c * G::kQChunk, &p.qmap, &sh.q_full[b], c * 64, at.h * p.group, at.r * p.T + p.t_base);
+        }
+      }
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      ++units;
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------------------------ MMA issuer
+    constexpr uint32_t id = idesc_f16(128, kN, true, false, false);
+    int st = 0, round = 0, units = -1;
+    for (int i = 0; i < count; ++i) {
+      const bool first = i == 0 || at.tile == 0;
+      if (first) ++units;
+      const int b = units % G::kQBufs;
+      const bool last = i + 1 == count || at.tile + 1 == at.tiles;
+      at.next(p);
+      bool ok = true;
+      if (first) ok = mbar_wait_suspend(&sh.q_full[b], (units / G::kQBufs) & 1, abort, wl);
+      if (ok && i >= 2) ok = mbar_wait_suspend(&sh.s_free[i & 1], ((i >> 1) - 1) & 1, abort, wl);
+      if (ok) ok = G::kWide ? mbar_wait_suspend(&sh.k_full[st], round & 1, abort, wl)
+                            : mbar_wait_suspend(&sh.a_ready[i & 1], (i >> 1) & 1, abort, wl);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const uint32_t q_base = smem_u32(smem) + b * G::kQBytes, k_base = smem_u32(smem) + G::kOffK + st * G::kStage;
+      const uint32_t d = tmem + G::kColS + (i & 1) * kN;
+      if (w_elect()) {
+#pragma unroll
+        for (int ks = 0; ks < 16; ++ks) {
+          const uint64_t qd = smem_desc(q_base + (ks >> 2) * G::kQChunk + (ks & 3) * 32, 16, 1024);
+          if constexpr (G::kWide)
+            umma_f16_ss(d, smem_desc(k_base + (ks >> 2) * G::kChunk + (ks & 3) * 32, 16, 1024), qd, id, ks > 0);
+          else
+            umma_f16_ts(d, tmem + G::kColA + (i & 1) * 128 + ks * 8, qd, id, ks > 0);
+        }
+        umma_commit(&sh.s_full[i & 1]);
+        umma_commit(G::kWide ? &sh.k_free[st] : &sh.a_free[i & 1]);
+        if (last) umma_commit(&sh.q_free[b]);
+      }
+      __syncwarp();
+      if (++st == G::kStages) st = 0, ++round;
+    }
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------------------------------ widening
+    // thread k has key row k: 256 codes -> 128 tensor-memory columns of its lane. Rows that are not loaded hold what the
+    // stage had before; a row meets its own lane's scores only, and those are masked.
+    if constexpr (!G::kWide) {
+      const int grp = (warp - 12) >> 2;
+      const int k = (warp & 3) * 32 + lane;
+      const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+      for (int i = grp; i < count; i += G::kConv) {
+        const int st = i % G::kStages;
+        const uint8_t* row = smem + G::kOffK + st * G::kStage + k * 128;
+        bool ok = mbar_wait_suspend(&sh.k_full[st], (i / G::kStages) & 1, abort, wl);
+        if (ok && i >= 2) ok = mbar_wait_suspend(&sh.a_free[i & 1], ((i >> 1) - 1) & 1, abort, wl);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        const uint32_t a = tmem + lane_off + G::kColA + (i & 1) * 128;
+        uint32_t nan = 0;
+#pragma unroll
+        for (int w8 = 0; w8 < 8; ++w8) {  // 32 codes, 16 columns a step
+          uint32_t o[16];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int piece = 2 * (w8 & 3) + j;
+            const uint4 v = *reinterpret_cast<const uint4*>(row + (w8 >> 2) * G::kChunk + ((piece ^ (k & 7)) * 16));
+            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (kFmt == PKV_KV_INT8) {
+                widen4_int8(x[e], o[8 * j + 2 * e], o[8 * j + 2 * e + 1]);
+              } else {
+                widen4_e4m3(x[e], o[8 * j + 2 * e], o[8 * j + 2 * e + 1]);
+                nan |= (x[e] & 0x7f7f7f7fu) + 0x01010101u;
+              }
+            }
+          }
+          tmem_st_32x32b_x16(a + 16 * w8, o);
+        }
+        if (kFmt == PKV_KV_FP8) {
+          // a NaN code anywhere makes every score of the key NaN: one NaN element does
+          if (__any_sync(0xffffffffu, (nan & 0x80808080u) != 0)) {
+            tmem_wait_st();
+            const uint32_t x = tmem_ld_32x32b_x1(a);
+            tmem_wait_ld();
+            tmem_st_32x32b_x1(a, nan & 0x80808080u ? 0x7fff7fffu : x);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&sh.a_ready[i & 1]);
+        mbar_arrive(&sh.k_free[st]);
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------------------------------ reducing
+    const int grp = (warp - 4) >> 2, quarter = warp & 3;
+    const int k = quarter * 32 + lane;  // this thread's key of a tile
+    const int kseg = k / p.seg;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const int c_first = kBoth ? grp * 64 : 0;  // the group's first column
+    const float per_tensor = kFmt == PKV_KV_FP8 ? __ldg(p.k_scale) : 1.0f;
+    bool dead = false;
+    int units = 0;
+
+    // int8: the scales of this thread's keys, loaded two tiles of its own ahead of the block ids' four
+    WWalk ahead = at;
+    int ahead_i = 0;
+    int blk_n = -1, slot_n = 0, h_n = 0;  // of the next but one tile of this group
+    float sc_0 = 0.0f, sc_1 = 0.0f;
+    constexpr int kStride = kBoth ? 1 : 2;  // tiles from one of this group's to the next
+    auto block_ahead = [&]() {
+      blk_n = -1;
+      if (ahead_i < count) {
+        const int pos = ahead.tile * kWTile + k;
+        if (pos < ahead.n) {
+          const int col = pos / p.block_size;
+          slot_n = pos - col * p.block_size;
+          h_n = ahead.h;
+          const int blk = __ldg(p.block_table + (int64_t)ahead.r * p.bt_stride + col);
+          blk_n = blk < 0 || (int64_t)blk >= p.num_blocks ? -1 : blk;
+        }
+      }
+      for (int s = 0; s < kStride; ++s, ++ahead_i)
+        if (ahead_i < count) ahead.next(p);
+    };
+    auto scale_ahead = [&]() {
+      return blk_n >= 0 ? __ldg(p.k_scale + (int64_t)blk_n * p.s_stride_blk + (int64_t)slot_n * p.s_stride_tok + h_n) : 0.0f;
+    };
+    if (kFmt == PKV_KV_INT8) {
+      if (!kBoth && grp == 1 && count) ahead.next(p), ++ahead_i;
+      block_ahead();
+      sc_0 = scale_ahead();
+      block_ahead();
+      sc_1 = scale_ahead();
+      block_ahead();
+    }
+
+    float l[kStats ? G::kHalf : 1];  // a thread's part of the columns' sums
+    int prefix = 0, nq = 0, prev_len = 0;
+    for (int i = 0; i < count; ++i) {
+      const bool first = i == 0 || at.tile == 0, last = i + 1 == count || at.tile + 1 == at.tiles;
+      if (first) {
+        prefix = __ldg(p.seq_lens + at.r) - p.T;  // token t sits at position prefix + t
+        if constexpr (kStats) {
+          nq = p.tpc * p.group;
+#pragma unroll
+          for (int c = 0; c < G::kHalf; ++c) l[c] = 0.0f;
+          for (int c = lane; c < G::kHalf; c += 32) sh.ref[warp - 4][c] = -1e30f;
+          __syncwarp();
+        } else {
+          const int valid = p.q_valid ? min(__ldg(p.q_valid + at.r), p.T) : p.T;
+          nq = max(0, min(valid - p.t_base, p.tpc)) * p.group;
+          prev_len = !p.prev ? 0 : p.prev_lens ? __ldg(p.prev_lens + at.r) : at.n;
+          w_bar(1 + grp, 128);  // the group has read the last unit's columns
+          if (k < kN) {
+            float c = INFINITY;
+            if (k < nq) {
+              const int t = p.t_base + k / p.group;
+              const int64_t row = ((int64_t)at.r * p.T + t) * p.num_q_heads + (int64_t)at.h * p.group + k % p.group;
+              if (p.part_lse) {
+                const int64_t rows = (int64_t)p.num_reqs * p.T * p.num_q_heads;
+                const int splits = min((at.n - 1) / p.split_tokens + 1, p.max_splits);
+                float m = -INFINITY, sum = 0.0f;
+                for (int s = 0; s < splits; ++s) {
+                  const float x = __ldg(p.part_lse + s * rows + row);
+                  if (x > m) {
+                    sum = sum * expf(m - x) + 1.0f;
+                    m = x;
+                  } else if (x != -INFINITY) {
+                    sum += x == m ? 1.0f : expf(x - m);  // (NaN comes in here)
+                  }
+                }
+                // m log2(e) in two parts, so that only the last addition rounds
+                const float hi = m * 1.4426950408889634f, lo = fmaf(m, 1.4426950408889634f, -hi) + m * 1.925963033500412e-8f;
+                if (sum != 0.0f && m < INFINITY) c = hi + (lo + log2f(sum));
+              } else {
+                // the unit's tiles, and the CTAs that have them
+                const long long u0 = sh.first + i - at.tile, u1 = u0 + at.tiles;
+                const int c0 = w_owner(u0, sh.total, sh.ctas), c1 = w_owner(u1 - 1, sh.total, sh.ctas);
+                if (c0 == c1) {
+                  c = __ldcg(p.lse2 + row);
+                } else {
+                  float m = -INFINITY, sum = 0.0f;
+                  for (int o = c0; o <= c1; ++o) {
+                    const int which = u0 > sh.total * o / sh.ctas;
+                    const float2 x = __ldcg(p.stat + ((int64_t)o * 2 + which) * kWMaxCols + k);
+                    if (x.y == 0.0f) continue;
+                    if (x.x > m) {
+                      sum = sum * exp2f(m - x.x) + x.y;
+                      m = x.x;
+                    } else {
+                      sum += x.y * exp2f(x.x - m);
+                    }
+                  }
+                  c = sum != 0.0f ? m + log2f(sum) : INFINITY;
+                }
+              }
+            }
+            sh.col[grp][k] = -c;
+          }
+          w_bar(1 + grp, 128);
+        }
+      }
+      if (kBoth || (i & 1) == grp) {
+        const int key = at.tile * kWTile + k;
+        float f = p.scale_log2 * per_tensor;
+        if (kFmt == PKV_KV_INT8) {
+          f *= sc_0;
+          sc_0 = sc_1;
+          sc_1 = scale_ahead();
+          block_ahead();
+        }
+        float before = 0.0f;
+        int64_t out = 0;
+        bool writes = false;
+        if constexpr (!kStats) {
+          out = (int64_t)at.r * p.w_stride_req + (int64_t)at.h * p.w_stride_head + key;
+          writes = key < at.n && key < p.max_ctx;
+          if (writes && key < prev_len) before = p.prev[out];
+        }
+        if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait_suspend(&sh.s_full[i & 1], (i >> 1) & 1, abort, wl));
+        if (!dead) {
+          tc_fence_after();
+          const uint32_t s_addr = tmem + lane_off + G::kColS + (i & 1) * kN + c_first;
+          // every key of the tile is seen by every column
+          const bool open = at.tile * kWTile + kWTile <= at.n && at.tile * kWTile + kWTile - 1 <= prefix + p.t_base;
+          const bool bad_key = (sh.bad[i & (kWBadRing - 1)] >> kseg) & 1u;
+          const int behind = key < at.n ? key - prefix - p.t_base : INT_MAX;  // columns of earlier tokens do not see it
+          float sum = 0.0f;
+#pragma unroll
+          for (int cc = 0; cc < (kStats ? G::kHalf : kN) / 16; ++cc) {
+            const int c0 = cc * 16;
+            if (c_first + c0 < nq) {
+              uint32_t v[16];
+              tmem_ld_32x32b_x16(s_addr + c0, v);
+              tmem_wait_ld();
+              float t[16];
+#pragma unroll
+              for (int q = 0; q < 16; ++q) t[q] = bad_key ? 0.0f : __uint_as_float(v[q]);
+              if constexpr (kStats) {
+                float* ref = sh.ref[warp - 4] + c0;
+                float m = -INFINITY;
+                if (open && c_first + c0 + 16 <= nq) {
+#pragma unroll
+                  for (int q = 0; q < 16; ++q) t[q] *= f;
+                } else {
+#pragma unroll
+                  for (int q = 0; q < 16; ++q) {
+                    const int c = c_first + c0 + q;
+                    t[q] = c < nq && behind <= c / p.group ? t[q] * f : -INFINITY;
+                  }
+                }
+#pragma unroll
+                for (int q = 0; q < 16; ++q) m = fmaxf(m, t[q] - ref[q]);
+                if (__any_sync(0xffffffffu, m > 64.0f)) {  // a reference moves: once a unit, as a rule
+#pragma unroll
+                  for (int q = 0; q < 16; ++q) {
+                    float x = t[q];
+#pragma unroll
+                    for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+                    const float old = ref[q], now = fmaxf(old, x);
+                    __syncwarp();
+                    l[c0 + q] *= ex2_approx(old - now);
+                    if (lane == 0) ref[q] = now;
+                  }
+                  __syncwarp();
+                }
+#pragma unroll
+                for (int q = 0; q < 16; ++q) l[c0 + q] += ex2_approx(t[q] - ref[q]);
+              } else {
+                const float* col = sh.col[grp] + c0;
+                if (open && c0 + 16 <= nq) {
+#pragma unroll
+                  for (int q = 0; q < 16; ++q) sum += ex2_approx(fmaf(t[q], f, col[q]));
+                } else {
+#pragma unroll
+                  for (int q = 0; q < 16; ++q) {
+                    const int c = c0 + q;
+                    const float e = ex2_approx(fmaf(t[q], f, col[q]));
+                    sum += c < nq && behind <= c / p.group ? e : 0.0f;
+                  }
+                }
+              }
+            }
+          }
+          tc_fence_before();
+          mbar_arrive(&sh.s_free[i & 1]);
+          if constexpr (!kStats) {
+            if (writes) p.weights[out] = before + sum;
+          }
+        }
+      }
+      if constexpr (kStats) {
+        if (last) {  // the warps' sums of this unit meet; both groups come here for every unit
+          float2* mine = sh.part[units & 1][warp - 4];
+#pragma unroll
+          for (int c0 = 0; c0 < G::kHalf; c0 += 32) {
+            float x[32];
+#pragma unroll
+            for (int q = 0; q < 32; ++q) x[q] = l[c0 + q];
+            const float y = w_reduce<32>(x, lane);
+            mine[c0 + lane] = make_float2(sh.ref[warp - 4][c0 + lane], y);
+          }
+          w_bar(3, 256);
+          const int c = (warp - 4) * 32 + lane;
+          if (c < nq && !dead) {
+            const int w0 = kBoth ? (c >> 6) * 4 : 0, w1 = kBoth ? w0 + 4 : 8;
+            const int cl = kBoth ? c & 63 : c;
+            float m = -INFINITY, sum = 0.0f;
+            for (int w = w0; w < w1; ++w) {
+              const float2 x = sh.part[units & 1][w][cl];
+              if (x.y != 0.0f) m = fmaxf(m, x.x);
+            }
+            for (int w = w0; w < w1; ++w) {
+              const float2 x = sh.part[units & 1][w][cl];
+              if (x.y != 0.0f) sum += x.y * exp2f(x.x - m);
+            }
+            const long long u0 = sh.first + i - at.tile;
+            if (u0 >= sh.first && u0 + at.tiles <= sh.last) {
+              const int64_t row = ((int64_t)at.r * p.T + p.t_base + c / p.group) * p.num_q_heads + (int64_t)at.h * p.group + c % p.group;
+              p.lse2[row] = sum != 0.0f ? m + log2f(sum) : INFINITY;
+            } else {
+              p.stat[((int64_t)blockIdx.x * 2 + (u0 > sh.first)) * kWMaxCols + c] = make_float2(m, sum);
+            }
+          }
+          ++units;
+        }
+      }
+      at.next(p);
+    }
+  }
+
+  tc_fence_before();
+  // every role has left its loop; the flag's final value, the same for every thread
+  const bool gave_up = __syncthreads_or(*abort != 0);
+  if (gave_up) {
+    // what this CTA still has in flight ends before its tensor memory is freed: the copies armed, the MMAs issued
+    if (warp == 0 && lane == 0)
+      for (int s = 0; s < G::kStages; ++s) drain_armed(&sh.k_full[s], sh.armed_k[s]);
+    if (warp == 3 && lane == 0)
+      for (int b = 0; b < G::kQBufs; ++b) drain_armed(&sh.q_full[b], sh.armed_q[b]);
+    if (warp == 1) {
+      if (w_elect()) {
+        umma_commit(&sh.drain);
+        mbar_wait_drain(&sh.drain, 0);
+      }
+      __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+  }
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, G::kTmemCols);
+  }
+  if (threadIdx.x == 0 && gave_up) record_error(p.dev_err, kErrTimeout);
+}
+
+template <int kFmt, int kN, bool kStats>
+inline pkv_status launch_attn_weights(const WeightParams& p, int ctas, cudaStream_t stream) {
+  using G = WGeo<kFmt, kN>;
+  constexpr int kSmem = 1024 + G::kTiles + (int)sizeof(WShared<kFmt, kN>);
+  static_assert(kSmem <= 227 * 1024, "dynamic shared memory of one CTA");
+  static std::atomic<uint64_t> attr_done{0};
+  once_per_device(attr_done, [] {
+    cudaFuncSetAttribute(kv_attn_weights_kernel<kFmt, kN, kStats>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  });
+  kv_attn_weights_kernel<kFmt, kN, kStats><<<ctas, G::kThreads, kSmem, stream>>>(p);
+  return check_launch("kv_attn_weights");
+}
+
+// One pass over the columns of p: the log-sum-exps first where they are not given, then the weights.
+template <int kFmt>
+inline pkv_status run_attn_weights(const WeightParams& p, int ctas, cudaStream_t stream) {
+  const bool few = p.tpc * p.group <= 32;
+  pkv_status s = PKV_OK;
+  if (!p.part_lse)
+    s = few ? launch_attn_weights<kFmt, 32, true>(p, ctas, stream) : launch_attn_weights<kFmt, 128, true>(p, ctas, stream);
+  if (s != PKV_OK) return s;
+  return few ? launch_attn_weights<kFmt, 32, false>(p, ctas, stream) : launch_attn_weights<kFmt, 128, false>(p, ctas, stream);
+}
+
+pkv_status run_attn_weights_bf16(const WeightParams& p, int ctas, cudaStream_t stream);
+pkv_status run_attn_weights_int8(const WeightParams& p, int ctas, cudaStream_t stream);
+pkv_status run_attn_weights_fp8(const WeightParams& p, int ctas, cudaStream_t stream);
+
+}  // namespace pkv

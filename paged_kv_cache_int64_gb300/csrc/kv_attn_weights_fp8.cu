@@ -1,0 +1,8 @@
+// kv_attn_weights_fp8.cu - the kernels of pkv_kv_attn_weights over a cache of this type (a file each, compiled side by side).
+#include "kv_attn_weights.cuh"
+
+namespace pkv {
+pkv_status run_attn_weights_fp8(const WeightParams& p, int ctas, cudaStream_t stream) {
+  return run_attn_weights<PKV_KV_FP8>(p, ctas, stream);
+}
+}  // namespace pkv
