@@ -1,15 +1,23 @@
 // kv_cache_compact.cu - pkv_kv_cache_compact: the rows that stay move to the front of their cache.
 //
 // Row j of (request r, KV head h) becomes row keep[r][h][j], in K, in V, in the scale caches and in the weights; in
-// place, or into other blocks. keep ascends, so keep[j] >= j: a row moves down or stays.
+// place, or into other blocks. keep ascends strictly, so keep[j] >= j: a row moves down or stays.
+//
+// A chunk is kRows rows of a (request, KV head): a CTA reads them all into registers and then writes them. In place, a
+// chunk's destinations are sources of earlier chunks only (of chunks whose j is below: keep[j'] = j has j' <= j), so it
+// writes once those have been read: each chunk raises a flag when it has its rows in registers, and waits, before it
+// writes, for the flags of the at most two chunks whose sources can lie in its destinations. The flags depend on
+// nothing but a chunk's own loads, and a CTA takes its chunks in ascending order, all CTAs resident (cooperative
+// launch): every wait ends. The waits are bounded all the same.
 #include "host_common.h"
 #include "sm103.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kRows = 64;  // rows of a chunk
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kRows = 32;  // rows of a chunk
 
 struct CompactParams {
   uint8_t* k;
@@ -24,106 +32,203 @@ struct CompactParams {
   int32_t src_blocks, dst_blocks;
   const int32_t* keep;
   const int32_t* new_lens;
-  int32_t num_kv_heads, budget, block_size;
+  int32_t num_kv_heads, budget, block_size, chunks;
+  int64_t total;  // chunks of all units
   float* weights;
   int64_t w_stride_req, w_stride_head, max_ctx;
+  uint32_t* flags;
   int* dev_err;
+  uint64_t wait_limit_ns;
 };
 
-struct Row {
-  int blk, slot;  // blk < 0: the row does not move
+// A row of a chunk: where it comes from and goes to.
+struct Move {
+  int src_blk, src_slot, dst_blk, dst_slot;  // src_blk < 0: it does not move
+  int from;  // its position; -1: the weight does not move
 };
+
+__device__ __forceinline__ uint32_t load_acquire(const uint32_t* p) {
+  uint32_t x;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
+  return x;
+}
+__device__ __forceinline__ void store_release(uint32_t* p, uint32_t x) {
+  asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(x) : "memory");
+}
+
+// Row j of the unit (r, h) with n rows.
+__device__ __forceinline__ Move find_move(const CompactParams& p, int unit, int r, int j, int n) {
+  Move m{-1, 0, -1, 0, -1};
+  if (j >= n) return m;
+  const int32_t* keep = p.keep + (int64_t)unit * p.budget;
+  const int from = __ldg(keep + j), above = j ? __ldg(keep + j - 1) : -1;
+  const int col = from / p.block_size, dcol = j / p.block_size;
+  bool ok = from >= j && from > above && col < p.src_blocks && dcol < p.dst_blocks && (!p.weights || from < p.max_ctx);
+  if (ok) {
+    m.src_blk = __ldg(p.src_table + (int64_t)r * p.src_stride + col);
+    m.dst_blk = __ldg(p.dst_table + (int64_t)r * p.dst_stride + dcol);
+    m.src_slot = from - col * p.block_size;
+    m.dst_slot = j - dcol * p.block_size;
+    ok = m.src_blk >= 0 && m.src_blk < p.num_blocks && m.dst_blk >= 0 && m.dst_blk < p.num_blocks;
+  }
+  if (!ok) {
+    record_error(p.dev_err, kErrDeviceBounds);
+    m.src_blk = -1;
+    return m;
+  }
+  if (from != j) m.from = from;
+  if (m.src_blk == m.dst_blk && m.src_slot == m.dst_slot) m.src_blk = -1;
+  return m;
+}
+
+// The first j of [0, n) with keep[j] >= x (n if there is none), by the whole warp, 32 places a step.
+__device__ int first_at_least(const int32_t* keep, int n, int x, int lane) {
+  int lo = 0, len = n;
+  while (len > 0) {
+    const int step = (len + 31) / 32;
+    const int i = lo + min(lane * step + step - 1, len - 1);  // the last of the lane's part
+    const uint32_t yes = __ballot_sync(0xffffffffu, lane * step < len && __ldg(keep + i) >= x);
+    if (!yes) return lo + len;
+    const int l = __ffs(yes) - 1;
+    const int part = min(step, len - l * step);
+    lo += l * step;
+    if (part == 1) return lo;
+    len = part - 1;  // its last is known to pass
+    if (step == 1) return lo;
+  }
+  return lo;
+}
 
 // kPieces: 16-byte pieces of a row; kScale: bytes of a row's scales (0, 4 or 16).
 template <int kPieces, int kScale>
 __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactParams p) {
   constexpr int kPer = 2 * kRows * kPieces / kThreads;  // pieces a thread, K and V
-  __shared__ Row s_src[kRows], s_dst[kRows];
-  const int unit = blockIdx.x;
-  const int r = unit / p.num_kv_heads, h = unit - r * p.num_kv_heads;
-  const int tid = threadIdx.x;
-  const int32_t* keep = p.keep + (int64_t)unit * p.budget;
-  const int32_t* src_table = p.src_table + (int64_t)r * p.src_stride;
-  const int32_t* dst_table = p.dst_table + (int64_t)r * p.dst_stride;
-  const int len = __ldg(p.new_lens + r);
-  const int n = max(0, min(len, p.budget));
-  if (tid == 0 && (len < 0 || len > p.budget)) record_error(p.dev_err, kErrDeviceBounds);
-  float* w = p.weights ? p.weights + (int64_t)r * p.w_stride_req + (int64_t)h * p.w_stride_head : nullptr;
-  for (int j0 = 0; j0 < n; j0 += kRows) {
-    float wv = 0.0f;
-    bool w_moves = false;
-    if (tid < kRows) {
-      Row a{-1, 0}, b{-1, 0};
-      const int j = j0 + tid;
-      if (j < n) {
-        const int from = __ldg(keep + j);
-        const int col = from / p.block_size, dcol = j / p.block_size;
-        bool ok = from >= j && (j == 0 || from > __ldg(keep + j - 1)) && col < p.src_blocks && dcol < p.dst_blocks;
-        if (ok) {
-          a = {__ldg(src_table + col), from - col * p.block_size};
-          b = {__ldg(dst_table + dcol), j - dcol * p.block_size};
-          ok = a.blk >= 0 && a.blk < p.num_blocks && b.blk >= 0 && b.blk < p.num_blocks;
-        }
-        if (ok && w) {
-          ok = from < p.max_ctx;
-          if (ok && from != j) {
-            wv = w[from];
-            w_moves = true;
-          }
-        }
-        if (!ok) record_error(p.dev_err, kErrDeviceBounds);
-        if (!ok || (a.blk == b.blk && a.slot == b.slot)) a.blk = -1;
-      }
-      s_src[tid] = a;
-      s_dst[tid] = b;
-    }
+  __shared__ Move s_move[kRows];
+  __shared__ int s_go;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the places of a chunk's rows are looked up a chunk ahead, by the first warp
+  auto chunk_of = [&](int64_t c, int& unit, int& j0, int& n) {
+    unit = (int)(c / p.chunks);
+    j0 = (int)(c - (int64_t)unit * p.chunks) * kRows;
+    const int len = __ldg(p.new_lens + unit / p.num_kv_heads);
+    n = max(0, min(len, p.budget));
+    if (j0 == 0 && tid == 0 && n != len) record_error(p.dev_err, kErrDeviceBounds);
+  };
+  int unit = 0, j0 = 0, n = 0;
+  Move next{-1, 0, -1, 0, -1};
+  if (blockIdx.x < p.total) {
+    chunk_of(blockIdx.x, unit, j0, n);
+    if (warp == 0) next = find_move(p, unit, unit / p.num_kv_heads, j0 + lane, n);
+  }
+  for (int64_t c = blockIdx.x; c < p.total; c += gridDim.x) {
+    const int r = unit / p.num_kv_heads, h = unit - r * p.num_kv_heads;
+    const int my_unit = unit, my_j0 = j0, my_n = n;
+    if (warp == 0) s_move[lane] = next;
+    if (tid == 0) s_go = 1;
     __syncthreads();
+    const int rows = min(kRows, my_n - my_j0);  // may be negative: nothing to do
     uint4 x[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int piece = i * kThreads + tid;
-      const int row = piece / kPieces & (kRows - 1);
-      const uint8_t* pool = i < kPer / 2 ? p.k : p.v;
-      const Row a = s_src[row];
-      if (a.blk >= 0)
-        x[i] = *reinterpret_cast<const uint4*>(pool + a.blk * p.stride_blk + a.slot * p.stride_tok + h * p.stride_head +
-                                               piece % kPieces * 16);
-    }
     uint4 sx = make_uint4(0, 0, 0, 0);
+    float wv = 0.0f;
+    float* w = p.weights + (int64_t)r * p.w_stride_req + (int64_t)h * p.w_stride_head;
     const int srow = tid & (kRows - 1);
     uint8_t* spool = tid < kRows ? p.ks : p.vs;
-    const bool scales = kScale && tid < 2 * kRows && s_src[srow].blk >= 0;
-    if (scales) {
-      const Row a = s_src[srow];
-      const uint8_t* at = spool + a.blk * p.s_stride_blk + a.slot * p.s_stride_tok + h * p.s_stride_head;
-      if (kScale == 4) sx.x = *reinterpret_cast<const uint32_t*>(at);
-      if (kScale == 16) sx = *reinterpret_cast<const uint4*>(at);
-    }
-    __syncthreads();
+    bool scales = false;
+    if (rows > 0) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int piece = i * kThreads + tid;
-      const int row = piece / kPieces & (kRows - 1);
-      uint8_t* pool = i < kPer / 2 ? p.k : p.v;
-      const Row b = s_dst[row];
-      if (s_src[row].blk >= 0)
-        *reinterpret_cast<uint4*>(pool + b.blk * p.stride_blk + b.slot * p.stride_tok + h * p.stride_head +
-                                  piece % kPieces * 16) = x[i];
+      for (int i = 0; i < kPer; ++i) {
+        const int piece = i * kThreads + tid;
+        const Move& m = s_move[piece / kPieces & (kRows - 1)];
+        const uint8_t* pool = i < kPer / 2 ? p.k : p.v;
+        if (m.src_blk >= 0)
+          x[i] = *reinterpret_cast<const uint4*>(pool + m.src_blk * p.stride_blk + m.src_slot * p.stride_tok + h * p.stride_head +
+                                                 piece % kPieces * 16);
+      }
+      scales = kScale && tid < 2 * kRows && s_move[srow].src_blk >= 0;
+      if (scales) {
+        const Move& m = s_move[srow];
+        const uint8_t* at = spool + m.src_blk * p.s_stride_blk + m.src_slot * p.s_stride_tok + h * p.s_stride_head;
+        if (kScale == 4) sx.x = *reinterpret_cast<const uint32_t*>(at);
+        if (kScale == 16) sx = *reinterpret_cast<const uint4*>(at);
+      }
+      if (p.weights && warp == 0 && s_move[lane].from >= 0) wv = w[s_move[lane].from];
     }
-    if (scales) {
-      const Row b = s_dst[srow];
-      uint8_t* at = spool + b.blk * p.s_stride_blk + b.slot * p.s_stride_tok + h * p.s_stride_head;
-      if (kScale == 4) *reinterpret_cast<uint32_t*>(at) = sx.x;
-      if (kScale == 16) *reinterpret_cast<uint4*>(at) = sx;
+    // the next chunk's places
+    if (c + gridDim.x < p.total) {
+      chunk_of(c + gridDim.x, unit, j0, n);
+      if (warp == 0) next = find_move(p, unit, unit / p.num_kv_heads, j0 + lane, n);
     }
-    if (w_moves) w[j0 + tid] = wv;
+    if (rows > 0) {
+      const int ci = my_j0 / kRows;
+      uint32_t* flags = p.flags + (int64_t)my_unit * p.chunks;
+      int dep = -1, dep_last = -1;
+      if (warp == kWarps - 1 && ci) {
+        // rows whose source lies in this chunk's destinations: at most kRows in a row from the first
+        const int j = first_at_least(p.keep + (int64_t)my_unit * p.budget, my_j0, my_j0, lane);
+        if (j < my_j0) {
+          dep = j / kRows;
+          dep_last = min(j + kRows - 1, my_j0 - 1) / kRows;
+        }
+      }
+      __syncthreads();  // every thread has its part of the rows
+      if (warp == kWarps - 1) {
+        if (lane == 0 && p.chunks > 1) store_release(flags + ci, 1u);
+        if (dep >= 0 && lane <= dep_last - dep) {
+          const uint64_t t0 = globaltimer_ns();
+          while (!load_acquire(flags + dep + lane)) {
+            if (globaltimer_ns() - t0 > p.wait_limit_ns) {
+              record_error(p.dev_err, kErrTimeout);
+              s_go = 0;  // the rows stay where they are
+              break;
+            }
+          }
+        }
+      }
+      __syncthreads();
+      if (s_go) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int piece = i * kThreads + tid;
+          const Move& m = s_move[piece / kPieces & (kRows - 1)];
+          uint8_t* pool = i < kPer / 2 ? p.k : p.v;
+          if (m.src_blk >= 0)
+            *reinterpret_cast<uint4*>(pool + m.dst_blk * p.stride_blk + m.dst_slot * p.stride_tok + h * p.stride_head +
+                                      piece % kPieces * 16) = x[i];
+        }
+        if (scales) {
+          const Move& m = s_move[srow];
+          uint8_t* at = spool + m.dst_blk * p.s_stride_blk + m.dst_slot * p.s_stride_tok + h * p.s_stride_head;
+          if (kScale == 4) *reinterpret_cast<uint32_t*>(at) = sx.x;
+          if (kScale == 16) *reinterpret_cast<uint4*>(at) = sx;
+        }
+        if (p.weights && warp == 0 && s_move[lane].from >= 0) w[my_j0 + lane] = wv;
+      }
+    }
     __syncthreads();
   }
 }
 
 template <int kPieces, int kScale>
-pkv_status launch(const CompactParams& p, int units, cudaStream_t st) {
-  compact_kernel<kPieces, kScale><<<units, kThreads, 0, st>>>(p);
+pkv_status launch(const CompactParams& p, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
+  static int per_sm = 1;
+  once_per_device(done, [] {
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, compact_kernel<kPieces, kScale>, kThreads, 0) == cudaSuccess && n > 0)
+      per_sm = n;
+  });
+  const int64_t most = (int64_t)per_sm * num_sms();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.total < most ? p.total : most));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (p.chunks > 1 && cudaMemsetAsync(p.flags, 0, (size_t)p.total * 4, st) != cudaSuccess) return check_launch("kv_cache_compact");
+  cudaLaunchKernelEx(&cfg, compact_kernel<kPieces, kScale>, p);
   return check_launch("kv_cache_compact");
 }
 
@@ -193,12 +298,15 @@ extern "C" pkv_status pkv_kv_cache_compact(void* k_cache, void* v_cache, int32_t
   p.num_kv_heads = num_kv_heads, p.budget = budget, p.block_size = block_size;
   p.weights = weights, p.w_stride_req = w_stride_req, p.w_stride_head = w_stride_head, p.max_ctx = max_ctx;
   p.dev_err = dev_err;
-  const int units = num_reqs * num_kv_heads;
+  p.chunks = (budget + kRows - 1) / kRows;
+  p.total = (int64_t)num_reqs * num_kv_heads * p.chunks;
+  p.flags = static_cast<uint32_t*>(workspace);
+  p.wait_limit_ns = take_wait_limit_ns();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (kv_dtype) {
-    case PKV_KV_BF16: return launch<32, 0>(p, units, st);
-    case PKV_KV_INT8: return launch<16, 4>(p, units, st);
-    case PKV_KV_FP8: return launch<16, 0>(p, units, st);
-    default: return launch<8, 16>(p, units, st);
+    case PKV_KV_BF16: return launch<32, 0>(p, st);
+    case PKV_KV_INT8: return launch<16, 4>(p, st);
+    case PKV_KV_FP8: return launch<16, 0>(p, st);
+    default: return launch<8, 16>(p, st);
   }
 }
