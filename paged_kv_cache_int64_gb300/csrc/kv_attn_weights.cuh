@@ -92,6 +92,7 @@ struct alignas(16) WShared {
   long long first, last;  // this CTA's tiles in the list
   long long total;
   alignas(16) float col[2][kN];              // per reducing group: minus the column's log-sum-exp (weights)
+  alignas(16) int token[kN];                 // a column's token of the pass
   alignas(16) float ref[8][G::kHalf];        // per reducing warp: the columns' references (log-sum-exps)
   alignas(16) float2 part[2][8][G::kHalf];   // per unit parity and warp: (reference, sum)
 };
@@ -172,8 +173,76 @@ __device__ __forceinline__ float w_reduce(float (&v)[kC], int lane) {
   return x;
 }
 
+// Maxima over the warp's lanes of 16 columns: lane l gets column l & 15's. The input is kept.
+__device__ __forceinline__ float w_max16(const float (&t)[16], int lane) {
+  float v[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const float keep = lane & 8 ? t[q + 8] : t[q], send = lane & 8 ? t[q] : t[q + 8];
+    v[q] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, 8));
+  }
+#pragma unroll
+  for (int o = 4; o >= 1; o >>= 1) {
+#pragma unroll
+    for (int q = 0; q < o; ++q) {
+      const float keep = lane & o ? v[q + o] : v[q], send = lane & o ? v[q] : v[q + o];
+      v[q] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, o));
+    }
+  }
+  return fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
+}
+
 // The list's owner of tile x when `ctas` CTAs share `total` tiles as [c total / ctas, (c + 1) total / ctas).
 __device__ __forceinline__ int w_owner(long long x, long long total, int ctas) { return (int)(((x + 1) * ctas - 1) / total); }
+
+// The log-sum-exp, base 2, of column c of the unit (r, h) of n keys, whose tiles are u0 .. u0 + tiles - 1 of the list; infinite for a
+// query that sees nothing.
+static __device__ __noinline__ float column_lse(const WeightParams& p, int r, int h, int n, int tiles, long long u0, long long total, int ctas, int c) {
+  const int64_t row = ((int64_t)r * p.T + p.t_base + c / p.group) * p.num_q_heads + (int64_t)h * p.group + c % p.group;
+  float m = -INFINITY, sum = 0.0f;
+  if (p.part_lse) {
+    const int64_t rows = (int64_t)p.num_reqs * p.T * p.num_q_heads;
+    const int splits = min((n - 1) / p.split_tokens + 1, p.max_splits);
+    for (int s0 = 0; s0 < splits; s0 += 8) {  // eight loads at a time
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = s0 + j < splits ? __ldg(p.part_lse + (s0 + j) * rows + row) : -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (x[j] > m) {
+          sum = sum * expf(m - x[j]) + 1.0f;
+          m = x[j];
+        } else if (x[j] != -INFINITY) {
+          sum += x[j] == m ? 1.0f : expf(x[j] - m);  // (NaN comes in here)
+        }
+      }
+    }
+    // m log2(e) in two parts, so that only the last addition rounds
+    const float hi = m * 1.4426950408889634f, lo = fmaf(m, 1.4426950408889634f, -hi) + m * 1.925963033500412e-8f;
+    return sum != 0.0f && m < INFINITY ? hi + (lo + log2f(sum)) : INFINITY;
+  }
+  // the CTAs that have the unit's tiles: only the first can have begun with another unit's
+  const int c0 = w_owner(u0, total, ctas), c1 = w_owner(u0 + tiles - 1, total, ctas);
+  if (c0 == c1) return __ldcg(p.lse2 + row);
+  const int which = u0 > total * c0 / ctas;
+  for (int o0 = c0; o0 <= c1; o0 += 8) {
+    float2 x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      x[j] = o0 + j <= c1 ? __ldcg(p.stat + ((int64_t)(o0 + j) * 2 + (o0 + j == c0 ? which : 0)) * kWMaxCols + c) : make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (x[j].y == 0.0f) continue;
+      if (x[j].x > m) {
+        sum = sum * exp2f(m - x[j].x) + x[j].y;
+        m = x[j].x;
+      } else {
+        sum += x[j].y * exp2f(x[j].x - m);
+      }
+    }
+  }
+  return sum != 0.0f ? m + log2f(sum) : INFINITY;
+}
 
 template <int kFmt, int kN, bool kStats>
 __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_kernel(const __grid_constant__ WeightParams p) {
@@ -262,6 +331,10 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
   } else if (warp == 2) {
     tmem_alloc(&sh.tmem_base, G::kTmemCols);
     tmem_relinquish();
+  }
+  if (warp >= 4 && threadIdx.x - 128 < kN) {
+    const int c = threadIdx.x - 128;
+    sh.token[c] = c < p.tpc * p.group ? c / p.group : INT_MIN;  // (padding: sees nothing)
   }
   tc_fence_before();
   __syncthreads();
@@ -390,7 +463,8 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
         tc_fence_after();
         const uint32_t a = tmem + lane_off + G::kColA + (i & 1) * 128;
         uint32_t nan = 0;
-#pragma unroll
+        // (rolled, as every loop of a role: together they have to fit the instruction cache)
+#pragma unroll 1
         for (int w8 = 0; w8 < 8; ++w8) {  // 32 codes, 16 columns a step
           uint32_t o[16];
 #pragma unroll
@@ -433,50 +507,62 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const int c_first = kBoth ? grp * 64 : 0;  // the group's first column
     const float per_tensor = kFmt == PKV_KV_FP8 ? __ldg(p.k_scale) : 1.0f;
+    constexpr int kStride = kBoth ? 1 : 2;  // tiles from one of this group's to the next
     bool dead = false;
     int units = 0;
 
-    // int8: the scales of this thread's keys, loaded two tiles of its own ahead of the block ids' four
-    WWalk ahead = at;
-    int ahead_i = 0;
-    int blk_n = -1, slot_n = 0, h_n = 0;  // of the next but one tile of this group
-    float sc_0 = 0.0f, sc_1 = 0.0f;
-    constexpr int kStride = kBoth ? 1 : 2;  // tiles from one of this group's to the next
-    auto block_ahead = [&]() {
-      blk_n = -1;
-      if (ahead_i < count) {
-        const int pos = ahead.tile * kWTile + k;
-        if (pos < ahead.n) {
+    // what a tile needs from memory is loaded a tile of this group's ahead (the block id of an int8 scale two)
+    WWalk far = at, near = at;
+    int far_i = kBoth ? 0 : grp, near_i = far_i;
+    if (far_i && count) far.next(p), near.next(p);
+    auto step = [&](WWalk& w, int& i) {
+#pragma unroll
+      for (int n = 0; n < kStride; ++n, ++i)
+        if (i < count) w.next(p);
+    };
+    int blk = -1, slot = 0, blk_h = 0;
+    auto load_block = [&]() {
+      blk = -1;
+      if (far_i < count) {
+        const int pos = far.tile * kWTile + k;
+        if (pos < far.n) {
           const int col = pos / p.block_size;
-          slot_n = pos - col * p.block_size;
-          h_n = ahead.h;
-          const int blk = __ldg(p.block_table + (int64_t)ahead.r * p.bt_stride + col);
-          blk_n = blk < 0 || (int64_t)blk >= p.num_blocks ? -1 : blk;
+          slot = pos - col * p.block_size;
+          blk_h = far.h;
+          blk = __ldg(p.block_table + (int64_t)far.r * p.bt_stride + col);
         }
       }
-      for (int s = 0; s < kStride; ++s, ++ahead_i)
-        if (ahead_i < count) ahead.next(p);
+      step(far, far_i);
     };
-    auto scale_ahead = [&]() {
-      return blk_n >= 0 ? __ldg(p.k_scale + (int64_t)blk_n * p.s_stride_blk + (int64_t)slot_n * p.s_stride_tok + h_n) : 0.0f;
+    auto load_scale = [&]() {
+      return blk >= 0 && (int64_t)blk < p.num_blocks
+                 ? __ldg(p.k_scale + (int64_t)blk * p.s_stride_blk + (int64_t)slot * p.s_stride_tok + blk_h) : 0.0f;
     };
+    auto load_prev = [&]() {
+      float x = 0.0f;
+      if (near_i < count && p.prev) {
+        const int key = near.tile * kWTile + k;
+        const int len = p.prev_lens ? min(__ldg(p.prev_lens + near.r), near.n) : near.n;
+        if (key < len && key < p.max_ctx) x = p.prev[(int64_t)near.r * p.w_stride_req + (int64_t)near.h * p.w_stride_head + key];
+      }
+      step(near, near_i);
+      return x;
+    };
+    float scale_next = 0.0f, prev_next = 0.0f;
     if (kFmt == PKV_KV_INT8) {
-      if (!kBoth && grp == 1 && count) ahead.next(p), ++ahead_i;
-      block_ahead();
-      sc_0 = scale_ahead();
-      block_ahead();
-      sc_1 = scale_ahead();
-      block_ahead();
+      load_block();
+      scale_next = load_scale();
+      load_block();
     }
+    if (!kStats) prev_next = load_prev();
 
     float l[kStats ? G::kHalf : 1];  // a thread's part of the columns' sums
-    int prefix = 0, nq = 0, prev_len = 0;
+    int prefix = 0, nq = kStats ? p.tpc * p.group : 0;
     for (int i = 0; i < count; ++i) {
       const bool first = i == 0 || at.tile == 0, last = i + 1 == count || at.tile + 1 == at.tiles;
       if (first) {
-        prefix = __ldg(p.seq_lens + at.r) - p.T;  // token t sits at position prefix + t
+        prefix = __ldg(p.seq_lens + at.r) - p.T + p.t_base;  // the pass's token t sits at position prefix + t
         if constexpr (kStats) {
-          nq = p.tpc * p.group;
 #pragma unroll
           for (int c = 0; c < G::kHalf; ++c) l[c] = 0.0f;
           for (int c = lane; c < G::kHalf; c += 32) sh.ref[warp - 4][c] = -1e30f;
@@ -484,143 +570,99 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
         } else {
           const int valid = p.q_valid ? min(__ldg(p.q_valid + at.r), p.T) : p.T;
           nq = max(0, min(valid - p.t_base, p.tpc)) * p.group;
-          prev_len = !p.prev ? 0 : p.prev_lens ? __ldg(p.prev_lens + at.r) : at.n;
           w_bar(1 + grp, 128);  // the group has read the last unit's columns
-          if (k < kN) {
-            float c = INFINITY;
-            if (k < nq) {
-              const int t = p.t_base + k / p.group;
-              const int64_t row = ((int64_t)at.r * p.T + t) * p.num_q_heads + (int64_t)at.h * p.group + k % p.group;
-              if (p.part_lse) {
-                const int64_t rows = (int64_t)p.num_reqs * p.T * p.num_q_heads;
-                const int splits = min((at.n - 1) / p.split_tokens + 1, p.max_splits);
-                float m = -INFINITY, sum = 0.0f;
-                for (int s = 0; s < splits; ++s) {
-                  const float x = __ldg(p.part_lse + s * rows + row);
-                  if (x > m) {
-                    sum = sum * expf(m - x) + 1.0f;
-                    m = x;
-                  } else if (x != -INFINITY) {
-                    sum += x == m ? 1.0f : expf(x - m);  // (NaN comes in here)
-                  }
-                }
-                // m log2(e) in two parts, so that only the last addition rounds
-                const float hi = m * 1.4426950408889634f, lo = fmaf(m, 1.4426950408889634f, -hi) + m * 1.925963033500412e-8f;
-                if (sum != 0.0f && m < INFINITY) c = hi + (lo + log2f(sum));
-              } else {
-                // the unit's tiles, and the CTAs that have them
-                const long long u0 = sh.first + i - at.tile, u1 = u0 + at.tiles;
-                const int c0 = w_owner(u0, sh.total, sh.ctas), c1 = w_owner(u1 - 1, sh.total, sh.ctas);
-                if (c0 == c1) {
-                  c = __ldcg(p.lse2 + row);
-                } else {
-                  float m = -INFINITY, sum = 0.0f;
-                  for (int o = c0; o <= c1; ++o) {
-                    const int which = u0 > sh.total * o / sh.ctas;
-                    const float2 x = __ldcg(p.stat + ((int64_t)o * 2 + which) * kWMaxCols + k);
-                    if (x.y == 0.0f) continue;
-                    if (x.x > m) {
-                      sum = sum * exp2f(m - x.x) + x.y;
-                      m = x.x;
-                    } else {
-                      sum += x.y * exp2f(x.x - m);
-                    }
-                  }
-                  c = sum != 0.0f ? m + log2f(sum) : INFINITY;
-                }
-              }
-            }
-            sh.col[grp][k] = -c;
-          }
+          if (k < kN) sh.col[grp][k] = k < nq ? -column_lse(p, at.r, at.h, at.n, at.tiles, sh.first + i - at.tile, sh.total, sh.ctas, k) : -INFINITY;
           w_bar(1 + grp, 128);
         }
       }
       if (kBoth || (i & 1) == grp) {
         const int key = at.tile * kWTile + k;
         float f = p.scale_log2 * per_tensor;
+        const float before = prev_next;
         if (kFmt == PKV_KV_INT8) {
-          f *= sc_0;
-          sc_0 = sc_1;
-          sc_1 = scale_ahead();
-          block_ahead();
+          f *= scale_next;
+          scale_next = load_scale();
+          load_block();
         }
-        float before = 0.0f;
-        int64_t out = 0;
-        bool writes = false;
-        if constexpr (!kStats) {
-          out = (int64_t)at.r * p.w_stride_req + (int64_t)at.h * p.w_stride_head + key;
-          writes = key < at.n && key < p.max_ctx;
-          if (writes && key < prev_len) before = p.prev[out];
-        }
+        if (!kStats) prev_next = load_prev();
         if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait_suspend(&sh.s_full[i & 1], (i >> 1) & 1, abort, wl));
         if (!dead) {
           tc_fence_after();
           const uint32_t s_addr = tmem + lane_off + G::kColS + (i & 1) * kN + c_first;
-          // every key of the tile is seen by every column
-          const bool open = at.tile * kWTile + kWTile <= at.n && at.tile * kWTile + kWTile - 1 <= prefix + p.t_base;
           const bool bad_key = (sh.bad[i & (kWBadRing - 1)] >> kseg) & 1u;
-          const int behind = key < at.n ? key - prefix - p.t_base : INT_MAX;  // columns of earlier tokens do not see it
-          float sum = 0.0f;
+          if (bad_key) f = 0.0f;
+          // columns of tokens before this do not see the key; every column does where it is not above 0
+          const int behind = key < at.n ? key - prefix : INT_MAX;
+          const bool open = __all_sync(0xffffffffu, behind <= 0);
+          if constexpr (kStats) {
 #pragma unroll
-          for (int cc = 0; cc < (kStats ? G::kHalf : kN) / 16; ++cc) {
-            const int c0 = cc * 16;
-            if (c_first + c0 < nq) {
-              uint32_t v[16];
-              tmem_ld_32x32b_x16(s_addr + c0, v);
-              tmem_wait_ld();
-              float t[16];
+            for (int cc = 0; cc < G::kHalf / 16; ++cc) {
+              const int c0 = c_first + cc * 16;
+              if (c0 < nq) {
+                uint32_t v[16];
+                tmem_ld_32x32b_x16(s_addr + cc * 16, v);
+                tmem_wait_ld();
+                float t[16];
 #pragma unroll
-              for (int q = 0; q < 16; ++q) t[q] = bad_key ? 0.0f : __uint_as_float(v[q]);
-              if constexpr (kStats) {
-                float* ref = sh.ref[warp - 4] + c0;
-                float m = -INFINITY;
-                if (open && c_first + c0 + 16 <= nq) {
+                for (int q = 0; q < 16; ++q) t[q] = (bad_key ? 0.0f : __uint_as_float(v[q])) * f;
+                if (!open || c0 + 16 > nq) {
+                  const int4* tok = reinterpret_cast<const int4*>(sh.token + c0);
 #pragma unroll
-                  for (int q = 0; q < 16; ++q) t[q] *= f;
-                } else {
-#pragma unroll
-                  for (int q = 0; q < 16; ++q) {
-                    const int c = c_first + c0 + q;
-                    t[q] = c < nq && behind <= c / p.group ? t[q] * f : -INFINITY;
-                  }
+                  for (int q = 0; q < 16; ++q) t[q] = behind <= reinterpret_cast<const int*>(tok)[q] ? t[q] : -INFINITY;
                 }
+                float* ref = sh.ref[warp - 4] + cc * 16;
+                float rv[16], m = -INFINITY;
 #pragma unroll
-                for (int q = 0; q < 16; ++q) m = fmaxf(m, t[q] - ref[q]);
+                for (int q = 0; q < 16; ++q) {
+                  rv[q] = ref[q];
+                  m = fmaxf(m, t[q] - rv[q]);
+                }
                 if (__any_sync(0xffffffffu, m > 64.0f)) {  // a reference moves: once a unit, as a rule
-#pragma unroll
-                  for (int q = 0; q < 16; ++q) {
-                    float x = t[q];
-#pragma unroll
-                    for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-                    const float old = ref[q], now = fmaxf(old, x);
-                    __syncwarp();
-                    l[c0 + q] *= ex2_approx(old - now);
-                    if (lane == 0) ref[q] = now;
-                  }
+                  const float x = w_max16(t, lane);          // lane l: column l & 15's maximum
+                  const float old = ref[lane & 15], now = fmaxf(old, x), a = ex2_approx(old - now);
                   __syncwarp();
-                }
-#pragma unroll
-                for (int q = 0; q < 16; ++q) l[c0 + q] += ex2_approx(t[q] - ref[q]);
-              } else {
-                const float* col = sh.col[grp] + c0;
-                if (open && c0 + 16 <= nq) {
-#pragma unroll
-                  for (int q = 0; q < 16; ++q) sum += ex2_approx(fmaf(t[q], f, col[q]));
-                } else {
+                  if (lane < 16) ref[lane] = now;
+                  __syncwarp();
 #pragma unroll
                   for (int q = 0; q < 16; ++q) {
-                    const int c = c0 + q;
-                    const float e = ex2_approx(fmaf(t[q], f, col[q]));
-                    sum += c < nq && behind <= c / p.group ? e : 0.0f;
+                    l[cc * 16 + q] *= __shfl_sync(0xffffffffu, a, q);
+                    rv[q] = ref[q];
                   }
                 }
+#pragma unroll
+                for (int q = 0; q < 16; ++q) l[cc * 16 + q] += ex2_approx(t[q] - rv[q]);
               }
             }
-          }
-          tc_fence_before();
-          mbar_arrive(&sh.s_free[i & 1]);
-          if constexpr (!kStats) {
-            if (writes) p.weights[out] = before + sum;
+            tc_fence_before();
+            mbar_arrive(&sh.s_free[i & 1]);
+          } else {
+            float sum = 0.0f;
+#pragma unroll 1
+            for (int c0 = 0; c0 < nq; c0 += 16) {
+              uint32_t v[16];
+              tmem_ld_32x32b_x16(s_addr + c0, v);
+              float cv[16];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const float4 x = *reinterpret_cast<const float4*>(sh.col[grp] + c0 + 4 * q);
+                cv[4 * q] = x.x, cv[4 * q + 1] = x.y, cv[4 * q + 2] = x.z, cv[4 * q + 3] = x.w;
+              }
+              tmem_wait_ld();
+              float e[16];
+#pragma unroll
+              for (int q = 0; q < 16; ++q) e[q] = ex2_approx(fmaf(bad_key ? 0.0f : __uint_as_float(v[q]), f, cv[q]));
+              if (!open || c0 + 16 > nq) {
+                const int* tok = sh.token + c0;
+#pragma unroll
+                for (int q = 0; q < 16; ++q) e[q] = behind <= tok[q] && c0 + q < nq ? e[q] : 0.0f;
+              }
+#pragma unroll
+              for (int q = 0; q < 16; q += 4) sum += (e[q] + e[q + 1]) + (e[q + 2] + e[q + 3]);
+            }
+            tc_fence_before();
+            mbar_arrive(&sh.s_free[i & 1]);
+            if (key < at.n && key < p.max_ctx)
+              p.weights[(int64_t)at.r * p.w_stride_req + (int64_t)at.h * p.w_stride_head + key] = before + sum;
           }
         }
       }
