@@ -486,12 +486,12 @@ PKV_API pkv_status pkv_spec_verify_attn_fp4(const void* q, const uint8_t* k_fp4,
  *   draft_probs null: q(x) = 1 and q is 0 elsewhere (drafts that no distribution proposed). At the first
  *   draft that is not accepted the next token is drawn from max(p - q, 0), after the last draft from p:
  *     the smallest i with w(0) + ... + w(i) > u_sample[r] * (w(0) + ... + w(vocab - 1)),
- *   each probability taken as the nearest multiple of 2^-58 (exact from 2^-34 up) and the rest exact. Where
+ *   each probability taken as the nearest multiple of 2^-46 (exact from 2^-22 up) and the rest exact. Where
  *   max(p - q, 0) is 0 everywhere, w = p. A one-hot target row decodes greedily.
  *   out_tokens [num_reqs][T]: the accepted drafts, the drawn token, then -1; num_out [num_reqs]: how many of
  *   these are tokens (the count of query tokens whose keys stay, q_valid of kv_attn_weights).
- * Probabilities are in [0, 1] (values outside are clamped, NaN counts as 0), a row's sum below 64; u in
- * [0, 1) (clamped to it, NaN as 0). A draft id outside [0, vocab) is not accepted and leaves p whole, a row
+ * Probabilities are in [0, 1] (for the drawing, values outside are clamped and NaN counts as 0), a row's sum below
+ * 2^17; u in [0, 1) (clamped to it, NaN as 0). A draft id outside [0, vocab) is not accepted and leaves p whole, a row
  * without a positive value gives token 0, num_drafts outside [0, T - 1] is clamped: each sets
  * PKV_ERR_DEVICE_BOUNDS. vocab at most 2^30. No workspace.
  */

@@ -4,16 +4,17 @@
 // where it is exact). At the first that does not, the next token is drawn from max(p_t - q_t, 0); after the last
 // draft, from p itself: the smallest i whose running sum passes u times the total.
 //
-// The sums are integers: each probability as a multiple of 2^-58 (exact from 2^-34 up), so they do not depend on
+// The sums are integers: each probability as the nearest multiple of 2^-46 (exact from 2^-22 up), so they do not depend on
 // the order in which they are added, and the token is the one that exact arithmetic gives.
 //
 // One cluster of CTAs a request, one pass over one row of p (and one of q). Each warp sums a contiguous segment of
-// the row; the segment sums meet in the first CTA's shared memory; its first warps find the segment that holds the
-// target and read that one again (it is in L2) to find the token.
+// the row and gives the sum to every CTA; the warp whose segment holds the target reads it again, from its own SM's
+// cache, to find the token.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
 #include <utility>
 
 #include "host_common.h"
@@ -24,8 +25,8 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kMaxThreads = 512;  // of a CTA; two of them an SM, or four of half the size (64 registers a thread)
+constexpr int kMaxWarps = kMaxThreads / 32;
 constexpr int kMaxCluster = 8;
 
 struct AcceptParams {
@@ -46,69 +47,101 @@ __device__ __forceinline__ float as_float(float x) { return x; }
 __device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float as_float(__half x) { return __half2float(x); }
 
-// A probability as a multiple of 2^-58: values outside [0, 1] are clamped, NaN counts as 0.
-__device__ __forceinline__ uint64_t fixed58(float p) {
-  p = fminf(fmaxf(p, 0.0f), 1.0f);  // fmaxf(NaN, 0) = 0
-  return __float2ull_rn(p * 0x1p58f);
-}
-
-// 16 bytes of a row as values.
-template <typename T>
-struct Vec {
-  static constexpr int kN = 16 / (int)sizeof(T);
-  T v[kN];
+// A probability in [0, 1] as the nearest multiple of 2^-46, in two parts: hi 2^23 + lo. Four fp32 operations: adding 1 (or
+// 1.5) to x rounds it to a multiple of 2^-23 and leaves that multiple in the sum's low bits. (The conversion to 64-bit
+// integers runs at a small part of their rate; 64-bit shifts of the mantissa take twice the instructions.)
+struct Fixed {
+  int hi, lo;
 };
-
-// kN values of row `row` from index i on (i a multiple of kN); 0 past the vocabulary.
-template <typename T>
-__device__ __forceinline__ Vec<T> load_vec(const T* row, int i, int vocab, bool wide) {
-  constexpr int kN = Vec<T>::kN;
-  Vec<T> o;
-  if (wide && i + kN <= vocab) {
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(row + i));
-    memcpy(&o, &x, 16);
-  } else {
-#pragma unroll
-    for (int e = 0; e < kN; ++e) o.v[e] = i + e < vocab ? row[i + e] : T(0.0f);
-  }
-  return o;
+__device__ __forceinline__ Fixed fixed46(float p) {
+  const float t = __fadd_rn(p, 1.0f);
+  const float rest = __fsub_rn(p, __fsub_rn(t, 1.0f));  // exact, at most 2^-24
+  return {__float_as_int(t) - 0x3f800000, __float_as_int(__fmaf_rn(rest, 0x1p23f, 1.5f)) - 0x3fc00000};
+}
+// To [0, 1], NaN to 0.
+__device__ __forceinline__ float saturated(float x) {
+  float y;
+  asm("add.rn.sat.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// What the token is drawn from: p, max(p - q, 0), or p without the draft's own token.
+// Elements [i, i + kN) of a row of `vocab` values, 0 outside of it. row + i is 16-byte aligned; elements before the row and
+// behind it are not read.
+template <typename T>
+__device__ __forceinline__ uint4 load_vec(const T* row, int i, int vocab) {
+  constexpr int kN = 16 / (int)sizeof(T);
+  if (i >= 0 && i + kN <= vocab) return __ldg(reinterpret_cast<const uint4*>(row + i));
+  T v[kN];
+#pragma unroll
+  for (int e = 0; e < kN; ++e) v[e] = i + e >= 0 && i + e < vocab ? row[i + e] : T(0.0f);
+  uint4 x;
+  memcpy(&x, v, 16);
+  return x;
+}
+
+// What the token is drawn from: p, max(p - q, 0), or p without the draft's own token. Indices run in vectors of 16 bytes
+// that are aligned in p's row, so the first may begin before the row; q's row is read in its own aligned vectors, two
+// for one of p's where the rows are not aligned alike, and shifted.
 template <typename T>
 struct Source {
+  static constexpr int kN = 16 / (int)sizeof(T);
   const T* p;
   const T* q;   // null: none
   int skip;     // index left out, or -1
   int vocab;
-  bool wide;    // both rows 16-byte aligned
+  int begin;    // index of the first vector, -(kN - 1) .. 0
+  int shift;    // elements by which p's vectors begin behind q's, 0 .. kN - 1
 
-  static constexpr int kN = Vec<T>::kN;
-  __device__ __forceinline__ void load(int i, Vec<T>& a, Vec<T>& b) const {
-    a = load_vec(p, i, vocab, wide);
-    if (q) b = load_vec(q, i, vocab, wide);
+  __device__ __forceinline__ void align() {
+    begin = -(int)(reinterpret_cast<uintptr_t>(p) % 16 / sizeof(T));
+    const int q_begin = -(int)(reinterpret_cast<uintptr_t>(q) % 16 / sizeof(T));
+    shift = q ? (begin - q_begin + kN) % kN : 0;
   }
-  __device__ __forceinline__ uint64_t weight(int i, int e, const Vec<T>& a, const Vec<T>& b) const {
-    const uint64_t x = fixed58(as_float(a.v[e]));
+  // the vector of index i (begin + a multiple of kN); a: p's, b: q's
+  __device__ __forceinline__ void load(int i, uint4& a, uint4& b) const {
+    a = load_vec(p, i, vocab);
     if (q) {
-      const uint64_t y = fixed58(as_float(b.v[e]));
-      return x > y ? x - y : 0;
-    }
-    return i + e == skip ? 0 : x;
-  }
-  __device__ __forceinline__ uint64_t sum(int i, const Vec<T>& a, const Vec<T>& b) const {
-    uint64_t s = 0;
+      b = load_vec(q, i - shift, vocab);
+      if (shift) {  // uniform
+        const uint4 c = load_vec(q, i - shift + kN, vocab);
+        uint32_t w[8] = {b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+        const int bytes = shift * (int)sizeof(T);
+        if (bytes & 8) {
 #pragma unroll
-    for (int e = 0; e < kN; ++e) s += weight(i, e, a, b);
-    return s;
+          for (int j = 0; j < 6; ++j) w[j] = w[j + 2];
+        }
+        if (bytes & 4) {
+#pragma unroll
+          for (int j = 0; j < 5; ++j) w[j] = w[j + 1];
+        }
+        if (bytes & 2) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], 16);
+        }
+        b = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+  static __device__ __forceinline__ float value(const uint4& x, int e) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    if (sizeof(T) == 4) return __uint_as_float(w[e]);
+    if (std::is_same<T, __half>::value) return __half2float(__ushort_as_half((unsigned short)(w[e / 2] >> (e & 1 ? 16 : 0))));
+    return __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+  }
+  __device__ __forceinline__ Fixed weight(int i, int e, const uint4& a, const uint4& b) const {
+    const float x = saturated(value(a, e));
+    Fixed f = fixed46(x);
+    if (q) {
+      const Fixed g = fixed46(fminf(saturated(value(b, e)), x));  // q, p at most: the difference is 0 where q is above
+      return {f.hi - g.hi, f.lo - g.lo};
+    }
+    if (i + e == skip) f = {0, 0};
+    return f;
   }
 };
+// (2^23 hi is 2^46 at most for a vector or two: the parts are added up in 32 bits, a batch at a time)
+__device__ __forceinline__ uint64_t joined(const Fixed& f) { return (uint64_t)((int64_t)f.hi * (1 << 23) + f.lo); }
 
-__device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
 __device__ __forceinline__ uint64_t warp_inclusive(uint64_t x, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -118,51 +151,81 @@ __device__ __forceinline__ uint64_t warp_inclusive(uint64_t x, int lane) {
   return x;
 }
 
-constexpr int kBatch = 4;  // loads in flight a lane and table
+constexpr int kBatch = 2;  // vectors a lane and table that are added up while as many are on their way
 
-// The warp's sum over [lo, hi), both multiples of a warp's load.
+// The sum of a step, a vector a lane: two 32-bit reductions (128 values, or 256 of bf16 or fp16, of 2^23 at most each and so
+// 2^31 together: unsigned).
 template <typename T>
-__device__ uint64_t segment_sum(const Source<T>& s, int lo, int hi, int lane) {
-  constexpr int kStep = 32 * Vec<T>::kN;
-  uint64_t acc = 0;
-  for (int i0 = lo; i0 < hi; i0 += kBatch * kStep) {
-    Vec<T> a[kBatch], b[kBatch];
+__device__ __forceinline__ uint64_t step_sum(const Source<T>& s, int i, const uint4& a, const uint4& b, Fixed& mine) {
+  mine = {0, 0};
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) s.load(i0 + k * kStep < hi ? i0 + k * kStep + lane * Vec<T>::kN : s.vocab, a[k], b[k]);
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) acc += s.sum(i0 + k * kStep + lane * Vec<T>::kN, a[k], b[k]);
+  for (int e = 0; e < Source<T>::kN; ++e) {
+    const Fixed f = s.weight(i, e, a, b);
+    mine.hi += f.hi, mine.lo += f.lo;
   }
-  return warp_sum(acc);
+  return ((uint64_t)__reduce_add_sync(0xffffffffu, (unsigned)mine.hi) << 23) +
+         (uint64_t)(int64_t)__reduce_add_sync(0xffffffffu, mine.lo);
 }
 
-// The smallest index of [lo, hi) whose running sum within the segment passes `target`; -1 if none does.
+// The warp's sum over [lo, hi), whole steps; lane l gets in `part` that of its l-th part of `per` steps.
 template <typename T>
-__device__ int segment_find(const Source<T>& s, int lo, int hi, uint64_t target, int lane) {
-  constexpr int kN = Vec<T>::kN, kStep = 32 * kN;
-  uint64_t before = 0;
-  for (int i0 = lo; i0 < hi; i0 += kBatch * kStep) {
-    Vec<T> a[kBatch], b[kBatch];
+__device__ __forceinline__ uint64_t segment_sum(const Source<T>& s, int lo, int hi, int per, int lane, uint64_t& part) {
+  constexpr int kN = Source<T>::kN, kStep = 32 * kN;
+  uint64_t acc = 0, in_part = 0;
+  int steps = 0, parts = 0;
+  part = 0;
+  uint4 a[kBatch], b[kBatch];
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) s.load(i0 + k * kStep < hi ? i0 + k * kStep + lane * kN : s.vocab, a[k], b[k]);
+  for (int k = 0; k < kBatch; ++k) s.load(lo + k * kStep < hi ? lo + k * kStep + lane * kN : s.vocab, a[k], b[k]);
+#pragma unroll 1
+  for (int i0 = lo; i0 < hi; i0 += kBatch * kStep) {
+    uint4 na[kBatch], nb[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const int i = i0 + k * kStep + lane * kN;
-      const uint64_t mine = s.sum(i, a[k], b[k]);
-      uint64_t run = before + warp_inclusive(mine, lane);
-      const uint32_t past = __ballot_sync(0xffffffffu, run > target);
-      if (past) {
-        const int l = __ffs(past) - 1;
-        int at = -1;
-        uint64_t c = run - mine;
-#pragma unroll
-        for (int e = 0; e < kN; ++e) {
-          c += s.weight(i, e, a[k], b[k]);
-          if (at < 0 && c > target) at = i + e;
-        }
-        return __shfl_sync(0xffffffffu, at, l);
-      }
-      before = __shfl_sync(0xffffffffu, run, 31);
+      const int i = i0 + (kBatch + k) * kStep;
+      s.load(i < hi ? i + lane * kN : s.vocab, na[k], nb[k]);
     }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      Fixed mine;
+      in_part += step_sum(s, i0 + k * kStep + lane * kN, a[k], b[k], mine);
+      if (++steps == per || i0 + (k + 1) * kStep >= hi) {
+        if (lane == parts) part += in_part;  // (a step behind the last one adds 0)
+        acc += in_part;
+        in_part = 0, steps = 0, ++parts;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) a[k] = na[k], b[k] = nb[k];
+  }
+  return acc;
+}
+
+// The smallest index of [lo, hi), whole steps, whose running sum from lo passes `target`; -1 if none does.
+template <typename T>
+__device__ __forceinline__ int find(const Source<T>& s, int lo, int hi, uint64_t target, int lane) {
+  constexpr int kN = Source<T>::kN, kStep = 32 * kN;
+  uint64_t before = 0;
+#pragma unroll 1
+  for (int i0 = lo; i0 < hi; i0 += kStep) {
+    const int i = i0 + lane * kN;
+    uint4 a, b;
+    s.load(i, a, b);
+    Fixed sum;
+    const uint64_t step = step_sum(s, i, a, b, sum);
+    if (before + step > target) {
+      const uint64_t mine = joined(sum), run = before + warp_inclusive(mine, lane);
+      int at = -1;
+      uint64_t c = run - mine;
+#pragma unroll
+      for (int e = 0; e < kN; ++e) {
+        c += joined(s.weight(i, e, a, b));
+        if (at < 0 && c > target) at = i + e;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, run > target);
+      return __shfl_sync(0xffffffffu, at, past ? __ffs(past) - 1 : 31);
+    }
+    before += step;
   }
   return -1;
 }
@@ -181,13 +244,13 @@ __device__ uint64_t scaled(float u, uint64_t total) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams p) {
+__global__ void __launch_bounds__(kMaxThreads, 2) accept_kernel(const AcceptParams p) {
   cg::cluster_group cluster = cg::this_cluster();
   const int ranks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int r = blockIdx.x / ranks;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto started = cluster.barrier_arrive();  // waited for before the first CTA's shared memory is written
-  __shared__ uint64_t s_sum[kMaxCluster * kWarps];  // the first CTA's: every segment's sum
+  auto started = cluster.barrier_arrive();  // waited for before another CTA's shared memory is written
+  __shared__ uint64_t s_sum[2][kMaxCluster * kMaxWarps];  // every segment's sum, of the first and of a second pass
   __shared__ int s_accepted;
 
   const T* P = static_cast<const T*>(p.target) + (int64_t)r * p.t_stride_req;
@@ -199,28 +262,31 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams p) 
 
   if (warp == 0) {  // how many drafts stay: 32 at a time
     int n = 0;
-    for (int t0 = 0; t0 < nd; t0 += 32) {
+    for (int t0 = 0; t0 < p.T - 1; t0 += 32) {
       const int t = t0 + lane;
       bool ok = false;
-      if (t < nd) {
-        const int x = __ldg(ids + t);
-        if (x >= 0 && x < p.vocab) {
-          const float pt = as_float(P[(int64_t)t * p.t_stride_tok + x]);
-          const float qt = Q ? as_float(Q[(int64_t)t * p.d_stride_tok + x]) : 1.0f;
-          ok = (double)p.u_accept[(int64_t)r * (p.T - 1) + t] * (double)qt < (double)pt;
-        } else if (rank == 0) {
-          record_error(p.dev_err, kErrDeviceBounds);
+      if (t < p.T - 1) {
+        const int x = __ldg(ids + t);  // (drafts behind the request's own too, while num_drafts is on its way)
+        const float u = p.u_accept[(int64_t)r * (p.T - 1) + t];
+        if (t < nd) {
+          if (x >= 0 && x < p.vocab) {
+            const float pt = as_float(P[(int64_t)t * p.t_stride_tok + x]);
+            const float qt = Q ? as_float(Q[(int64_t)t * p.d_stride_tok + x]) : 1.0f;
+            ok = (double)u * (double)qt < (double)pt;
+          } else if (rank == 0) {
+            record_error(p.dev_err, kErrDeviceBounds);
+          }
         }
       }
-      const uint32_t no = __ballot_sync(0xffffffffu, t < nd && !ok);
+      const uint32_t no = __ballot_sync(0xffffffffu, !ok);
       if (no) {
-        n = t0 + __ffs(no) - 1;
+        n = t0 + __ffs(no) - 1;  // the first that goes, or the first behind the last
         break;
       }
-      n = min(t0 + 32, nd);
+      n = t0 + 32;
     }
     if (lane == 0) {
-      s_accepted = n;
+      s_accepted = min(n, nd);
       if (rank == 0 && bad_count) record_error(p.dev_err, kErrDeviceBounds);
     }
   }
@@ -232,58 +298,72 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams p) 
   src.q = (n < nd && Q) ? Q + (int64_t)n * p.d_stride_tok : nullptr;
   src.skip = (n < nd && !Q) ? __ldg(ids + n) : -1;
   src.vocab = p.vocab;
-  src.wide = ((reinterpret_cast<uintptr_t>(src.p) | reinterpret_cast<uintptr_t>(src.q)) & 15) == 0;
+  src.align();
 
   // segments: one a warp of the cluster, whole warp loads each
-  constexpr int kStep = 32 * Vec<T>::kN;
-  const int segs = ranks * kWarps;
-  const int steps = (p.vocab + kStep - 1) / kStep;
-  const int seg_len = (steps + segs - 1) / segs * kStep;
+  constexpr int kStep = 32 * Source<T>::kN;
+  const int warps = blockDim.x >> 5;
+  const int segs = ranks * warps;
+  const int steps = (p.vocab - src.begin + kStep - 1) / kStep;
+  const int seg_steps = (steps + segs - 1) / segs, seg_len = seg_steps * kStep;
+  const int per = (seg_steps + 31) / 32;  // steps of a lane's part of the segment
+  const int mine = rank * warps + warp;
   // (64-bit: a segment's start may pass 2^31 for the largest vocabularies)
-  auto lo_of = [&](int s) { return (int)min((int64_t)s * seg_len, (int64_t)steps * kStep); };
-  const int mine = rank * kWarps + warp;
-  const uint64_t sum = segment_sum(src, lo_of(mine), lo_of(mine + 1), lane);
-  cluster.barrier_wait(std::move(started));
-  if (lane == 0) cluster.map_shared_rank(s_sum, 0)[mine] = sum;
-  cluster.sync();
-  if (rank) return;
+  const int lo = src.begin + (int)min((int64_t)mine * seg_len, (int64_t)steps * kStep);
+  const int hi = src.begin + (int)min((int64_t)(mine + 1) * seg_len, (int64_t)steps * kStep);
 
-  for (int pass = 0; pass < 2; ++pass) {
-    uint64_t total = 0;
-    for (int s = lane; s < segs; s += 32) total += s_sum[s];
-    total = warp_sum(total);
-    if (total == 0 && pass == 0 && (src.q || src.skip >= 0)) {
-      // nothing of p is left over (p = q up to rounding): draw from p
-      src.q = nullptr;
-      src.skip = -1;
-      __syncthreads();
-      for (int s = warp; s < segs; s += kWarps) {
-        const uint64_t x = segment_sum(src, lo_of(s), lo_of(s + 1), lane);
-        if (lane == 0) s_sum[s] = x;
-      }
-      __syncthreads();
-      continue;
+#pragma unroll 1
+  for (int pass = 0;; ++pass) {
+    uint64_t part;
+    const uint64_t sum = segment_sum(src, lo, hi, per, lane, part);
+    if (pass == 0) cluster.barrier_wait(std::move(started));
+    // every CTA gets every segment's sum: the warp whose segment holds the target goes on, from its own SM's cache
+    if (lane < ranks) cluster.map_shared_rank(&s_sum[pass][0], lane)[mine] = sum;
+    cluster.sync();
+    // the running sums: each lane has kMaxCluster * kMaxWarps / 32 segments in a row
+    constexpr int kPer = kMaxCluster * kMaxWarps / 32;
+    uint64_t x[kPer], own = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int sg = lane * kPer + j;
+      x[j] = sg < segs ? s_sum[pass][sg] : 0;
+      own += x[j];
     }
-    if (warp) return;
+    const uint64_t run = warp_inclusive(own, lane), total = __shfl_sync(0xffffffffu, run, 31);
     int token = 0;
     if (total == 0) {
+      if (pass == 0 && (src.q || src.skip >= 0)) {
+        // nothing of p is left over (p = q up to rounding): from p. Uniform over the cluster.
+        src.q = nullptr;
+        src.skip = -1;
+        src.shift = 0;
+        continue;
+      }
+      if (mine) return;
       if (lane == 0) record_error(p.dev_err, kErrDeviceBounds);
     } else {
-      uint64_t target = scaled(p.u_sample[r], total), before = 0;
-      token = p.vocab - 1;  // unless the sums wrapped around, one segment holds it
-      for (int s0 = 0; s0 < segs; s0 += 32) {
-        const uint64_t x = s0 + lane < segs ? s_sum[s0 + lane] : 0;
-        const uint64_t run = before + warp_inclusive(x, lane);
-        const uint32_t past = __ballot_sync(0xffffffffu, run > target);
-        if (past) {
-          const int l = __ffs(past) - 1;
-          const uint64_t start = __shfl_sync(0xffffffffu, run - x, l);
-          const int at = segment_find(src, lo_of(s0 + l), lo_of(s0 + l + 1), target - start, lane);
-          if (at >= 0) token = at;
-          break;
-        }
-        before = __shfl_sync(0xffffffffu, run, 31);
+      // the segment that holds the target; every warp finds the same one (the last, where sums wrapped around and
+      // none does)
+      const uint64_t target = scaled(p.u_sample[r], total);
+      const uint32_t past = __ballot_sync(0xffffffffu, run > target);
+      int chosen = segs - 1;
+      uint64_t start = run - own;
+      if (past) {
+        int j = 0;
+#pragma unroll
+        for (int t = 0; t < kPer - 1; ++t)
+          if (j == t && start + x[t] <= target) start += x[t], ++j;
+        chosen = __shfl_sync(0xffffffffu, lane * kPer + j, __ffs(past) - 1);
+        start = __shfl_sync(0xffffffffu, start, __ffs(past) - 1);
       }
+      if (chosen != mine) return;
+      // the part of the segment that holds it, then its steps
+      const uint64_t left = past ? target - start : 0, upto = warp_inclusive(part, lane);
+      const uint32_t in = __ballot_sync(0xffffffffu, upto > left);
+      const int l = in ? __ffs(in) - 1 : 31;
+      const int from = min(lo + l * per * kStep, hi);
+      token = find(src, from, min(from + per * kStep, hi), left - __shfl_sync(0xffffffffu, upto - part, l), lane);
+      if (token < 0) token = p.vocab - 1;
     }
     for (int t = lane; t < p.T; t += 32)
       p.out_tokens[(int64_t)r * p.T + t] = t < n ? __ldg(ids + t) : t == n ? token : -1;
@@ -294,17 +374,23 @@ __global__ void __launch_bounds__(kThreads) accept_kernel(const AcceptParams p) 
 
 template <typename T>
 pkv_status launch(const AcceptParams& p, int num_reqs, cudaStream_t stream) {
+  // Every request's CTAs on the device at once, as many threads a request as that leaves: a cluster of eight CTAs of 512
+  // (two an SM) or 256 threads (four), or a smaller one.
+  const int room = num_sms() * 4;  // CTAs of 256 threads
+  int ctas = kMaxCluster;
+  while (ctas > 1 && (int64_t)num_reqs * ctas > room) ctas /= 2;
+  const int threads = (int64_t)num_reqs * ctas * 2 <= room ? kMaxThreads : kMaxThreads / 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)num_reqs * kMaxCluster);
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3((unsigned)(num_reqs * ctas));
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kMaxCluster;
+  attr[0].val.clusterDim.x = (unsigned)ctas;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, accept_kernel<T>, p) != cudaSuccess) return check_launch("spec_verify_accept");
+  cudaLaunchKernelEx(&cfg, accept_kernel<T>, p);
   return check_launch("spec_verify_accept");
 }
 

@@ -11,7 +11,9 @@ def accept(P, Q, ids, u_accept, u_sample, num_drafts):
     """P [R][T][V] and Q [R][T-1][V] or None: the values as fp32. -> tokens [R][T], num_out [R]."""
     R, T, V = P.shape
     tokens, count = np.full((R, T), -1, dtype=np.int32), np.zeros(R, dtype=np.int32)
-    fixed = lambda x: np.rint(np.clip(np.nan_to_num(x.astype(np.float64), nan=0.0), 0.0, 1.0) * 2.0 ** 58).astype(np.uint64)  # noqa: E731
+    def fixed(x):  # the nearest multiple of 2^-46, of x taken to [0, 1]
+        return np.rint(np.clip(np.nan_to_num(x.astype(np.float64), nan=0.0), 0.0, 1.0) * 2.0 ** 46).astype(np.uint64)
+
     for r in range(R):
         nd = int(np.clip(num_drafts[r], 0, T - 1))
         t = 0
