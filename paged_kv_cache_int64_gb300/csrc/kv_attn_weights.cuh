@@ -139,19 +139,27 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// 4 int8 codes -> 4 bf16 integers, exact: a code is its low seven bits minus 128 where its sign bit is set, and bf16
-// bits 0x4300 | x are 128 + x for x < 128, 0x4380 is 256.
-__device__ __forceinline__ void widen4_int8(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t a = __byte_perm(w, 0, 0x4140), b = __byte_perm(w, 0, 0x4342);  // a byte in each half
-  lo = bf16x2_sub((a & 0x007f007fu) | 0x43004300u, (a & 0x00800080u) | 0x43004300u);
-  hi = bf16x2_sub((b & 0x007f007fu) | 0x43004300u, (b & 0x00800080u) | 0x43004300u);
+// 4 int8 codes -> 4 bf16 integers, exact. With u = code + 128, bf16 bits 0x4300 + u are f = 128 + u below u = 128 and 2 u from
+// there on (the mantissa has seven bits), so that u - 128 = (f - 256) - max(f / 2 - 128, 0): every step is exact, and three of
+// the four run beside the byte permutes on the FMA pipe.
+__device__ __forceinline__ uint32_t widen2_int8(uint32_t f) {
+  uint32_t half, y, r;
+  asm("fma.rn.relu.bf16x2 %0, %1, %2, %3;" : "=r"(half) : "r"(f), "r"(0x3f003f00u), "r"(0xc300c300u));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(f), "r"(0x3f803f80u), "r"(0xc380c380u));
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(half), "r"(0xbf80bf80u), "r"(y));
+  return r;
 }
-// 4 e4m3 codes -> 4 bf16 values, exact: the code's exponent and mantissa at bf16's low exponent bits are the value
-// times 2^-120. NaN codes (0x7f) come out as 480 and are told apart by the caller.
+__device__ __forceinline__ void widen4_int8(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  lo = widen2_int8(__byte_perm(u, 0x43434343u, 0x4140));
+  hi = widen2_int8(__byte_perm(u, 0x43434343u, 0x4342));
+}
+// 4 e4m3 codes -> 4 bf16 values, exact: the hardware's conversion to fp16, then fp32, then bf16.
 __device__ __forceinline__ void widen4_e4m3(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);  // a byte in each half's upper byte
-  lo = bf16x2_mul((a & 0x80008000u) | ((a >> 4) & 0x07f007f0u), 0x7b807b80u);
-  hi = bf16x2_mul((b & 0x80008000u) | ((b >> 4) & 0x07f007f0u), 0x7b807b80u);
+  const uint32_t a = e4m3x2_to_f16x2((uint16_t)w), b = e4m3x2_to_f16x2((uint16_t)(w >> 16));
+  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a)), y = __half22float2(*reinterpret_cast<const __half2*>(&b));
+  lo = pack_bf16x2(x.x, x.y);
+  hi = pack_bf16x2(y.x, y.y);
 }
 
 // Sums over the warp's lanes of kC (16 or 32 at a time) columns: lane l gets column l's (kC = 16: l & 15's).
@@ -462,7 +470,6 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
         const uint32_t a = tmem + lane_off + G::kColA + (i & 1) * 128;
-        uint32_t nan = 0;
         // (rolled, as every loop of a role: together they have to fit the instruction cache)
 #pragma unroll 1
         for (int w8 = 0; w8 < 8; ++w8) {  // 32 codes, 16 columns a step
@@ -474,24 +481,13 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
             const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              if (kFmt == PKV_KV_INT8) {
+              if (kFmt == PKV_KV_INT8)
                 widen4_int8(x[e], o[8 * j + 2 * e], o[8 * j + 2 * e + 1]);
-              } else {
+              else
                 widen4_e4m3(x[e], o[8 * j + 2 * e], o[8 * j + 2 * e + 1]);
-                nan |= (x[e] & 0x7f7f7f7fu) + 0x01010101u;
-              }
             }
           }
           tmem_st_32x32b_x16(a + 16 * w8, o);
-        }
-        if (kFmt == PKV_KV_FP8) {
-          // a NaN code anywhere makes every score of the key NaN: one NaN element does
-          if (__any_sync(0xffffffffu, (nan & 0x80808080u) != 0)) {
-            tmem_wait_st();
-            const uint32_t x = tmem_ld_32x32b_x1(a);
-            tmem_wait_ld();
-            tmem_st_32x32b_x1(a, nan & 0x80808080u ? 0x7fff7fffu : x);
-          }
         }
         tmem_wait_st();
         tc_fence_before();
