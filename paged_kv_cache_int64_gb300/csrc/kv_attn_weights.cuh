@@ -71,8 +71,12 @@ struct WGeo {
   static constexpr int kOffK = kQBufs * kQBytes;
   static constexpr int kTiles = kOffK + kStages * kStage;
   static constexpr int kHalf = kN == 128 ? 64 : kN;    // columns of a warp's sums
-  static constexpr uint32_t kColA = 0;                 // widened K: 2 x 128 columns
-  static constexpr uint32_t kColS = kWide ? 0 : 256;   // 2 x kN columns
+  // widened K: three buffers of 128 columns, so that a tile's MMAs need not be done before the group that widened it goes on
+  // (32 requests of up to 40,960 keys in int8: 163 us with two); two beside 2 x 128 columns of scores
+  static constexpr int kABufs = kWide ? 1 : kN == 128 ? 2 : 3;
+  static constexpr uint32_t kColA = 0;
+  static constexpr uint32_t kColS = kWide ? 0 : 128 * kABufs;  // 2 x kN columns
+  static_assert(kColS + 2 * kN <= 512, "tensor memory");
   static constexpr uint32_t kTmemCols = kWide ? (2 * kN <= 64 ? 64 : 256) : 512;
 };
 
@@ -81,7 +85,7 @@ struct alignas(16) WShared {
   using G = WGeo<kFmt, kN>;
   uint64_t q_full[2], q_free[2];
   uint64_t k_full[G::kStages], k_free[G::kStages];
-  uint64_t a_ready[2], a_free[2];
+  uint64_t a_ready[G::kABufs], a_free[G::kABufs];
   uint64_t s_full[2], s_free[2];
   uint64_t drain;
   uint32_t armed_k[G::kStages], armed_q[2];
@@ -322,11 +326,13 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], 1);
       mbar_init(&sh.q_free[i], 1);
-      mbar_init(&sh.a_ready[i], 128);
-      mbar_init(&sh.a_free[i], 1);
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.s_free[i], kBoth ? 256 : 128);
       sh.armed_q[i] = 0;
+    }
+    for (int i = 0; i < G::kABufs; ++i) {
+      mbar_init(&sh.a_ready[i], 128);
+      mbar_init(&sh.a_free[i], 1);
     }
     for (int i = 0; i < G::kStages; ++i) {
       mbar_init(&sh.k_full[i], 1);
@@ -348,6 +354,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem_base;
+  if (kStats) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   volatile int* abort = &sh.abort;
   const int count = (int)(sh.last - sh.first);
   WWalk at;
@@ -426,14 +433,14 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
     for (int i = 0; i < count; ++i) {
       const bool first = i == 0 || at.tile == 0;
       if (first) ++units;
-      const int b = units % G::kQBufs;
+      const int b = units % G::kQBufs, ab = i % G::kABufs;
       const bool last = i + 1 == count || at.tile + 1 == at.tiles;
       at.next(p);
       bool ok = true;
       if (first) ok = mbar_wait_suspend(&sh.q_full[b], (units / G::kQBufs) & 1, abort, wl);
       if (ok && i >= 2) ok = mbar_wait_suspend(&sh.s_free[i & 1], ((i >> 1) - 1) & 1, abort, wl);
       if (ok) ok = G::kWide ? mbar_wait_suspend(&sh.k_full[st], round & 1, abort, wl)
-                            : mbar_wait_suspend(&sh.a_ready[i & 1], (i >> 1) & 1, abort, wl);
+                            : mbar_wait_suspend(&sh.a_ready[ab], (i / G::kABufs) & 1, abort, wl);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const uint32_t q_base = smem_u32(smem) + b * G::kQBytes, k_base = smem_u32(smem) + G::kOffK + st * G::kStage;
@@ -445,10 +452,10 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
           if constexpr (G::kWide)
             umma_f16_ss(d, smem_desc(k_base + (ks >> 2) * G::kChunk + (ks & 3) * 32, 16, 1024), qd, id, ks > 0);
           else
-            umma_f16_ts(d, tmem + G::kColA + (i & 1) * 128 + ks * 8, qd, id, ks > 0);
+            umma_f16_ts(d, tmem + G::kColA + ab * 128 + ks * 8, qd, id, ks > 0);
         }
         umma_commit(&sh.s_full[i & 1]);
-        umma_commit(G::kWide ? &sh.k_free[st] : &sh.a_free[i & 1]);
+        umma_commit(G::kWide ? &sh.k_free[st] : &sh.a_free[ab]);
         if (last) umma_commit(&sh.q_free[b]);
       }
       __syncwarp();
@@ -466,12 +473,13 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
         const int st = i % G::kStages;
         const uint8_t* row = smem + G::kOffK + st * G::kStage + k * 128;
         bool ok = mbar_wait_suspend(&sh.k_full[st], (i / G::kStages) & 1, abort, wl);
-        if (ok && i >= 2) ok = mbar_wait_suspend(&sh.a_free[i & 1], ((i >> 1) - 1) & 1, abort, wl);
+        const int ab = i % G::kABufs;
+        if (ok && i >= G::kABufs) ok = mbar_wait_suspend(&sh.a_free[ab], (i / G::kABufs - 1) & 1, abort, wl);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-        const uint32_t a = tmem + lane_off + G::kColA + (i & 1) * 128;
+        const uint32_t a = tmem + lane_off + G::kColA + ab * 128;
         // (rolled, as every loop of a role: together they have to fit the instruction cache)
-#pragma unroll 1
+#pragma unroll 4
         for (int w8 = 0; w8 < 8; ++w8) {  // 32 codes, 16 columns a step
           uint32_t o[16];
 #pragma unroll
@@ -491,7 +499,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
         }
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&sh.a_ready[i & 1]);
+        mbar_arrive(&sh.a_ready[ab]);
         mbar_arrive(&sh.k_free[st]);
       }
     }
@@ -516,7 +524,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
       for (int n = 0; n < kStride; ++n, ++i)
         if (i < count) w.next(p);
     };
-    int blk = -1, slot = 0, blk_h = 0;
+    int blk = -1, slot = 0, blk_h = 0, near_r = -1, near_len = 0;
     auto load_block = [&]() {
       blk = -1;
       if (far_i < count) {
@@ -538,8 +546,11 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
       float x = 0.0f;
       if (near_i < count && p.prev) {
         const int key = near.tile * kWTile + k;
-        const int len = p.prev_lens ? min(__ldg(p.prev_lens + near.r), near.n) : near.n;
-        if (key < len && key < p.max_ctx) x = p.prev[(int64_t)near.r * p.w_stride_req + (int64_t)near.h * p.w_stride_head + key];
+        if (near.r != near_r) {
+          near_r = near.r;
+          near_len = (int)min((int64_t)(p.prev_lens ? min(__ldg(p.prev_lens + near_r), near.n) : near.n), p.max_ctx);
+        }
+        if (key < near_len) x = p.prev[(int64_t)near.r * p.w_stride_req + (int64_t)near.h * p.w_stride_head + key];
       }
       step(near, near_i);
       return x;
@@ -552,6 +563,8 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
     }
     if (!kStats) prev_next = load_prev();
 
+    // the weights' launch begins before the log-sum-exps' has ended: these are waited for, the keys are not
+    if (!kStats) asm volatile("griddepcontrol.wait;" ::: "memory");
     float l[kStats ? G::kHalf : 1];  // a thread's part of the columns' sums
     int prefix = 0, nq = kStats ? p.tpc * p.group : 0;
     for (int i = 0; i < count; ++i) {
@@ -726,6 +739,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
     tmem_dealloc(tmem, G::kTmemCols);
   }
   if (threadIdx.x == 0 && gave_up) record_error(p.dev_err, kErrTimeout);
+  if (!kStats) asm volatile("griddepcontrol.wait;" ::: "memory");  // (no thread ends before the launch it follows)
 }
 
 template <int kFmt, int kN, bool kStats>
@@ -737,7 +751,17 @@ inline pkv_status launch_attn_weights(const WeightParams& p, int ctas, cudaStrea
   once_per_device(attr_done, [] {
     cudaFuncSetAttribute(kv_attn_weights_kernel<kFmt, kN, kStats>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   });
-  kv_attn_weights_kernel<kFmt, kN, kStats><<<ctas, G::kThreads, kSmem, stream>>>(p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(G::kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = !kStats && !p.part_lse ? 1 : 0;
+  cudaLaunchKernelEx(&cfg, kv_attn_weights_kernel<kFmt, kN, kStats>, p);
   return check_launch("kv_attn_weights");
 }
 
