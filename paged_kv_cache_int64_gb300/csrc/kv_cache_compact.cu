@@ -15,7 +15,7 @@
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRows = 32;  // rows of a chunk
 
@@ -107,10 +107,14 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactParams p
   __shared__ int s_go;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // the places of a chunk's rows are looked up a chunk ahead, by the first warp
+  // chunks in the order (request, rows, KV head): the heads of the same rows run side by side, so that the pieces of a
+  // token's row are written (and mostly read) together (16 requests of up to 32,768 keys: 218 us with a head after the other)
   auto chunk_of = [&](int64_t c, int& unit, int& j0, int& n) {
-    unit = (int)(c / p.chunks);
-    j0 = (int)(c - (int64_t)unit * p.chunks) * kRows;
-    const int len = __ldg(p.new_lens + unit / p.num_kv_heads);
+    const int per = p.chunks * p.num_kv_heads;
+    const int r = (int)(c / per), in = (int)(c - (int64_t)r * per), at = in / p.num_kv_heads;
+    unit = r * p.num_kv_heads + in - at * p.num_kv_heads;
+    j0 = at * kRows;
+    const int len = __ldg(p.new_lens + r);
     n = max(0, min(len, p.budget));
     if (j0 == 0 && tid == 0 && n != len) record_error(p.dev_err, kErrDeviceBounds);
   };
@@ -260,7 +264,7 @@ extern "C" pkv_status pkv_kv_cache_compact(void* k_cache, void* v_cache, int32_t
               src_stride >= src_blocks && dst_stride >= dst_blocks && budget > 0,
           "%s: bad size argument", name);
   const bool scaled = kv_dtype == PKV_KV_INT8 || kv_dtype == PKV_KV_FP4;
-  PKV_UNSUP((int64_t)num_reqs * num_kv_heads <= INT32_MAX, "%s: too many requests", name);
+  PKV_UNSUP((int64_t)num_reqs * num_kv_heads <= INT32_MAX && ((int64_t)budget + kRows) * num_kv_heads <= INT32_MAX, "%s: too many rows", name);
   if (num_reqs == 0) return PKV_OK;
   PKV_ARG(k_cache && v_cache && src_table && dst_table && keep && new_lens && workspace && (!scaled || (k_scale && v_scale)),
           "%s: null pointer argument", name);
