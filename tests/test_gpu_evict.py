@@ -333,7 +333,7 @@ def test_select(pkv, lens, budget, sinks, recent, hkv):
     check_pick(pkv, sc, lens, sinks, recent, budget)
 
 
-@pytest.mark.parametrize("kind", ["equal", "few", "signed", "odd", "close"])
+@pytest.mark.parametrize("kind", ["equal", "few", "signed", "odd", "close", "wide", "outlier"])
 def test_select_ties_and_odd_scores(pkv, kind):
     g = torch.Generator().manual_seed(4)
     sc = torch.rand(2, 2, 3001, generator=g)
@@ -348,6 +348,11 @@ def test_select_ties_and_odd_scores(pkv, kind):
     elif kind == "odd":
         x = torch.tensor([float("nan"), -float("nan"), float("inf"), -float("inf"), 0.0, -0.0, 1e-45, -1e-45, 3.4e38, -3.4e38])
         sc = x[torch.randint(0, 10, sc.shape, generator=g)]
+    elif kind == "wide":  # over the whole exponent range
+        sc = torch.exp2(200 * torch.rand(sc.shape, generator=g) - 100)
+    elif kind == "outlier":  # a few far above all others
+        sc = torch.rand(sc.shape, generator=g) * 1e-20
+        sc[:, :, ::1000] = 1e30
     else:  # neighbours in the last digit
         sc = (torch.randint(0, 1500, sc.shape, generator=g) + 0x3F800000).int().view(torch.float32)
     for budget in (1, 700, 1500, 2990):
@@ -357,7 +362,7 @@ def test_select_ties_and_odd_scores(pkv, kind):
 
 def test_select_longer_than_shared_memory(pkv):
     """A slice that shared memory does not hold is read again."""
-    n = 8 * 49152 + 8 * 700 + 3
+    n = 16 * 49152 + 16 * 700 + 3
     sc = torch.rand(1, 1, n, generator=torch.Generator().manual_seed(1))
     check_pick(pkv, sc, [n], 4, 100, 60001)
 
