@@ -3,9 +3,9 @@
 // Row j of (request r, KV head h) becomes row keep[r][h][j], in K, in V, in the scale caches and in the weights; in
 // place, or into other blocks. keep ascends strictly, so keep[j] >= j: a row moves down or stays.
 //
-// A chunk is kRows rows of a (request, KV head): a CTA reads them all into registers and then writes them. In place, a
+// A chunk is kRows rows of a (request, KV head): a CTA reads them all into shared memory and then writes them. In place, a
 // chunk's destinations are sources of earlier chunks only (of chunks whose j is below: keep[j'] = j has j' <= j), so it
-// writes once those have been read: each chunk raises a flag when it has its rows in registers, and waits, before it
+// writes once those have been read: each chunk raises a flag when it has its rows, and waits, before it
 // writes, for the flags of the at most two chunks whose sources can lie in its destinations. The flags depend on
 // nothing but a chunk's own loads, and a CTA takes its chunks in ascending order, all CTAs resident (cooperative
 // launch): every wait ends. The waits are bounded all the same.
@@ -18,6 +18,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRows = 32;  // rows of a chunk
+static_assert(kRows * 8 % kThreads == 0 && 2 * kRows <= kThreads, "pieces and scales a thread");
 
 struct CompactParams {
   uint8_t* k;
@@ -102,11 +103,11 @@ __device__ int first_at_least(const int32_t* keep, int n, int x, int lane) {
 // kPieces: 16-byte pieces of a row; kScale: bytes of a row's scales (0, 4 or 16).
 template <int kPieces, int kScale>
 __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactParams p) {
-  constexpr int kPer = 2 * kRows * kPieces / kThreads;  // pieces a thread, K and V
+  constexpr int kPer = kRows * kPieces / kThreads;  // pieces a thread, of K and of V
+  extern __shared__ __align__(16) uint8_t s_rows[];  // [K, V][kRows][row]
   __shared__ Move s_move[kRows];
   __shared__ int s_go;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // the places of a chunk's rows are looked up a chunk ahead, by the first warp
   // chunks in the order (request, rows, KV head): the heads of the same rows run side by side, so that the pieces of a
   // token's row are written (and mostly read) together (16 requests of up to 32,768 keys: 218 us with a head after the other)
   auto chunk_of = [&](int64_t c, int& unit, int& j0, int& n) {
@@ -118,35 +119,38 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactParams p
     n = max(0, min(len, p.budget));
     if (j0 == 0 && tid == 0 && n != len) record_error(p.dev_err, kErrDeviceBounds);
   };
+  // the places of a chunk's rows are looked up a chunk ahead, by the first kRows threads
   int unit = 0, j0 = 0, n = 0;
   Move next{-1, 0, -1, 0, -1};
   if (blockIdx.x < p.total) {
     chunk_of(blockIdx.x, unit, j0, n);
-    if (warp == 0) next = find_move(p, unit, unit / p.num_kv_heads, j0 + lane, n);
+    if (tid < kRows) next = find_move(p, unit, unit / p.num_kv_heads, j0 + tid, n);
   }
   for (int64_t c = blockIdx.x; c < p.total; c += gridDim.x) {
     const int r = unit / p.num_kv_heads, h = unit - r * p.num_kv_heads;
-    const int my_unit = unit, my_j0 = j0, my_n = n;
-    if (warp == 0) s_move[lane] = next;
+    const int my_unit = unit, my_j0 = j0;
+    if (tid < kRows) s_move[tid] = next;
     if (tid == 0) s_go = 1;
-    __syncthreads();
-    const int rows = min(kRows, my_n - my_j0);  // may be negative: nothing to do
-    uint4 x[kPer];
-    uint4 sx = make_uint4(0, 0, 0, 0);
-    float wv = 0.0f;
+    // (a chunk all of whose rows stay has nothing to do but its flag)
+    const bool moves = __syncthreads_or(tid < kRows && (next.src_blk >= 0 || next.from >= 0));
+    const bool last_chunk = my_j0 + kRows >= n;
     float* w = p.weights + (int64_t)r * p.w_stride_req + (int64_t)h * p.w_stride_head;
     const int srow = tid & (kRows - 1);
     uint8_t* spool = tid < kRows ? p.ks : p.vs;
+    uint4 sx = make_uint4(0, 0, 0, 0);
+    float wv = 0.0f;
     bool scales = false;
-    if (rows > 0) {
+    if (moves) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int piece = i * kThreads + tid;
-        const Move& m = s_move[piece / kPieces & (kRows - 1)];
-        const uint8_t* pool = i < kPer / 2 ? p.k : p.v;
-        if (m.src_blk >= 0)
-          x[i] = *reinterpret_cast<const uint4*>(pool + m.src_blk * p.stride_blk + m.src_slot * p.stride_tok + h * p.stride_head +
-                                                 piece % kPieces * 16);
+        const int piece = i * kThreads + tid, row = piece / kPieces;
+        const Move& m = s_move[row];
+        if (m.src_blk >= 0) {
+          const int64_t at = m.src_blk * p.stride_blk + m.src_slot * p.stride_tok + h * p.stride_head + piece % kPieces * 16;
+          const uint32_t to = smem_u32(s_rows + piece * 16);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(p.k + at) : "memory");
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + kRows * kPieces * 16), "l"(p.v + at) : "memory");
+        }
       }
       scales = kScale && tid < 2 * kRows && s_move[srow].src_blk >= 0;
       if (scales) {
@@ -155,16 +159,16 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactParams p
         if (kScale == 4) sx.x = *reinterpret_cast<const uint32_t*>(at);
         if (kScale == 16) sx = *reinterpret_cast<const uint4*>(at);
       }
-      if (p.weights && warp == 0 && s_move[lane].from >= 0) wv = w[s_move[lane].from];
+      if (p.weights && tid < kRows && s_move[tid].from >= 0) wv = w[s_move[tid].from];
     }
     // the next chunk's places
     if (c + gridDim.x < p.total) {
       chunk_of(c + gridDim.x, unit, j0, n);
-      if (warp == 0) next = find_move(p, unit, unit / p.num_kv_heads, j0 + lane, n);
+      if (tid < kRows) next = find_move(p, unit, unit / p.num_kv_heads, j0 + tid, n);
     }
-    if (rows > 0) {
-      const int ci = my_j0 / kRows;
-      uint32_t* flags = p.flags + (int64_t)my_unit * p.chunks;
+    const int ci = my_j0 / kRows;
+    uint32_t* flags = p.flags + (int64_t)my_unit * p.chunks;
+    if (moves) {
       int dep = -1, dep_last = -1;
       if (warp == kWarps - 1 && ci) {
         // rows whose source lies in this chunk's destinations: at most kRows in a row from the first
@@ -174,9 +178,10 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactParams p
           dep_last = min(j + kRows - 1, my_j0 - 1) / kRows;
         }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
       __syncthreads();  // every thread has its part of the rows
       if (warp == kWarps - 1) {
-        if (lane == 0 && p.chunks > 1) store_release(flags + ci, 1u);
+        if (lane == 0 && !last_chunk) store_release(flags + ci, 1u);
         if (dep >= 0 && lane <= dep_last - dep) {
           const uint64_t t0 = globaltimer_ns();
           while (!load_acquire(flags + dep + lane)) {
@@ -192,12 +197,13 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactParams p
       if (s_go) {
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-          const int piece = i * kThreads + tid;
-          const Move& m = s_move[piece / kPieces & (kRows - 1)];
-          uint8_t* pool = i < kPer / 2 ? p.k : p.v;
-          if (m.src_blk >= 0)
-            *reinterpret_cast<uint4*>(pool + m.dst_blk * p.stride_blk + m.dst_slot * p.stride_tok + h * p.stride_head +
-                                      piece % kPieces * 16) = x[i];
+          const int piece = i * kThreads + tid, row = piece / kPieces;
+          const Move& m = s_move[row];
+          if (m.src_blk >= 0) {
+            const int64_t at = m.dst_blk * p.stride_blk + m.dst_slot * p.stride_tok + h * p.stride_head + piece % kPieces * 16;
+            *reinterpret_cast<uint4*>(p.k + at) = *reinterpret_cast<const uint4*>(s_rows + piece * 16);
+            *reinterpret_cast<uint4*>(p.v + at) = *reinterpret_cast<const uint4*>(s_rows + (kRows * kPieces + piece) * 16);
+          }
         }
         if (scales) {
           const Move& m = s_move[srow];
@@ -205,8 +211,10 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactParams p
           if (kScale == 4) *reinterpret_cast<uint32_t*>(at) = sx.x;
           if (kScale == 16) *reinterpret_cast<uint4*>(at) = sx;
         }
-        if (p.weights && warp == 0 && s_move[lane].from >= 0) w[my_j0 + lane] = wv;
+        if (p.weights && tid < kRows && s_move[tid].from >= 0) w[my_j0 + tid] = wv;
       }
+    } else if (tid == 0 && !last_chunk) {
+      store_release(flags + ci, 1u);
     }
     __syncthreads();
   }
@@ -216,15 +224,17 @@ template <int kPieces, int kScale>
 pkv_status launch(const CompactParams& p, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   static int per_sm = 1;
+  constexpr int kSmem = 2 * kRows * kPieces * 16;
   once_per_device(done, [] {
     int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, compact_kernel<kPieces, kScale>, kThreads, 0) == cudaSuccess && n > 0)
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, compact_kernel<kPieces, kScale>, kThreads, kSmem) == cudaSuccess && n > 0)
       per_sm = n;
   });
   const int64_t most = (int64_t)per_sm * num_sms();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.total < most ? p.total : most));
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;
