@@ -451,7 +451,7 @@ _PROBS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 _KV_TYPES = {PKV_KV_BF16: torch.bfloat16, PKV_KV_INT8: torch.int8, PKV_KV_FP8: torch.uint8, PKV_KV_FP4: torch.uint8}
 
 
-def _flat(t, dtype, *shape):
+def _flat(t, dtype, shape):
     """t's pointer; t: contiguous, of that type and shape."""
     assert t.dtype is dtype and t.shape == shape and t.is_contiguous(), f"expected contiguous {dtype} {list(shape)}"
     return t.data_ptr()
@@ -467,26 +467,30 @@ def spec_verify_accept(target_probs, draft_probs, draft_ids, u_accept, u_sample,
     draft_ids int32 [R][T-1] drawn from draft_probs [R][T-1][vocab] (None: proposed by no distribution), uniform
     numbers u_accept [R][T-1] and u_sample [R] fp32; num_drafts int32 [R] (None: T-1 each). out_tokens int32 [R][T]:
     the accepted drafts, the token drawn after them, -1; num_out int32 [R]: how many are tokens."""
-    R, T, V = target_probs.shape
-    ts = target_probs.stride()
+    shape = target_probs.shape
+    R, T, V = shape
+    sr, st, se = target_probs.stride()
     dev = target_probs.get_device()
-    kind = _PROBS.get(target_probs.dtype)
-    assert kind is not None and (ts[2] == 1 or V == 1), "target_probs: fp32, bf16 or fp16 [R][T][vocab], rows contiguous"
+    dtype = target_probs.dtype
+    assert dtype in _PROBS and (se == 1 or V == 1), "target_probs: fp32, bf16 or fp16 [R][T][vocab], rows contiguous"
     assert dev >= 0, "target_probs must be a CUDA tensor"
-    others = [draft_ids, u_accept, u_sample, out_tokens, num_out]
-    ds = (0, 0)
+    others = (draft_ids, u_accept, u_sample, out_tokens, num_out)
+    q, qr, qt = None, 0, 0
     if draft_probs is not None:
-        ds = draft_probs.stride()
-        assert draft_probs.dtype is target_probs.dtype and draft_probs.shape == (R, T - 1, V) and (ds[2] == 1 or V == 1), \
+        qr, qt, qe = draft_probs.stride()
+        assert draft_probs.dtype is dtype and draft_probs.shape == (R, T - 1, V) and (qe == 1 or V == 1), \
             "draft_probs: [R][T-1][vocab], of target_probs' type, rows contiguous"
-        others.append(draft_probs)
+        q = draft_probs.data_ptr()
+        others += (draft_probs,)
+    nd = None
     if num_drafts is not None:
-        _flat(num_drafts, _I32, R)
-        others.append(num_drafts)
+        nd = _flat(num_drafts, _I32, (R,))
+        others += (num_drafts,)
+    drafts = (R, T - 1)
     _launch(lib.pkv_spec_verify_accept, dev, others,
-            (target_probs.data_ptr(), ts[0], ts[1], _maybe(draft_probs), ds[0], ds[1], kind, _flat(draft_ids, _I32, R, T - 1),
-             _flat(u_accept, _F32, R, T - 1), _flat(u_sample, _F32, R), _maybe(num_drafts), R, T, V,
-             _flat(out_tokens, _I32, R, T), _flat(num_out, _I32, R), _err(dev_err, dev), _raw_stream(dev, stream)))
+            (target_probs.data_ptr(), sr, st, q, qr, qt, _PROBS[dtype], _flat(draft_ids, _I32, drafts),
+             _flat(u_accept, _F32, drafts), _flat(u_sample, _F32, (R,)), nd, R, T, V, _flat(out_tokens, _I32, (R, T)),
+             _flat(num_out, _I32, (R,)), _err(dev_err, dev), _raw_stream(dev, stream)))
 
 
 def kv_attn_weights_workspace_bytes(num_rows, num_q_heads, num_ctas=None) -> int:
@@ -504,45 +508,51 @@ def kv_attn_weights(q, k_cache, block_table, seq_lens, T, softmax_scale, weights
     collects from tokens t < q_valid[r] of the step's T, all query heads of its KV head; q bf16 [R*T][Hq][256]. k_cache:
     bf16, int8 (k_scale fp32 [nb][bs][hkv]) or uint8 e4m3 (k_scale a device scalar), by kv_dtype. part_lse [S][R*T][Hq] with
     its split_tokens: what a verify call left for the same queries (None: computed first)."""
-    nb, bs, hkv, d, sb, st, sh = _cache_strides(k_cache)
+    nb, bs, hkv, d = k_cache.shape
+    sb, st, sh, se = k_cache.stride()
     dev = k_cache.get_device()
-    assert dev >= 0 and k_cache.dtype is {PKV_KV_BF16: _BF16, PKV_KV_INT8: torch.int8, PKV_KV_FP8: _U8}[kv_dtype], \
-        "k_cache: a CUDA tensor of kv_dtype"
+    assert dev >= 0 and se == 1 and kv_dtype != PKV_KV_FP4 and k_cache.dtype is _KV_TYPES[kv_dtype], \
+        "k_cache: a CUDA tensor [nb][bs][hkv][D] of kv_dtype, D contiguous"
     R, cols, row = _table(block_table, seq_lens)
     rows, hq, dq = q.shape
     assert q.dtype is _BF16 and rows == R * T and dq == d and q.is_contiguous(), "q: contiguous bf16 [R*T][Hq][256]"
-    ws = weights.stride()
-    max_ctx = weights.shape[2]
-    assert weights.dtype is _F32 and weights.shape == (R, hkv, max_ctx) and (ws[2] == 1 or max_ctx == 1), \
+    shape, (wr, wh, we) = weights.shape, weights.stride()
+    max_ctx = shape[2]
+    assert weights.dtype is _F32 and shape[0] == R and shape[1] == hkv and (we == 1 or max_ctx == 1), \
         "weights: fp32 [R][hkv][max_ctx], positions contiguous"
     assert seq_lens.shape[0] == R, "seq_lens [R]"
     assert workspace.is_contiguous(), "workspace must be a contiguous CUDA tensor"
-    others = [q, block_table, seq_lens, weights, workspace]
-    ssb = sst = splits = 0
-    if kv_dtype == PKV_KV_INT8:
-        assert k_scale.dtype is _F32 and k_scale.shape == (nb, bs, hkv) and (k_scale.stride(2) == 1 or hkv == 1), \
-            "k_scale: fp32 [nb][bs][hkv], heads contiguous"
-        ssb, sst = k_scale.stride(0), k_scale.stride(1)
-    elif kv_dtype == PKV_KV_FP8:
-        assert k_scale.dtype is _F32 and k_scale.numel() == 1, "k_scale: an fp32 device scalar"
+    others = (q, block_table, seq_lens, weights, workspace)
+    scale, ssb, sst = None, 0, 0
     if kv_dtype != PKV_KV_BF16:
-        others.append(k_scale)
+        if kv_dtype == PKV_KV_INT8:
+            ssb, sst, ssh = k_scale.stride()
+            assert k_scale.dtype is _F32 and k_scale.shape == (nb, bs, hkv) and (ssh == 1 or hkv == 1), \
+                "k_scale: fp32 [nb][bs][hkv], heads contiguous"
+        else:
+            assert k_scale.dtype is _F32 and k_scale.numel() == 1, "k_scale: an fp32 device scalar"
+        scale = k_scale.data_ptr()
+        others += (k_scale,)
+    old = lens = valid = lse = None
+    splits = 0
     if prev is not None:
-        assert prev.dtype is _F32 and prev.shape == weights.shape and prev.stride() == ws, "prev: laid out as weights"
-        others.append(prev)
-    for t in (prev_lens, q_valid):
-        if t is not None:
-            _flat(t, _I32, R)
-            others.append(t)
+        assert prev.dtype is _F32 and prev.shape == shape and prev.stride() == (wr, wh, we), "prev: laid out as weights"
+        old = prev.data_ptr()
+        others += (prev,)
+    if prev_lens is not None:
+        lens = _flat(prev_lens, _I32, (R,))
+        others += (prev_lens,)
+    if q_valid is not None:
+        valid = _flat(q_valid, _I32, (R,))
+        others += (q_valid,)
     if part_lse is not None:
         splits = part_lse.shape[0]
-        _flat(part_lse, _F32, splits, rows, hq)
-        others.append(part_lse)
+        lse = _flat(part_lse, _F32, (splits, rows, hq))
+        others += (part_lse,)
     _launch(lib.pkv_kv_attn_weights, dev, others,
-            (q.data_ptr(), k_cache.data_ptr(), kv_dtype, None if kv_dtype == PKV_KV_BF16 else k_scale.data_ptr(), nb, sb, st,
-             sh, ssb, sst, block_table.data_ptr(), row, cols, seq_lens.data_ptr(), _maybe(q_valid), R, int(T), hq, hkv, d, bs,
-             float(softmax_scale), _maybe(part_lse), int(split_tokens), splits, _maybe(prev), _maybe(prev_lens),
-             weights.data_ptr(), ws[0], ws[1], max_ctx, workspace.data_ptr(), workspace.nbytes, _err(dev_err, dev),
+            (q.data_ptr(), k_cache.data_ptr(), kv_dtype, scale, nb, sb, st, sh, ssb, sst, block_table.data_ptr(), row, cols,
+             seq_lens.data_ptr(), valid, R, int(T), hq, hkv, d, bs, float(softmax_scale), lse, int(split_tokens), splits, old,
+             lens, weights.data_ptr(), wr, wh, max_ctx, workspace.data_ptr(), workspace.nbytes, _err(dev_err, dev),
              _raw_stream(dev, stream)))
 
 
@@ -550,12 +560,13 @@ def kv_evict_select(scores, seq_lens, sinks, recent, budget, keep, new_lens, dev
     """keep int32 [R][hkv][budget] := the positions of each (request, KV head) that stay, ascending: the first `sinks`,
     the last `recent`, the highest of scores (fp32 [R][hkv][max_ctx]) in between; new_lens int32 [R] := how many."""
     R, hkv, max_ctx = scores.shape
-    ss = scores.stride()
+    sr, sh, se = scores.stride()
     dev = scores.get_device()
-    assert dev >= 0 and scores.dtype is _F32 and (ss[2] == 1 or max_ctx == 1), "scores: fp32 [R][hkv][max_ctx] on the GPU, positions contiguous"
+    assert dev >= 0 and scores.dtype is _F32 and (se == 1 or max_ctx == 1), "scores: fp32 [R][hkv][max_ctx] on the GPU, positions contiguous"
+    budget = int(budget)
     _launch(lib.pkv_kv_evict_select, dev, (seq_lens, keep, new_lens),
-            (scores.data_ptr(), ss[0], ss[1], max_ctx, _flat(seq_lens, _I32, R), R, hkv, int(sinks), int(recent), int(budget),
-             _flat(keep, _I32, R, hkv, int(budget)), _flat(new_lens, _I32, R), _err(dev_err, dev), _raw_stream(dev, stream)))
+            (scores.data_ptr(), sr, sh, max_ctx, _flat(seq_lens, _I32, (R,)), R, hkv, int(sinks), int(recent), budget,
+             _flat(keep, _I32, (R, hkv, budget)), _flat(new_lens, _I32, (R,)), _err(dev_err, dev), _raw_stream(dev, stream)))
 
 
 def kv_cache_compact_workspace_bytes(num_reqs, num_kv_heads, budget) -> int:
@@ -567,16 +578,19 @@ def kv_cache_compact(k_cache, v_cache, src_table, dst_table, keep, new_lens, wor
     """Row j of (r, h) := row keep[r][h][j] (int32 [R][hkv][budget], ascending), j < new_lens[r], in K, V, the scale
     caches (int8: fp32 [nb][bs][hkv]; 4-bit: uint8 [nb][bs][hkv][16]) and weights (fp32 [R][hkv][max_ctx]). Read through
     src_table, written through dst_table: the same table, or other blocks."""
-    nb, bs, hkv, d, sb, st, sh = _cache_strides(k_cache)
+    shape, strides = k_cache.shape, k_cache.stride()
+    nb, bs, hkv, d = shape
+    sb, st, sh, se = strides
     dev = k_cache.get_device()
-    assert dev >= 0 and k_cache.dtype is v_cache.dtype is _KV_TYPES[kv_dtype], "caches: CUDA tensors of kv_dtype"
-    assert v_cache.shape == k_cache.shape and v_cache.stride() == k_cache.stride(), "K and V strides must agree"
+    assert dev >= 0 and se == 1 and k_cache.dtype is v_cache.dtype is _KV_TYPES[kv_dtype], \
+        "caches: CUDA tensors [nb][bs][hkv][D] of kv_dtype, D contiguous"
+    assert v_cache.shape == shape and v_cache.stride() == strides, "K and V strides must agree"
     R, cols, row = _table(src_table, new_lens)
-    reqs, dcols, drow = _table(dst_table)
+    reqs, dcols, drow = (R, cols, row) if dst_table is src_table else _table(dst_table)
     budget = keep.shape[2]
     assert reqs == R == new_lens.shape[0], "src_table, dst_table, new_lens: the same requests"
     assert workspace.is_contiguous(), "workspace must be a contiguous CUDA tensor"
-    others = [v_cache, src_table, dst_table, keep, new_lens, workspace]
+    others = (v_cache, src_table, dst_table, keep, new_lens, workspace)
     scale = (None, None, 0, 0, 0)
     if kv_dtype in (PKV_KV_INT8, PKV_KV_FP4):
         want = (nb, bs, hkv) if kv_dtype == PKV_KV_INT8 else (nb, bs, hkv, 16)
@@ -584,16 +598,16 @@ def kv_cache_compact(k_cache, v_cache, src_table, dst_table, keep, new_lens, wor
         assert k_scale.dtype is v_scale.dtype is (_F32 if kv_dtype == PKV_KV_INT8 else _U8) and k_scale.shape == v_scale.shape == want \
             and v_scale.stride() == ss and ss[3:] in ((), (1,)), "scale caches: fp32 [nb][bs][hkv] (int8) or uint8 [nb][bs][hkv][16] (4-bit)"
         scale = (k_scale.data_ptr(), v_scale.data_ptr(), ss[0], ss[1], ss[2])
-        others += [k_scale, v_scale]
+        others += (k_scale, v_scale)
     w = (None, 0, 0, 0)
     if weights is not None:
-        max_ctx = weights.shape[2]
-        assert weights.dtype is _F32 and weights.shape == (R, hkv, max_ctx) and (weights.stride(2) == 1 or max_ctx == 1), \
+        (wR, wh, max_ctx), (wr, whs, we) = weights.shape, weights.stride()
+        assert weights.dtype is _F32 and wR == R and wh == hkv and (we == 1 or max_ctx == 1), \
             "weights: fp32 [R][hkv][max_ctx], positions contiguous"
-        w = (weights.data_ptr(), weights.stride(0), weights.stride(1), max_ctx)
-        others.append(weights)
+        w = (weights.data_ptr(), wr, whs, max_ctx)
+        others += (weights,)
     _launch(lib.pkv_kv_cache_compact, dev, others,
             (k_cache.data_ptr(), v_cache.data_ptr(), kv_dtype, nb, sb, st, sh, *scale, src_table.data_ptr(), row, cols,
-             dst_table.data_ptr(), drow, dcols, _flat(keep, _I32, R, hkv, budget), new_lens.data_ptr(), R, hkv, budget, bs,
+             dst_table.data_ptr(), drow, dcols, _flat(keep, _I32, (R, hkv, budget)), new_lens.data_ptr(), R, hkv, budget, bs,
              d * 2 if kv_dtype == PKV_KV_FP4 else d, *w, workspace.data_ptr(), workspace.nbytes, _err(dev_err, dev),
              _raw_stream(dev, stream)))
