@@ -97,10 +97,11 @@ struct Source {
     const int q_begin = -(int)(reinterpret_cast<uintptr_t>(q) % 16 / sizeof(T));
     shift = q ? (begin - q_begin + kN) % kN : 0;
   }
-  // the vector of index i (begin + a multiple of kN); a: p's, b: q's
+  // the vector of index i (begin + a multiple of kN); a: p's, b: q's (kTwo: there is q)
+  template <bool kTwo>
   __device__ __forceinline__ void load(int i, uint4& a, uint4& b) const {
     a = load_vec(p, i, vocab);
-    if (q) {
+    if constexpr (kTwo) {
       b = load_vec(q, i - shift, vocab);
       if (shift) {  // uniform
         const uint4 c = load_vec(q, i - shift + kN, vocab);
@@ -128,10 +129,11 @@ struct Source {
     if (std::is_same<T, __half>::value) return __half2float(__ushort_as_half((unsigned short)(w[e / 2] >> (e & 1 ? 16 : 0))));
     return __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
   }
+  template <bool kTwo>
   __device__ __forceinline__ Fixed weight(int i, int e, const uint4& a, const uint4& b) const {
     const float x = saturated(value(a, e));
     Fixed f = fixed46(x);
-    if (q) {
+    if constexpr (kTwo) {
       const Fixed g = fixed46(fminf(saturated(value(b, e)), x));  // q, p at most: the difference is 0 where q is above
       return {f.hi - g.hi, f.lo - g.lo};
     }
@@ -151,16 +153,18 @@ __device__ __forceinline__ uint64_t warp_inclusive(uint64_t x, int lane) {
   return x;
 }
 
-constexpr int kBatch = 2;  // vectors a lane and table that are added up while as many are on their way
+// vectors a lane and table that are added up while as many are on their way: as many as fit 64 registers
+template <bool kTwo>
+constexpr int kBatchOf = kTwo ? 2 : 4;
 
 // The sum of a step, a vector a lane: two 32-bit reductions (128 values, or 256 of bf16 or fp16, of 2^23 at most each and so
 // 2^31 together: unsigned).
-template <typename T>
+template <bool kTwo, typename T>
 __device__ __forceinline__ uint64_t step_sum(const Source<T>& s, int i, const uint4& a, const uint4& b, Fixed& mine) {
   mine = {0, 0};
 #pragma unroll
   for (int e = 0; e < Source<T>::kN; ++e) {
-    const Fixed f = s.weight(i, e, a, b);
+    const Fixed f = s.template weight<kTwo>(i, e, a, b);
     mine.hi += f.hi, mine.lo += f.lo;
   }
   return ((uint64_t)__reduce_add_sync(0xffffffffu, (unsigned)mine.hi) << 23) +
@@ -168,27 +172,27 @@ __device__ __forceinline__ uint64_t step_sum(const Source<T>& s, int i, const ui
 }
 
 // The warp's sum over [lo, hi), whole steps; lane l gets in `part` that of its l-th part of `per` steps.
-template <typename T>
+template <bool kTwo, typename T>
 __device__ __forceinline__ uint64_t segment_sum(const Source<T>& s, int lo, int hi, int per, int lane, uint64_t& part) {
-  constexpr int kN = Source<T>::kN, kStep = 32 * kN;
+  constexpr int kN = Source<T>::kN, kStep = 32 * kN, kBatch = kBatchOf<kTwo>;
   uint64_t acc = 0, in_part = 0;
   int steps = 0, parts = 0;
   part = 0;
   uint4 a[kBatch], b[kBatch];
 #pragma unroll
-  for (int k = 0; k < kBatch; ++k) s.load(lo + k * kStep < hi ? lo + k * kStep + lane * kN : s.vocab, a[k], b[k]);
+  for (int k = 0; k < kBatch; ++k) s.template load<kTwo>(lo + k * kStep < hi ? lo + k * kStep + lane * kN : s.vocab, a[k], b[k]);
 #pragma unroll 1
   for (int i0 = lo; i0 < hi; i0 += kBatch * kStep) {
     uint4 na[kBatch], nb[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int i = i0 + (kBatch + k) * kStep;
-      s.load(i < hi ? i + lane * kN : s.vocab, na[k], nb[k]);
+      s.template load<kTwo>(i < hi ? i + lane * kN : s.vocab, na[k], nb[k]);
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       Fixed mine;
-      in_part += step_sum(s, i0 + k * kStep + lane * kN, a[k], b[k], mine);
+      in_part += step_sum<kTwo>(s, i0 + k * kStep + lane * kN, a[k], b[k], mine);
       if (++steps == per || i0 + (k + 1) * kStep >= hi) {
         if (lane == parts) part += in_part;  // (a step behind the last one adds 0)
         acc += in_part;
@@ -202,7 +206,7 @@ __device__ __forceinline__ uint64_t segment_sum(const Source<T>& s, int lo, int 
 }
 
 // The smallest index of [lo, hi), whole steps, whose running sum from lo passes `target`; -1 if none does.
-template <typename T>
+template <bool kTwo, typename T>
 __device__ __forceinline__ int find(const Source<T>& s, int lo, int hi, uint64_t target, int lane) {
   constexpr int kN = Source<T>::kN, kStep = 32 * kN;
   uint64_t before = 0;
@@ -210,16 +214,16 @@ __device__ __forceinline__ int find(const Source<T>& s, int lo, int hi, uint64_t
   for (int i0 = lo; i0 < hi; i0 += kStep) {
     const int i = i0 + lane * kN;
     uint4 a, b;
-    s.load(i, a, b);
+    s.template load<kTwo>(i, a, b);
     Fixed sum;
-    const uint64_t step = step_sum(s, i, a, b, sum);
+    const uint64_t step = step_sum<kTwo>(s, i, a, b, sum);
     if (before + step > target) {
       const uint64_t mine = joined(sum), run = before + warp_inclusive(mine, lane);
       int at = -1;
       uint64_t c = run - mine;
 #pragma unroll
       for (int e = 0; e < kN; ++e) {
-        c += joined(s.weight(i, e, a, b));
+        c += joined(s.template weight<kTwo>(i, e, a, b));
         if (at < 0 && c > target) at = i + e;
       }
       const uint32_t past = __ballot_sync(0xffffffffu, run > target);
@@ -315,7 +319,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) accept_kernel(const AcceptPara
 #pragma unroll 1
   for (int pass = 0;; ++pass) {
     uint64_t part;
-    const uint64_t sum = segment_sum(src, lo, hi, per, lane, part);
+    const uint64_t sum = src.q ? segment_sum<true>(src, lo, hi, per, lane, part) : segment_sum<false>(src, lo, hi, per, lane, part);
     if (pass == 0) cluster.barrier_wait(std::move(started));
     // every CTA gets every segment's sum: the warp whose segment holds the target goes on, from its own SM's cache
     if (lane < ranks) cluster.map_shared_rank(&s_sum[pass][0], lane)[mine] = sum;
@@ -362,7 +366,9 @@ __global__ void __launch_bounds__(kMaxThreads, 2) accept_kernel(const AcceptPara
       const uint32_t in = __ballot_sync(0xffffffffu, upto > left);
       const int l = in ? __ffs(in) - 1 : 31;
       const int from = min(lo + l * per * kStep, hi);
-      token = find(src, from, min(from + per * kStep, hi), left - __shfl_sync(0xffffffffu, upto - part, l), lane);
+      const int to = min(from + per * kStep, hi);
+      const uint64_t behind = left - __shfl_sync(0xffffffffu, upto - part, l);
+      token = src.q ? find<true>(src, from, to, behind, lane) : find<false>(src, from, to, behind, lane);
       if (token < 0) token = p.vocab - 1;
     }
     for (int t = lane; t < p.T; t += 32)
