@@ -106,9 +106,15 @@ extern "C" pkv_status pkv_kv_attn_weights(const void* q, const void* k_cache, in
     const uint32_t box[3] = {64, (uint32_t)group, (uint32_t)p.tpc};
     pkv_status s = encode_tiled(&p.qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, dims, strides, box, "q");
     if (s != PKV_OK) return s;
-    s = kv_dtype == PKV_KV_BF16 ? run_attn_weights_bf16(p, ctas, st)
-        : kv_dtype == PKV_KV_INT8 ? run_attn_weights_int8(p, ctas, st) : run_attn_weights_fp8(p, ctas, st);
-    if (s != PKV_OK) return s;
+    // a CTA a KV head and range of tiles; more heads than CTAs: in turns
+    for (int h = 0; h < num_kv_heads; h += ctas) {
+      p.h_base = h;
+      p.heads = num_kv_heads - h < ctas ? num_kv_heads - h : ctas;
+      const int grid = ctas / p.heads * p.heads;
+      s = kv_dtype == PKV_KV_BF16 ? run_attn_weights_bf16(p, grid, st)
+          : kv_dtype == PKV_KV_INT8 ? run_attn_weights_int8(p, grid, st) : run_attn_weights_fp8(p, grid, st);
+      if (s != PKV_OK) return s;
+    }
     p.prev = weights;
     p.prev_lens = nullptr;
   }

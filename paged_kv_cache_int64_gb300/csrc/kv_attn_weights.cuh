@@ -11,8 +11,9 @@
 // rows are widened to bf16 in registers (every code is a bf16 value) and stored to tensor memory as the A operand, so
 // that the queries stay the bf16 that they are.
 //
-// The tiles of all (request, KV head, 128 keys) are one list, cut into equal ranges, one a CTA, from the lengths on the
-// device. Roles: warp 0 K producer, warp 1 MMA issuer, warp 2 tensor memory, warp 3 Q producer, warps 4-11 two
+// The tiles of all (request, 128 keys) are one list, cut into equal ranges from the lengths on the device. A range has a
+// CTA a KV head, side by side, so that the heads' parts of a token's row are read together (a head's tiles of all
+// requests after another's: the same bytes, scattered, take longer). Roles: warp 0 K producer, warp 1 MMA issuer, warp 2 tensor memory, warp 3 Q producer, warps 4-11 two
 // reducing warpgroups (tiles in turn; with kN = 128 the log-sum-exp's take half of the columns each), warps 12 on the
 // widening ones (tiles in turn where there are two).
 #pragma once
@@ -42,6 +43,7 @@ struct WeightParams {
   const int32_t* q_valid;
   int32_t num_reqs, T, group, num_q_heads, num_kv_heads, block_size;
   int32_t t_base, tpc;  // tokens of this pass: t_base .. t_base + tpc - 1
+  int32_t h_base, heads;  // KV heads of this launch: h_base .. h_base + heads - 1
   float scale_log2;
   const float* part_lse;
   int32_t split_tokens, max_splits;
@@ -49,8 +51,8 @@ struct WeightParams {
   const int32_t* prev_lens;
   float* weights;
   int64_t w_stride_req, w_stride_head, max_ctx;
-  float2* stat;   // workspace: [CTAs][2][kWMaxCols] (reference, sum) of the units that a CTA has a part of
-  float* lse2;    // workspace: [R*T*Hq], base 2, of the units that one CTA has whole
+  float2* stat;   // workspace: [CTAs][2][kWMaxCols] (reference, sum) of the requests that a CTA has a part of
+  float* lse2;    // workspace: [R*T*Hq], base 2, of the requests that one CTA has whole
   int* dev_err;
   uint64_t wait_limit_ns;
 };
@@ -92,7 +94,7 @@ struct alignas(16) WShared {
   uint32_t bad[kWBadRing];
   uint32_t tmem_base;
   int abort;
-  int start_r, start_h, start_tile, ctas;
+  int start_r, start_tile, ranges;
   long long first, last;  // this CTA's tiles in the list
   long long total;
   alignas(16) float col[2][kN];              // per reducing group: minus the column's log-sum-exp (weights)
@@ -103,22 +105,20 @@ struct alignas(16) WShared {
 
 // A place in the list of tiles.
 struct WWalk {
-  int r, h, tile, tiles, n;
+  int r, tile, tiles, n;
   __device__ __forceinline__ void length(const WeightParams& p) {
     const int64_t most = (int64_t)p.max_blocks * p.block_size;
     n = (int)max((int64_t)0, min((int64_t)__ldg(p.seq_lens + r), most));
     tiles = (n + kWTile - 1) / kWTile;
   }
-  __device__ __forceinline__ void start(const WeightParams& p, int r0, int h0, int t0) {
-    r = r0, h = h0, tile = t0;
+  __device__ __forceinline__ void start(const WeightParams& p, int r0, int t0) {
+    r = r0, tile = t0;
     if (r < p.num_reqs) length(p);
   }
   // to the next tile; r = num_reqs past the last
   __device__ __forceinline__ void next(const WeightParams& p) {
     if (++tile < tiles) return;
     tile = 0;
-    if (++h < p.num_kv_heads) return;
-    h = 0;
     for (++r; r < p.num_reqs; ++r) {
       length(p);
       if (tiles) return;
@@ -204,12 +204,12 @@ __device__ __forceinline__ float w_max16(const float (&t)[16], int lane) {
   return fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
 }
 
-// The list's owner of tile x when `ctas` CTAs share `total` tiles as [c total / ctas, (c + 1) total / ctas).
-__device__ __forceinline__ int w_owner(long long x, long long total, int ctas) { return (int)(((x + 1) * ctas - 1) / total); }
+// The range that has tile x when `ranges` ranges share `total` tiles as [c total / ranges, (c + 1) total / ranges).
+__device__ __forceinline__ int w_owner(long long x, long long total, int ranges) { return (int)(((x + 1) * ranges - 1) / total); }
 
-// The log-sum-exp, base 2, of column c of the unit (r, h) of n keys, whose tiles are u0 .. u0 + tiles - 1 of the list; infinite for a
+// The log-sum-exp, base 2, of column c of request r of n keys and KV head h, whose tiles are u0 .. u0 + tiles - 1 of the list; infinite for a
 // query that sees nothing.
-static __device__ __noinline__ float column_lse(const WeightParams& p, int r, int h, int n, int tiles, long long u0, long long total, int ctas, int c) {
+static __device__ __noinline__ float column_lse(const WeightParams& p, int r, int h, int n, int tiles, long long u0, long long total, int ranges, int c) {
   const int64_t row = ((int64_t)r * p.T + p.t_base + c / p.group) * p.num_q_heads + (int64_t)h * p.group + c % p.group;
   float m = -INFINITY, sum = 0.0f;
   if (p.part_lse) {
@@ -233,15 +233,15 @@ static __device__ __noinline__ float column_lse(const WeightParams& p, int r, in
     const float hi = m * 1.4426950408889634f, lo = fmaf(m, 1.4426950408889634f, -hi) + m * 1.925963033500412e-8f;
     return sum != 0.0f && m < INFINITY ? hi + (lo + log2f(sum)) : INFINITY;
   }
-  // the CTAs that have the unit's tiles: only the first can have begun with another unit's
-  const int c0 = w_owner(u0, total, ctas), c1 = w_owner(u0 + tiles - 1, total, ctas);
+  // the ranges that have the request's tiles: only the first can have begun with another request's
+  const int c0 = w_owner(u0, total, ranges), c1 = w_owner(u0 + tiles - 1, total, ranges);
   if (c0 == c1) return __ldcg(p.lse2 + row);
-  const int which = u0 > total * c0 / ctas;
+  const int which = u0 > total * c0 / ranges;
   for (int o0 = c0; o0 <= c1; o0 += 8) {
     float2 x[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      x[j] = o0 + j <= c1 ? __ldcg(p.stat + ((int64_t)(o0 + j) * 2 + (o0 + j == c0 ? which : 0)) * kWMaxCols + c) : make_float2(0.0f, 0.0f);
+      x[j] = o0 + j <= c1 ? __ldcg(p.stat + (((int64_t)(o0 + j) * p.heads + h - p.h_base) * 2 + (o0 + j == c0 ? which : 0)) * kWMaxCols + c) : make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if (x[j].y == 0.0f) continue;
@@ -263,6 +263,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   WShared<kFmt, kN>& sh = *reinterpret_cast<WShared<kFmt, kN>*>(smem + G::kTiles);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int range = (int)blockIdx.x / p.heads, h = p.h_base + (int)blockIdx.x - range * p.heads;
   const uint64_t wl = p.wait_limit_ns;
   // every tile's scores are read by one reducing group, or by both where each has half of the columns
   constexpr bool kBoth = kStats && kN == 128;
@@ -280,23 +281,20 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    total *= p.num_kv_heads;
     odd = __any_sync(0xffffffffu, odd);
-    // a tile each, where there are fewer tiles than CTAs (so that none between a unit's CTAs is without a part)
-    const int ctas = (int)min((long long)gridDim.x, max(total, 1ll));
-    const bool idle = blockIdx.x >= ctas;
-    const long long first = idle ? total : total * blockIdx.x / ctas, last = idle ? total : total * (blockIdx.x + 1) / ctas;
-    int at_r = p.num_reqs, at_h = 0, at_t = 0;
+    // a tile each, where there are fewer tiles than ranges (so that none between a request's ranges is without a part)
+    const int ranges = (int)min((long long)gridDim.x / p.heads, max(total, 1ll));
+    const bool idle = range >= ranges;
+    const long long first = idle ? total : total * range / ranges, last = idle ? total : total * (range + 1) / ranges;
+    int at_r = p.num_reqs, at_t = 0;
     long long before = 0;  // tiles of the requests before
     if (first < last)
       for (int r0 = 0; r0 < p.num_reqs; r0 += 32) {
         const int r = r0 + lane;
         long long mine = 0;
-        int tiles = 0;
         if (r < p.num_reqs) {
           const int n = (int)max((int64_t)0, min((int64_t)__ldg(p.seq_lens + r), most));
-          tiles = (n + kWTile - 1) / kWTile;
-          mine = (long long)tiles * p.num_kv_heads;
+          mine = (n + kWTile - 1) / kWTile;
         }
         long long run = mine;
 #pragma unroll
@@ -308,18 +306,15 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
         const uint32_t past = __ballot_sync(0xffffffffu, run > first);
         if (past) {
           const int l = __ffs(past) - 1;
-          const int in = (int)__shfl_sync(0xffffffffu, first - (run - mine), l);
-          tiles = __shfl_sync(0xffffffffu, tiles, l);
+          at_t = (int)__shfl_sync(0xffffffffu, first - (run - mine), l);
           at_r = r0 + l;
-          at_h = in / tiles;
-          at_t = in - at_h * tiles;
           break;
         }
         before = __shfl_sync(0xffffffffu, run, 31);
       }
     if (lane == 0) {
-      sh.first = first, sh.last = last, sh.total = total, sh.ctas = ctas;
-      sh.start_r = at_r, sh.start_h = at_h, sh.start_tile = at_t;
+      sh.first = first, sh.last = last, sh.total = total, sh.ranges = ranges;
+      sh.start_r = at_r, sh.start_tile = at_t;
       if (odd && blockIdx.x == 0) record_error(p.dev_err, kErrDeviceBounds);
     }
   } else if (warp == 1 && lane == 0) {
@@ -358,7 +353,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
   volatile int* abort = &sh.abort;
   const int count = (int)(sh.last - sh.first);
   WWalk at;
-  at.start(p, sh.start_r, sh.start_h, sh.start_tile);
+  at.start(p, sh.start_r, sh.start_tile);
 
   if (warp == 0) {
     // ------------------------------------------------------------------------------------ K producer
@@ -377,7 +372,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
     if (count) blk = look_up(at, slot);
     for (int i = 0; i < count; ++i) {
       uint8_t* stage = smem + G::kOffK + st * G::kStage;
-      const int h = at.h, my_blk = blk, my_slot = slot;
+      const int my_blk = blk, my_slot = slot;
       at.next(p);
       if (i + 1 < count) blk = look_up(at, slot);
       bool ok = true;
@@ -420,7 +415,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
         if (ok) {
           mbar_arm_tx(&sh.q_full[b], 512u * (uint32_t)(p.tpc * p.group), &sh.armed_q[b]);
           for (int c = 0; c < 4; ++c)
-            tma_load_3d(smem + b * G::kQBytes + c * G::kQChunk, &p.qmap, &sh.q_full[b], c * 64, at.h * p.group, at.r * p.T + p.t_base);
+            tma_load_3d(smem + b * G::kQBytes + c * G::kQChunk, &p.qmap, &sh.q_full[b], c * 64, h * p.group, at.r * p.T + p.t_base);
         }
       }
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
@@ -524,7 +519,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
       for (int n = 0; n < kStride; ++n, ++i)
         if (i < count) w.next(p);
     };
-    int blk = -1, slot = 0, blk_h = 0, near_r = -1, near_len = 0;
+    int blk = -1, slot = 0, near_r = -1, near_len = 0;
     auto load_block = [&]() {
       blk = -1;
       if (far_i < count) {
@@ -532,7 +527,6 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
         if (pos < far.n) {
           const int col = pos / p.block_size;
           slot = pos - col * p.block_size;
-          blk_h = far.h;
           blk = __ldg(p.block_table + (int64_t)far.r * p.bt_stride + col);
         }
       }
@@ -540,7 +534,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
     };
     auto load_scale = [&]() {
       return blk >= 0 && (int64_t)blk < p.num_blocks
-                 ? __ldg(p.k_scale + (int64_t)blk * p.s_stride_blk + (int64_t)slot * p.s_stride_tok + blk_h) : 0.0f;
+                 ? __ldg(p.k_scale + (int64_t)blk * p.s_stride_blk + (int64_t)slot * p.s_stride_tok + h) : 0.0f;
     };
     auto load_prev = [&]() {
       float x = 0.0f;
@@ -550,7 +544,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
           near_r = near.r;
           near_len = (int)min((int64_t)(p.prev_lens ? min(__ldg(p.prev_lens + near_r), near.n) : near.n), p.max_ctx);
         }
-        if (key < near_len) x = p.prev[(int64_t)near.r * p.w_stride_req + (int64_t)near.h * p.w_stride_head + key];
+        if (key < near_len) x = p.prev[(int64_t)near.r * p.w_stride_req + (int64_t)h * p.w_stride_head + key];
       }
       step(near, near_i);
       return x;
@@ -580,7 +574,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
           const int valid = p.q_valid ? min(__ldg(p.q_valid + at.r), p.T) : p.T;
           nq = max(0, min(valid - p.t_base, p.tpc)) * p.group;
           w_bar(1 + grp, 128);  // the group has read the last unit's columns
-          if (k < kN) sh.col[grp][k] = k < nq ? -column_lse(p, at.r, at.h, at.n, at.tiles, sh.first + i - at.tile, sh.total, sh.ctas, k) : -INFINITY;
+          if (k < kN) sh.col[grp][k] = k < nq ? -column_lse(p, at.r, h, at.n, at.tiles, sh.first + i - at.tile, sh.total, sh.ranges, k) : -INFINITY;
           w_bar(1 + grp, 128);
         }
       }
@@ -671,7 +665,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
             tc_fence_before();
             mbar_arrive(&sh.s_free[i & 1]);
             if (key < at.n && key < p.max_ctx)
-              p.weights[(int64_t)at.r * p.w_stride_req + (int64_t)at.h * p.w_stride_head + key] = before + sum;
+              p.weights[(int64_t)at.r * p.w_stride_req + (int64_t)h * p.w_stride_head + key] = before + sum;
           }
         }
       }
@@ -702,7 +696,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
             }
             const long long u0 = sh.first + i - at.tile;
             if (u0 >= sh.first && u0 + at.tiles <= sh.last) {
-              const int64_t row = ((int64_t)at.r * p.T + p.t_base + c / p.group) * p.num_q_heads + (int64_t)at.h * p.group + c % p.group;
+              const int64_t row = ((int64_t)at.r * p.T + p.t_base + c / p.group) * p.num_q_heads + (int64_t)h * p.group + c % p.group;
               p.lse2[row] = sum != 0.0f ? m + log2f(sum) : INFINITY;
             } else {
               p.stat[((int64_t)blockIdx.x * 2 + (u0 > sh.first)) * kWMaxCols + c] = make_float2(m, sum);
