@@ -8,8 +8,11 @@
 // warp (moved only when a score passes its reference by 2^64, so that a tile has no exchange between threads).
 //
 // The K cache is what is read: bf16 tiles go to the tensor core as TMA leaves them (128-byte swizzle); int8 and e4m3
-// rows are widened to bf16 in registers (every code is a bf16 value) and stored to tensor memory as the A operand, so
-// that the queries stay the bf16 that they are.
+// rows are widened to fp16 in registers (every code is an fp16 value) and stored to tensor memory as the A operand. Both
+// operands have one type, so the queries of a (request, KV head) then become fp16 too, times the power of two that takes
+// the largest of them to [2^14, 2^15): elements down to 2^-28 of the largest keep all of their bits, smaller ones are
+// taken to 2^-39 of it. (Widening to bf16 instead, which needs no change to the queries, takes twice the instructions,
+// and these are what bounds the kernel: int8 137 us, e4m3 131 for eight tokens over 32 requests of up to 40,960 keys.)
 //
 // The tiles of all (request, 128 keys) are one list, cut into equal ranges from the lengths on the device. A range has a
 // CTA a KV head, side by side, so that the heads' parts of a token's row are read together (a head's tiles of all
@@ -85,7 +88,7 @@ struct WGeo {
 template <int kFmt, int kN>
 struct alignas(16) WShared {
   using G = WGeo<kFmt, kN>;
-  uint64_t q_full[2], q_free[2];
+  uint64_t q_full[2], q_ready[2], q_free[2];  // q_ready: as fp16
   uint64_t k_full[G::kStages], k_free[G::kStages];
   uint64_t a_ready[G::kABufs], a_free[G::kABufs];
   uint64_t s_full[2], s_free[2];
@@ -99,6 +102,8 @@ struct alignas(16) WShared {
   long long total;
   alignas(16) float col[2][kN];              // per reducing group: minus the column's log-sum-exp (weights)
   alignas(16) int token[kN];                 // a column's token of the pass
+  float q_unscale[8];                        // of the last requests' queries: the power of two back
+  uint32_t q_max[2][4];                      // per widening group and warp
   alignas(16) float ref[8][G::kHalf];        // per reducing warp: the columns' references (log-sum-exps)
   alignas(16) float2 part[2][8][G::kHalf];   // per unit parity and warp: (reference, sum)
 };
@@ -133,37 +138,18 @@ __device__ __forceinline__ bool w_elect() {
 }
 __device__ __forceinline__ void w_bar(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
-__device__ __forceinline__ uint32_t bf16x2_sub(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-// 4 int8 codes -> 4 bf16 integers, exact. With u = code + 128, bf16 bits 0x4300 + u are f = 128 + u below u = 128 and 2 u from
-// there on (the mantissa has seven bits), so that u - 128 = (f - 256) - max(f / 2 - 128, 0): every step is exact, and three of
-// the four run beside the byte permutes on the FMA pipe.
-__device__ __forceinline__ uint32_t widen2_int8(uint32_t f) {
-  uint32_t half, y, r;
-  asm("fma.rn.relu.bf16x2 %0, %1, %2, %3;" : "=r"(half) : "r"(f), "r"(0x3f003f00u), "r"(0xc300c300u));
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(f), "r"(0x3f803f80u), "r"(0xc380c380u));
-  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(half), "r"(0xbf80bf80u), "r"(y));
-  return r;
-}
+// 4 int8 codes -> 4 fp16 integers, exact: fp16 bits 0x6400 | u are 1024 + u, u = code + 128.
 __device__ __forceinline__ void widen4_int8(uint32_t w, uint32_t& lo, uint32_t& hi) {
   const uint32_t u = w ^ 0x80808080u;
-  lo = widen2_int8(__byte_perm(u, 0x43434343u, 0x4140));
-  hi = widen2_int8(__byte_perm(u, 0x43434343u, 0x4342));
+  lo = __byte_perm(u, 0x64646464u, 0x5140);
+  hi = __byte_perm(u, 0x64646464u, 0x7362);
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(0x64806480u));  // 1152
+  asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(0x64806480u));
 }
-// 4 e4m3 codes -> 4 bf16 values, exact: the hardware's conversion to fp16, then fp32, then bf16.
+// 4 e4m3 codes -> 4 fp16 values, exact: the hardware's conversion.
 __device__ __forceinline__ void widen4_e4m3(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t a = e4m3x2_to_f16x2((uint16_t)w), b = e4m3x2_to_f16x2((uint16_t)(w >> 16));
-  const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a)), y = __half22float2(*reinterpret_cast<const __half2*>(&b));
-  lo = pack_bf16x2(x.x, x.y);
-  hi = pack_bf16x2(y.x, y.y);
+  lo = e4m3x2_to_f16x2((uint16_t)w);
+  hi = e4m3x2_to_f16x2((uint16_t)(w >> 16));
 }
 
 // Sums over the warp's lanes of kC (16 or 32 at a time) columns: lane l gets column l's (kC = 16: l & 15's).
@@ -320,6 +306,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
   } else if (warp == 1 && lane == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.q_full[i], 1);
+      mbar_init(&sh.q_ready[i], 128);
       mbar_init(&sh.q_free[i], 1);
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.s_free[i], kBoth ? 256 : 128);
@@ -423,7 +410,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------------------------ MMA issuer
-    constexpr uint32_t id = idesc_f16(128, kN, true, false, false);
+    constexpr uint32_t id = idesc_f16(128, kN, G::kWide, false, false);
     int st = 0, round = 0, units = -1;
     for (int i = 0; i < count; ++i) {
       const bool first = i == 0 || at.tile == 0;
@@ -432,7 +419,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
       const bool last = i + 1 == count || at.tile + 1 == at.tiles;
       at.next(p);
       bool ok = true;
-      if (first) ok = mbar_wait_suspend(&sh.q_full[b], (units / G::kQBufs) & 1, abort, wl);
+      if (first) ok = mbar_wait_suspend(G::kWide ? &sh.q_full[b] : &sh.q_ready[b], (units / G::kQBufs) & 1, abort, wl);
       if (ok && i >= 2) ok = mbar_wait_suspend(&sh.s_free[i & 1], ((i >> 1) - 1) & 1, abort, wl);
       if (ok) ok = G::kWide ? mbar_wait_suspend(&sh.k_full[st], round & 1, abort, wl)
                             : mbar_wait_suspend(&sh.a_ready[ab], (i / G::kABufs) & 1, abort, wl);
@@ -464,13 +451,63 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
       const int grp = (warp - 12) >> 2;
       const int k = (warp & 3) * 32 + lane;
       const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-      for (int i = grp; i < count; i += G::kConv) {
+      int units = -1;
+      bool dead = false;  // (the groups' own barrier is reached as often by every warp)
+      for (int i = 0; i < count; ++i, at.next(p)) {
+        const bool first = i == 0 || at.tile == 0;
+        units += first;
+        if (i % G::kConv != grp) continue;
+        if (first) {
+          // the request's queries, by the group that has its first tile
+          const int b = units % G::kQBufs;
+          uint8_t* q = smem + b * G::kQBytes;
+          const int pieces = 4 * kN * 8;  // of 16 bytes; the columns behind the pass's tokens are nobody's
+          if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait_suspend(&sh.q_full[b], (units / G::kQBufs) & 1, abort, wl));
+          const int cols = p.tpc * p.group;
+          uint32_t big = 0;  // the largest finite magnitude's bits, in the upper half
+#pragma unroll 1
+          for (int j = k; j < pieces; j += 128) {
+            if ((j >> 3) % kN >= cols) continue;
+            const uint4 v = *reinterpret_cast<const uint4*>(q + j * 16);
+            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t lo = x[e] << 16 & 0x7fff0000u, hi = x[e] & 0x7fff0000u;
+              big = max(big, max(lo < 0x7f800000u ? lo : 0u, hi < 0x7f800000u ? hi : 0u));
+            }
+          }
+          big = __reduce_max_sync(0xffffffffu, big);
+          if (lane == 0) sh.q_max[grp][warp & 3] = big;
+          w_bar(4 + grp, 128);
+          big = max(max(sh.q_max[grp][0], sh.q_max[grp][1]), max(sh.q_max[grp][2], sh.q_max[grp][3]));
+          // 2^(14 - e) for a largest of exponent e, in two factors that stay finite
+          const int up = max(-126, min(14 - ((int)(big >> 23) - 127), 141));
+          const int up1 = up / 2;
+          const float s0 = __int_as_float((127 + up1) << 23), s1 = __int_as_float((127 + up - up1) << 23);
+#pragma unroll 1
+          for (int j = k; j < pieces; j += 128) {
+            if ((j >> 3) % kN >= cols) continue;
+            uint4* ptr = reinterpret_cast<uint4*>(q + j * 16);
+            const uint4 v = *ptr;
+            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              o[e] = pack_f16x2(__uint_as_float(x[e] << 16) * s0 * s1, __uint_as_float(x[e] & 0xffff0000u) * s0 * s1);
+            *ptr = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+          if (k == 0) sh.q_unscale[units & 7] = __int_as_float((127 - up1) << 23) * __int_as_float((127 - (up - up1)) << 23);
+          fence_proxy_async_smem();
+          w_bar(4 + grp, 128);  // (q_max may be written again)
+          if (!dead) mbar_arrive(&sh.q_ready[b]);
+        }
         const int st = i % G::kStages;
         const uint8_t* row = smem + G::kOffK + st * G::kStage + k * 128;
-        bool ok = mbar_wait_suspend(&sh.k_full[st], (i / G::kStages) & 1, abort, wl);
+        bool ok = !dead && mbar_wait_suspend(&sh.k_full[st], (i / G::kStages) & 1, abort, wl);
         const int ab = i % G::kABufs;
         if (ok && i >= G::kABufs) ok = mbar_wait_suspend(&sh.a_free[ab], (i / G::kABufs - 1) & 1, abort, wl);
-        if (!__all_sync(0xffffffffu, ok)) break;
+        dead = !__all_sync(0xffffffffu, ok);
+        if (dead) continue;
         tc_fence_after();
         const uint32_t a = tmem + lane_off + G::kColA + ab * 128;
         // (rolled, as every loop of a role: together they have to fit the instruction cache)
@@ -560,9 +597,10 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
     // the weights' launch begins before the log-sum-exps' has ended: these are waited for, the keys are not
     if (!kStats) asm volatile("griddepcontrol.wait;" ::: "memory");
     float l[kStats ? G::kHalf : 1];  // a thread's part of the columns' sums
-    int prefix = 0, nq = kStats ? p.tpc * p.group : 0;
+    int prefix = 0, nq = kStats ? p.tpc * p.group : 0, seen = -1;  // seen: requests so far
     for (int i = 0; i < count; ++i) {
       const bool first = i == 0 || at.tile == 0, last = i + 1 == count || at.tile + 1 == at.tiles;
+      seen += first;
       if (first) {
         prefix = __ldg(p.seq_lens + at.r) - p.T + p.t_base;  // the pass's token t sits at position prefix + t
         if constexpr (kStats) {
@@ -593,6 +631,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
           tc_fence_after();
           const uint32_t s_addr = tmem + lane_off + G::kColS + (i & 1) * kN + c_first;
           const bool bad_key = (sh.bad[i & (kWBadRing - 1)] >> kseg) & 1u;
+          if (!G::kWide) f *= sh.q_unscale[seen & 7];
           if (bad_key) f = 0.0f;
           // columns of tokens before this do not see the key; every column does where it is not above 0
           const int behind = key < at.n ? key - prefix : INT_MAX;

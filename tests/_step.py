@@ -57,7 +57,7 @@ def select(scores, n, sinks, recent, budget):
     return np.sort(kept).astype(np.int32)
 
 
-def weights(q, k, n, T, scale, valid, lse=None):
+def weights(q, k, n, T, scale, valid, lse=None, rounded=False):
     """One request: q [T][Hq][256], k [n][Hkv][256] in 64 bits, n keys; lse [T][Hq] or None.
     -> w [Hkv][n] and a bound on the error of an fp32 kernel of it (u = 2^-24 the rounding of one operation).
 
@@ -66,11 +66,13 @@ def weights(q, k, n, T, scale, valid, lse=None):
     64 u m. Scale, log2(e) and the subtraction: 4 u (|s| + |lse|). exp2 in hardware: 2^-22 = 4 u relative. Where the
     kernel computes lse itself, it has the largest of the scores' errors, a sum of n positive terms kept in at
     most n + 128 additions (their running sums never pass the total): (n + 128) u, and a logarithm, 4 u |lse|. Adding up
-    the columns: one rounding each of the running sum."""
+    the columns: one rounding each of the running sum. rounded: the queries are taken to 2^-39 of the largest of the
+    request's and KV head's."""
     u = 2.0 ** -24
     hq, hkv = q.shape[1], k.shape[1]
     g = hq // hkv
     w, bound = np.zeros((hkv, n)), np.zeros((hkv, n))
+    q_max = np.abs(q).reshape(q.shape[0], hkv, -1).max((0, 2))
     for t in range(min(T, valid)):
         m = n - T + t + 1
         if m <= 0:
@@ -79,13 +81,14 @@ def weights(q, k, n, T, scale, valid, lse=None):
             key = k[:m, h // g]
             s = scale * (key @ q[t, h])
             mag = scale * (np.abs(key) @ np.abs(q[t, h]))
+            off = scale * 2.0 ** -39 * q_max[h // g] * np.abs(key).sum(1) if rounded else np.zeros(m)
             L = lse[t, h] if lse is not None else s.max() + np.log(np.exp(s - s.max()).sum())
             if L == -np.inf:
                 continue
             p = np.exp(s - L)
-            rel = 64 * u * mag + 4 * u * (np.abs(s) + abs(L)) + 4 * u
+            rel = off + 64 * u * mag + 4 * u * (np.abs(s) + abs(L)) + 4 * u
             if lse is None:
-                rel = rel + 64 * u * mag.max() + 4 * u * (np.abs(s).max() + abs(L)) + (m + 128) * u + 4 * u
+                rel = rel + off.max() + 64 * u * mag.max() + 4 * u * (np.abs(s).max() + abs(L)) + (m + 128) * u + 4 * u
             else:
                 rel = rel + 16 * u * (1.0 + abs(L))  # the splits' log-sum-exps put together
             w[h // g, :m] += p

@@ -88,7 +88,7 @@ def expect(c, q, T, scale, valid=None, lse=None):
     out = []
     for r, n in enumerate(c.lens):
         out.append(S.weights(qd[r * T:(r + 1) * T], c.rows[r], n, T, scale, T if valid is None else max(0, min(valid[r], T)),
-                             None if lse is None else lse[r * T:(r + 1) * T]))
+                             None if lse is None else lse[r * T:(r + 1) * T], rounded=c.fmt != "bf16"))
     return out
 
 
@@ -211,6 +211,29 @@ def test_weights_of_far_apart_scores(pkv):
         d.__dict__.update(c.__dict__, rows=[rows])
         assert weigh(pkv, d, q.to(DEV), 2, 1.0, w) == 0
         verify_weights(w, expect(d, q, 2, 1.0), [700])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "fp8"])
+def test_weights_of_queries_of_unlike_sizes(pkv, fmt):
+    """Query heads and elements from 2^-60 to 2^9 side by side, rows of zeros, requests whose queries are all tiny, and the
+    largest that bf16 holds beside keys of zeros."""
+    lens, T, hkv, g = [300, 200, 140, 130], 3, 2, 4
+    c = Cache(fmt, lens, hkv, 16, seed=31)
+    gen = torch.Generator().manual_seed(31)
+    q = torch.randn(4 * T, hkv * g, 256, generator=gen) * torch.exp2(torch.randint(-60, 4, (4 * T, hkv * g, 1), generator=gen).float())
+    q[:T] *= torch.exp2(torch.randint(-20, 3, (T, hkv * g, 256), generator=gen).float())
+    q[0, 3] = 0.0
+    q[T:2 * T] *= 2.0 ** -40
+    q[2 * T:3 * T] *= 2.0 ** -80
+    q[3 * T:, :, 8:] = 0.0
+    q[3 * T:, :, :8] = 3e38
+    pos = np.arange(130)
+    c.pool[torch.from_numpy(c.bt[3, pos // 16].astype(np.int64)).to(DEV), torch.from_numpy(pos % 16).to(DEV), :, :8] = 0
+    c.rows[3][:, :, :8] = 0.0
+    q = q.to(torch.bfloat16)
+    w = torch.zeros(4, hkv, 300, device=DEV)
+    assert weigh(pkv, c, q.to(DEV), T, 1 / 16, w) == 0
+    verify_weights(w, expect(c, q, T, 1 / 16), lens)
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "int8", "fp8"])
