@@ -66,17 +66,19 @@ extern "C" pkv_status pkv_kv_attn_weights(const void* q, const void* k_cache, in
   p.seg = seg;
   p.big_ok = block_size >= kWTile;
   {
-    const uint64_t dims[4] = {(uint64_t)kWD, (uint64_t)num_kv_heads, (uint64_t)block_size, (uint64_t)num_blocks};
-    const uint64_t strides[3] = {(uint64_t)(stride_head * es), (uint64_t)(stride_tok * es), (uint64_t)(stride_blk * es)};
-    const CUtensorMapDataType type = kv_dtype == PKV_KV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8;
-    uint32_t box[4] = {(uint32_t)(128 / es), 1, (uint32_t)seg, 1};
-    pkv_status s = encode_tiled(&p.kmap, type, 4, k_cache, dims, strides, box, "k_cache");
+    const uint64_t head = (uint64_t)(stride_head * es), tok = (uint64_t)(stride_tok * es), blk = (uint64_t)(stride_blk * es);
+    const uint64_t hkv = (uint64_t)num_kv_heads, bs = (uint64_t)block_size, nb = (uint64_t)num_blocks;
+    const bool wide = kv_dtype == PKV_KV_BF16;
+    const uint64_t dims4[4] = {(uint64_t)kWD, hkv, bs, nb}, strides4[3] = {head, tok, blk};
+    const uint64_t dims5[5] = {128, bs, 2, hkv, nb}, strides5[4] = {tok, 128, head, blk};
+    auto encode = [&](CUtensorMap* map, uint32_t rows) {
+      const uint32_t box4[4] = {64, 1, rows, 1}, box5[5] = {128, rows, 2, 1, 1};
+      return wide ? encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, k_cache, dims4, strides4, box4, "k_cache")
+                  : encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, k_cache, dims5, strides5, box5, "k_cache");
+    };
+    pkv_status s = encode(&p.kmap, (uint32_t)seg);
+    if (s == PKV_OK && p.big_ok) s = encode(&p.kmap_big, kWTile);
     if (s != PKV_OK) return s;
-    if (p.big_ok) {
-      box[2] = kWTile;
-      s = encode_tiled(&p.kmap_big, type, 4, k_cache, dims, strides, box, "k_cache");
-      if (s != PKV_OK) return s;
-    }
   }
   p.k_scale = k_scale;
   p.num_blocks = num_blocks;

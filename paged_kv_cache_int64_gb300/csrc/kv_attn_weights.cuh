@@ -34,8 +34,10 @@ constexpr int kWBadRing = 16;   // tiles whose bad segments are remembered: more
 
 struct WeightParams {
   CUtensorMap qmap;   // bf16 [R*T][Hq][256]: dims {256, Hq, R*T}, box {64, group, tpc}
-  CUtensorMap kmap;   // dims {256, Hkv, bs, nb}, box {128 bytes, 1, seg, 1}
-  CUtensorMap kmap_big;  // box {128 bytes, 1, 128, 1}: a whole tile inside one block
+  // bf16: dims {256, Hkv, bs, nb}, box {64, 1, seg, 1}. int8, e4m3: dims {128, bs, 2, Hkv, nb} (a row's halves are the third),
+  // box {128, seg, 2, 1, 1}, one copy a segment.
+  CUtensorMap kmap;
+  CUtensorMap kmap_big;  // the same with 128 rows: a whole tile inside one block
   int32_t big_ok, seg;
   const float* k_scale;
   int64_t num_blocks, s_stride_blk, s_stride_tok;
@@ -95,6 +97,7 @@ struct alignas(16) WShared {
   uint64_t drain;
   uint32_t armed_k[G::kStages], armed_q[2];
   uint32_t bad[kWBadRing];
+  int rows_log2[kWBadRing];  // rows of a tile's segments
   uint32_t tmem_base;
   int abort;
   int start_r, start_tile, ranges;
@@ -345,7 +348,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
   if (warp == 0) {
     // ------------------------------------------------------------------------------------ K producer
     // the table entries of a tile's segments, a lane each, are looked up a tile ahead
-    const int nseg = kWTile / p.seg;
+    const int nseg = kWTile / p.seg, seg_log2 = 31 - __clz(p.seg);
     auto look_up = [&](const WWalk& w, int& slot) -> int {
       const int pos = w.tile * kWTile + lane * p.seg;
       slot = 0;
@@ -372,20 +375,29 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
       if (lane == 0) {
         if (bad) record_error(p.dev_err, kErrDeviceBounds);
         sh.bad[i & (kWBadRing - 1)] = bad;
+        sh.rows_log2[i & (kWBadRing - 1)] = big ? 7 : seg_log2;
         mbar_arm_tx(&sh.k_full[st], (big ? (uint32_t)kWTile : loaded * (uint32_t)p.seg) * (uint32_t)G::kRowBytes, &sh.armed_k[st]);
       }
       __syncwarp();
-      constexpr int kInner = G::kWide ? 64 : 128;  // elements of a 128-byte column
-      if (big) {
-        if (w_elect()) {
+      if constexpr (G::kWide) {
+        if (big) {
+          if (w_elect()) {
+#pragma unroll
+            for (int c = 0; c < G::kChunks; ++c)
+              tma_load_4d(stage + c * G::kChunk, &p.kmap_big, &sh.k_full[st], c * 64, h, slot0, blk0);
+          }
+        } else if (my_blk >= 0) {
 #pragma unroll
           for (int c = 0; c < G::kChunks; ++c)
-            tma_load_4d(stage + c * G::kChunk, &p.kmap_big, &sh.k_full[st], c * kInner, h, slot0, blk0);
+            tma_load_4d(stage + c * G::kChunk + lane * p.seg * 128, &p.kmap, &sh.k_full[st], c * 64, h, my_slot, my_blk);
         }
-      } else if (my_blk >= 0) {
-#pragma unroll
-        for (int c = 0; c < G::kChunks; ++c)
-          tma_load_4d(stage + c * G::kChunk + lane * p.seg * 128, &p.kmap, &sh.k_full[st], c * kInner, h, my_slot, my_blk);
+      } else {
+        // [segment][half][rows][128 bytes]
+        if (big) {
+          if (w_elect()) tma_load_5d(stage, &p.kmap_big, &sh.k_full[st], 0, slot0, 0, h, blk0);
+        } else if (my_blk >= 0) {
+          tma_load_5d(stage + lane * p.seg * 256, &p.kmap, &sh.k_full[st], 0, my_slot, 0, h, my_blk);
+        }
       }
       __syncwarp();
       if (++st == G::kStages) st = 0, ++round;
@@ -502,7 +514,6 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
           if (!dead) mbar_arrive(&sh.q_ready[b]);
         }
         const int st = i % G::kStages;
-        const uint8_t* row = smem + G::kOffK + st * G::kStage + k * 128;
         bool ok = !dead && mbar_wait_suspend(&sh.k_full[st], (i / G::kStages) & 1, abort, wl);
         const int ab = i % G::kABufs;
         if (ok && i >= G::kABufs) ok = mbar_wait_suspend(&sh.a_free[ab], (i / G::kABufs - 1) & 1, abort, wl);
@@ -510,6 +521,8 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
         if (dead) continue;
         tc_fence_after();
         const uint32_t a = tmem + lane_off + G::kColA + ab * 128;
+        const int rows_log2 = sh.rows_log2[i & (kWBadRing - 1)], half = 128 << rows_log2;  // of the key's segment
+        const uint8_t* row = smem + G::kOffK + st * G::kStage + (k >> rows_log2) * 2 * half + (k & ((1 << rows_log2) - 1)) * 128;
         // (rolled, as every loop of a role: together they have to fit the instruction cache)
 #pragma unroll 4
         for (int w8 = 0; w8 < 8; ++w8) {  // 32 codes, 16 columns a step
@@ -517,7 +530,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const int piece = 2 * (w8 & 3) + j;
-            const uint4 v = *reinterpret_cast<const uint4*>(row + (w8 >> 2) * G::kChunk + ((piece ^ (k & 7)) * 16));
+            const uint4 v = *reinterpret_cast<const uint4*>(row + (w8 >> 2) * half + ((piece ^ (k & 7)) * 16));
             const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
