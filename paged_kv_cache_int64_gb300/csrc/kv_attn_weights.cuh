@@ -139,6 +139,29 @@ __device__ __forceinline__ bool w_elect() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
   return r != 0;
 }
+// The wait for a request's queries: with a bound below the time that a suspended wait may sleep (a test of the give-up
+// path) it polls. (The same in every wait: 2 to 4 % of the kernel's time.)
+static __device__ __noinline__ bool w_wait_brief(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if (*abort || globaltimer_ns() - t0 > limit_ns) {
+      *abort = 1;
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool w_wait_q(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+  return limit_ns < kSuspendHintNs ? w_wait_brief(bar, parity, abort, limit_ns) : mbar_wait_suspend(bar, parity, abort, limit_ns);
+}
 __device__ __forceinline__ void w_bar(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
 // 4 int8 codes -> 4 fp16 integers, exact: fp16 bits 0x6400 | u are 1024 + u, u = code + 128.
@@ -431,7 +454,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
       const bool last = i + 1 == count || at.tile + 1 == at.tiles;
       at.next(p);
       bool ok = true;
-      if (first) ok = mbar_wait_suspend(G::kWide ? &sh.q_full[b] : &sh.q_ready[b], (units / G::kQBufs) & 1, abort, wl);
+      if (first) ok = w_wait_q(G::kWide ? &sh.q_full[b] : &sh.q_ready[b], (units / G::kQBufs) & 1, abort, wl);
       if (ok && i >= 2) ok = mbar_wait_suspend(&sh.s_free[i & 1], ((i >> 1) - 1) & 1, abort, wl);
       if (ok) ok = G::kWide ? mbar_wait_suspend(&sh.k_full[st], round & 1, abort, wl)
                             : mbar_wait_suspend(&sh.a_ready[ab], (i / G::kABufs) & 1, abort, wl);
@@ -474,7 +497,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
           const int b = units % G::kQBufs;
           uint8_t* q = smem + b * G::kQBytes;
           const int pieces = 4 * kN * 8;  // of 16 bytes; the columns behind the pass's tokens are nobody's
-          if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait_suspend(&sh.q_full[b], (units / G::kQBufs) & 1, abort, wl));
+          if (!dead) dead = !__all_sync(0xffffffffu, w_wait_q(&sh.q_full[b], (units / G::kQBufs) & 1, abort, wl));
           const int cols = p.tpc * p.group;
           uint32_t big = 0;  // the largest finite magnitude's bits, in the upper half
 #pragma unroll 1

@@ -158,6 +158,40 @@ def test_weights_on_top_of_earlier_ones(pkv, fmt, in_place):
     verify_weights(w2, expect(c, q, T, 1 / 16, valid), lens, [before[r, :, :n].double().cpu().numpy() for r, n in enumerate(lens)])
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "fp8"])
+@pytest.mark.parametrize("T,hkv,g", [(20, 1, 16), (5, 2, 32), (3, 1, 100)])
+def test_weights_of_more_columns_than_a_pass_takes(pkv, fmt, T, hkv, g):
+    """Tokens in several passes, each on top of the one before: earlier weights and rejected tokens count once."""
+    lens = [400, 150, 2]
+    c = Cache(fmt, lens, hkv, 48, seed=T)
+    q = queries(3, T, hkv * g, seed=T)
+    w = torch.rand(3, hkv, 400, generator=torch.Generator().manual_seed(2)).to(DEV)
+    before = w.clone()
+    valid, prev_lens = [T - 1, T, 1], [400, 100, 1]
+    assert weigh(pkv, c, q.to(DEV), T, 1 / 16, w, prev=w, prev_lens=prev_lens, q_valid=valid) == 0
+    base = []
+    for r, n in enumerate(lens):
+        b = before[r, :, :n].double().cpu().numpy()
+        b[:, prev_lens[r]:] = 0.0
+        base.append(b)
+    verify_weights(w, expect(c, q, T, 1 / 16, valid), lens, base)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "fp8"])
+@pytest.mark.parametrize("given", [False, True])
+def test_weights_wait_that_runs_out(pkv, fmt, given):
+    """Waits of 1 ns: the call gives up and says so; the one after it is whole."""
+    lens, T, hkv, g = [3000, 2000], 2, 2, 4
+    c = Cache(fmt, lens, hkv, 16, seed=41)
+    q = queries(2, T, hkv * g, seed=41)
+    kw = dict(part_lse=torch.full((1, 2 * T, hkv * g), 5.0, device=DEV), split_tokens=4096) if given else {}
+    w = torch.zeros(2, hkv, 3000, device=DEV)
+    pkv.lib.pkv_testing_set_wait_limit_ns(1)
+    assert weigh(pkv, c, q.to(DEV), T, 1 / 16, w, **kw) == pkv.PKV_ERR_TIMEOUT
+    assert weigh(pkv, c, q.to(DEV), T, 1 / 16, w, **kw) == 0
+    verify_weights(w, expect(c, q, T, 1 / 16, lse=np.full((2 * T, hkv * g), 5.0) if given else None), lens)
+
+
 @pytest.mark.parametrize("fmt", ["int8", "fp8"])
 @pytest.mark.parametrize("T,split", [(1, 128), (8, 512)])
 def test_weights_from_the_verify_calls_partials(pkv, fmt, T, split):
@@ -571,6 +605,16 @@ def test_compact_in_a_pool_past_32_bits(pkv):
     x.pools = [b[torch.from_numpy(place).to(DEV)] for b in big]
     x.same(want)
     del small
+
+
+def test_compact_wait_that_runs_out(pkv):
+    """Waits of 1 ns: a chunk that gives up leaves its rows where they are and says so; the next call is whole."""
+    x = Rows("bf16", [6000, 5999], 2, 16, 5990, seed=15, dense="front")
+    pkv.lib.pkv_testing_set_wait_limit_ns(1)
+    assert x.run(pkv) in (0, pkv.PKV_ERR_TIMEOUT)
+    want = x.expect()
+    assert x.run(pkv) == 0
+    x.same(want)
 
 
 def test_compact_graph(pkv):
