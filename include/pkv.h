@@ -508,7 +508,10 @@ PKV_API pkv_status pkv_spec_verify_accept(const void* target_probs, int64_t targ
  *                        + sum over t < q_valid[r], query heads of KV head h, of exp(s - lse)
  *   for every pos < seq_lens[r]; s = softmax_scale q . k as for pkv_spec_verify_attn_partial (token t at
  *   position seq_lens[r] - T + t attends the keys up to it; a token before position 0 attends nothing and
- *   adds nothing), lse the log-sum-exp of that query's scores. fp32 throughout, on the exact stored k.
+ *   adds nothing), lse the log-sum-exp of that query's scores. Exact products of the stored k, fp32 sums. One
+ *   rounding of the inputs: beside int8 and e4m3 keys the queries are taken as fp16 times a power of two for
+ *   each (request, KV head), exact down to 2^-28 of the largest magnitude among these queries, to 2^-39 of it
+ *   below.
  *   q bf16 [num_reqs*T][num_q_heads][256]; the K cache by kv_dtype: bf16, int8 with k_scale fp32
  *   [num_blocks][block_size][num_kv_heads] (strides scale_stride_*), e4m3 with k_scale one device fp32.
  *   part_lse (nullable): the split log-sum-exps that a verify call left for the same q, cache and lengths,
@@ -518,8 +521,8 @@ PKV_API pkv_status pkv_spec_verify_accept(const void* target_probs, int64_t targ
  *   rejected drafts add nothing. Values outside [0, T] are clamped.
  *   prev (nullable): earlier weights, laid out as weights, which may be the same buffer; prev_lens (nullable:
  *   seq_lens): positions from prev_lens[r] on take nothing from prev, as for keys that are new.
- *   weights fp32, element strides w_stride_req and w_stride_head, positions contiguous, max_ctx of them;
- *   positions from seq_lens[r] on are left as they were.
+ *   weights fp32, element strides w_stride_req and w_stride_head (rows must not overlap), positions
+ *   contiguous, max_ctx of them; positions from seq_lens[r] on are left as they were.
  * Keys in a bad block, or past the table, read as zero and set PKV_ERR_DEVICE_BOUNDS; so does a seq_lens[r]
  * past max_ctx or the table (positions past them are left out).
  * workspace: caller-owned, 16-byte aligned, contents scratch; calls that may overlap on the GPU need one

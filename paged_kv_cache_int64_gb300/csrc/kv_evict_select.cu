@@ -442,10 +442,13 @@ extern "C" pkv_status pkv_kv_evict_select(const float* scores, int64_t stride_re
   PKV_ARG((reinterpret_cast<uintptr_t>(scores) & 3) == 0, "%s: scores must be 4-byte aligned", name);
   SelectParams p{scores, stride_req, stride_head, seq_lens, num_kv_heads, sinks, recent, budget, max_ctx, keep, new_lens, 0, dev_err};
   const int units = num_reqs * num_kv_heads;
-  // Slices: as many CTAs a unit as the device holds of them at once (two an SM), of 4,096 positions at least.
+  // Slices: as many CTAs a unit as the device holds of them at once (two an SM), of 4,096 positions at least; more where
+  // shared memory would not hold the slices.
   const int most = max_ctx > 8 * 4096 && sixteen_fit() ? kMaxCluster : 8;
   int ctas = 1;
-  while (ctas < most && (int64_t)units * ctas * 2 <= 2 * num_sms() && max_ctx > (int64_t)ctas * 4096) ctas *= 2;
+  while (ctas < most && (max_ctx > (int64_t)ctas * kMaxCached ||
+                         ((int64_t)units * ctas * 2 <= 2 * num_sms() && max_ctx > (int64_t)ctas * 4096)))
+    ctas *= 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (ctas) {
     case 1: return launch<1>(p, units, st);

@@ -424,6 +424,14 @@ def test_select_longer_than_shared_memory(pkv):
     check_pick(pkv, sc, [n], 4, 100, 60001)
 
 
+def test_select_many_requests_of_a_long_buffer(pkv):
+    """More (request, KV head) pairs than the device holds clusters for, in a buffer whose slices shared memory does not hold
+    whole."""
+    lens = [60000] + [500] * 90 + [59999, 0, 300, 47105]
+    sc = torch.rand(len(lens), 2, 60000, generator=torch.Generator().manual_seed(3))
+    check_pick(pkv, sc, lens, 4, 32, 400)
+
+
 def test_select_strides_bad_lengths_graph(pkv):
     g = torch.Generator().manual_seed(9)
     wide = torch.rand(3, 6, 900, generator=g).to(DEV)

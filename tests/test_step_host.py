@@ -70,6 +70,8 @@ FP4 = dict(fmt=3, ks=16, vs=16, ssb=1024, sst=64, ssh=16, sb=8192, st=512, sh=12
     ("pkv_kv_attn_weights", WEIGHTS, dict(scale=float("nan")), 1),
     ("pkv_kv_attn_weights", WEIGHTS, dict(lse=16), 1),
     ("pkv_kv_attn_weights", WEIGHTS, dict(lse=16, split=128), 1),
+    ("pkv_kv_attn_weights", WEIGHTS, dict(wh=15), 1),
+    ("pkv_kv_attn_weights", WEIGHTS, dict(R=2, wr=8), 1),
     ("pkv_kv_attn_weights", WEIGHTS, dict(wsb=8), 1),
     ("pkv_kv_attn_weights", WEIGHTS, dict(ws=20), 1),
     ("pkv_kv_evict_select", SELECT, dict(R=0, s=None), 0),
@@ -100,6 +102,7 @@ FP4 = dict(fmt=3, ks=16, vs=16, ssb=1024, sst=64, ssh=16, sb=8192, st=512, sh=12
     ("pkv_kv_cache_compact", COMPACT, dict(sh=0), 1),
     ("pkv_kv_cache_compact", COMPACT, dict(w=16), 1),
     ("pkv_kv_cache_compact", COMPACT, dict(w=18, mc=16), 1),
+    ("pkv_kv_cache_compact", COMPACT, dict(w=16, mc=16, wr=64, wh=8), 1),
     ("pkv_kv_cache_compact", COMPACT, dict(fmt=1), 1),
     ("pkv_kv_cache_compact", COMPACT, {**INT8, "vs": 18}, 1),
     ("pkv_kv_cache_compact", COMPACT, {**INT8, "sst": 0}, 1),
