@@ -14,6 +14,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <limits.h>
+
 #include <type_traits>
 #include <utility>
 
@@ -79,6 +81,9 @@ __device__ __forceinline__ uint4 load_vec(const T* row, int i, int vocab) {
   return x;
 }
 
+// The rows that are read: p alone; p and q, aligned alike; p and q, not so.
+enum { kOne, kAlike, kShifted };
+
 // What the token is drawn from: p, max(p - q, 0), or p without the draft's own token. Indices run in vectors of 16 bytes
 // that are aligned in p's row, so the first may begin before the row; q's row is read in its own aligned vectors, two
 // for one of p's where the rows are not aligned alike, and shifted.
@@ -87,7 +92,7 @@ struct Source {
   static constexpr int kN = 16 / (int)sizeof(T);
   const T* p;
   const T* q;   // null: none
-  int skip;     // index left out, or -1
+  int skip;     // index left out, or below every index
   int vocab;
   int begin;    // index of the first vector, -(kN - 1) .. 0
   int shift;    // elements by which p's vectors begin behind q's, 0 .. kN - 1
@@ -97,14 +102,31 @@ struct Source {
     const int q_begin = -(int)(reinterpret_cast<uintptr_t>(q) % 16 / sizeof(T));
     shift = q ? (begin - q_begin + kN) % kN : 0;
   }
-  // the vector of index i (begin + a multiple of kN); a: p's, b: q's (kTwo: there is q)
-  template <bool kTwo>
-  __device__ __forceinline__ void load(int i, uint4& a, uint4& b) const {
-    a = load_vec(p, i, vocab);
-    if constexpr (kTwo) {
-      b = load_vec(q, i - shift, vocab);
-      if (shift) {  // uniform
-        const uint4 c = load_vec(q, i - shift + kN, vocab);
+  // x with element e set to 0
+  static __device__ __forceinline__ uint4 without(const uint4& x, int e) {
+    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    const int word = e * (int)sizeof(T) / 4;
+    const uint32_t left = sizeof(T) == 4 ? 0u : e & 1 ? 0xffffu : 0xffff0000u;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j == word) w[j] &= left;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  // The lane's vectors of the step that begins at index i0 (begin + a multiple of a warp's load); a: p's, b: q's (kOne: none).
+  // Steps from `end` on are 0. inside: the step is before `end`, and no vector that it reads passes the row's ends.
+  template <int kMode>
+  __device__ __forceinline__ void load(int i0, int end, int lane, bool inside, uint4& a, uint4& b) const {
+    const int i = i0 + lane * kN;
+    a = b = make_uint4(0, 0, 0, 0);
+    if (!inside && i0 >= end) return;
+    a = inside ? __ldg(reinterpret_cast<const uint4*>(p + i)) : load_vec(p, i, vocab);
+    if constexpr (kMode == kOne) {
+      if ((unsigned)skip - (unsigned)i < (unsigned)kN) a = without(a, skip - i);
+    } else {
+      const T* at = q + (i - shift);
+      b = inside ? __ldg(reinterpret_cast<const uint4*>(at)) : load_vec(q, i - shift, vocab);
+      if constexpr (kMode == kShifted) {
+        const uint4 c = inside ? __ldg(reinterpret_cast<const uint4*>(at + kN)) : load_vec(q, i - shift + kN, vocab);
         uint32_t w[8] = {b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
         const int bytes = shift * (int)sizeof(T);
         if (bytes & 8) {
@@ -129,15 +151,14 @@ struct Source {
     if (std::is_same<T, __half>::value) return __half2float(__ushort_as_half((unsigned short)(w[e / 2] >> (e & 1 ? 16 : 0))));
     return __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
   }
-  template <bool kTwo>
-  __device__ __forceinline__ Fixed weight(int i, int e, const uint4& a, const uint4& b) const {
+  template <int kMode>
+  static __device__ __forceinline__ Fixed weight(int e, const uint4& a, const uint4& b) {
     const float x = saturated(value(a, e));
-    Fixed f = fixed46(x);
-    if constexpr (kTwo) {
+    const Fixed f = fixed46(x);
+    if constexpr (kMode != kOne) {
       const Fixed g = fixed46(fminf(saturated(value(b, e)), x));  // q, p at most: the difference is 0 where q is above
       return {f.hi - g.hi, f.lo - g.lo};
     }
-    if (i + e == skip) f = {0, 0};
     return f;
   }
 };
@@ -153,60 +174,63 @@ __device__ __forceinline__ uint64_t warp_inclusive(uint64_t x, int lane) {
   return x;
 }
 
-// vectors a lane and table that are added up while as many are on their way: as many as fit 64 registers
-template <bool kTwo>
-constexpr int kBatchOf = kTwo ? 2 : 4;
+// Steps (a vector a lane and table) whose loads go out together: no more than 64 registers hold without spilling, as 32
+// warps an SM stream better than 16 (64 requests over 131,072 tokens: 26 us). The next batch is not loaded ahead: with
+// it the registers spill (21 us; 19.2 without).
+template <int kMode>
+constexpr int kBatchOf = kMode == kOne ? 4 : 2;
+// steps (a vector a lane) that are reduced together: 256 values of 2^23 at most each, 2^31 together
+template <typename T>
+constexpr int kGroupOf = (int)sizeof(T) / 2;
 
-// The sum of a step, a vector a lane: two 32-bit reductions (128 values, or 256 of bf16 or fp16, of 2^23 at most each and so
-// 2^31 together: unsigned).
-template <bool kTwo, typename T>
-__device__ __forceinline__ uint64_t step_sum(const Source<T>& s, int i, const uint4& a, const uint4& b, Fixed& mine) {
+// The sum of kSteps steps: two 32-bit reductions (unsigned).
+template <int kMode, typename T, int kSteps>
+__device__ __forceinline__ uint64_t steps_sum(const uint4* a, const uint4* b, Fixed& mine) {
+  static_assert(kSteps * 32 * Source<T>::kN <= 256, "32 bits");
   mine = {0, 0};
 #pragma unroll
-  for (int e = 0; e < Source<T>::kN; ++e) {
-    const Fixed f = s.template weight<kTwo>(i, e, a, b);
-    mine.hi += f.hi, mine.lo += f.lo;
-  }
+  for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+    for (int e = 0; e < Source<T>::kN; ++e) {
+      const Fixed f = Source<T>::template weight<kMode>(e, a[k], b[k]);
+      mine.hi += f.hi, mine.lo += f.lo;
+    }
   return ((uint64_t)__reduce_add_sync(0xffffffffu, (unsigned)mine.hi) << 23) +
          (uint64_t)(int64_t)__reduce_add_sync(0xffffffffu, mine.lo);
 }
 
-// The warp's sum over [lo, hi), whole steps; lane l gets in `part` that of its l-th part of `per` steps.
-template <bool kTwo, typename T>
+// The warp's sum over [lo, hi), whole groups of steps; lane l gets in `part` that of its l-th part of `per` groups.
+template <int kMode, typename T>
 __device__ __forceinline__ uint64_t segment_sum(const Source<T>& s, int lo, int hi, int per, int lane, uint64_t& part) {
-  constexpr int kN = Source<T>::kN, kStep = 32 * kN, kBatch = kBatchOf<kTwo>;
-  uint64_t acc = 0, in_part = 0;
-  int steps = 0, parts = 0;
+  constexpr int kStep = 32 * Source<T>::kN, kBatch = kBatchOf<kMode>, kGroup = kGroupOf<T>;
+  uint64_t acc = 0;
+  int groups = 0, parts = 0;
   part = 0;
-  uint4 a[kBatch], b[kBatch];
-#pragma unroll
-  for (int k = 0; k < kBatch; ++k) s.template load<kTwo>(lo + k * kStep < hi ? lo + k * kStep + lane * kN : s.vocab, a[k], b[k]);
 #pragma unroll 1
   for (int i0 = lo; i0 < hi; i0 += kBatch * kStep) {
-    uint4 na[kBatch], nb[kBatch];
+    uint4 a[kBatch], b[kBatch];
+    constexpr int kAll = kBatch * kStep;
+    if (i0 - Source<T>::kN >= 0 && i0 + kAll <= hi && i0 + kAll + Source<T>::kN <= s.vocab) {
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int i = i0 + (kBatch + k) * kStep;
-      s.template load<kTwo>(i < hi ? i + lane * kN : s.vocab, na[k], nb[k]);
+      for (int k = 0; k < kBatch; ++k) s.template load<kMode>(i0 + k * kStep, hi, lane, true, a[k], b[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) s.template load<kMode>(i0 + k * kStep, hi, lane, false, a[k], b[k]);
     }
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
+    for (int k = 0; k < kBatch; k += kGroup) {
       Fixed mine;
-      in_part += step_sum<kTwo>(s, i0 + k * kStep + lane * kN, a[k], b[k], mine);
-      if (++steps == per || i0 + (k + 1) * kStep >= hi) {
-        if (lane == parts) part += in_part;  // (a step behind the last one adds 0)
-        acc += in_part;
-        in_part = 0, steps = 0, ++parts;
-      }
+      const uint64_t x = steps_sum<kMode, T, kGroup>(a + k, b + k, mine);  // (groups behind the last one add 0)
+      if (lane == parts) part += x;
+      acc += x;
+      if (++groups == per) groups = 0, ++parts;
     }
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) a[k] = na[k], b[k] = nb[k];
   }
   return acc;
 }
 
 // The smallest index of [lo, hi), whole steps, whose running sum from lo passes `target`; -1 if none does.
-template <bool kTwo, typename T>
+template <int kMode, typename T>
 __device__ __forceinline__ int find(const Source<T>& s, int lo, int hi, uint64_t target, int lane) {
   constexpr int kN = Source<T>::kN, kStep = 32 * kN;
   uint64_t before = 0;
@@ -214,16 +238,16 @@ __device__ __forceinline__ int find(const Source<T>& s, int lo, int hi, uint64_t
   for (int i0 = lo; i0 < hi; i0 += kStep) {
     const int i = i0 + lane * kN;
     uint4 a, b;
-    s.template load<kTwo>(i, a, b);
+    s.template load<kMode>(i0, hi, lane, false, a, b);
     Fixed sum;
-    const uint64_t step = step_sum<kTwo>(s, i, a, b, sum);
+    const uint64_t step = steps_sum<kMode, T, 1>(&a, &b, sum);
     if (before + step > target) {
       const uint64_t mine = joined(sum), run = before + warp_inclusive(mine, lane);
       int at = -1;
       uint64_t c = run - mine;
 #pragma unroll
       for (int e = 0; e < kN; ++e) {
-        c += joined(s.template weight<kTwo>(i, e, a, b));
+        c += joined(Source<T>::template weight<kMode>(e, a, b));
         if (at < 0 && c > target) at = i + e;
       }
       const uint32_t past = __ballot_sync(0xffffffffu, run > target);
@@ -300,7 +324,8 @@ __global__ void __launch_bounds__(kMaxThreads, 2) accept_kernel(const AcceptPara
   Source<T> src;
   src.p = P + (int64_t)n * p.t_stride_tok;
   src.q = (n < nd && Q) ? Q + (int64_t)n * p.d_stride_tok : nullptr;
-  src.skip = (n < nd && !Q) ? __ldg(ids + n) : -1;
+  src.skip = (n < nd && !Q) ? __ldg(ids + n) : INT_MIN;
+  if (src.skip < 0) src.skip = INT_MIN;  // (a draft id out of range leaves p whole)
   src.vocab = p.vocab;
   src.align();
 
@@ -309,8 +334,9 @@ __global__ void __launch_bounds__(kMaxThreads, 2) accept_kernel(const AcceptPara
   const int warps = blockDim.x >> 5;
   const int segs = ranks * warps;
   const int steps = (p.vocab - src.begin + kStep - 1) / kStep;
-  const int seg_steps = (steps + segs - 1) / segs, seg_len = seg_steps * kStep;
-  const int per = (seg_steps + 31) / 32;  // steps of a lane's part of the segment
+  constexpr int kGroup = kGroupOf<T>;
+  const int seg_groups = (steps + segs * kGroup - 1) / (segs * kGroup), seg_len = seg_groups * kGroup * kStep;
+  const int per = (seg_groups + 31) / 32;  // groups of a lane's part of the segment
   const int mine = rank * warps + warp;
   // (64-bit: a segment's start may pass 2^31 for the largest vocabularies)
   const int lo = src.begin + (int)min((int64_t)mine * seg_len, (int64_t)steps * kStep);
@@ -319,7 +345,9 @@ __global__ void __launch_bounds__(kMaxThreads, 2) accept_kernel(const AcceptPara
 #pragma unroll 1
   for (int pass = 0;; ++pass) {
     uint64_t part;
-    const uint64_t sum = src.q ? segment_sum<true>(src, lo, hi, per, lane, part) : segment_sum<false>(src, lo, hi, per, lane, part);
+    const uint64_t sum = !src.q ? segment_sum<kOne>(src, lo, hi, per, lane, part)
+                         : src.shift ? segment_sum<kShifted>(src, lo, hi, per, lane, part)
+                                     : segment_sum<kAlike>(src, lo, hi, per, lane, part);
     if (pass == 0) cluster.barrier_wait(std::move(started));
     // every CTA gets every segment's sum: the warp whose segment holds the target goes on, from its own SM's cache
     if (lane < ranks) cluster.map_shared_rank(&s_sum[pass][0], lane)[mine] = sum;
@@ -336,10 +364,10 @@ __global__ void __launch_bounds__(kMaxThreads, 2) accept_kernel(const AcceptPara
     const uint64_t run = warp_inclusive(own, lane), total = __shfl_sync(0xffffffffu, run, 31);
     int token = 0;
     if (total == 0) {
-      if (pass == 0 && (src.q || src.skip >= 0)) {
+      if (pass == 0 && (src.q || src.skip != INT_MIN)) {
         // nothing of p is left over (p = q up to rounding): from p. Uniform over the cluster.
         src.q = nullptr;
-        src.skip = -1;
+        src.skip = INT_MIN;
         src.shift = 0;
         continue;
       }
@@ -365,10 +393,11 @@ __global__ void __launch_bounds__(kMaxThreads, 2) accept_kernel(const AcceptPara
       const uint64_t left = past ? target - start : 0, upto = warp_inclusive(part, lane);
       const uint32_t in = __ballot_sync(0xffffffffu, upto > left);
       const int l = in ? __ffs(in) - 1 : 31;
-      const int from = min(lo + l * per * kStep, hi);
-      const int to = min(from + per * kStep, hi);
+      const int from = min(lo + l * per * kGroup * kStep, hi);
+      const int to = min(from + per * kGroup * kStep, hi);
       const uint64_t behind = left - __shfl_sync(0xffffffffu, upto - part, l);
-      token = src.q ? find<true>(src, from, to, behind, lane) : find<false>(src, from, to, behind, lane);
+      token = !src.q ? find<kOne>(src, from, to, behind, lane)
+              : src.shift ? find<kShifted>(src, from, to, behind, lane) : find<kAlike>(src, from, to, behind, lane);
       if (token < 0) token = p.vocab - 1;
     }
     for (int t = lane; t < p.T; t += 32)
