@@ -843,348 +843,6 @@ inline pkv_status run_attn_weights(const WeightParams& p, int ctas, cudaStream_t
   // 6 heads over 8 requests of 20,008 e4m3 keys 90 and 75. Up to 32 as 32: eight tokens of 4 heads over 32 requests of up to
   // 16,384 bf16 keys 84 us as 64 columns, 76 as 32.
   const int cols = p.tpc * p.group;
-          uint32_t big = 0;  // the largest finite magnitude's bits, in the upper half
-#pragma unroll 1
-          for (int j = k; j < pieces; j += 128) {
-            if ((j >> 3) % kN >= cols) continue;
-            const uint4 v = *reinterpret_cast<const uint4*>(q + j * 16);
-            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t lo = x[e] << 16 & 0x7fff0000u, hi = x[e] & 0x7fff0000u;
-              big = max(big, max(lo < 0x7f800000u ? lo : 0u, hi < 0x7f800000u ? hi : 0u));
-            }
-          }
-          big = __reduce_max_sync(0xffffffffu, big);
-          if (lane == 0) sh.q_max[grp][warp & 3] = big;
-          w_bar(4 + grp, 128);
-          big = max(max(sh.q_max[grp][0], sh.q_max[grp][1]), max(sh.q_max[grp][2], sh.q_max[grp][3]));
-          // 2^(14 - e) for a largest of exponent e, in two factors that stay finite
-          const int up = max(-126, min(14 - ((int)(big >> 23) - 127), 141));
-          const int up1 = up / 2;
-          const float s0 = __int_as_float((127 + up1) << 23), s1 = __int_as_float((127 + up - up1) << 23);
-#pragma unroll 1
-          for (int j = k; j < pieces; j += 128) {
-            if ((j >> 3) % kN >= cols) continue;
-            uint4* ptr = reinterpret_cast<uint4*>(q + j * 16);
-            const uint4 v = *ptr;
-            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-            uint32_t o[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              o[e] = pack_f16x2(__uint_as_float(x[e] << 16) * s0 * s1, __uint_as_float(x[e] & 0xffff0000u) * s0 * s1);
-            *ptr = make_uint4(o[0], o[1], o[2], o[3]);
-          }
-          if (k == 0) sh.q_unscale[units & 7] = __int_as_float((127 - up1) << 23) * __int_as_float((127 - (up - up1)) << 23);
-          fence_proxy_async_smem();
-          w_bar(4 + grp, 128);  // (q_max may be written again)
-          if (!dead) mbar_arrive(&sh.q_ready[b]);
-        }
-        const int st = i % G::kStages;
-        bool ok = !dead && mbar_wait_suspend(&sh.k_full[st], (i / G::kStages) & 1, abort, wl);
-        const int ab = i % G::kABufs;
-        if (ok && i >= G::kABufs) ok = mbar_wait_suspend(&sh.a_free[ab], (i / G::kABufs - 1) & 1, abort, wl);
-        dead = !__all_sync(0xffffffffu, ok);
-        if (dead) continue;
-        tc_fence_after();
-        const uint32_t a = tmem + lane_off + G::kColA + ab * 128;
-        const int rows_log2 = sh.rows_log2[i & (kWBadRing - 1)], half = 128 << rows_log2;  // of the key's segment
-        const uint8_t* row = smem + G::kOffK + st * G::kStage + (k >> rows_log2) * 2 * half + (k & ((1 << rows_log2) - 1)) * 128;
-        // (rolled, as every loop of a role: together they have to fit the instruction cache)
-#pragma unroll 4
-        for (int w8 = 0; w8 < 8; ++w8) {  // 32 codes, 16 columns a step
-          uint32_t o[16];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int piece = 2 * (w8 & 3) + j;
-            const uint4 v = *reinterpret_cast<const uint4*>(row + (w8 >> 2) * half + ((piece ^ (k & 7)) * 16));
-            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (kFmt == PKV_KV_INT8)
-                widen4_int8(x[e], o[8 * j + 2 * e], o[8 * j + 2 * e + 1]);
-              else
-                widen4_e4m3(x[e], o[8 * j + 2 * e], o[8 * j + 2 * e + 1]);
-            }
-          }
-          tmem_st_32x32b_x16(a + 16 * w8, o);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&sh.a_ready[ab]);
-        mbar_arrive(&sh.k_free[st]);
-      }
-    }
-  } else if (warp >= 4) {
-    // ------------------------------------------------------------------------------------ reducing
-    const int grp = (warp - 4) >> 2, quarter = warp & 3;
-    const int k = quarter * 32 + lane;  // this thread's key of a tile
-    const int kseg = k / p.seg;
-    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const int c_first = kBoth ? grp * G::kHalf : 0;  // the group's first column
-    const float per_tensor = kFmt == PKV_KV_FP8 ? __ldg(p.k_scale) : 1.0f;
-    constexpr int kStride = kBoth ? 1 : 2;  // tiles from one of this group's to the next
-    bool dead = false;
-    int units = 0;
-
-    // what a tile needs from memory is loaded a tile of this group's ahead (the block id of an int8 scale two)
-    WWalk far = at, near = at;
-    int far_i = kBoth ? 0 : grp, near_i = far_i;
-    if (far_i && count) far.next(p), near.next(p);
-    auto step = [&](WWalk& w, int& i) {
-#pragma unroll
-      for (int n = 0; n < kStride; ++n, ++i)
-        if (i < count) w.next(p);
-    };
-    int blk = -1, slot = 0, near_r = -1, near_len = 0;
-    auto load_block = [&]() {
-      blk = -1;
-      if (far_i < count) {
-        const int pos = far.tile * kWTile + k;
-        if (pos < far.n) {
-          const int col = pos / p.block_size;
-          slot = pos - col * p.block_size;
-          blk = __ldg(p.block_table + (int64_t)far.r * p.bt_stride + col);
-        }
-      }
-      step(far, far_i);
-    };
-    auto load_scale = [&]() {
-      return blk >= 0 && (int64_t)blk < p.num_blocks
-                 ? __ldg(p.k_scale + (int64_t)blk * p.s_stride_blk + (int64_t)slot * p.s_stride_tok + h) : 0.0f;
-    };
-    auto load_prev = [&]() {
-      float x = 0.0f;
-      if (near_i < count && p.prev) {
-        const int key = near.tile * kWTile + k;
-        if (near.r != near_r) {
-          near_r = near.r;
-          near_len = (int)min((int64_t)(p.prev_lens ? min(__ldg(p.prev_lens + near_r), near.n) : near.n), p.max_ctx);
-        }
-        if (key < near_len) x = p.prev[(int64_t)near.r * p.w_stride_req + (int64_t)h * p.w_stride_head + key];
-      }
-      step(near, near_i);
-      return x;
-    };
-    float scale_next = 0.0f, prev_next = 0.0f;
-    if (kFmt == PKV_KV_INT8) {
-      load_block();
-      scale_next = load_scale();
-      load_block();
-    }
-    if (!kStats) prev_next = load_prev();
-
-    // the weights' launch begins before the log-sum-exps' has ended: these are waited for, the keys are not
-    if (!kStats) asm volatile("griddepcontrol.wait;" ::: "memory");
-    float l[kStats ? G::kHalf : 1];  // a thread's part of the columns' sums
-    int prefix = 0, nq = kStats ? p.tpc * p.group : 0, seen = -1;  // seen: requests so far
-    for (int i = 0; i < count; ++i) {
-      const bool first = i == 0 || at.tile == 0, last = i + 1 == count || at.tile + 1 == at.tiles;
-      seen += first;
-      if (first) {
-        prefix = __ldg(p.seq_lens + at.r) - p.T + p.t_base;  // the pass's token t sits at position prefix + t
-        if constexpr (kStats) {
-#pragma unroll
-          for (int c = 0; c < G::kHalf; ++c) l[c] = 0.0f;
-          for (int c = lane; c < G::kHalf; c += 32) sh.ref[warp - 4][c] = -1e30f;
-          __syncwarp();
-        } else {
-          const int valid = p.q_valid ? min(__ldg(p.q_valid + at.r), p.T) : p.T;
-          nq = max(0, min(valid - p.t_base, p.tpc)) * p.group;
-          w_bar(1 + grp, 128);  // the group has read the last unit's columns
-          if (k < kN) sh.col[grp][k] = k < nq ? -column_lse(p, at.r, h, at.n, at.tiles, sh.first + i - at.tile, sh.total, sh.ranges, k) : -INFINITY;
-          w_bar(1 + grp, 128);
-        }
-      }
-      if (kBoth || (i & 1) == grp) {
-        const int key = at.tile * kWTile + k;
-        float f = p.scale_log2 * per_tensor;
-        const float before = prev_next;
-        if (kFmt == PKV_KV_INT8) {
-          f *= scale_next;
-          scale_next = load_scale();
-          load_block();
-        }
-        if (!kStats) prev_next = load_prev();
-        if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait_suspend(&sh.s_full[i & 1], (i >> 1) & 1, abort, wl));
-        if (!dead) {
-          tc_fence_after();
-          const uint32_t s_addr = tmem + lane_off + G::kColS + (i & 1) * kN + c_first;
-          const bool bad_key = (sh.bad[i & (kWBadRing - 1)] >> kseg) & 1u;
-          if (!G::kWide) f *= sh.q_unscale[seen & 7];
-          if (bad_key) f = 0.0f;
-          // columns of tokens before this do not see the key; every column does where it is not above 0
-          const int behind = key < at.n ? key - prefix : INT_MAX;
-          const bool open = __all_sync(0xffffffffu, behind <= 0);
-          if constexpr (kStats) {
-#pragma unroll
-            for (int cc = 0; cc < G::kHalf / 16; ++cc) {
-              const int c0 = c_first + cc * 16;
-              if (c0 < nq) {
-                uint32_t v[16];
-                tmem_ld_32x32b_x16(s_addr + cc * 16, v);
-                tmem_wait_ld();
-                float t[16];
-#pragma unroll
-                for (int q = 0; q < 16; ++q) t[q] = (bad_key ? 0.0f : __uint_as_float(v[q])) * f;
-                if (!open || c0 + 16 > nq) {
-                  const int4* tok = reinterpret_cast<const int4*>(sh.token + c0);
-#pragma unroll
-                  for (int q = 0; q < 16; ++q) t[q] = behind <= reinterpret_cast<const int*>(tok)[q] ? t[q] : -INFINITY;
-                }
-                float* ref = sh.ref[warp - 4] + cc * 16;
-                float rv[16], m = -INFINITY;
-#pragma unroll
-                for (int q = 0; q < 16; ++q) {
-                  rv[q] = ref[q];
-                  m = fmaxf(m, t[q] - rv[q]);
-                }
-                if (__any_sync(0xffffffffu, m > 64.0f)) {  // a reference moves: once a unit, as a rule
-                  const float x = w_max16(t, lane);          // lane l: column l & 15's maximum
-                  const float old = ref[lane & 15], now = fmaxf(old, x), a = ex2_approx(old - now);
-                  __syncwarp();
-                  if (lane < 16) ref[lane] = now;
-                  __syncwarp();
-#pragma unroll
-                  for (int q = 0; q < 16; ++q) {
-                    l[cc * 16 + q] *= __shfl_sync(0xffffffffu, a, q);
-                    rv[q] = ref[q];
-                  }
-                }
-#pragma unroll
-                for (int q = 0; q < 16; ++q) l[cc * 16 + q] += ex2_approx(t[q] - rv[q]);
-              }
-            }
-            tc_fence_before();
-            mbar_arrive(&sh.s_free[i & 1]);
-          } else {
-            float sum = 0.0f;
-#pragma unroll 1
-            for (int c0 = 0; c0 < nq; c0 += 16) {
-              uint32_t v[16];
-              tmem_ld_32x32b_x16(s_addr + c0, v);
-              float cv[16];
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const float4 x = *reinterpret_cast<const float4*>(sh.col[grp] + c0 + 4 * q);
-                cv[4 * q] = x.x, cv[4 * q + 1] = x.y, cv[4 * q + 2] = x.z, cv[4 * q + 3] = x.w;
-              }
-              tmem_wait_ld();
-              float e[16];
-#pragma unroll
-              for (int q = 0; q < 16; ++q) e[q] = ex2_approx(fmaf(bad_key ? 0.0f : __uint_as_float(v[q]), f, cv[q]));
-              if (!open || c0 + 16 > nq) {
-                const int* tok = sh.token + c0;
-#pragma unroll
-                for (int q = 0; q < 16; ++q) e[q] = behind <= tok[q] && c0 + q < nq ? e[q] : 0.0f;
-              }
-#pragma unroll
-              for (int q = 0; q < 16; q += 4) sum += (e[q] + e[q + 1]) + (e[q + 2] + e[q + 3]);
-            }
-            tc_fence_before();
-            mbar_arrive(&sh.s_free[i & 1]);
-            if (key < at.n && key < p.max_ctx)
-              p.weights[(int64_t)at.r * p.w_stride_req + (int64_t)h * p.w_stride_head + key] = before + sum;
-          }
-        }
-      }
-      if constexpr (kStats) {
-        if (last) {  // the warps' sums of this unit meet; both groups come here for every unit
-          float2* mine = sh.part[units & 1][warp - 4];
-#pragma unroll
-          for (int c0 = 0; c0 < G::kHalf; c0 += 32) {
-            float x[32];
-#pragma unroll
-            for (int q = 0; q < 32; ++q) x[q] = l[c0 + q];
-            const float y = w_reduce<32>(x, lane);
-            mine[c0 + lane] = make_float2(sh.ref[warp - 4][c0 + lane], y);
-          }
-          w_bar(3, 256);
-          const int c = (warp - 4) * 32 + lane;
-          if (c < nq && !dead) {
-            const int w0 = kBoth ? c / G::kHalf * 4 : 0, w1 = kBoth ? w0 + 4 : 8;
-            const int cl = c % G::kHalf;
-            float m = -INFINITY, sum = 0.0f;
-            for (int w = w0; w < w1; ++w) {
-              const float2 x = sh.part[units & 1][w][cl];
-              if (x.y != 0.0f) m = fmaxf(m, x.x);
-            }
-            for (int w = w0; w < w1; ++w) {
-              const float2 x = sh.part[units & 1][w][cl];
-              if (x.y != 0.0f) sum += x.y * exp2f(x.x - m);
-            }
-            const long long u0 = sh.first + i - at.tile;
-            if (u0 >= sh.first && u0 + at.tiles <= sh.last) {
-              const int64_t row = ((int64_t)at.r * p.T + p.t_base + c / p.group) * p.num_q_heads + (int64_t)h * p.group + c % p.group;
-              p.lse2[row] = sum != 0.0f ? m + log2f(sum) : INFINITY;
-            } else {
-              p.stat[((int64_t)blockIdx.x * 2 + (u0 > sh.first)) * kWMaxCols + c] = make_float2(m, sum);
-            }
-          }
-          ++units;
-        }
-      }
-      at.next(p);
-    }
-  }
-
-  tc_fence_before();
-  // every role has left its loop; the flag's final value, the same for every thread
-  const bool gave_up = __syncthreads_or(*abort != 0);
-  if (gave_up) {
-    // what this CTA still has in flight ends before its tensor memory is freed: the copies armed, the MMAs issued
-    if (warp == 0 && lane == 0)
-      for (int s = 0; s < G::kStages; ++s) drain_armed(&sh.k_full[s], sh.armed_k[s]);
-    if (warp == 3 && lane == 0)
-      for (int b = 0; b < G::kQBufs; ++b) drain_armed(&sh.q_full[b], sh.armed_q[b]);
-    if (warp == 1) {
-      if (w_elect()) {
-        umma_commit(&sh.drain);
-        mbar_wait_drain(&sh.drain, 0);
-      }
-      __syncwarp();
-    }
-    tc_fence_before();
-    __syncthreads();
-  }
-  if (warp == 2) {
-    tc_fence_after();
-    tmem_dealloc(tmem, G::kTmemCols);
-  }
-  if (threadIdx.x == 0 && gave_up) record_error(p.dev_err, kErrTimeout);
-  if (!kStats) asm volatile("griddepcontrol.wait;" ::: "memory");  // (no thread ends before the launch it follows)
-}
-
-template <int kFmt, int kN, bool kStats>
-inline pkv_status launch_attn_weights(const WeightParams& p, int ctas, cudaStream_t stream) {
-  using G = WGeo<kFmt, kN>;
-  constexpr int kSmem = 1024 + G::kTiles + (int)sizeof(WShared<kFmt, kN>);
-  static_assert(kSmem <= 227 * 1024, "dynamic shared memory of one CTA");
-  static std::atomic<uint64_t> attr_done{0};
-  once_per_device(attr_done, [] {
-    cudaFuncSetAttribute(kv_attn_weights_kernel<kFmt, kN, kStats>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  });
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(G::kThreads);
-  cfg.dynamicSmemBytes = kSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = !kStats && !p.part_lse ? 1 : 0;
-  cudaLaunchKernelEx(&cfg, kv_attn_weights_kernel<kFmt, kN, kStats>, p);
-  return check_launch("kv_attn_weights");
-}
-
-// One pass over the columns of p: the log-sum-exps first where they are not given, then the weights.
-template <int kFmt>
-inline pkv_status run_attn_weights(const WeightParams& p, int ctas, cudaStream_t stream) {
-  // 33 to 64 columns as 64: four bf16 prompts of 24,576 and 16 tokens of 4 heads 89 us as 128 columns, 72 as 64; eight tokens of 6
-  // heads over 8 requests of 20,008 e4m3 keys 90 and 75. Up to 32 as 32: eight tokens of 4 heads over 32 requests of up to 40,960
-  // e4m3 keys FIG as 64, 114 as 32.
-  const int cols = p.tpc * p.group;
   auto launch = [&](auto stats) {
     constexpr bool kStats = decltype(stats)::value;
     return cols <= 32   ? launch_attn_weights<kFmt, 32, kStats>(p, ctas, stream)
