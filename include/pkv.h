@@ -94,7 +94,8 @@ PKV_API int32_t pkv_abi_version(void);
 /*
  * testing_set_wait_limit_ns - a testing hook with no counterpart on the pages: the next attention
  * kernel launched by the calling host thread (pkv_paged_prefill_attn, pkv_paged_prefill_attn_fp8,
- * pkv_spec_verify_attn_partial, pkv_spec_verify_attn_partial_fp8, pkv_spec_verify_attn_fp4) bounds
+ * pkv_spec_verify_attn_partial, pkv_spec_verify_attn_partial_fp8, pkv_spec_verify_attn_fp4,
+ * pkv_kv_attn_weights; and pkv_kv_cache_compact, whose chunks that give up leave their rows) bounds
  * each of its internal waits by ns nanoseconds instead of the default one second; later launches use the default
  * again. ns = 0 keeps the default. With a bound far below the time a copy or an MMA takes, the
  * launch's CTAs give up at their first wait that is not already satisfied: each records
