@@ -16,9 +16,9 @@
 //
 // The tiles of all (request, 128 keys) are one list, cut into equal ranges from the lengths on the device. A range has a
 // CTA a KV head, side by side, so that the heads' parts of a token's row are read together (a head's tiles of all
-// requests after another's: the same bytes, scattered, take longer). Roles: warp 0 K producer, warp 1 MMA issuer, warp 2 tensor memory, warp 3 Q producer, warps 4-11 two
-// reducing warpgroups (tiles in turn; with kN above 32 the log-sum-exp's take half of the columns each), warps 12 on the
-// widening ones (tiles in turn where there are two).
+// requests after another's: the same bytes, scattered, take longer). Roles: warp 0 K producer, warp 1 MMA issuer, warp 2
+// tensor memory, warp 3 Q producer, warps 4-11 two reducing warpgroups (tiles in turn; with kN above 32 the log-sum-exps' take
+// half of the columns each), warps 12 on the widening ones (tiles in turn where there are two).
 #pragma once
 #include <cuda_bf16.h>
 
@@ -89,6 +89,20 @@ struct WGeo {
   static constexpr uint32_t kTmemCols = kWide ? (uint32_t)(2 * kN) : 512;
 };
 
+// The list's ranges, [c total / count, (c + 1) total / count): the longer ones spread evenly, so that requests of one length
+// begin with a range where their number divides that of the ranges.
+struct WRanges {
+  int total, count;
+  // (divisions of 32 bits where the products fit: 0.2 us less a launch, of 8)
+  __device__ __forceinline__ int first(int c) const {
+    return total < 1 << 24 && count <= 256 ? (int)((unsigned)total * c / (unsigned)count) : (int)((long long)total * c / count);
+  }
+  __device__ __forceinline__ int owner(int x) const {
+    return total < 1 << 24 && count <= 256 ? (int)((((unsigned)x + 1) * count - 1) / (unsigned)total)
+                                           : (int)((((long long)x + 1) * count - 1) / total);
+  }
+};
+
 template <int kFmt, int kN>
 struct alignas(16) WShared {
   using G = WGeo<kFmt, kN>;
@@ -102,9 +116,9 @@ struct alignas(16) WShared {
   int rows_log2[kWBadRing];  // rows of a tile's segments
   uint32_t tmem_base;
   int abort;
-  int start_r, start_tile, ranges;
-  long long first, last;  // this CTA's tiles in the list
-  long long total;
+  int start_r, start_tile;
+  int first, last;  // this CTA's tiles in the list
+  WRanges ranges;
   alignas(16) float col[2][kN];              // per reducing group: minus the column's log-sum-exp (weights)
   alignas(16) int token[kN];                 // a column's token of the pass
   float q_unscale[8];                        // of the last requests' queries: the power of two back
@@ -218,12 +232,9 @@ __device__ __forceinline__ float w_max16(const float (&t)[16], int lane) {
   return fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], 16));
 }
 
-// The range that has tile x when `ranges` ranges share `total` tiles as [c total / ranges, (c + 1) total / ranges).
-__device__ __forceinline__ int w_owner(long long x, long long total, int ranges) { return (int)(((x + 1) * ranges - 1) / total); }
-
 // The log-sum-exp, base 2, of column c of request r of n keys and KV head h, whose tiles are u0 .. u0 + tiles - 1 of the list; infinite for a
 // query that sees nothing.
-static __device__ __noinline__ float column_lse(const WeightParams& p, int r, int h, int n, int tiles, long long u0, long long total, int ranges, int c) {
+static __device__ __noinline__ float column_lse(const WeightParams& p, int r, int h, int n, int tiles, int u0, WRanges ranges, int c) {
   const int64_t row = ((int64_t)r * p.T + p.t_base + c / p.group) * p.num_q_heads + (int64_t)h * p.group + c % p.group;
   float m = -INFINITY, sum = 0.0f;
   if (p.part_lse) {
@@ -248,9 +259,9 @@ static __device__ __noinline__ float column_lse(const WeightParams& p, int r, in
     return sum != 0.0f && m < INFINITY ? hi + (lo + log2f(sum)) : INFINITY;
   }
   // the ranges that have the request's tiles: only the first can have begun with another request's
-  const int c0 = w_owner(u0, total, ranges), c1 = w_owner(u0 + tiles - 1, total, ranges);
+  const int c0 = ranges.owner(u0), c1 = ranges.owner(u0 + tiles - 1);
   if (c0 == c1) return __ldcg(p.lse2 + row);
-  const int which = u0 > total * c0 / ranges;
+  const int which = u0 > ranges.first(c0);
   for (int o0 = c0; o0 <= c1; o0 += 8) {
     float2 x[8];
 #pragma unroll
@@ -283,51 +294,51 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
   constexpr bool kBoth = kStats && kN > 32;
 
   if (warp == 0) {
-    // the list's length and this CTA's range of it
+    // the list's length and this CTA's range of it (32 bits: the host has checked)
     const int64_t most = (int64_t)p.max_blocks * p.block_size;
-    long long total = 0;
+    int total = 0, tiles0 = 0;  // tiles0: of request `lane`
     bool odd = false;
     for (int r = lane; r < p.num_reqs; r += 32) {
       const int len = __ldg(p.seq_lens + r);
-      const int n = (int)max((int64_t)0, min((int64_t)len, most));
+      const int n = (int)max((int64_t)0, min((int64_t)len, most)), tiles = (n + kWTile - 1) / kWTile;
       odd |= len < 0 || len > most || (!kStats && len > p.max_ctx);
-      total += (n + kWTile - 1) / kWTile;
+      if (r == lane) tiles0 = tiles;
+      total += tiles;
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    total = __reduce_add_sync(0xffffffffu, total);
     odd = __any_sync(0xffffffffu, odd);
     // a tile each, where there are fewer tiles than ranges (so that none between a request's ranges is without a part)
-    const int ranges = (int)min((long long)gridDim.x / p.heads, max(total, 1ll));
+    const int ranges = min((int)gridDim.x / p.heads, max(total, 1));
+    const WRanges cut{total, ranges};
     const bool idle = range >= ranges;
-    const long long first = idle ? total : total * range / ranges, last = idle ? total : total * (range + 1) / ranges;
-    int at_r = p.num_reqs, at_t = 0;
-    long long before = 0;  // tiles of the requests before
+    const int first = idle ? total : cut.first(range), last = idle ? total : cut.first(range + 1);
+    int at_r = p.num_reqs, at_t = 0, before = 0;  // before: tiles of the requests before
     if (first < last)
       for (int r0 = 0; r0 < p.num_reqs; r0 += 32) {
         const int r = r0 + lane;
-        long long mine = 0;
-        if (r < p.num_reqs) {
+        int mine = r0 ? 0 : tiles0;
+        if (r0 && r < p.num_reqs) {
           const int n = (int)max((int64_t)0, min((int64_t)__ldg(p.seq_lens + r), most));
           mine = (n + kWTile - 1) / kWTile;
         }
-        long long run = mine;
+        int run = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const long long y = __shfl_up_sync(0xffffffffu, run, o);
+          const int y = __shfl_up_sync(0xffffffffu, run, o);
           if (lane >= o) run += y;
         }
         run += before;
         const uint32_t past = __ballot_sync(0xffffffffu, run > first);
         if (past) {
           const int l = __ffs(past) - 1;
-          at_t = (int)__shfl_sync(0xffffffffu, first - (run - mine), l);
+          at_t = __shfl_sync(0xffffffffu, first - (run - mine), l);
           at_r = r0 + l;
           break;
         }
         before = __shfl_sync(0xffffffffu, run, 31);
       }
     if (lane == 0) {
-      sh.first = first, sh.last = last, sh.total = total, sh.ranges = ranges;
+      sh.first = first, sh.last = last, sh.ranges = cut;
       sh.start_r = at_r, sh.start_tile = at_t;
       if (odd && blockIdx.x == 0) record_error(p.dev_err, kErrDeviceBounds);
     }
@@ -355,6 +366,10 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
   } else if (warp == 2) {
     tmem_alloc(&sh.tmem_base, G::kTmemCols);
     tmem_relinquish();
+  } else if (warp == 3 && lane == 0) {
+    prefetch_tensormap(&p.qmap);
+    prefetch_tensormap(&p.kmap);
+    if (p.big_ok) prefetch_tensormap(&p.kmap_big);
   }
   if (warp >= 4 && threadIdx.x - 128 < kN) {
     const int c = threadIdx.x - 128;
@@ -366,7 +381,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
   const uint32_t tmem = sh.tmem_base;
   if (kStats) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   volatile int* abort = &sh.abort;
-  const int count = (int)(sh.last - sh.first);
+  const int count = sh.last - sh.first;
   WWalk at;
   at.start(p, sh.start_r, sh.start_tile);
 
@@ -493,18 +508,17 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
       for (int i = 0; i < count; ++i, at.next(p)) {
         const bool first = i == 0 || at.tile == 0;
         units += first;
-        if (i % G::kConv != grp) continue;
-        if (first) {
-          // the request's queries, by the group that has its first tile
+        if (first && (i + 1) % G::kConv == grp % G::kConv) {
+          // the request's queries, by the group that does not have its first tile
           const int b = units % G::kQBufs;
           uint8_t* q = smem + b * G::kQBytes;
           const int pieces = 4 * kN * 8;  // of 16 bytes; the columns behind the pass's tokens are nobody's
           if (!dead) dead = !__all_sync(0xffffffffu, w_wait_q(&sh.q_full[b], (units / G::kQBufs) & 1, abort, wl));
           const int cols = p.tpc * p.group;
           uint32_t big = 0;  // the largest finite magnitude's bits, in the upper half
-#pragma unroll 1
+#pragma unroll 2
           for (int j = k; j < pieces; j += 128) {
-            if ((j >> 3) % kN >= cols) continue;
+            if ((j >> 3 & (kN - 1)) >= cols) continue;
             const uint4 v = *reinterpret_cast<const uint4*>(q + j * 16);
             const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -521,9 +535,9 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
           const int up = max(-126, min(14 - ((int)(big >> 23) - 127), 141));
           const int up1 = up / 2;
           const float s0 = __int_as_float((127 + up1) << 23), s1 = __int_as_float((127 + up - up1) << 23);
-#pragma unroll 1
+#pragma unroll 2
           for (int j = k; j < pieces; j += 128) {
-            if ((j >> 3) % kN >= cols) continue;
+            if ((j >> 3 & (kN - 1)) >= cols) continue;
             uint4* ptr = reinterpret_cast<uint4*>(q + j * 16);
             const uint4 v = *ptr;
             const uint32_t x[4] = {v.x, v.y, v.z, v.w};
@@ -538,6 +552,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
           w_bar(4 + grp, 128);  // (q_max may be written again)
           if (!dead) mbar_arrive(&sh.q_ready[b]);
         }
+        if (i % G::kConv != grp) continue;
         const int st = i % G::kStages;
         bool ok = !dead && mbar_wait_suspend(&sh.k_full[st], (i / G::kStages) & 1, abort, wl);
         const int ab = i % G::kABufs;
@@ -650,7 +665,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
           const int valid = p.q_valid ? min(__ldg(p.q_valid + at.r), p.T) : p.T;
           nq = max(0, min(valid - p.t_base, p.tpc)) * p.group;
           w_bar(1 + grp, 128);  // the group has read the last unit's columns
-          if (k < kN) sh.col[grp][k] = k < nq ? -column_lse(p, at.r, h, at.n, at.tiles, sh.first + i - at.tile, sh.total, sh.ranges, k) : -INFINITY;
+          if (k < kN) sh.col[grp][k] = k < nq ? -column_lse(p, at.r, h, at.n, at.tiles, sh.first + i - at.tile, sh.ranges, k) : -INFINITY;
           w_bar(1 + grp, 128);
         }
       }
@@ -697,7 +712,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
                   rv[q] = ref[q];
                   m = fmaxf(m, t[q] - rv[q]);
                 }
-                if (__any_sync(0xffffffffu, m > 64.0f)) {  // a reference moves: once a unit, as a rule
+                if (__any_sync(0xffffffffu, m > 64.0f)) {  // a reference moves
                   const float x = w_max16(t, lane);          // lane l: column l & 15's maximum
                   const float old = ref[lane & 15], now = fmaxf(old, x), a = ex2_approx(old - now);
                   __syncwarp();
@@ -771,7 +786,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
               const float2 x = sh.part[units & 1][w][cl];
               if (x.y != 0.0f) sum += x.y * exp2f(x.x - m);
             }
-            const long long u0 = sh.first + i - at.tile;
+            const int u0 = sh.first + i - at.tile;
             if (u0 >= sh.first && u0 + at.tiles <= sh.last) {
               const int64_t row = ((int64_t)at.r * p.T + p.t_base + c / p.group) * p.num_q_heads + (int64_t)h * p.group + c % p.group;
               p.lse2[row] = sum != 0.0f ? m + log2f(sum) : INFINITY;
