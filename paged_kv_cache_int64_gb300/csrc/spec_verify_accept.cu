@@ -195,8 +195,11 @@ __device__ __forceinline__ uint64_t steps_sum(const uint4* a, const uint4* b, Fi
       const Fixed f = Source<T>::template weight<kMode>(e, a[k], b[k]);
       mine.hi += f.hi, mine.lo += f.lo;
     }
+  // the low parts of 256 differences may add up to 2^31 (each p half a multiple of 2^-23 above one, each q half below):
+  // a lane's go into its high part first, so that both sums are of what is not negative
+  mine.hi += mine.lo >> 23, mine.lo &= (1 << 23) - 1;
   return ((uint64_t)__reduce_add_sync(0xffffffffu, (unsigned)mine.hi) << 23) +
-         (uint64_t)(int64_t)__reduce_add_sync(0xffffffffu, mine.lo);
+         __reduce_add_sync(0xffffffffu, (unsigned)mine.lo);
 }
 
 // The warp's sum over [lo, hi), whole groups of steps; lane l gets in `part` that of its l-th part of `per` groups.

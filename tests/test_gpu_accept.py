@@ -93,6 +93,21 @@ def test_residual_that_is_empty_draws_from_the_target(pkv):
     check(pkv, P1, None, torch.tensor([[16]], dtype=torch.int32), torch.tensor([[0.5]]), torch.tensor([0.9]), None)
 
 
+@pytest.mark.parametrize("V", [4096, 50021])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+def test_low_parts_of_one_sign(pkv, V, dtype):
+    """p halfway between two multiples of 2^-23 and q one less, everywhere: every difference is 2^-23, all of it from the
+    parts below 2^-23 (p rounds down to the even multiple, q up to it)."""
+    R = 16
+    P = torch.full((R, 2, V), 64.5 * 2.0 ** -23).to(TYPES[dtype])
+    Q = torch.full((R, 1, V), 63.5 * 2.0 ** -23).to(TYPES[dtype])
+    assert (P.double() == 64.5 * 2.0 ** -23).all() and (Q.double() == 63.5 * 2.0 ** -23).all()
+    ids = torch.arange(R, dtype=torch.int32)[:, None]
+    P[torch.arange(R), 0, ids[:, 0].long()] = 0.0  # the draft goes
+    us = (torch.arange(R) + 0.25) / R
+    check(pkv, P, Q, ids, torch.full((R, 1), 0.5), us, None)
+
+
 def test_values_out_of_range(pkv):
     P, Q, ids, ua, us, _ = make(4, 4, 600, "fp32", True, seed=6)
     P[0, 0, :300] = float("nan")
