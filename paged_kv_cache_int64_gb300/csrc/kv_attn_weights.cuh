@@ -659,7 +659,7 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
         if constexpr (kStats) {
 #pragma unroll
           for (int c = 0; c < G::kHalf; ++c) l[c] = 0.0f;
-          for (int c = lane; c < G::kHalf; c += 32) sh.ref[warp - 4][c] = -1e30f;
+          for (int c = lane; c < G::kHalf; c += 32) sh.ref[warp - 4][c] = -3.4028235e38f;  // below every finite score
           __syncwarp();
         } else {
           const int valid = p.q_valid ? min(__ldg(p.q_valid + at.r), p.T) : p.T;
@@ -745,7 +745,8 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
               tmem_wait_ld();
               float e[16];
 #pragma unroll
-              for (int q = 0; q < 16; ++q) e[q] = ex2_approx(fmaf(bad_key ? 0.0f : __uint_as_float(v[q]), f, cv[q]));
+              for (int q = 0; q < 16; ++q)  // (the product rounded as for the log-sum-exp: else a score of 2^30 and its own maximum differ by 2^6)
+                e[q] = ex2_approx(__fadd_rn(__fmul_rn(bad_key ? 0.0f : __uint_as_float(v[q]), f), cv[q]));
               if (!open || c0 + 16 > nq) {
                 const int* tok = sh.token + c0;
 #pragma unroll

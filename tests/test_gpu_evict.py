@@ -247,6 +247,24 @@ def test_weights_of_far_apart_scores(pkv):
         verify_weights(w, expect(d, q, 2, 1.0), [700])
 
 
+@pytest.mark.parametrize("x,y", [(1.0, 1.0), (175 / 128, 147 / 128)])  # of the second's scores every factor rounds
+@pytest.mark.parametrize("T,g", [(1, 4), (4, 8), (8, 8), (8, 16)])
+def test_weights_of_very_low_scores(pkv, T, g, x, y):
+    """Every score far below -1e30 and no two of them near: each query's weight is its largest key's, the first."""
+    lens = [300, 5, 1]
+    c = Cache("bf16", lens, 1, 16)
+    for r, n in enumerate(lens):
+        for pos in range(n):
+            c.pool[int(c.bt[r, pos // 16]), pos % 16, 0] = y * 2.0 ** 60 * (1.0 if pos == 0 else 2.0)
+    q = torch.full((len(lens) * T, g, 256), -x * 2.0 ** 50, dtype=torch.bfloat16, device=DEV)  # scores of about -2^114, -2^115
+    w = torch.full((len(lens), 1, 320), 7.0, device=DEV)
+    assert weigh(pkv, c, q, T, 1.0 / 16, w) == 0
+    for r, n in enumerate(lens):
+        seeing = sum(n - T + t >= 0 for t in range(T))
+        assert w[r, 0, 0].item() == seeing * g
+        assert (w[r, 0, 1:n] == 0).all() and (w[r, 0, n:] == 7.0).all()
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "int8", "fp8"])
 def test_weights_of_queries_of_unlike_sizes(pkv, fmt):
     """Query heads and elements from 2^-60 to 2^9 side by side, rows of zeros, requests whose queries are all tiny, and the
