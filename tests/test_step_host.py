@@ -59,6 +59,7 @@ FP4 = dict(fmt=3, ks=16, vs=16, ssb=1024, sst=64, ssh=16, sb=8192, st=512, sh=12
     ("pkv_kv_attn_weights", WEIGHTS, dict(bts=0), 1),
     ("pkv_kv_attn_weights", WEIGHTS, dict(mc=0), 1),
     ("pkv_kv_attn_weights", WEIGHTS, dict(mb=1 << 28, bts=1 << 28), 2),
+    ("pkv_kv_attn_weights", WEIGHTS, dict(mb=1 << 20, bts=1 << 20, bs=2040, R=1000), 2),
     ("pkv_kv_attn_weights", WEIGHTS, dict(q=24), 1),
     ("pkv_kv_attn_weights", WEIGHTS, dict(k=24), 1),
     ("pkv_kv_attn_weights", WEIGHTS, dict(sh=260), 1),
