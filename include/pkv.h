@@ -590,6 +590,22 @@ PKV_API pkv_status pkv_kv_cache_compact(void* k_cache, void* v_cache, int32_t kv
                                         int64_t max_ctx, void* workspace, int64_t workspace_bytes, int32_t* dev_err,
                                         void* stream);
 
+/*
+ * call_packed - one of the four calls after the verify, with its arguments in one array: for bindings in which the
+ * conversion of each argument costs more than the array does.
+ *   args (host): the call's arguments in their order, 8 bytes each: pointers and integers as int64, a float as a
+ *   double. bytes: the size of args, 8 times their number.
+ * Returns what the call returns; PKV_ERR_INVALID_ARG for another size, an unknown call or an integer that does
+ * not fit its argument.
+ */
+typedef enum pkv_packed_call {
+  PKV_CALL_SPEC_VERIFY_ACCEPT = 0,
+  PKV_CALL_KV_ATTN_WEIGHTS = 1,
+  PKV_CALL_KV_EVICT_SELECT = 2,
+  PKV_CALL_KV_CACHE_COMPACT = 3
+} pkv_packed_call;
+PKV_API pkv_status pkv_call_packed(int32_t call, const void* args, int64_t bytes);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,5 +1,6 @@
 """Refusals of the calls after the verify attention: no GPU needed, nothing is launched."""
 import ctypes as C
+import struct
 
 import numpy as np
 import pytest
@@ -115,6 +116,38 @@ def test_refusals(pkv, call, base, change, status):
     got = getattr(pkv.lib, call)(*{**base, **change}.values())
     assert got == status, pkv.lib.pkv_last_error()
     assert bool(pkv.lib.pkv_last_error()) == bool(status)
+
+
+CALLS = ("pkv_spec_verify_accept", "pkv_kv_attn_weights", "pkv_kv_evict_select", "pkv_kv_cache_compact")
+
+
+def packed(pkv, call, values, size=None):
+    b = b"".join(struct.pack("=d" if isinstance(v, float) else "=q", v or 0) for v in values)
+    return pkv.lib.pkv_call_packed(call, b, len(b) if size is None else size)
+
+
+def test_packed_calls_refuse_alike(pkv):
+    cases = test_refusals.pytestmark[0].args[1]
+    assert {c[0] for c in cases} == set(CALLS)
+    for call, base, change, status in cases:
+        values = list({**base, **change}.values())
+        assert getattr(pkv.lib, call)(*values) == status
+        message = pkv.lib.pkv_last_error()
+        assert packed(pkv, CALLS.index(call), values) == status
+        assert pkv.lib.pkv_last_error() == message
+
+
+def test_packed_calls_refuse_what_does_not_fit(pkv):
+    for i, base in enumerate((ACCEPT, WEIGHTS, SELECT, COMPACT)):
+        values = list({**base, "R": 0}.values())
+        assert packed(pkv, i, values) == 0
+        for bad in (values[:-1], values + [0]):
+            assert packed(pkv, i, bad) == 1 and b"bytes" in pkv.lib.pkv_last_error()
+        for r in (1 << 32, -(1 << 31) - 1):
+            assert packed(pkv, i, list({**base, "R": r}.values())) == 1 and b"range" in pkv.lib.pkv_last_error()
+        assert pkv.lib.pkv_call_packed(i, None, 8 * len(values)) == 1
+    for i in (-1, 4):
+        assert packed(pkv, i, [0]) == 1 and b"unknown" in pkv.lib.pkv_last_error()
 
 
 def test_workspace_bytes(pkv):
