@@ -554,6 +554,7 @@ PKV_API pkv_status pkv_kv_attn_weights(const void* q, const void* k_cache, int32
  *   weights of kv_attn_weights. keep int32 [num_reqs][num_kv_heads][budget]: the positions, ascending, in the
  *   first new_lens[r] = min(seq_lens[r], budget) entries; the others are left as they were.
  * sinks + recent <= budget. seq_lens[r] outside [0, max_ctx] is clamped and sets PKV_ERR_DEVICE_BOUNDS.
+ * seq_lens, keep and new_lens must not overlap: lengths are not updated in place.
  */
 PKV_API pkv_status pkv_kv_evict_select(const float* scores, int64_t stride_req, int64_t stride_head, int64_t max_ctx,
                                        const int32_t* seq_lens, int32_t num_reqs, int32_t num_kv_heads, int32_t sinks,

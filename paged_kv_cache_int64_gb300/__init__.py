@@ -573,7 +573,8 @@ def kv_attn_weights(q, k_cache, block_table, seq_lens, T, softmax_scale, weights
 
 def kv_evict_select(scores, seq_lens, sinks, recent, budget, keep, new_lens, dev_err=None, stream=None):
     """keep int32 [R][hkv][budget] := the positions of each (request, KV head) that stay, ascending: the first `sinks`,
-    the last `recent`, the highest of scores (fp32 [R][hkv][max_ctx]) in between; new_lens int32 [R] := how many."""
+    the last `recent`, the highest of scores (fp32 [R][hkv][max_ctx]) in between; new_lens int32 [R] := how many (a buffer of
+    its own, not seq_lens)."""
     R, hkv, max_ctx = scores.shape
     sr, sh, se = scores.stride()
     dev = scores.get_device()

@@ -28,6 +28,12 @@ pkv_status encode_tiled(CUtensorMap* map, CUtensorMapDataType dtype, int rank, c
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Whether two arrays of that many bytes share one.
+inline bool overlaps(const void* a, uint64_t a_bytes, const void* b, uint64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y ? y - x < a_bytes : x - y < b_bytes;
+}
+
 // Runs fn once per (flag, current device): for kernel attributes the driver keeps per device, such
 // as the dynamic shared-memory opt-in. Devices 64 and up run fn on every call.
 template <typename F>

@@ -440,6 +440,12 @@ extern "C" pkv_status pkv_kv_evict_select(const float* scores, int64_t stride_re
   if (num_reqs == 0) return PKV_OK;
   PKV_ARG(scores && seq_lens && keep && new_lens, "%s: null pointer argument", name);
   PKV_ARG((reinterpret_cast<uintptr_t>(scores) & 3) == 0, "%s: scores must be 4-byte aligned", name);
+  // every CTA of a request reads its length, at its own time: nothing may be written there (lengths updated in place would
+  // make the later ones take the cache for one within the budget)
+  const uint64_t lens_bytes = (uint64_t)num_reqs * 4, keep_bytes = (uint64_t)num_reqs * num_kv_heads * (uint64_t)budget * 4;
+  PKV_ARG(!overlaps(seq_lens, lens_bytes, new_lens, lens_bytes) && !overlaps(seq_lens, lens_bytes, keep, keep_bytes) &&
+              !overlaps(new_lens, lens_bytes, keep, keep_bytes),
+          "%s: seq_lens, keep and new_lens must not overlap", name);
   SelectParams p{scores, stride_req, stride_head, seq_lens, num_kv_heads, sinks, recent, budget, max_ctx, keep, new_lens, 0, dev_err};
   const int units = num_reqs * num_kv_heads;
   // Slices: as many CTAs a unit as the device holds of them at once (two an SM), of 4,096 positions at least; more where
