@@ -574,8 +574,8 @@ PKV_API pkv_status pkv_kv_evict_select(const float* scores, int64_t stride_req, 
  *   (4-bit). The later calls read the cache with seq_lens = new_lens: keys carry their rotary position in
  *   themselves, and order does not matter to attention.
  * An entry of keep below its own index, not above the one before it, past the table or past max_ctx, and rows
- * in a bad block: the row is not moved and PKV_ERR_DEVICE_BOUNDS is set; so does new_lens[r] outside
- * [0, budget], which is clamped.
+ * in a bad block: the row is not moved and PKV_ERR_DEVICE_BOUNDS is set (the other rows are moved, whatever order that
+ * leaves keep in); so does new_lens[r] outside [0, budget], which is clamped.
  * workspace: pkv_kv_cache_compact_workspace_bytes bytes, 4-byte aligned, contents scratch; calls that may
  * overlap on the GPU need one each. Caches and strides 16-byte aligned (4-bit scales too).
  */

@@ -1,0 +1,58 @@
+"""The calls after the verify attention at the borders of what they take: kept lists out of order."""
+import numpy as np
+import pytest
+
+from test_gpu_evict import FORMATS, Rows
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def pkv():
+    import paged_kv_cache_int64_gb300 as m
+    return m
+
+
+# ------------------------------------------------------------------------------------------------
+# the move
+# ------------------------------------------------------------------------------------------------
+
+def not_ascending(kind, budget, rng):
+    """Entries for a request of 2 * budget + 40 positions."""
+    j = np.arange(budget)
+    if kind == "below":  # the part of the search that the entry ends is taken for one without a reader
+        k = j + 34
+        k[31::64] = -1
+    elif kind == "high":  # the window of readers begins at the entry
+        k = j + 1
+        k[20::97] = budget + 20 + np.arange(len(k[20::97]))
+    elif kind == "repeated":
+        k = j + 40
+        k[5::40] = k[4::40][:len(k[5::40])]
+    elif kind == "stairs":  # ascending for a while, then again from further down, never below the row itself
+        k = j + 1 + (j % 113) * (1 + j % 113 > 50) // 2
+    elif kind == "late":  # one entry, in the list's last part
+        k = j + 33
+        k[budget - 70] = 2 * budget
+    else:
+        k = j + rng.integers(0, 70, budget)
+    return k.astype(np.int32)
+
+
+@pytest.mark.parametrize("fmt", list(FORMATS))
+@pytest.mark.parametrize("kind", ["below", "high", "repeated", "stairs", "late", "random"])
+@pytest.mark.parametrize("budget", [700, 9000])
+def test_compact_in_place_with_a_list_out_of_order(pkv, fmt, kind, budget):
+    """Lists that do not ascend, in place, every row's destination another row's source: an entry below its index or not above
+    the one before it moves nothing, every other row arrives whole; requests in order beside it too."""
+    n, hkv = 2 * budget + 40, 2
+    x = Rows(fmt, [n, n, 300], hkv, 16, budget, seed=budget, dense="front")
+    for h in range(hkv):
+        x.keep[1, h] = not_ascending(kind, budget, np.random.default_rng(h))
+    k = x.keep[1]
+    bad = (k < np.arange(budget)) | np.concatenate((np.zeros((hkv, 1), bool), k[:, 1:] <= k[:, :-1]), 1)
+    assert bad.any(1).all()
+    assert (k[:, 1:] < k[:, :-1]).any() or kind == "repeated"
+    want = x.expect(skip=lambda r, h, j: r == 1 and bad[h, j])
+    assert x.run(pkv) == pkv.PKV_ERR_DEVICE_BOUNDS
+    x.same(want)
