@@ -95,7 +95,7 @@ PKV_API int32_t pkv_abi_version(void);
  * testing_set_wait_limit_ns - a testing hook with no counterpart on the pages: the next attention
  * kernel launched by the calling host thread (pkv_paged_prefill_attn, pkv_paged_prefill_attn_fp8,
  * pkv_spec_verify_attn_partial, pkv_spec_verify_attn_partial_fp8, pkv_spec_verify_attn_fp4,
- * pkv_kv_attn_weights; and pkv_kv_cache_compact, whose chunks that give up leave their rows) bounds
+ * pkv_kv_attn_weights; and pkv_kv_cache_compact, where a bound below 20 us counts as run out at once) bounds
  * each of its internal waits by ns nanoseconds instead of the default one second; later launches use the default
  * again. ns = 0 keeps the default. With a bound far below the time a copy or an MMA takes, the
  * launch's CTAs give up at their first wait that is not already satisfied: each records
@@ -576,6 +576,9 @@ PKV_API pkv_status pkv_kv_evict_select(const float* scores, int64_t stride_req, 
  * An entry of keep below its own index, not above the one before it, past the table or past max_ctx, and rows
  * in a bad block: the row is not moved and PKV_ERR_DEVICE_BOUNDS is set (the other rows are moved, whatever order that
  * leaves keep in); so does new_lens[r] outside [0, budget], which is clamped.
+ * PKV_ERR_TIMEOUT (a wait for another CTA's reads that ran out, one second): the first new_lens[r] rows of requests with
+ * more than 32 are undefined, in the caches, the scales and the weights, and the call cannot be repeated on them; no
+ * other row is written.
  * workspace: pkv_kv_cache_compact_workspace_bytes bytes, 4-byte aligned, contents scratch; calls that may
  * overlap on the GPU need one each. Caches and strides 16-byte aligned (4-bit scales too).
  */

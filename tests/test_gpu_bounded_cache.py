@@ -1,4 +1,5 @@
-"""The calls after the verify attention at the borders of what they take: kept lists out of order."""
+"""The calls after the verify attention at the borders of what they take: kept lists out of order, waits
+that run out."""
 import numpy as np
 import pytest
 
@@ -56,3 +57,24 @@ def test_compact_in_place_with_a_list_out_of_order(pkv, fmt, kind, budget):
     want = x.expect(skip=lambda r, h, j: r == 1 and bad[h, j])
     assert x.run(pkv) == pkv.PKV_ERR_DEVICE_BOUNDS
     x.same(want)
+
+
+@pytest.mark.parametrize("fmt", list(FORMATS))
+@pytest.mark.parametrize("lens,budget", [([700, 30, 650], 600), ([9000, 32, 8000], 7000)])
+def test_compact_waits_that_run_out(pkv, fmt, lens, budget):
+    """A bound below 20 us counts as run out at once. It is reported; chunks that wait for nothing (the first 32 rows of a
+    request and KV head) are moved, the others write nothing; the next call is whole."""
+    x = Rows(fmt, lens, 2, 16, budget, seed=budget, dense="front")
+    x.keep[1, :, :x.new[1]] = np.arange(x.new[1])
+    x.keep[1, 0, 5:x.new[1] - 1] += 1  # rows of the short request move by one
+    x.new[1] -= 1
+    first = [t.clone() for t in (*x.pools, *x.scales, x.weights) if t is not None]
+    partly, whole = x.expect(skip=lambda r, h, j: j >= 32), x.expect()
+    for limit in (1, 19999):
+        pkv.lib.pkv_testing_set_wait_limit_ns(limit)
+        assert x.run(pkv) == pkv.PKV_ERR_TIMEOUT
+        x.same(partly)
+        for t, f in zip([t for t in (*x.pools, *x.scales, x.weights) if t is not None], first):
+            t.copy_(f)
+    assert x.run(pkv) == 0
+    x.same(whole)
