@@ -261,9 +261,12 @@ __device__ __forceinline__ int find(const Source<T>& s, int lo, int hi, uint64_t
   return -1;
 }
 
+// A uniform number, to [0, 1 - 2^-24], NaN to 0.
+__device__ __forceinline__ float in_range(float u) { return fminf(fmaxf(u, 0.0f), 0x1.fffffep-1f); }
+
 // floor(u * total), u in [0, 1) taken exactly.
 __device__ uint64_t scaled(float u, uint64_t total) {
-  u = fminf(fmaxf(u, 0.0f), 0x1.fffffep-1f);
+  u = in_range(u);
   const uint32_t bits = __float_as_uint(u);
   const int e = (int)(bits >> 23);
   const uint64_t m = e ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;
@@ -298,7 +301,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) accept_kernel(const AcceptPara
       bool ok = false;
       if (t < p.T - 1) {
         const int x = __ldg(ids + t);  // (drafts behind the request's own too, while num_drafts is on its way)
-        const float u = p.u_accept[(int64_t)r * (p.T - 1) + t];
+        const float u = in_range(p.u_accept[(int64_t)r * (p.T - 1) + t]);
         if (t < nd) {
           if (x >= 0 && x < p.vocab) {
             const float pt = as_float(P[(int64_t)t * p.t_stride_tok + x]);

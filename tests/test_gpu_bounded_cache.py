@@ -1,8 +1,11 @@
-"""The calls after the verify attention at the borders of what they take: kept lists out of order, waits
-that run out."""
+"""The calls after the verify attention at the borders of what they take: uniform numbers out of
+range, kept lists out of order, waits that run out."""
 import numpy as np
 import pytest
+import torch
 
+import _step as S
+from test_gpu_accept import run as accept
 from test_gpu_evict import FORMATS, Rows
 
 pytestmark = pytest.mark.gpu
@@ -12,6 +15,39 @@ pytestmark = pytest.mark.gpu
 def pkv():
     import paged_kv_cache_int64_gb300 as m
     return m
+
+
+# ------------------------------------------------------------------------------------------------
+# accept
+# ------------------------------------------------------------------------------------------------
+
+def clamped(u):
+    """To [0, 1 - 2^-24], NaN to 0."""
+    return np.clip(np.nan_to_num(u.astype(np.float64), nan=0.0, posinf=2.0, neginf=-2.0), 0.0, 1.0 - 2.0 ** -24).astype(np.float32)
+
+
+ODD_U = [-1.0, -1e-30, -0.0, 0.0, 1.0 - 2.0 ** -24, 1.0, 1.5, float("nan"), float("inf"), float("-inf")]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("drafted", [True, False])
+def test_accept_takes_u_to_its_range(pkv, dtype, drafted):
+    """Each odd u against a draft of p = 0, p = q and p = q / 2: below 0 is 0, 1 and above the largest below 1, NaN 0."""
+    V, ratios = 64, (0.0, 1.0, 0.5)
+    R = len(ODD_U) * len(ratios)
+    P, Q = torch.full((R, 2, V), 2.0 ** -7), torch.full((R, 1, V), 2.0 ** -6)
+    ids = (torch.arange(R, dtype=torch.int32) % V)[:, None]
+    q = 2.0 ** -6 if drafted else 1.0
+    for i in range(R):
+        P[i, 0, ids[i, 0]] = ratios[i % 3] * q
+    ua = torch.tensor(ODD_U).repeat_interleave(3)[:, None]
+    us = (torch.arange(R) + 0.5) / R
+    got = accept(pkv, P.to(dtype), Q.to(dtype) if drafted else None, ids, ua, us, None)
+    want = S.accept(P.numpy(), Q.numpy() if drafted else None, ids.numpy(), clamped(ua.numpy()), us.numpy(), [1] * R)
+    assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1]) and got[2] == 0
+    for i in range(R):  # by hand: u q < p
+        u = float(clamped(ua.numpy())[i, 0])
+        assert got[1][i] == 1 + (u < ratios[i % 3])
 
 
 # ------------------------------------------------------------------------------------------------
