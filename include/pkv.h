@@ -492,9 +492,11 @@ PKV_API pkv_status pkv_spec_verify_attn_fp4(const void* q, const uint8_t* k_fp4,
  *   out_tokens [num_reqs][T]: the accepted drafts, the drawn token, then -1; num_out [num_reqs]: how many of
  *   these are tokens (the count of query tokens whose keys stay, q_valid of kv_attn_weights).
  * Probabilities are in [0, 1] (for the drawing, values outside are clamped and NaN counts as 0), a row's sum below
- * 2^17; each u in [0, 1) (taken to [0, 1 - 2^-24], NaN to 0). A draft id outside [0, vocab) is not accepted and leaves p whole, a row
+ * 2^17; each u in [0, 1) (taken to [0, 1 - 2^-24], NaN to 0). A draft id outside [0, vocab) is not accepted (the next
+ * token is then drawn from max(p - q, 0) as after any other, and without draft_probs from the whole of p), a row
  * without a positive value gives token 0, num_drafts outside [0, T - 1] is clamped: each sets
- * PKV_ERR_DEVICE_BOUNDS. vocab at most 2^30. No workspace.
+ * PKV_ERR_DEVICE_BOUNDS (a bad id behind the first draft that is not accepted may not be looked at). vocab at most
+ * 2^30. No workspace.
  */
 PKV_API pkv_status pkv_spec_verify_accept(const void* target_probs, int64_t target_stride_req,
                                           int64_t target_stride_tok, const void* draft_probs,

@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2) accept_kernel(const AcceptPara
   src.p = P + (int64_t)n * p.t_stride_tok;
   src.q = (n < nd && Q) ? Q + (int64_t)n * p.d_stride_tok : nullptr;
   src.skip = (n < nd && !Q) ? __ldg(ids + n) : INT_MIN;
-  if (src.skip < 0) src.skip = INT_MIN;  // (a draft id out of range leaves p whole)
+  if (src.skip < 0) src.skip = INT_MIN;  // (a draft id out of range leaves p whole; beside q it changes nothing)
   src.vocab = p.vocab;
   src.align();
 

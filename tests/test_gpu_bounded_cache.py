@@ -50,6 +50,18 @@ def test_accept_takes_u_to_its_range(pkv, dtype, drafted):
         assert got[1][i] == 1 + (u < ratios[i % 3])
 
 
+@pytest.mark.parametrize("bad", [-1, 4, 2 ** 31 - 1, -2 ** 31])
+def test_accept_ids_out_of_range(pkv, bad):
+    """By hand: the draft goes; with draft probabilities the token comes from max(p - q, 0), without from all of p."""
+    P = torch.tensor([[[0.125, 0.5, 0.25, 0.125], [1.0, 0.0, 0.0, 0.0]]]).expand(4, 2, 4).contiguous()
+    Q = torch.tensor([[[0.5, 0.25, 0.25, 0.0]]]).expand(4, 1, 4).contiguous()  # what is left: 0, 1/4, 0, 1/8
+    ids, us = torch.full((4, 1), bad, dtype=torch.int64).int(), torch.tensor([0.0, 0.6, 0.7, 0.9])
+    for q, tokens in ((Q, [1, 1, 3, 3]), (None, [0, 1, 2, 3])):
+        got = accept(pkv, P, q, ids, torch.zeros(4, 1), us, None)
+        assert got[0].tolist() == [[x, -1] for x in tokens] and got[1].tolist() == [1] * 4
+        assert got[2] == pkv.PKV_ERR_DEVICE_BOUNDS
+
+
 # ------------------------------------------------------------------------------------------------
 # the move
 # ------------------------------------------------------------------------------------------------
