@@ -519,7 +519,8 @@ PKV_API pkv_status pkv_spec_verify_accept(const void* target_probs, int64_t targ
  *   [num_blocks][block_size][num_kv_heads] (strides scale_stride_*), e4m3 with k_scale one device fp32.
  *   part_lse (nullable): the split log-sum-exps that a verify call left for the same q, cache and lengths,
  *   [max_splits][num_reqs*T][num_q_heads] with its split_tokens. Without it they are computed first, which
- *   reads K twice.
+ *   reads K twice. A seq_lens[r] past max_splits * split_tokens sets PKV_ERR_DEVICE_BOUNDS: that request's weights
+ *   then come from the splits that there are, and are too large.
  *   q_valid (nullable: T each): the first tokens that count, such as num_out of spec_verify_accept; the
  *   rejected drafts add nothing. Values outside [0, T] are clamped.
  *   prev (nullable): earlier weights, laid out as weights, which may be the same buffer; prev_lens (nullable:

@@ -296,12 +296,13 @@ __global__ void __launch_bounds__(WGeo<kFmt, kN>::kThreads, 1) kv_attn_weights_k
   if (warp == 0) {
     // the list's length and this CTA's range of it (32 bits: the host has checked)
     const int64_t most = (int64_t)p.max_blocks * p.block_size;
+    const int64_t reach = !kStats && p.part_lse ? (int64_t)p.max_splits * p.split_tokens : most;  // of the log-sum-exps given
     int total = 0, tiles0 = 0;  // tiles0: of request `lane`
     bool odd = false;
     for (int r = lane; r < p.num_reqs; r += 32) {
       const int len = __ldg(p.seq_lens + r);
       const int n = (int)max((int64_t)0, min((int64_t)len, most)), tiles = (n + kWTile - 1) / kWTile;
-      odd |= len < 0 || len > most || (!kStats && len > p.max_ctx);
+      odd |= len < 0 || len > most || n > reach || (!kStats && len > p.max_ctx);
       if (r == lane) tiles0 = tiles;
       total += tiles;
     }

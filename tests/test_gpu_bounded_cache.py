@@ -1,12 +1,13 @@
 """The calls after the verify attention at the borders of what they take: uniform numbers out of
-range, kept lists out of order, waits that run out."""
+range, log-sum-exps that do not reach, kept lists out of order, waits that run out."""
 import numpy as np
 import pytest
 import torch
 
 import _step as S
+from _devsetup import DEV
 from test_gpu_accept import run as accept
-from test_gpu_evict import FORMATS, Rows
+from test_gpu_evict import FORMATS, Cache, Rows, expect, queries, verify_weights, weigh
 
 pytestmark = pytest.mark.gpu
 
@@ -60,6 +61,28 @@ def test_accept_ids_out_of_range(pkv, bad):
         got = accept(pkv, P, q, ids, torch.zeros(4, 1), us, None)
         assert got[0].tolist() == [[x, -1] for x in tokens] and got[1].tolist() == [1] * 4
         assert got[2] == pkv.PKV_ERR_DEVICE_BOUNDS
+
+
+# ------------------------------------------------------------------------------------------------
+# attention weights
+# ------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "fp8"])
+@pytest.mark.parametrize("lens,split,splits", [([700, 100, 512], 256, 2), ([129, 128, 1], 128, 1), ([300, 0, 5], 100, 2)])
+def test_weights_report_log_sum_exps_that_do_not_reach(pkv, fmt, lens, split, splits):
+    """A request longer than the given splits reach is reported, as by the verify call that made them; the others are
+    whole, and its own come from the splits that there are."""
+    T, hkv, g = 2, 2, 3
+    c = Cache(fmt, lens, hkv, 16, seed=2)
+    q = queries(3, T, hkv * g, seed=2)
+    gen = torch.Generator().manual_seed(3)
+    for s, status in ((splits, pkv.PKV_ERR_DEVICE_BOUNDS), (-(-max(lens) // split), 0)):
+        part = 4.0 + torch.rand(s, 3 * T, hkv * g, generator=gen)
+        lse = np.stack([np.logaddexp.reduce(part.double().numpy()[:max(1, min(s, -(-lens[r] // split))), r * T + t], 0)
+                        for r in range(3) for t in range(T)])
+        w = torch.full((3, hkv, max(lens) + 1), -7.0, device=DEV)
+        assert weigh(pkv, c, q.to(DEV), T, 1 / 16, w, part_lse=part.to(DEV), split_tokens=split) == status
+        verify_weights(w, expect(c, q, T, 1 / 16, lse=lse), lens, tail=-7.0)
 
 
 # ------------------------------------------------------------------------------------------------
