@@ -34,6 +34,13 @@ inline bool overlaps(const void* a, uint64_t a_bytes, const void* b, uint64_t b_
   return x < y ? y - x < a_bytes : x - y < b_bytes;
 }
 
+// Whether the rows of `len` elements at r stride_req + h stride_head (r < reqs, h < heads) are known to share none: each
+// stride that is used is a row at least, and one of them clears all that the other reaches.
+inline bool rows_apart(int64_t reqs, int64_t stride_req, int64_t heads, int64_t stride_head, int64_t len) {
+  if ((reqs > 1 && stride_req < len) || (heads > 1 && stride_head < len)) return false;
+  return reqs == 1 || heads == 1 || (stride_req - len) / (heads - 1) >= stride_head || (stride_head - len) / (reqs - 1) >= stride_req;
+}
+
 // Runs fn once per (flag, current device): for kernel attributes the driver keeps per device, such
 // as the dynamic shared-memory opt-in. Devices 64 and up run fn on every call.
 template <typename F>

@@ -350,7 +350,7 @@ extern "C" pkv_status pkv_kv_cache_compact(void* k_cache, void* v_cache, int32_t
             "%s: scale caches and their strides must be 16-byte aligned", name);
   PKV_ARG(!weights || (max_ctx > 0 && w_stride_req >= 0 && w_stride_head >= 0 && (reinterpret_cast<uintptr_t>(weights) & 3) == 0),
           "%s: bad weights", name);
-  PKV_ARG(!weights || ((num_reqs == 1 || w_stride_req >= max_ctx) && (num_kv_heads == 1 || w_stride_head >= max_ctx)),
+  PKV_ARG(!weights || rows_apart(num_reqs, w_stride_req, num_kv_heads, w_stride_head, max_ctx),
           "%s: rows of weights must not overlap", name);
   const int64_t need = (int64_t)pkv_kv_cache_compact_workspace_bytes(num_reqs, num_kv_heads, budget);
   PKV_ARG((reinterpret_cast<uintptr_t>(workspace) & 3) == 0 && workspace_bytes >= need,

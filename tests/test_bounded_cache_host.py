@@ -2,7 +2,7 @@
 import numpy as np
 import pytest
 
-from test_step_host import SELECT, pkv  # noqa: F401
+from test_step_host import COMPACT, SELECT, WEIGHTS, pkv  # noqa: F401
 
 
 def refused(pkv, call, values, word):  # noqa: F811
@@ -20,3 +20,23 @@ def test_select_refuses_outputs_over_its_lengths(pkv, change):  # noqa: F811
     """Every CTA of a request reads its length while one of them writes the new one."""
     base = {**SELECT, "s": 0x100000, "R": 2, "sl": 0x1000, "keep": 0x2000, "nl": 0x3000}
     refused(pkv, "pkv_kv_evict_select", {**base, **change}, b"overlap")
+
+
+@pytest.mark.parametrize("call,base", [("pkv_kv_attn_weights", dict(WEIGHTS)), ("pkv_kv_cache_compact", {**COMPACT, "w": 16})])
+def test_rows_of_weights_that_overlap_are_refused(pkv, call, base):  # noqa: F811
+    """Each stride holds a row, but request 0's next head, or its third, is another request's."""
+    base = {**base, "hkv": 2, "mc": 16, "R": 2}
+    for change in (dict(wr=16, wh=16), dict(wr=31, wh=16), dict(wr=16, wh=31), dict(wr=2 ** 62, wh=15), dict(wr=15, wh=2 ** 62),
+                   dict(hkv=4, wr=48, wh=16), dict(hkv=4, wr=63, wh=16), dict(R=5, wr=16, wh=79),
+                   dict(R=2 ** 20, wr=2 ** 44, wh=2 ** 63 - 1)):
+        refused(pkv, call, {**base, **change}, b"rows of weights")
+
+
+@pytest.mark.parametrize("call,base", [("pkv_kv_attn_weights", dict(WEIGHTS)), ("pkv_kv_cache_compact", {**COMPACT, "w": 16})])
+def test_rows_of_weights_in_any_order_are_taken(pkv, call, base):  # noqa: F811
+    """Requests inside heads or heads inside requests, one of either with any stride: the check after this one refuses."""
+    last = dict(ws=20, d=256) if call == "pkv_kv_attn_weights" else dict(ws=18)
+    base = {**base, "hkv": 2, "mc": 16, "R": 3, **last}
+    for change in (dict(wr=32, wh=16), dict(wr=16, wh=48), dict(wr=2 ** 62, wh=16), dict(R=1, wr=0, wh=16), dict(hkv=1, wr=16, wh=0),
+                   dict(R=1, hkv=1, wr=0, wh=0)):
+        refused(pkv, call, {**base, **change}, b"workspace")
