@@ -53,6 +53,20 @@ inline void once_per_device(std::atomic<uint64_t>& done, F&& fn) {
   if (bit) done.fetch_or(bit, std::memory_order_relaxed);
 }
 
+// A positive figure of the current device: `known`'s, or what ask() gives, which is kept there. Devices 64 and up ask on every
+// call.
+template <typename F>
+inline int per_device(std::atomic<int> (&known)[64], F&& ask) {
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const bool kept = dev >= 0 && dev < 64;
+  int n = kept ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n > 0) return n;
+  n = ask();
+  if (kept) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 // SM count of the current device (cached per device).
 int num_sms();
 

@@ -270,13 +270,12 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactParams p
 
 template <int kPieces, int kScale>
 pkv_status launch(const CompactParams& p, cudaStream_t st) {
-  static std::atomic<uint64_t> done{0};
-  static int per_sm = 1;
+  static std::atomic<int> known[64];
   constexpr int kSmem = 2 * kRows * kPieces * 16;
-  once_per_device(done, [] {
+  const int per_sm = per_device(known, [] {
     int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, compact_kernel<kPieces, kScale>, kThreads, kSmem) == cudaSuccess && n > 0)
-      per_sm = n;
+    const bool ok = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, compact_kernel<kPieces, kScale>, kThreads, kSmem) == cudaSuccess;
+    return ok && n > 0 ? n : 1;
   });
   const int64_t most = (int64_t)per_sm * num_sms();
   cudaLaunchConfig_t cfg = {};
