@@ -490,7 +490,8 @@ PKV_API pkv_status pkv_spec_verify_attn_fp4(const void* q, const uint8_t* k_fp4,
  *   each probability taken as the nearest multiple of 2^-46 (exact from 2^-22 up) and the rest exact. Where
  *   max(p - q, 0) is 0 everywhere, w = p. A one-hot target row decodes greedily.
  *   out_tokens [num_reqs][T]: the accepted drafts, the drawn token, then -1; num_out [num_reqs]: how many of
- *   these are tokens (the count of query tokens whose keys stay, q_valid of kv_attn_weights).
+ *   these are tokens (the count of query tokens whose keys stay, q_valid of kv_attn_weights). Neither may overlap
+ *   draft_ids or num_drafts (num_out may be num_drafts itself).
  * Probabilities are in [0, 1] (for the drawing, values outside are clamped and NaN counts as 0), a row's sum below
  * 2^17; each u in [0, 1) (taken to [0, 1 - 2^-24], NaN to 0). A draft id outside [0, vocab) is not accepted (the next
  * token is then drawn from max(p - q, 0) as after any other, and without draft_probs from the whole of p), a row

@@ -459,6 +459,13 @@ extern "C" pkv_status pkv_spec_verify_accept(const void* target_probs, int64_t t
           "%s: probabilities must be aligned to their type", name);
   PKV_ARG(target_stride_tok >= 0 && target_stride_req >= 0 && draft_stride_tok >= 0 && draft_stride_req >= 0,
           "%s: strides must not be negative", name);
+  // a request's CTAs read its drafts while another's write their tokens (num_out over num_drafts: each after it has been read)
+  const uint64_t reqs = (uint64_t)num_reqs * 4, tokens = reqs * (uint64_t)T, ids = reqs * (uint64_t)(T - 1);
+  PKV_ARG((T == 1 || (!overlaps(out_tokens, tokens, draft_ids, ids) && !overlaps(num_out, reqs, draft_ids, ids))) &&
+              !overlaps(out_tokens, tokens, num_out, reqs) &&
+              (!num_drafts || (!overlaps(out_tokens, tokens, num_drafts, reqs) &&
+                               (num_out == num_drafts || !overlaps(num_out, reqs, num_drafts, reqs)))),
+          "%s: out_tokens and num_out must not overlap draft_ids, num_drafts or each other", name);
   AcceptParams p{target_probs, T > 1 ? draft_probs : nullptr, target_stride_req, target_stride_tok, draft_stride_req,
                  draft_stride_tok, draft_ids, u_accept, u_sample, num_drafts, T, vocab, out_tokens, num_out, dev_err};
   cudaStream_t st = static_cast<cudaStream_t>(stream);

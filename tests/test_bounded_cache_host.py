@@ -2,7 +2,7 @@
 import numpy as np
 import pytest
 
-from test_step_host import COMPACT, SELECT, WEIGHTS, pkv  # noqa: F401
+from test_step_host import ACCEPT, COMPACT, SELECT, WEIGHTS, pkv  # noqa: F401
 
 
 def refused(pkv, call, values, word):  # noqa: F811
@@ -40,3 +40,14 @@ def test_rows_of_weights_in_any_order_are_taken(pkv, call, base):  # noqa: F811
     for change in (dict(wr=32, wh=16), dict(wr=16, wh=48), dict(wr=2 ** 62, wh=16), dict(R=1, wr=0, wh=16), dict(hkv=1, wr=16, wh=0),
                    dict(R=1, hkv=1, wr=0, wh=0)):
         refused(pkv, call, {**base, **change}, b"workspace")
+
+
+@pytest.mark.parametrize("change", [
+    dict(out=0x1000), dict(out=0x1000 + 4 * 2 * 3 - 4), dict(out=0x1000 - 4 * 2 * 4 + 4),  # tokens over the drafts
+    dict(num=0x1000), dict(num=0x1000 - 4), dict(num=0x2000), dict(num=0x2000 + 4 * 2 * 4 - 4),
+    dict(nd=0x2004), dict(nd=0x3004), dict(nd=0x2ffc),
+])
+def test_accept_refuses_outputs_over_its_drafts(pkv, change):  # noqa: F811
+    """A request's drafts are read while another's tokens are written."""
+    base = {**ACCEPT, "tp": 0x100000, "dp": 0x200000, "R": 2, "ids": 0x1000, "out": 0x2000, "num": 0x3000, "nd": 0x4000}
+    refused(pkv, "pkv_spec_verify_accept", {**base, **change}, b"overlap")

@@ -63,6 +63,21 @@ def test_accept_ids_out_of_range(pkv, bad):
         assert got[2] == pkv.PKV_ERR_DEVICE_BOUNDS
 
 
+def test_accept_counts_in_place(pkv):
+    """num_out over num_drafts, many requests: each count is read before its own is written."""
+    R, T, V = 700, 4, 300
+    g = torch.Generator().manual_seed(4)
+    P, Q = torch.softmax(torch.randn(R, T, V, generator=g), -1).to(DEV), torch.softmax(torch.randn(R, T - 1, V, generator=g), -1).to(DEV)
+    ids = torch.randint(0, V, (R, T - 1), generator=g, dtype=torch.int32).to(DEV)
+    ua, us = torch.rand(R, T - 1, generator=g).to(DEV), torch.rand(R, generator=g).to(DEV)
+    nd = torch.randint(0, T, (R,), generator=g, dtype=torch.int32).to(DEV)
+    want = accept(pkv, P, Q, ids, ua, us, nd)
+    out = torch.zeros(R, T, dtype=torch.int32, device=DEV)
+    pkv.spec_verify_accept(P, Q, ids, ua, us, out, nd, num_drafts=nd)
+    torch.cuda.synchronize()
+    assert np.array_equal(out.cpu().numpy(), want[0]) and np.array_equal(nd.cpu().numpy(), want[1])
+
+
 # ------------------------------------------------------------------------------------------------
 # attention weights
 # ------------------------------------------------------------------------------------------------
