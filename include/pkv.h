@@ -524,7 +524,8 @@ PKV_API pkv_status pkv_spec_verify_accept(const void* target_probs, int64_t targ
  *   then come from the splits that there are, and are too large.
  *   q_valid (nullable: T each): the first tokens that count, such as num_out of spec_verify_accept; the
  *   rejected drafts add nothing. Values outside [0, T] are clamped.
- *   prev (nullable): earlier weights, laid out as weights, which may be the same buffer; prev_lens (nullable:
+ *   prev (nullable): earlier weights, laid out as weights: the same buffer, or one that shares no element with
+ *   it; prev_lens (nullable:
  *   seq_lens): positions from prev_lens[r] on take nothing from prev, as for keys that are new.
  *   weights fp32, element strides w_stride_req and w_stride_head (rows must not overlap), positions
  *   contiguous, max_ctx of them; positions from seq_lens[r] on are left as they were.

@@ -41,6 +41,18 @@ inline bool rows_apart(int64_t reqs, int64_t stride_req, int64_t heads, int64_t 
   return reqs == 1 || heads == 1 || (stride_req - len) / (heads - 1) >= stride_head || (stride_head - len) / (reqs - 1) >= stride_req;
 }
 
+// Whether two arrays of such rows, the second's `shift` elements behind the first's, share an element.
+inline bool rows_meet(int64_t reqs, int64_t stride_req, int64_t heads, int64_t stride_head, int64_t len, int64_t shift) {
+  const __int128 reach = (__int128)(reqs - 1) * stride_req + (__int128)(heads - 1) * stride_head + len;
+  if (shift >= reach || -(__int128)shift >= reach) return false;
+  for (int64_t r = 1 - reqs; r < reqs; ++r)
+    for (int64_t h = 1 - heads; h < heads; ++h) {
+      const __int128 apart = shift - (__int128)r * stride_req - (__int128)h * stride_head;
+      if (apart < len && -apart < len) return true;
+    }
+  return false;
+}
+
 // Runs fn once per (flag, current device): for kernel attributes the driver keeps per device, such
 // as the dynamic shared-memory opt-in. Devices 64 and up run fn on every call.
 template <typename F>

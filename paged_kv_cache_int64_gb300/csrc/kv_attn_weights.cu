@@ -47,6 +47,11 @@ extern "C" pkv_status pkv_kv_attn_weights(const void* q, const void* k_cache, in
   PKV_UNSUP((int64_t)num_reqs * T <= INT32_MAX / num_q_heads, "%s: too many query rows", name);
   PKV_UNSUP(((int64_t)max_blocks * block_size / kWTile + 1) * num_reqs <= INT32_MAX / 2, "%s: too many keys", name);
   PKV_ARG(rows_apart(num_reqs, w_stride_req, num_kv_heads, w_stride_head, max_ctx), "%s: rows of weights must not overlap", name);
+  // (each key's earlier weight is read by the thread that writes the new one, at its own time)
+  PKV_ARG(!prev || prev == weights ||
+              !rows_meet(num_reqs, w_stride_req, num_kv_heads, w_stride_head, max_ctx,
+                         ((int64_t)reinterpret_cast<uintptr_t>(prev) - (int64_t)reinterpret_cast<uintptr_t>(weights)) / 4),
+          "%s: prev must be weights itself or share no element with it", name);
   const int64_t es = kv_dtype == PKV_KV_BF16 ? 2 : 1;
   PKV_ARG(stride_blk > 0 && stride_tok > 0 && stride_head > 0, "%s: strides must be positive", name);
   PKV_ARG(aligned16(q) && aligned16(k_cache) && stride_blk * es % 16 == 0 && stride_tok * es % 16 == 0 && stride_head * es % 16 == 0,

@@ -42,6 +42,31 @@ def test_rows_of_weights_in_any_order_are_taken(pkv, call, base):  # noqa: F811
         refused(pkv, call, {**base, **change}, b"workspace")
 
 
+W0 = 0x100000
+
+
+@pytest.mark.parametrize("R,hkv,wr,wh,mc,shift", [
+    (1, 1, 16, 16, 16, 1), (1, 1, 16, 16, 16, -15),                 # a key's place against another's
+    (2, 3, 48, 16, 16, 16), (2, 3, 48, 16, 16, 48), (2, 3, 48, 16, 16, -95), (2, 3, 48, 16, 16, 95),  # a head's, a request's
+    (2, 3, 96, 32, 16, 1), (2, 3, 96, 32, 16, 32 + 15), (2, 3, 96, 32, 16, 17),  # rows with room in between
+    (3, 2, 32, 96, 16, -64 + 15),
+])
+def test_earlier_weights_beside_their_own_place_are_refused(pkv, R, hkv, wr, wh, mc, shift):  # noqa: F811
+    base = {**WEIGHTS, "R": R, "hkv": hkv, "hq": hkv, "wr": wr, "wh": wh, "mc": mc, "w": W0}
+    refused(pkv, "pkv_kv_attn_weights", {**base, "prev": W0 + 4 * shift}, b"prev must be")
+
+
+@pytest.mark.parametrize("R,hkv,wr,wh,mc,shift", [
+    (1, 1, 16, 16, 16, 0), (2, 3, 48, 16, 16, 0), (1, 1, 16, 16, 16, 16), (2, 3, 48, 16, 16, -96), (2, 3, 48, 16, 16, 96),
+    (2, 3, 96, 32, 16, 16), (2, 3, 96, 32, 16, -16),                # interleaved rows
+    (2, 3, 192, 32, 16, 96), (3, 2, 32, 96, 16, 16), (20000, 4, 64, 16, 16, 20000 * 64),
+])
+def test_earlier_weights_apart_or_in_place_are_taken(pkv, R, hkv, wr, wh, mc, shift):  # noqa: F811
+    """The check after this one refuses."""
+    base = {**WEIGHTS, "R": R, "hkv": hkv, "hq": hkv, "wr": wr, "wh": wh, "mc": mc, "w": W0, "ws": 20}
+    refused(pkv, "pkv_kv_attn_weights", {**base, "prev": W0 + 4 * shift}, b"workspace")
+
+
 @pytest.mark.parametrize("change", [
     dict(out=0x1000), dict(out=0x1000 + 4 * 2 * 3 - 4), dict(out=0x1000 - 4 * 2 * 4 + 4),  # tokens over the drafts
     dict(num=0x1000), dict(num=0x1000 - 4), dict(num=0x2000), dict(num=0x2000 + 4 * 2 * 4 - 4),
