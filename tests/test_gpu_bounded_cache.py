@@ -1,5 +1,6 @@
 """The calls after the verify attention at the borders of what they take: uniform numbers out of
-range, log-sum-exps that do not reach, kept lists out of order, waits that run out."""
+range, log-sum-exps that do not reach, kept lists out of order, waits that run out, offsets past 32
+bits, sums that no rounding has touched."""
 import numpy as np
 import pytest
 import torch
@@ -76,6 +77,42 @@ def test_accept_counts_in_place(pkv):
     pkv.spec_verify_accept(P, Q, ids, ua, us, out, nd, num_drafts=nd)
     torch.cuda.synchronize()
     assert np.array_equal(out.cpu().numpy(), want[0]) and np.array_equal(nd.cpu().numpy(), want[1])
+
+
+def exact(x):
+    """fp32 values as integers in 2^-149."""
+    return [int(v) for v in np.ldexp(x.astype(np.float64), 149)]
+
+
+@pytest.mark.parametrize("sharp,near", [(2.0, 0.7), (12.0, 0.7), (12.0, 0.01), (2.0, 0.001)])
+def test_tokens_beside_unrounded_probabilities(pkv, sharp, near):
+    """The drawn token against sums that no rounding has touched. A value is taken to a multiple of 2^-46, so off by 2^-47
+    at most, a difference of two by 2^-46, a sum of V of them by V 2^-46; u times the total by as much, and by the one
+    unit that its floor takes: the token's own range of the exact sums, widened by (2 V + 1) 2^-46, holds u times the
+    exact total. More than a fifth of the sharp rows' values lie below 2^-47 and are taken to 0."""
+    R, V = 24, 4001
+    g = torch.Generator().manual_seed(int(sharp * 100 + near * 10))
+    base = sharp * torch.randn(R, 2, V, generator=g)
+    P = torch.softmax(base, -1)
+    Q = torch.softmax(base[:, :1] + near * torch.randn(R, 1, V, generator=g), -1)
+    ids = torch.randint(0, V, (R, 1), generator=g, dtype=torch.int32)
+    P[: R // 2, 0, 7], ids[: R // 2, 0] = 0.0, 7  # half of the drafts go
+    if sharp > 10:
+        assert (P < 2.0 ** -47).float().mean() > 0.2
+    us = torch.rand(R, generator=g)
+    tokens, num, status = accept(pkv, P, Q, ids, torch.zeros(R, 1), us, None)
+    assert status == 0
+    slack = (2 * V + 1) << (149 - 46)
+    for r in range(R):
+        goes = r < R // 2 or P[r, 0, ids[r, 0]].item() == 0.0
+        assert num[r] == (1 if goes else 2)
+        p = exact(P[r, 0 if goes else 1].numpy())
+        w = [max(a - b, 0) for a, b in zip(p, exact(Q[r, 0].numpy()))] if goes else p
+        total, i = sum(w), int(tokens[r, num[r] - 1])
+        assert total > 4 * slack
+        num_u, den_u = float(us[r]).as_integer_ratio()
+        before = sum(w[:i])
+        assert (before - slack) * den_u <= num_u * total < (before + w[i] + slack) * den_u
 
 
 # ------------------------------------------------------------------------------------------------
@@ -164,3 +201,54 @@ def test_compact_waits_that_run_out(pkv, fmt, lens, budget):
             t.copy_(f)
     assert x.run(pkv) == 0
     x.same(whole)
+
+
+# ------------------------------------------------------------------------------------------------
+# offsets past 32 bits
+# ------------------------------------------------------------------------------------------------
+
+def test_accept_over_rows_past_32_bits(pkv):
+    """Requests, then tokens, 2^32 elements apart."""
+    V = 1021
+    big = torch.empty(2 ** 32 + 3 * V, dtype=torch.bfloat16, device=DEV)
+    g = torch.Generator().manual_seed(1)
+    for R, T in ((2, 3), (1, 2)):
+        P = torch.softmax(2 * torch.randn(R, T, V, generator=g), -1).to(torch.bfloat16)
+        Q = torch.softmax(2 * torch.randn(R, T - 1, V, generator=g), -1).to(torch.bfloat16)
+        ids = torch.randint(0, V, (R, T - 1), generator=g, dtype=torch.int32)
+        ua, us = torch.zeros(R, T - 1), torch.rand(R, generator=g)  # every draft stays: the last row is read
+        strides = (2 ** 32, V, 1) if R == 2 else (0, 2 ** 32, 1)
+        far = big.as_strided((R, T, V), strides)
+        far.copy_(P)
+        want = accept(pkv, P, Q, ids, ua, us, None)
+        got = accept(pkv, far, Q, ids, ua, us, None)
+        assert (want[1] == T).all() and np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+        if R == 2:  # the draft's rows there, and every draft goes
+            gone = P.clone()
+            gone.scatter_(2, torch.nn.functional.pad(ids, (0, 1))[..., None].long(), 0.0)
+            far_q = big.as_strided((R, T - 1, V), strides)
+            far_q.copy_(Q)
+            want, got = accept(pkv, gone, Q, ids, ua, us, None), accept(pkv, gone, far_q, ids, ua, us, None)
+            assert (want[1] == 1).all() and np.array_equal(got[0], want[0])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "fp8"])
+def test_weights_in_a_pool_and_an_array_past_32_bits(pkv, fmt):
+    """Blocks, and requests of the weights, whose element offsets pass 2^32."""
+    bs, hkv, lens, T, g = 880, 4, [1700, 300], 2, 2
+    nb = 2 ** 32 // (bs * hkv * 256) + 8
+    c = Cache(fmt, lens, hkv, bs, seed=8, spare=0, extra_cols=0)
+    q = queries(2, T, hkv * g, seed=9)
+    place = torch.from_numpy(np.array([nb - 1, 5, nb - 3][:c.nb])).to(DEV)
+    pool = torch.empty(nb, bs, hkv, 256, dtype=c.pool.dtype, device=DEV)
+    pool[place] = c.pool
+    if fmt == "int8":
+        scale = torch.empty(nb, bs, hkv, device=DEV)
+        scale[place] = c.scale
+        c.scale = scale
+    c.pool, c.table = pool, place[c.table.clamp(min=0).long()].int()
+    buffer = torch.empty(2 ** 32 + hkv * 1800, device=DEV)
+    w = buffer.as_strided((2, hkv, 1800), (2 ** 32, 1800, 1))
+    w.fill_(-7.0)
+    assert weigh(pkv, c, q.to(DEV), T, 1 / 16, w) == 0
+    verify_weights(w, expect(c, q, T, 1 / 16), lens, tail=-7.0)
