@@ -11,8 +11,9 @@
 // rows are widened to fp16 in registers (every code is an fp16 value) and stored to tensor memory as the A operand. Both
 // operands have one type, so the queries of a (request, KV head) then become fp16 too, times the power of two that takes
 // the largest of them to [2^14, 2^15): elements down to 2^-28 of the largest keep all of their bits, smaller ones are
-// taken to 2^-39 of it. (Widening to bf16 instead, which needs no change to the queries, takes twice the instructions,
-// and these are what bounds the kernel: int8 137 us, e4m3 131 for eight tokens over 32 requests of up to 40,960 keys.)
+// taken to 2^-39 of it (a score moves by that times the key's sum of magnitudes at most). (Widening to bf16 instead, which
+// needs no change to the queries, takes twice the instructions, and these are what bounds the kernel: int8 137 us, e4m3 131
+// for eight tokens over 32 requests of up to 40,960 keys.)
 //
 // The tiles of all (request, 128 keys) are one list, cut into equal ranges from the lengths on the device. A range has a
 // CTA a KV head, side by side, so that the heads' parts of a token's row are read together (a head's tiles of all

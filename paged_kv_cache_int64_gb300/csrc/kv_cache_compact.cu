@@ -145,7 +145,8 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactParams p
   __shared__ int s_go;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // chunks in the order (request, rows, KV head): the heads of the same rows run side by side, so that the pieces of a
-  // token's row are written (and mostly read) together (16 requests of up to 32,768 keys: 218 us with a head after the other)
+  // token's row are written (and mostly read) together (16 requests of up to 32,768 keys, before later steps: 215 us with a
+  // head after the other, 179 so)
   auto chunk_of = [&](int64_t c, int& unit, int& j0, int& n) {
     const int per = p.chunks * p.num_kv_heads;
     const int r = (int)(c / per), in = (int)(c - (int64_t)r * per), at = in / p.num_kv_heads;

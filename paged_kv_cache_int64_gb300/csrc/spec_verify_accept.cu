@@ -5,7 +5,12 @@
 // draft, from p itself: the smallest i whose running sum passes u times the total.
 //
 // The sums are integers: each probability as the nearest multiple of 2^-46 (exact from 2^-22 up), so they do not depend on
-// the order in which they are added, and the token is the one that exact arithmetic gives.
+// the order in which they are added, and the token is the one that exact arithmetic gives for these multiples. What the
+// rounding does: a value moves by 2^-47 at most (one below that becomes 0 and is not drawn), a running sum over V tokens by
+// V 2^-47, that of a difference by V 2^-46: 2^-30 and 2^-29 over 131,072 tokens, where u itself comes in steps of
+// 2^-24. Where little is left of p (q close to it), that is more beside what is left, but then a draft goes as rarely. Multiples
+// of 2^-58 would take sums of 64-bit integers in the loop: 31 us where the parts below took 25 (64 requests over 131,072
+// tokens, fp32; 19 since).
 //
 // One cluster of CTAs a request, one pass over one row of p (and one of q). Each warp sums a contiguous segment of
 // the row and gives the sum to every CTA; the warp whose segment holds the target reads it again, from its own SM's
