@@ -182,6 +182,16 @@ def test_compact_in_place_with_a_list_out_of_order(pkv, fmt, kind, budget):
     x.same(want)
 
 
+def test_compact_in_place_with_a_long_list_out_of_order(pkv):
+    """More parts of a list than a warp has lanes: one entry, in the last of them."""
+    budget = 32 * 4096 + 9000
+    x = Rows("fp4", [2 * budget + 40, 300], 1, 16, budget, seed=1, dense="front")
+    x.keep[0, 0] = not_ascending("late", budget, None)
+    want = x.expect(skip=lambda r, h, j: r == 0 and j == budget - 69)
+    assert x.run(pkv) == pkv.PKV_ERR_DEVICE_BOUNDS
+    x.same(want)
+
+
 @pytest.mark.parametrize("fmt", list(FORMATS))
 @pytest.mark.parametrize("lens,budget", [([700, 30, 650], 600), ([9000, 32, 8000], 7000)])
 def test_compact_waits_that_run_out(pkv, fmt, lens, budget):
