@@ -12,10 +12,11 @@
 // then (raised after the wait, flags would hang on each other in a row, a chunk's time each, where rows move by a little), so
 // its rows may be written over: after such a status the rows of its (request, KV head) are undefined.
 //
-// Those two chunks are searched for, which takes a keep that ascends. Whether it does is looked at by the kernel that sets the
-// flags to 0: where it does not, a chunk waits for all lower chunks, as an entry that is not valid moves nothing, and one
-// that is valid, from >= j, is read by a lower chunk or the chunk itself. In small calls it waits for all lower ones in any case,
-// and a memset sets the flags.
+// Those two chunks are searched for, which takes a keep that ascends. Whether it does the CTAs look at together, each at some
+// parts of it while its first chunk's rows are on their way, and a word a unit counts the parts that do. Where one does not,
+// a chunk waits for all lower chunks: an entry that is not valid moves nothing, and one that is valid, from >= j, is read by
+// a lower chunk or the chunk itself. (16 requests of up to 32,768 in bf16 / int8 / e4m3 / 4 bits: 164 / 118 / 105 / 100 us, and
+// 164 / 114 / 104 / 100 for an order taken on trust; a launch of its own that looks at it: 166 / 121 / 109 / 105.)
 #include "host_common.h"
 #include "sm103.cuh"
 
@@ -26,11 +27,8 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRows = 32;  // rows of a chunk
 static_assert(kRows * 8 % kThreads == 0 && 2 * kRows <= kThreads, "pieces and scales a thread");
-// chunks of a unit up to which, where an SM has no more than one, all lower ones are waited for: a load a lane
-constexpr int kAllChunks = 32;
-constexpr int kPartChunks = 128;                // chunks of a part of keep, whose order is looked at by one CTA
-constexpr int kPartRows = kPartChunks * kRows;  // (16 a thread, all on their way at once)
-static_assert(kPartChunks <= kThreads && kPartRows % kThreads == 0, "flags and entries a thread");
+constexpr int kPartRows = 1024;  // of keep, whose order one CTA looks at (4 a thread, on their way at once)
+constexpr uint32_t kUnordered = 1u << 31;
 
 struct CompactParams {
   uint8_t* k;
@@ -49,10 +47,10 @@ struct CompactParams {
   int64_t total;  // chunks of all units
   float* weights;
   int64_t w_stride_req, w_stride_head, max_ctx;
-  int32_t parts;        // of keep, a unit
-  int64_t units;
-  uint32_t* flags;      // workspace: [units][chunks], the chunk has its rows
-  uint32_t* unordered;  // workspace: [units][parts], an entry of the part is not above the one before it; null: all lower chunks
+  int32_t parts;    // of a unit's keep
+  int64_t all_parts;
+  uint32_t* flags;  // workspace: [units][chunks], the chunk has its rows
+  uint32_t* order;  // workspace: [units], the parts that ascend; kUnordered: one does not
   int* dev_err;
   uint64_t wait_limit_ns;
 };
@@ -66,6 +64,11 @@ struct Move {
 __device__ __forceinline__ uint32_t load_acquire(const uint32_t* p) {
   uint32_t x;
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
+  return x;
+}
+__device__ __forceinline__ uint32_t load_relaxed(const uint32_t* p) {
+  uint32_t x;
+  asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(x) : "l"(p) : "memory");
   return x;
 }
 __device__ __forceinline__ void store_release(uint32_t* p, uint32_t x) {
@@ -115,30 +118,32 @@ __device__ int first_at_least(const int32_t* keep, int n, int x, int lane) {
   return lo;
 }
 
-// Flags to 0, and whether each part of keep ascends.
-__global__ void __launch_bounds__(kThreads) prepare_kernel(const CompactParams p) {
-  const int tid = threadIdx.x;
-  for (int64_t at = blockIdx.x; at < p.units * p.parts; at += gridDim.x) {
+// Whether each of the CTA's parts of keep ascends.
+__device__ __forceinline__ void look_at_order(const CompactParams& p) {
+#pragma unroll 1
+  for (int64_t at = blockIdx.x; at < p.all_parts; at += gridDim.x) {
     const int64_t unit = at / p.parts;
     const int part = (int)(at - unit * p.parts);
     const int len = __ldg(p.new_lens + unit / p.num_kv_heads);
     const int32_t* keep = p.keep + unit * p.budget;
-    const int chunk = part * kPartChunks + tid;
-    if (tid < kPartChunks && chunk < p.chunks) p.flags[unit * p.chunks + chunk] = 0;
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < kPartRows / kThreads; ++i) {
-      const int64_t j = (int64_t)part * kPartRows + i * kThreads + tid;
-      if (j > 0 && j < p.budget) bad |= __ldg(keep + j) <= __ldg(keep + j - 1) && j < len;  // (len may be on its way)
+      const int64_t j = (int64_t)part * kPartRows + i * kThreads + threadIdx.x;
+      if (j > 0 && j < p.budget) bad |= __ldg(keep + j) <= __ldg(keep + j - 1) && j < len;
     }
     bad = __syncthreads_or(bad);
-    if (tid == 0) p.unordered[at] = bad;
+    if (threadIdx.x == 0) {
+      if (bad) atomicOr(p.order + unit, kUnordered);
+      else atomicAdd(p.order + unit, 1u);
+    }
   }
 }
 
 // kPieces: 16-byte pieces of a row; kScale: bytes of a row's scales (0, 4 or 16).
+// (registers: with a CTA an SM fewer than these, 4 bits take 111 us where they take 100)
 template <int kPieces, int kScale>
-__global__ void __launch_bounds__(kThreads) compact_kernel(const CompactParams p) {
+__global__ void __launch_bounds__(kThreads, kPieces == 16 && !kScale ? 8 : 6) compact_kernel(const CompactParams p) {
   constexpr int kPer = kRows * kPieces / kThreads;  // pieces a thread, of K and of V
   extern __shared__ __align__(16) uint8_t s_rows[];  // [K, V][kRows][row]
   __shared__ Move s_move[kRows];
@@ -198,6 +203,7 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactParams p
       }
       if (p.weights && tid < kRows && s_move[tid].from >= 0) wv = w[s_move[tid].from];
     }
+    if (c == blockIdx.x && p.chunks > 1) look_at_order(p);  // (while the first chunk's rows are on their way)
     // the next chunk's places
     if (c + gridDim.x < p.total) {
       chunk_of(c + gridDim.x, unit, j0, n);
@@ -207,38 +213,38 @@ __global__ void __launch_bounds__(kThreads) compact_kernel(const CompactParams p
     uint32_t* flags = p.flags + (int64_t)my_unit * p.chunks;
     if (moves) {
       int dep = 0, dep_last = -1;
+      uint32_t seen = 0;
       if (warp == kWarps - 1 && ci) {
-        // whether a part that has lower chunks is out of order (of 32 parts a load a lane, on its way beside the search)
-        const uint32_t* parts = p.unordered + (int64_t)my_unit * p.parts;
-        const int last_part = (ci - 1) / kPartChunks;
-        uint32_t odd = !p.unordered;
-        if (p.unordered) {
-          if (lane <= last_part) odd = parts[lane];
-          // rows whose source lies in this chunk's destinations: at most kRows in a row from the first
-          const int j = first_at_least(p.keep + (int64_t)my_unit * p.budget, my_j0, my_j0, lane);
-          if (j < my_j0) {
-            dep = j / kRows;
-            dep_last = min(j + kRows - 1, my_j0 - 1) / kRows;
-          }
-          for (int i = lane + 32; i <= last_part; i += 32) odd |= parts[i];
+        seen = load_relaxed(p.order + my_unit);
+        // rows whose source lies in this chunk's destinations: at most kRows in a row from the first
+        const int j = first_at_least(p.keep + (int64_t)my_unit * p.budget, my_j0, my_j0, lane);
+        if (j < my_j0) {
+          dep = j / kRows;
+          dep_last = min(j + kRows - 1, my_j0 - 1) / kRows;
         }
-        if (__any_sync(0xffffffffu, odd)) dep = 0, dep_last = ci - 1;
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
       __syncthreads();  // every thread has its part of the rows
       if (warp == kWarps - 1) {
         if (lane == 0 && !last_chunk) store_release(flags + ci, 1u);
-        if (dep + lane <= dep_last) {
+        if (ci) {
           const uint64_t t0 = globaltimer_ns();
           const bool brief = p.wait_limit_ns < kSuspendHintNs;  // (a test's bound: it counts as run out at once)
-          for (int i = dep + lane; i <= dep_last;) {
-            if (!brief && load_acquire(flags + i)) {
+          bool ok = true;
+          while (seen < (uint32_t)p.parts && ok) {  // (kUnordered is above)
+            ok = !brief && globaltimer_ns() - t0 <= p.wait_limit_ns;
+            seen = load_relaxed(p.order + my_unit);
+          }
+          if (seen & kUnordered) dep = 0, dep_last = ci - 1;
+          for (int i = dep + lane; ok && i <= dep_last;) {
+            if (!brief && load_acquire(flags + i))
               i += 32;
-            } else if (brief || globaltimer_ns() - t0 > p.wait_limit_ns) {
-              record_error(p.dev_err, kErrTimeout);
-              s_go = 0;
-              break;
-            }
+            else
+              ok = !brief && globaltimer_ns() - t0 <= p.wait_limit_ns;
+          }
+          if (!ok) {
+            record_error(p.dev_err, kErrTimeout);
+            s_go = 0;
           }
         }
       }
@@ -289,14 +295,8 @@ pkv_status launch(const CompactParams& p, cudaStream_t st) {
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (p.chunks > 1 && !p.unordered) {
-    if (cudaMemsetAsync(p.flags, 0, (size_t)p.total * 4, st) != cudaSuccess) return check_launch("kv_cache_compact");
-  } else if (p.chunks > 1) {
-    const int64_t parts = p.units * p.parts;
-    prepare_kernel<<<(unsigned)(parts < INT32_MAX ? parts : INT32_MAX), kThreads, 0, st>>>(p);
-    const pkv_status s = check_launch("kv_cache_compact");
-    if (s != PKV_OK) return s;
-  }
+  if (p.chunks > 1 && cudaMemsetAsync(p.flags, 0, (size_t)(p.total + p.total / p.chunks) * 4, st) != cudaSuccess)
+    return check_launch("kv_cache_compact");
   cudaLaunchKernelEx(&cfg, compact_kernel<kPieces, kScale>, p);
   return check_launch("kv_cache_compact");
 }
@@ -307,8 +307,7 @@ pkv_status launch(const CompactParams& p, cudaStream_t st) {
 extern "C" size_t pkv_kv_cache_compact_workspace_bytes(int32_t num_reqs, int32_t num_kv_heads, int32_t budget) {
   if (num_reqs <= 0 || num_kv_heads <= 0 || budget <= 0) return 0;
   const size_t chunks = ((size_t)budget + pkv::kRows - 1) / pkv::kRows;
-  const size_t parts = (chunks + pkv::kPartChunks - 1) / pkv::kPartChunks;
-  return ((size_t)num_reqs * (size_t)num_kv_heads * (chunks + parts) * 4 + 255) & ~(size_t)255;
+  return ((size_t)num_reqs * (size_t)num_kv_heads * (chunks + 1) * 4 + 255) & ~(size_t)255;
 }
 
 extern "C" pkv_status pkv_kv_cache_compact(void* k_cache, void* v_cache, int32_t kv_dtype, int64_t num_blocks,
@@ -372,12 +371,10 @@ extern "C" pkv_status pkv_kv_cache_compact(void* k_cache, void* v_cache, int32_t
   p.dev_err = dev_err;
   p.chunks = (budget + kRows - 1) / kRows;
   p.total = (int64_t)num_reqs * num_kv_heads * p.chunks;
-  p.parts = (p.chunks + kPartChunks - 1) / kPartChunks;
-  p.units = (int64_t)num_reqs * num_kv_heads;
+  p.parts = (budget + kPartRows - 1) / kPartRows;
+  p.all_parts = (int64_t)num_reqs * num_kv_heads * p.parts;
   p.flags = static_cast<uint32_t*>(workspace);
-  // The kernel takes 2 us more than a memset (one request of 1,024, budget 512: 12.5 us and 10.3), waiting for every lower chunk
-  // more where many run at once (16 of up to 4,096, budget 1,024: 35.0 us searched for, 36.6 without; budget 8,192: 167 and 185).
-  p.unordered = p.chunks > kAllChunks || p.total > num_sms() ? p.flags + p.total : nullptr;
+  p.order = p.flags + p.total;
   p.wait_limit_ns = take_wait_limit_ns();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (kv_dtype) {
