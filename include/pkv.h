@@ -525,8 +525,8 @@ PKV_API pkv_status pkv_spec_verify_accept(const void* target_probs, int64_t targ
  *   q_valid (nullable: T each): the first tokens that count, such as num_out of spec_verify_accept; the
  *   rejected drafts add nothing. Values outside [0, T] are clamped.
  *   prev (nullable): earlier weights, laid out as weights: the same buffer, or one that shares no element with
- *   it; prev_lens (nullable:
- *   seq_lens): positions from prev_lens[r] on take nothing from prev, as for keys that are new.
+ *   it; prev_lens (nullable: seq_lens): positions from prev_lens[r] on take nothing from prev, as for keys that are
+ *   new.
  *   weights fp32, element strides w_stride_req and w_stride_head (rows must not overlap), positions
  *   contiguous, max_ctx of them; positions from seq_lens[r] on are left as they were.
  * Keys in a bad block, or past the table, read as zero and set PKV_ERR_DEVICE_BOUNDS; so does a seq_lens[r]
