@@ -15,8 +15,8 @@
 // Those two chunks are searched for, which takes a keep that ascends. Whether it does the CTAs look at together, each at some
 // parts of it while its first chunk's rows are on their way, and a word a unit counts the parts that do. Where one does not,
 // a chunk waits for all lower chunks: an entry that is not valid moves nothing, and one that is valid, from >= j, is read by
-// a lower chunk or the chunk itself. (16 requests of up to 32,768 in bf16 / int8 / e4m3 / 4 bits: 164 / 118 / 105 / 100 us, and
-// 164 / 114 / 104 / 100 for an order taken on trust; a launch of its own that looks at it: 166 / 121 / 109 / 105.)
+// a lower chunk or the chunk itself. (16 requests of up to 32,768 in int8 / e4m3 / 4 bits, six, eight and six CTAs an SM:
+// 120 / 106 / 101 us, 116 / 105 / 101 for an order taken on trust, 121 / 109 / 105 with a launch of its own that looks at it.)
 #include "host_common.h"
 #include "sm103.cuh"
 
@@ -141,9 +141,10 @@ __device__ __forceinline__ void look_at_order(const CompactParams& p) {
 }
 
 // kPieces: 16-byte pieces of a row; kScale: bytes of a row's scales (0, 4 or 16).
-// (registers: with a CTA an SM fewer than these, 4 bits take 111 us where they take 100)
+// (CTAs an SM: as many as shared memory holds of bf16's; the others eight, a few registers spilled: int8 112 us, 4 bits 94, with
+// six 120 and 101)
 template <int kPieces, int kScale>
-__global__ void __launch_bounds__(kThreads, kPieces == 16 && !kScale ? 8 : 6) compact_kernel(const CompactParams p) {
+__global__ void __launch_bounds__(kThreads, kPieces == 32 ? 6 : 8) compact_kernel(const CompactParams p) {
   constexpr int kPer = kRows * kPieces / kThreads;  // pieces a thread, of K and of V
   extern __shared__ __align__(16) uint8_t s_rows[];  // [K, V][kRows][row]
   __shared__ Move s_move[kRows];
